@@ -8,6 +8,7 @@ the library is missing or CUDA is unavailable the call fails.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -18,13 +19,13 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 # bounds checks, libfathom_debug.so) to load instead of the default one.
 LIB_PATH = os.environ.get("FATHOM_LIB") or os.path.join(_PKG, "_build", "libfathom.so")
 
-F32, BF16 = 0, 1
+F32, BF16, F16 = 0, 1, 2
 WS_SCAN_TOPK, WS_SPARSE_ATTN, WS_DENSE_ATTN, WS_KLT_ONLINE = 0, 1, 2, 3
 SRC_STORE, SRC_STAGING = 0, 1
 MAX_D, MAX_G, MAX_K = 128, 8, 2048
 
 # (name, restype, argtypes) of every symbol include/fathom.h declares
-_vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+_vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
 
 class Shape(ctypes.Structure):
@@ -41,6 +42,30 @@ class Shape(ctypes.Structure):
     def cap(self) -> int:
         """Tokens the per-unit arrays are laid out for."""
         return self.n_cap if self.n_cap > 0 else self.n
+
+
+class Prompts(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("seqs", "heads", "kv_heads", "D", "dtype", "total_q", "total_k")] + \
+               [(f, ctypes.c_int64) for f in ("q_token", "q_head", "k_token", "k_head", "v_token", "v_head",
+                                              "out_token", "out_head")]
+
+
+class Pages(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("seqs", "kv_heads", "D", "dtype", "page_tokens", "num_pages",
+                                              "max_pages")] + \
+               [(f, ctypes.c_int64) for f in ("page_stride", "head_stride", "token_stride")]
+
+    def __repr__(self):
+        return "Pages(" + ", ".join(f"{f}={getattr(self, f)}" for f, _ in self._fields_) + ")"
+
+    @property
+    def units(self) -> int:
+        return self.seqs * self.kv_heads
+
+    @property
+    def cap(self) -> int:
+        """Tokens a row of the page table can name."""
+        return self.max_pages * self.page_tokens
 
 
 RUN_FIELDS = ("src_word", "n_words", "dst_word", "src_scale", "n_scales", "dst_scale")
@@ -69,6 +94,14 @@ SIGNATURES = {
                                                  _vp]),
     "fathom_sparse_attn_noalloc": (ctypes.c_int, [ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp, _vp]),
     "fathom_klt_online": (ctypes.c_int, [ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "fathom_prefill_attn": (ctypes.c_int, [ctypes.POINTER(Prompts), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "fathom_paged_append": (ctypes.c_int, [ctypes.POINTER(Pages), _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _vp, _vp,
+                                           _vp]),
+    "fathom_paged_attn": (ctypes.c_int, [ctypes.POINTER(Pages), _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _sz,
+                                         _vp]),
+    "fathom_paged_evict": (ctypes.c_int, [ctypes.POINTER(Pages), _vp, _vp, _vp, _vp, _vp, _sz, _i32, _i32, _i32, _vp,
+                                          _i32, _vp, _vp, _vp, _sz, _vp]),
+    "fathom_paged_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(Pages), _i32, ctypes.c_int]),
     "fathom_rel_err": (ctypes.c_int, [_i32, _i32, _vp, _vp, _vp, _vp]),
     "fathom_set_overlap": (ctypes.c_int, [_i32, _i32, _vp, _vp, _vp, _vp]),
     "fathom_greedy_budgets": (ctypes.c_int, [_i32, _i32, _vp, _i32, _i32, _i32, _vp]),
@@ -562,6 +595,225 @@ def fathom_sparse_attn(shape: Shape, k_rows, v_rows, q, topk_idx, workspace, out
     _call("fathom_sparse_attn", ctypes.byref(shape), _p(k_rows), _p(v_rows), _p(q), _p(topk_idx),
           _p(out), _p(workspace), workspace.numel(), _stream(stream))
     return out
+
+
+# ------------------------------------------------------- prompts and paged caches
+_ROW_TYPES = {torch.bfloat16: BF16, torch.float16: F16}
+
+
+@contextlib.contextmanager
+def _on(stream, *tensors):
+    """The tensors' device made current (one device: the library launches on the
+    current one) and, when a stream is given, that stream: outputs allocated inside
+    belong to the stream that writes them."""
+    devices = {t.device for t in tensors if t is not None and t.is_cuda}
+    if len(devices) > 1:
+        raise ValueError(f"tensors on several devices: {sorted(map(str, devices))}")
+    with contextlib.ExitStack() as stack:
+        if devices:
+            device = devices.pop()
+            if stream is not None and stream.device != device:
+                raise ValueError(f"stream on {stream.device}, tensors on {device}")
+            if device.index != torch.cuda.current_device():
+                stack.enter_context(torch.cuda.device(device))
+        if stream is not None:
+            stack.enter_context(torch.cuda.stream(stream))
+        yield
+
+
+def _check_strided(t, name, dtypes, shape, pinned=False):
+    """A tensor of these sizes whose last axis is contiguous, the others strided as
+    they are; every element behind its pointer lies in the tensor's storage.  Device
+    memory (pinned: or pinned host memory)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    if not (_reachable(t) if pinned else _on_device(t)):
+        raise ValueError(f"{name} must be a CUDA tensor" + (" or pinned host memory" if pinned else ""))
+    return t
+
+
+def _on_device(t) -> bool:
+    return t.is_cuda
+
+
+def fathom_prefill_attn(q, k, v, cu_q, cu_k=None, out=None, lse=None, want_lse=False, stream=None):
+    """Causal attention of packed prompts (or of their next chunks): q [Tq][heads][D],
+    k, v [Tk][kv_heads][D] bf16 or fp16, any strides with the last axis contiguous;
+    cu_q, cu_k [seqs + 1] int32 (cu_k None: cu_q, whole prompts).  -> (out [Tq][heads][D]
+    of q's type, lse [Tq][heads] fp32 or None; rows behind cu_q[-1] are not written)."""
+    if q is None or q.dim() != 3:
+        raise ValueError("q: expected [tokens][heads][D]")
+    Tq, H, D = q.shape
+    _check_strided(q, "q", tuple(_ROW_TYPES), (Tq, H, D))
+    if k is None or k.dim() != 3:
+        raise ValueError("k: expected [tokens][kv_heads][D]")
+    Tk, Hkv = k.shape[0], k.shape[1]
+    _check_strided(k, "k", (q.dtype,), (Tk, Hkv, D))
+    _check_strided(v, "v", (q.dtype,), (Tk, Hkv, D))
+    cu_k = cu_q if cu_k is None else cu_k
+    _check(cu_q, "cu_q", (torch.int32,))
+    _check(cu_k, "cu_k", (torch.int32,), tuple(cu_q.shape))
+    if cu_q.dim() != 1 or cu_q.shape[0] < 2:
+        raise ValueError(f"cu_q: shape {tuple(cu_q.shape)} is not [seqs + 1]")
+    if out is not None:
+        _check_strided(out, "out", (q.dtype,), (Tq, H, D))
+    if lse is not None:
+        _check(lse, "lse", (torch.float32,), (Tq, H))
+    with _on(stream, q, k, v, cu_q, cu_k, out, lse):
+        if out is None:
+            out = torch.empty(Tq, H, D, dtype=q.dtype, device=q.device)
+        if lse is None and want_lse:
+            lse = torch.empty(Tq, H, dtype=torch.float32, device=q.device)
+        p = Prompts(cu_q.shape[0] - 1, H, Hkv, D, _ROW_TYPES[q.dtype], Tq, Tk, q.stride(0), q.stride(1), k.stride(0),
+                    k.stride(1), v.stride(0), v.stride(1), out.stride(0), out.stride(1))
+        _call("fathom_prefill_attn", ctypes.byref(p), _p(q), _p(k), _p(v), _p(cu_q), _p(cu_k), _p(out), _p(lse),
+              _stream(stream))
+    return out, lse
+
+
+def make_pages(k_pages, page_table) -> Pages:
+    """The layout of a paged cache: k_pages a [pages][kv_heads][page_tokens][D] view of
+    bf16 or fp16 rows (any strides, the last axis contiguous; v_pages must have the
+    same), page_table [seqs][max_pages] int32."""
+    if k_pages.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("k_pages: expected [pages][kv_heads][page_tokens][D], page_table: [seqs][max_pages]")
+    if k_pages.dtype not in _ROW_TYPES:
+        raise TypeError(f"k_pages: dtype {k_pages.dtype} not in {tuple(_ROW_TYPES)}")
+    n, H, P, D = k_pages.shape
+    sn, sh, sp, _ = k_pages.stride()
+    return Pages(page_table.shape[0], H, D, _ROW_TYPES[k_pages.dtype], P, n, page_table.shape[1], sn, sh, sp)
+
+
+def rows_as_pages(rows, kv_heads, page_tokens=64, device=None):
+    """Rows [units][C][D] of the other calls (units packed sequence, KV head; page_tokens
+    divides C) seen as a paged cache: (view [pages][kv_heads][page_tokens][D], page_table
+    [seqs][C / page_tokens] on `device`, the rows' by default).  The view shares the
+    rows' memory."""
+    U, C, D = rows.shape
+    if not rows.is_contiguous() or U % kv_heads or C % page_tokens:
+        raise ValueError("rows: contiguous [units][C][D], kv_heads dividing units and page_tokens dividing C")
+    seqs, per = U // kv_heads, C // page_tokens
+    # page number x page_tokens * D elements; a sequence's pages are those of its first head
+    count = (seqs - 1) * kv_heads * per + per
+    view = rows.as_strided((count, kv_heads, page_tokens, D), (page_tokens * D, C * D, D, 1))
+    table = (torch.arange(seqs, dtype=torch.int32)[:, None] * (kv_heads * per) +
+             torch.arange(per, dtype=torch.int32)[None, :]).to(device or rows.device)
+    return view, table
+
+
+def _check_cache(pages, k_pages, v_pages, page_table):
+    dtype = torch.bfloat16 if pages.dtype == BF16 else torch.float16
+    shape = (pages.num_pages, pages.kv_heads, pages.page_tokens, pages.D)
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        _check_strided(t, name, (dtype,), shape, pinned=True)
+        st = t.stride()
+        if any(a > 1 and x != y for a, x, y in zip(shape, st, (pages.page_stride, pages.head_stride,
+                                                               pages.token_stride))):
+            raise ValueError(f"{name}: strides {st[:3]} are not those of pages")
+    _check(page_table, "page_table", (torch.int32,), (pages.seqs, pages.max_pages))
+
+
+def paged_workspace_size(pages: Pages, G: int, mass=False) -> int:
+    return int(lib().fathom_paged_workspace_size(ctypes.byref(pages), int(G), int(bool(mass))))
+
+
+def alloc_paged_workspace(pages: Pages, G=4, mass=False, device="cuda") -> torch.Tensor:
+    """Workspace of fathom_paged_attn (mass: also large enough for calls with it)."""
+    nbytes = paged_workspace_size(pages, G, mass)
+    if nbytes == 0:
+        raise FathomError("fathom_paged_workspace_size", 1, lib().fathom_last_error().decode())
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def fathom_paged_append(pages: Pages, k_pages, v_pages, page_table, k_new, v_new, start, cu_new=None, stream=None):
+    """Write new rows k_new, v_new [T][kv_heads][D] (strided alike, the last axis contiguous)
+    into the cache, in place: token i of sequence s at position start[s] + i.  start [seqs]
+    int32; cu_new [seqs + 1] int32, or None: one token per sequence."""
+    _check_cache(pages, k_pages, v_pages, page_table)
+    if k_new is None or k_new.dim() != 3:
+        raise ValueError("k_new: expected [tokens][kv_heads][D]")
+    T = k_new.shape[0]
+    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+        _check_strided(t, name, (k_pages.dtype,), (T, pages.kv_heads, pages.D))
+    if any(a > 1 and x != y for a, x, y in zip(k_new.shape[:2], k_new.stride(), v_new.stride())):
+        raise ValueError("v_new: strides differ from k_new's")
+    _check(start, "start", (torch.int32,), (pages.seqs,))
+    if cu_new is not None:
+        _check(cu_new, "cu_new", (torch.int32,), (pages.seqs + 1,))
+    elif T != pages.seqs:
+        raise ValueError(f"k_new: {T} tokens for {pages.seqs} sequences without cu_new")
+    with _on(stream, k_pages, v_pages, page_table, k_new, v_new, start, cu_new):
+        _call("fathom_paged_append", ctypes.byref(pages), _p(k_pages), _p(v_pages), _p(page_table), _p(k_new),
+              _p(v_new), T, k_new.stride(0), k_new.stride(1), _p(start), _p(cu_new), _stream(stream))
+    return k_pages, v_pages
+
+
+def fathom_paged_attn(pages: Pages, q, k_pages, v_pages, page_table, lens, workspace, out=None, mass=None,
+                      stream=None):
+    """Decode attention over the cache: q [units][G][D] fp32, lens [seqs] int32 -> out
+    [units][G][D] fp32.  mass [units][M] fp32, M >= pages.cap: each token's attention
+    weights, summed over the G heads, are added to it (workspace allocated with mass)."""
+    _check_cache(pages, k_pages, v_pages, page_table)
+    if q is None or q.dim() != 3:
+        raise ValueError("q: expected [units][G][D]")
+    G = q.shape[1]
+    _check(q, "q", (torch.float32,), (pages.units, G, pages.D))
+    _check(lens, "lens", (torch.int32,), (pages.seqs,))
+    _check(workspace, "workspace", (torch.uint8,))
+    if out is not None:
+        _check(out, "out", (torch.float32,), (pages.units, G, pages.D))
+    if mass is not None:
+        _check_mass(mass, "mass", pages.units, pages.cap)
+    with _on(stream, q, k_pages, v_pages, page_table, lens, workspace, out, mass):
+        if out is None:
+            out = torch.empty(pages.units, G, pages.D, dtype=torch.float32, device=q.device)
+        _call("fathom_paged_attn", ctypes.byref(pages), G, _p(q), _p(k_pages), _p(v_pages), _p(page_table), _p(lens),
+              _p(out), _p(mass), mass.shape[1] if mass is not None else 0, _p(workspace), workspace.numel(),
+              _stream(stream))
+    return out
+
+
+def _check_mass(t, name, units, least):
+    _check(t, name, (torch.float32,))
+    if t.dim() != 2 or t.shape[0] != units or t.shape[1] < least:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} is not [{units}][at least {least}]")
+
+
+def fathom_paged_evict(pages: Pages, k_pages, v_pages, page_table, lens, mass, keep, dst_table, n_sink=4,
+                       n_recent=32, kept_idx=None, lens_out=None, mass_out=None, stream=None):
+    """Cut every unit back to `keep` tokens by attention mass; the kept rows move, in order,
+    to the pages of dst_table [seqs][pages] (page_table itself: in place).  -> (kept_idx
+    [units][keep] int32, ascending and then -1, lens_out [seqs] int32, mass_out
+    [units][M] fp32; mass_out None: mass itself, in place)."""
+    _check_cache(pages, k_pages, v_pages, page_table)
+    keep = int(keep)
+    _check(lens, "lens", (torch.int32,), (pages.seqs,))
+    _check_mass(mass, "mass", pages.units, pages.cap)
+    _check(dst_table, "dst_table", (torch.int32,))
+    if dst_table.dim() != 2 or dst_table.shape[0] != pages.seqs:
+        raise ValueError(f"dst_table: shape {tuple(dst_table.shape)} is not [{pages.seqs}][pages]")
+    if mass_out is None:
+        mass_out = mass
+    _check_mass(mass_out, "mass_out", pages.units, keep)
+    if kept_idx is not None:
+        _check(kept_idx, "kept_idx", (torch.int32,), (pages.units, keep))
+    if lens_out is not None:
+        _check(lens_out, "lens_out", (torch.int32,), (pages.seqs,))
+    with _on(stream, k_pages, v_pages, page_table, lens, mass, dst_table, kept_idx, lens_out, mass_out):
+        if kept_idx is None:
+            kept_idx = torch.empty(pages.units, keep, dtype=torch.int32, device=mass.device)
+        if lens_out is None:
+            lens_out = torch.empty(pages.seqs, dtype=torch.int32, device=mass.device)
+        _call("fathom_paged_evict", ctypes.byref(pages), _p(k_pages), _p(v_pages), _p(page_table), _p(lens), _p(mass),
+              mass.shape[1], keep, int(n_sink), int(n_recent), _p(dst_table), dst_table.shape[1], _p(kept_idx),
+              _p(lens_out), _p(mass_out), mass_out.shape[1], _stream(stream))
+    return kept_idx, lens_out, mass_out
 
 
 def fathom_debug_status(mode=0):

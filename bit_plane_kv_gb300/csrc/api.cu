@@ -791,4 +791,198 @@ int fathom_sparse_attn_noalloc(const fathom_shape *shape, const uint16_t *k_rows
     return launch_sparse_attn_noalloc(*shape, k_rows, v_rows, q, topk_idx, out, (cudaStream_t)stream);
 }
 
+// Every stride a positive multiple of 8 elements (16 bytes) unless its axis has
+// one entry, which is never stepped over.
+static bool stride_ok(int64_t stride, int64_t count) {
+    return count <= 1 || (stride >= 8 && stride % 8 == 0 && stride < ((int64_t)1 << 38));
+}
+static bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+
+static int check_row_type(const char *what, int D, int dtype) {
+    if (D < 8 || D > FATHOM_MAX_D || D % 8) {
+        set_error("%s: D must be a multiple of 8 in [8, %d] (got %d)", what, FATHOM_MAX_D, D); return FATHOM_EINVAL;
+    }
+    if (dtype != FATHOM_BF16 && dtype != FATHOM_F16) {
+        set_error("%s: dtype must be FATHOM_BF16 or FATHOM_F16 (got %d)", what, dtype); return FATHOM_EINVAL;
+    }
+    return FATHOM_OK;
+}
+
+int fathom_prefill_attn(const fathom_prompts *prompts, const void *q, const void *k, const void *v,
+                        const int32_t *cu_q, const int32_t *cu_k, void *out, float *lse_opt, void *stream) {
+    g_err[0] = 0;
+    NONNULL(prompts);
+    const fathom_prompts &p = *prompts;
+    if (p.seqs < 1 || p.seqs > 65535) { set_error("prefill_attn: seqs must be in [1, 65535] (got %d)", p.seqs); return FATHOM_EINVAL; }
+    if (p.kv_heads < 1 || p.heads < 1 || p.heads > 65535 || p.heads % p.kv_heads) {
+        set_error("prefill_attn: heads (%d) must be a multiple of kv_heads (%d), at most 65535", p.heads, p.kv_heads);
+        return FATHOM_EINVAL;
+    }
+    const int rc = check_row_type("prefill_attn", p.D, p.dtype);
+    if (rc) return rc;
+    if (p.total_q < 0 || p.total_q > (1 << 28) || p.total_k < 0 || p.total_k > (1 << 28)) {
+        set_error("prefill_attn: total_q and total_k must be in [0, 2^28] (got %d, %d)", p.total_q, p.total_k);
+        return FATHOM_EINVAL;
+    }
+    if (!stride_ok(p.q_token, p.total_q) || !stride_ok(p.k_token, p.total_k) || !stride_ok(p.v_token, p.total_k) ||
+        !stride_ok(p.out_token, p.total_q) || !stride_ok(p.q_head, p.heads) || !stride_ok(p.k_head, p.kv_heads) ||
+        !stride_ok(p.v_head, p.kv_heads) || !stride_ok(p.out_head, p.heads)) {
+        set_error("prefill_attn: strides must be positive multiples of 8 elements"); return FATHOM_EINVAL;
+    }
+    if (p.total_q == 0) return FATHOM_OK;
+    NONNULL(q);
+    NONNULL(cu_q);
+    NONNULL(cu_k);
+    NONNULL(out);
+    if (p.total_k > 0) { NONNULL(k); NONNULL(v); }
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) {
+        set_error("prefill_attn: q, k, v and out must be 16-byte aligned"); return FATHOM_EINVAL;
+    }
+    FAULT_POINT("fathom_prefill_attn");
+    return launch_prefill_attn(p, q, k, v, cu_q, cu_k, out, lse_opt, (cudaStream_t)stream);
+}
+
+static int check_pages(const fathom_pages *pages) {
+    NONNULL(pages);
+    const fathom_pages &p = *pages;
+    if (p.seqs < 1 || p.kv_heads < 1 || (long long)p.seqs * p.kv_heads > 65535) {
+        set_error("pages: need seqs, kv_heads >= 1 and seqs * kv_heads <= 65535 (got %d, %d)", p.seqs, p.kv_heads);
+        return FATHOM_EINVAL;
+    }
+    const int rc = check_row_type("pages", p.D, p.dtype);
+    if (rc) return rc;
+    if (p.page_tokens < 1 || (p.page_tokens & (p.page_tokens - 1))) {
+        set_error("pages: page_tokens must be a power of two (got %d)", p.page_tokens); return FATHOM_EINVAL;
+    }
+    if (p.num_pages < 1 || p.max_pages < 1 || (long long)p.max_pages * p.page_tokens > (1 << 28)) {
+        set_error("pages: need num_pages, max_pages >= 1 and max_pages * page_tokens <= 2^28 (got %d, %d, %d)",
+                  p.num_pages, p.max_pages, p.page_tokens);
+        return FATHOM_EINVAL;
+    }
+    if (!stride_ok(p.page_stride, p.num_pages) || !stride_ok(p.head_stride, p.kv_heads) ||
+        !stride_ok(p.token_stride, p.page_tokens)) {
+        set_error("pages: strides must be positive multiples of 8 elements"); return FATHOM_EINVAL;
+    }
+    return FATHOM_OK;
+}
+
+static int check_page_pointers(const void *k_pages, const void *v_pages, const int32_t *page_table) {
+    NONNULL(k_pages);
+    NONNULL(v_pages);
+    NONNULL(page_table);
+    if (!aligned16(k_pages) || !aligned16(v_pages)) {
+        set_error("k_pages and v_pages must be 16-byte aligned"); return FATHOM_EINVAL;
+    }
+    return FATHOM_OK;
+}
+
+int fathom_paged_append(const fathom_pages *pages, void *k_pages, void *v_pages, const int32_t *page_table,
+                        const void *k_new, const void *v_new, int32_t total_new, int64_t new_token,
+                        int64_t new_head, const int32_t *start, const int32_t *cu_new, void *stream) {
+    g_err[0] = 0;
+    int rc = check_pages(pages);
+    if (rc) return rc;
+    if (total_new < 0 || total_new > (1 << 28) || (!cu_new && total_new > pages->seqs)) {
+        set_error("paged_append: total_new must be in [0, 2^28], at most seqs without cu_new (got %d)", total_new);
+        return FATHOM_EINVAL;
+    }
+    if (!stride_ok(new_token, total_new) || !stride_ok(new_head, pages->kv_heads)) {
+        set_error("paged_append: strides must be positive multiples of 8 elements"); return FATHOM_EINVAL;
+    }
+    if (total_new == 0) return FATHOM_OK;
+    rc = check_page_pointers(k_pages, v_pages, page_table);
+    if (rc) return rc;
+    NONNULL(k_new);
+    NONNULL(v_new);
+    NONNULL(start);
+    if (!aligned16(k_new) || !aligned16(v_new)) {
+        set_error("paged_append: k_new and v_new must be 16-byte aligned"); return FATHOM_EINVAL;
+    }
+    FAULT_POINT("fathom_paged_append");
+    return launch_paged_append(*pages, k_pages, v_pages, page_table, k_new, v_new, total_new, new_token, new_head,
+                               start, cu_new, (cudaStream_t)stream);
+}
+
+static int check_paged_heads(const fathom_pages *pages, int32_t G) {
+    const int rc = check_pages(pages);
+    if (rc) return rc;
+    if (G < 1 || G > FATHOM_MAX_G) { set_error("paged_attn: G must be in [1, %d] (got %d)", FATHOM_MAX_G, G); return FATHOM_EINVAL; }
+    return FATHOM_OK;
+}
+
+size_t fathom_paged_workspace_size(const fathom_pages *pages, int32_t G, int mass) {
+    g_err[0] = 0;
+    if (check_paged_heads(pages, G)) return 0;
+    return paged_workspace_layout(*pages, G, mass != 0).total;
+}
+
+int fathom_paged_attn(const fathom_pages *pages, int32_t G, const float *q, const void *k_pages,
+                      const void *v_pages, const int32_t *page_table, const int32_t *lens, float *out,
+                      float *mass_opt, size_t mass_stride, void *workspace, size_t workspace_bytes, void *stream) {
+    g_err[0] = 0;
+    int rc = check_paged_heads(pages, G);
+    if (rc) return rc;
+    NONNULL(q);
+    rc = check_page_pointers(k_pages, v_pages, page_table);
+    if (rc) return rc;
+    NONNULL(lens);
+    NONNULL(out);
+    NONNULL(workspace);
+    if (mass_opt && mass_stride < (size_t)pages->max_pages * pages->page_tokens) {
+        set_error("paged_attn: mass_stride %zu is less than the %d tokens a sequence may hold", mass_stride,
+                  pages->max_pages * pages->page_tokens);
+        return FATHOM_EINVAL;
+    }
+    const size_t need = paged_workspace_layout(*pages, G, mass_opt != nullptr).total;
+    if (workspace_bytes < need) {
+        set_error("paged_attn workspace too small: %zu < %zu bytes", workspace_bytes, need);
+        return FATHOM_ENOMEM;
+    }
+    if (((uintptr_t)workspace & 255) != 0) { set_error("workspace must be 256-byte aligned"); return FATHOM_EINVAL; }
+    FAULT_POINT("fathom_paged_attn");
+    return launch_paged_attn(*pages, G, q, k_pages, v_pages, page_table, lens, out, mass_opt, mass_stride, workspace,
+                             (cudaStream_t)stream);
+}
+
+int fathom_paged_evict(const fathom_pages *pages, void *k_pages, void *v_pages, const int32_t *page_table,
+                       const int32_t *lens, const float *mass, size_t mass_stride, int32_t keep, int32_t n_sink,
+                       int32_t n_recent, const int32_t *dst_table, int32_t dst_pages, int32_t *kept_idx,
+                       int32_t *lens_out, float *mass_out, size_t mass_out_stride, void *stream) {
+    g_err[0] = 0;
+    int rc = check_pages(pages);
+    if (rc) return rc;
+    if (keep < 1 || keep > (1 << 28)) { set_error("paged_evict: keep must be in [1, 2^28] (got %d)", keep); return FATHOM_EINVAL; }
+    if (n_sink < 0 || n_recent < 0 || (long long)n_sink + n_recent > keep) {
+        set_error("paged_evict: need n_sink, n_recent >= 0 and n_sink + n_recent <= keep (got %d, %d, %d)", n_sink,
+                  n_recent, keep);
+        return FATHOM_EINVAL;
+    }
+    if (dst_pages < 1 || (long long)dst_pages * pages->page_tokens < keep) {
+        set_error("paged_evict: dst_pages * page_tokens must be at least keep (got %d * %d, %d)", dst_pages,
+                  pages->page_tokens, keep);
+        return FATHOM_EINVAL;
+    }
+    if (mass_stride < (size_t)pages->max_pages * pages->page_tokens || mass_out_stride < (size_t)keep) {
+        set_error("paged_evict: mass_stride must be at least max_pages * page_tokens and mass_out_stride at least "
+                  "keep (got %zu, %zu)", mass_stride, mass_out_stride);
+        return FATHOM_EINVAL;
+    }
+    rc = check_page_pointers(k_pages, v_pages, page_table);
+    if (rc) return rc;
+    NONNULL(lens);
+    NONNULL(mass);
+    NONNULL(dst_table);
+    NONNULL(kept_idx);
+    NONNULL(lens_out);
+    NONNULL(mass_out);
+    if (lens_out == lens) { set_error("paged_evict: lens_out may not be lens"); return FATHOM_EINVAL; }
+    if (mass_out == mass && mass_out_stride != mass_stride) {
+        set_error("paged_evict: mass_out may be mass only with the same stride"); return FATHOM_EINVAL;
+    }
+    FAULT_POINT("fathom_paged_evict");
+    return launch_paged_evict(*pages, k_pages, v_pages, page_table, lens, mass, mass_stride, keep, n_sink, n_recent,
+                              dst_table, dst_pages, kept_idx, lens_out, mass_out, mass_out_stride,
+                              (cudaStream_t)stream);
+}
+
 }  // extern "C"

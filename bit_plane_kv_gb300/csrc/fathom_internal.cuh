@@ -259,6 +259,29 @@ struct KltOnlineWs {
 KltOnlineWs klt_online_layout(const fathom_shape &s);
 int launch_klt_online(const fathom_shape &s, const uint16_t *rows, double *mean, double *vec, float *lambda,
                       void *ws, cudaStream_t st);
+
+// ---------------------------------------------------------------- prompts and paged caches
+int launch_prefill_attn(const fathom_prompts &p, const void *q, const void *k, const void *v, const int32_t *cu_q,
+                        const int32_t *cu_k, void *out, float *lse, cudaStream_t st);
+int launch_paged_append(const fathom_pages &p, void *kp, void *vp, const int32_t *table, const void *kn,
+                        const void *vn, int total, int64_t new_token, int64_t new_head, const int32_t *start,
+                        const int32_t *cu_new, cudaStream_t st);
+// Scratch of the paged decode attention: partial softmax states (two per CTA), a
+// ticket per unit and, with the mass, every token's logits and each row's
+// normaliser.
+struct PagedWorkspace {
+    int ctas;
+    size_t ticket_off, lse_off, part_off, logit_off, total;
+};
+PagedWorkspace paged_workspace_layout(const fathom_pages &p, int G, bool mass);
+int launch_paged_attn(const fathom_pages &p, int G, const float *q, const void *kp, const void *vp,
+                      const int32_t *table, const int32_t *lens, float *out, float *mass, size_t mass_stride,
+                      void *ws, cudaStream_t st);
+int launch_paged_evict(const fathom_pages &p, void *kp, void *vp, const int32_t *table, const int32_t *lens,
+                       const float *mass, size_t mass_stride, int keep, int n_sink, int n_recent,
+                       const int32_t *dst_table, int dst_pages, int32_t *kept, int32_t *lens_out, float *mass_out,
+                       size_t mass_out_stride, cudaStream_t st);
+
 int launch_rel_err(int rows, int D, const float *a, const float *ref, double *err, cudaStream_t st);
 int launch_set_overlap(int rows, int k, const int32_t *a, const int32_t *b, int32_t *count, cudaStream_t st);
 int greedy_budgets(int layers, int levels, const double *err, int b_min, int step, int b_mean, int32_t *budgets);

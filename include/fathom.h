@@ -75,7 +75,11 @@ typedef enum {
     FATHOM_ETIMEOUT = 4  /* reserved for bounded device waits */
 } fathom_status;
 
-typedef enum { FATHOM_F32 = 0, FATHOM_BF16 = 1 } fathom_dtype;
+typedef enum {
+    FATHOM_F32 = 0,
+    FATHOM_BF16 = 1,
+    FATHOM_F16 = 2       /* fathom_prefill_attn and the paged calls only */
+} fathom_dtype;
 
 typedef enum {
     FATHOM_WS_SCAN_TOPK = 0,
@@ -120,6 +124,46 @@ typedef struct {
                          kernels that other streams run beside the scan (a host-resident scan is
                          bound by the host link, not by its CTAs).  The workspace size follows it. */
 } fathom_shape;
+
+/* Packed prompts (fathom_prefill_attn): the tokens of all sequences one after
+ * the other, total_q query tokens and total_k key/value tokens.  Rows of D
+ * channels, each contiguous; the strides say how far apart tokens and heads
+ * lie, in elements, so slices of a fused projection and per-head rows serve
+ * as they are.  Strides of q, k and v are positive multiples of 8, their
+ * pointers 16-byte aligned (the same for out); the stride of an axis of
+ * length 1 is not used. */
+typedef struct {
+    int32_t seqs;      /* sequences, 1 .. 65535 */
+    int32_t heads;     /* query heads, a multiple of kv_heads; head h reads KV head h / (heads / kv_heads) */
+    int32_t kv_heads;  /* >= 1 */
+    int32_t D;         /* channels, a multiple of 8 in 8 .. 128 */
+    int32_t dtype;     /* of q, k, v and out: FATHOM_BF16 or FATHOM_F16 */
+    int32_t total_q;   /* query tokens, 0 .. 2^28 */
+    int32_t total_k;   /* key/value tokens, 0 .. 2^28 */
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
+} fathom_prompts;
+
+/* A paged KV cache of one layer: K and V rows in pages of page_tokens tokens
+ * each, element (page, head, token, channel) at
+ *   page * page_stride + head * head_stride + token * token_stride + channel
+ * of k_pages and of v_pages alike, and a page table [seqs][max_pages] int32:
+ * token i of sequence s lies in page table[s][i / page_tokens] at
+ * i % page_tokens.  Unit u = s * kv_heads + head, as everywhere.  Rows
+ * [units][C][D] are such a cache too (page_stride = page_tokens * D,
+ * head_stride = C * D, token_stride = D, table[s][p] = s * kv_heads * C /
+ * page_tokens + p, when page_tokens divides C).  A table entry outside
+ * [0, num_pages) names no page: its tokens are skipped, never read or
+ * written. */
+typedef struct {
+    int32_t seqs;         /* sequences, 1 .. 65535 */
+    int32_t kv_heads;     /* KV heads per sequence; seqs * kv_heads <= 65535 */
+    int32_t D;            /* channels, a multiple of 8 in 8 .. 128 */
+    int32_t dtype;        /* FATHOM_BF16 or FATHOM_F16 */
+    int32_t page_tokens;  /* a power of two */
+    int32_t num_pages;    /* >= 1 */
+    int32_t max_pages;    /* entries of a page table row; max_pages * page_tokens <= 2^28 */
+    int64_t page_stride, head_stride, token_stride;   /* elements, positive multiples of 8 */
+} fathom_pages;
 
 /* ---------------------------------------------------------------------- */
 
@@ -430,6 +474,90 @@ int fathom_sparse_attn_planes(const fathom_shape *shape, const uint64_t *planes,
 int fathom_sparse_attn_noalloc(const fathom_shape *shape, const uint16_t *k_rows,
                                const uint16_t *v_rows, const float *q, const int32_t *topk_idx,
                                float *out, void *stream);
+
+/* Attention of whole prompts, or of their next chunks, causal, over packed
+ * sequences (the step before a cache exists).  Sequence s has query tokens
+ * cu_q[s] .. cu_q[s+1] - 1 and key tokens cu_k[s] .. cu_k[s+1] - 1 of the packed
+ * arrays, lq and lk of them; its queries are the last lq of its lk tokens, so
+ * query i (from 0) sees keys j <= i + lk - lq.  Per query and head
+ *   o = sum_j softmax_j(q . k_j / sqrt(D)) v_j,   lse = log sum_j exp(q . k_j / sqrt(D)),
+ * a query that sees no key (lk < lq) gives o = 0 and lse = -inf.  Scores, softmax
+ * statistics and sums in fp32; the softmax weights are rounded to the rows'
+ * type for the second product and o once at the end.
+ *   q [total_q][heads][D], k, v [total_k][kv_heads][D], out [total_q][heads][D] at
+ *   the strides of `prompts` (device memory)
+ *   cu_q, cu_k [seqs + 1] int32, ascending from 0 (device); values are clamped
+ *   to [0, total], and rows of out behind cu_q[seqs] are left as they were
+ *   lse_opt NULL, or [total_q][heads] fp32 (out)
+ * Rows behind a sequence's end (padding, other sequences) never reach its
+ * outputs, whatever they hold; a NaN or infinity in a value row j of the
+ * sequence itself may reach every query of it. */
+int fathom_prefill_attn(const fathom_prompts *prompts, const void *q, const void *k, const void *v,
+                        const int32_t *cu_q, const int32_t *cu_k, void *out, float *lse_opt, void *stream);
+
+/* Append rows to a paged cache: token i of sequence s's new tokens is written at
+ * position start[s] + i.  New tokens are packed, cu_new[s] .. cu_new[s+1] - 1 for
+ * sequence s (cu_new NULL: token s is sequence s's one new token, total_new <=
+ * seqs).  Tokens whose position lies outside [0, max_pages * page_tokens), or in
+ * no page, or behind cu_new[seqs], are not written.
+ *   k_pages, v_pages (device or pinned host, in and out), page_table [seqs][max_pages]
+ *   k_new, v_new [total_new][kv_heads][D] of the cache's type, element (t, h, c) at
+ *   t * new_token + h * new_head + c (positive multiples of 8, pointers 16-byte
+ *   aligned), start [seqs] int32, cu_new [seqs + 1] int32 or NULL; device
+ * Two new tokens for one place: one of the two rows, unspecified which. */
+int fathom_paged_append(const fathom_pages *pages, void *k_pages, void *v_pages, const int32_t *page_table,
+                        const void *k_new, const void *v_new, int32_t total_new, int64_t new_token,
+                        int64_t new_head, const int32_t *start, const int32_t *cu_new, void *stream);
+
+/* Decode attention of one new token per sequence over a paged cache, dense:
+ * fathom_dense_attn's arithmetic with each sequence at its own length.  Per
+ * unit u = s * kv_heads + head and query head h, over the tokens i < lens[s]
+ *   o_h = sum_i softmax_i(q_h . k_i / sqrt(D)) v_i      (0 when there is none)
+ * and, with mass_opt, the attention weight each token draws is added up:
+ *   mass[u][i] += sum_h softmax_i(q_h . k_i / sqrt(D))   (i < lens[s]; others untouched)
+ * fp32 queries and results as in every decode call; q and the softmax weights
+ * enter the tensor cores as sums of pieces of the rows' type, so nothing is
+ * rounded to 16 bits.  No atomics on values: the same inputs give the same bits.
+ *   G query heads per KV head, 1 .. 8
+ *   q [units][G][D] fp32, k_pages, v_pages (device or pinned host), page_table,
+ *   lens [seqs] int32 (clamped to [0, max_pages * page_tokens]), out [units][G][D]
+ *   fp32 (out), mass_opt NULL or [units][mass_stride] fp32 (in and out;
+ *   mass_stride >= max_pages * page_tokens); device
+ *   workspace: at least fathom_paged_workspace_size(pages, G, mass) bytes, same
+ *   rules as fathom_scan_topk's. */
+int fathom_paged_attn(const fathom_pages *pages, int32_t G, const float *q, const void *k_pages,
+                      const void *v_pages, const int32_t *page_table, const int32_t *lens, float *out,
+                      float *mass_opt, size_t mass_stride, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+/* Eviction by accumulated attention weight: every unit of a sequence longer
+ * than `keep` is cut back to the rows of fathom_scan_topk's kept-set rule with
+ * the mass as the score -- the first n_sink and the last n_recent tokens and the
+ * keep - n_sink - n_recent others of largest mass (ties: lower index; a NaN counts
+ * as the largest) -- and their K and V rows and mass are moved, in ascending
+ * order, to positions 0 .. keep - 1 of the sequence's row of dst_table.  A
+ * sequence of at most `keep` tokens keeps them all.  The units of a sequence
+ * keep different tokens.
+ *   mass [units][mass_stride] fp32, mass_stride >= max_pages * page_tokens
+ *   dst_table [seqs][dst_pages] int32, dst_pages * page_tokens >= keep: either pages
+ *   that no table row names, or page_table itself (in place: the rows move down
+ *   within the sequence's own pages); no page may belong to two sequences
+ *   kept_idx [units][keep] int32 (out): the kept tokens, ascending, then -1
+ *   lens_out [seqs] int32 (out, not lens): min(lens[s], keep)
+ *   mass_out [units][mass_out_stride] fp32 (out), mass_out_stride >= keep: may be
+ *   mass itself with the same stride
+ * Destination rows and mass behind the kept ones are left as they were.
+ * n_sink, n_recent >= 0, n_sink + n_recent <= keep, keep in 1 .. 2^28.  All device
+ * (the pages: device or pinned host). */
+int fathom_paged_evict(const fathom_pages *pages, void *k_pages, void *v_pages, const int32_t *page_table,
+                       const int32_t *lens, const float *mass, size_t mass_stride, int32_t keep,
+                       int32_t n_sink, int32_t n_recent, const int32_t *dst_table, int32_t dst_pages,
+                       int32_t *kept_idx, int32_t *lens_out, float *mass_out, size_t mass_out_stride,
+                       void *stream);
+
+/* Workspace bytes of fathom_paged_attn, with (mass != 0) or without its mass
+ * argument (0 if an argument is invalid). */
+size_t fathom_paged_workspace_size(const fathom_pages *pages, int32_t G, int mass);
 
 /* Workspace bytes a call needs for this shape (0 if the shape is invalid). */
 size_t fathom_workspace_size(const fathom_shape *shape, int which);

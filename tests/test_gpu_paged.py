@@ -1,0 +1,421 @@
+"""The paged cache on the GPU (append, decode attention with attention mass,
+eviction) against plain 64-bit forms; the tolerances are derived in paged_cases."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from bit_plane_kv_gb300 import binding as B
+
+import paged_cases as P
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float16
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ decode
+def attend(q, kp, vp, table, lens, mass=None, ws=None, **kw):
+    pages = B.make_pages(kp, table)
+    ws = B.alloc_paged_workspace(pages, G=q.shape[1], mass=mass is not None) if ws is None else ws
+    return B.fathom_paged_attn(pages, q, kp, vp, table, i32(lens) if isinstance(lens, list) else lens, ws, mass=mass,
+                               **kw)
+
+
+def query(units, G, D, seed=1, scale=2.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return scale * torch.randn(units, G, D, generator=g, device="cuda")
+
+
+def check_decode(out, q, kp, vp, table, lens, before=None, mass=None):
+    o, w, tol, tol_w = P.decode(q, kp, vp, table, lens)
+    assert torch.isfinite(out).all()
+    far = (out.double() - o).abs()
+    assert bool((far <= tol).all()), f"worst {(far / tol.clamp(min=1e-30)).max().item():.3f} of the tolerance"
+    if mass is not None:
+        want = before.double()
+        want[:, : w.shape[1]] += w
+        tol = torch.zeros_like(want)
+        tol[:, : w.shape[1]] = tol_w
+        tol += 2.0 ** -24 * want.abs() * (tol > 0)
+        assert bool(((mass.double() - want).abs() <= tol).all())
+
+
+LENS = [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 500, 0, 1000]
+DECODE = {
+    "G 4, page 16": (LENS, 2, 4, 128, 16, BF, "token"),
+    "G 1, fp16": (LENS, 3, 1, 128, 64, FP, "head"),
+    "G 8": (LENS, 2, 8, 128, 32, BF, "token"),
+    "G 8, fp16, 64 channels": (LENS, 2, 8, 64, 32, FP, "token"),
+    "G 2, 96 channels": (LENS, 2, 2, 96, 128, BF, "head"),
+    "G 3, 8 channels, page 1": ([1, 40, 7], 1, 3, 8, 1, FP, "token"),
+    "G 5, 72 channels": ([300, 4], 2, 5, 72, 16, BF, "token"),
+    "G 6, page 256": ([300, 4, 256, 257], 1, 6, 128, 256, FP, "head"),
+    "G 7": ([100, 33], 1, 7, 64, 8, BF, "token"),
+    "one token": ([1], 1, 1, 8, 16, BF, "token"),
+    "all idle": ([0, 0, 0], 2, 4, 128, 16, BF, "token"),
+    "long and short": ([9000, 3, 0, 700], 2, 4, 128, 64, BF, "token"),
+    "many units": ([(37 * i) % 90 for i in range(300)], 4, 4, 64, 16, BF, "token"),
+}
+
+
+@pytest.mark.parametrize("with_mass", [False, True])
+@pytest.mark.parametrize("name", list(DECODE))
+def test_decode_matches_the_plain_form(name, with_mass):
+    lens, H, G, D, page, dt, layout = DECODE[name]
+    kp, vp, table, _ = P.pool(len(lens), H, D, page, -(-max(max(lens), 1) // page), dt, layout=layout)
+    q = query(len(lens) * H, G, D)
+    mass = torch.rand(len(lens) * H, table.shape[1] * page + 5, device="cuda") if with_mass else None
+    before = mass.clone() if with_mass else None
+    out = attend(q, kp, vp, table, lens, mass)
+    check_decode(out, q, kp, vp, table, lens, before, mass)
+
+
+def test_empty_sequences_give_zero():
+    kp, vp, table, _ = P.pool(2, 2, 64, 16, 2, BF)
+    out = attend(query(4, 4, 64), kp, vp, table, [0, -5])
+    assert bool((out == 0).all())
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("scale", [0.0, 1e-6, 60.0])
+def test_flat_tiny_and_sharp_queries(dt, scale):
+    lens = [513, 70]
+    kp, vp, table, _ = P.pool(2, 2, 128, 16, 40, dt)
+    q = query(4, 4, 128, scale=scale)
+    check_decode(attend(q, kp, vp, table, lens), q, kp, vp, table, lens)
+
+
+def test_queries_beyond_the_cache_type_stay_finite():
+    """fp32 queries larger than fp16 holds, against small fp16 keys."""
+    kp, vp, table, _ = P.pool(1, 1, 64, 16, 10, FP)
+    kp.mul_(2.0 ** -12)
+    q = query(1, 4, 64) * 2.0 ** 18
+    check_decode(attend(q, kp, vp, table, [150]), q, kp, vp, table, [150])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_behind_the_length_and_unnamed_pages_are_never_read(bad):
+    lens, H, page = [70, 16, 1], 2, 16
+    kp, vp, table, _ = P.pool(3, H, 128, page, 8, BF)
+    q = query(6, 4, 128)
+    want = attend(q, kp, vp, table, lens).clone()
+    live = torch.zeros(kp.shape[0], page, dtype=torch.bool, device="cuda")
+    for s, n in enumerate(lens):
+        for i in range(n):
+            live[int(table[s, i // page]), i % page] = True
+    dead = ~live[:, None, :, None]
+    kp.masked_fill_(dead, bad), vp.masked_fill_(dead, bad)
+    assert torch.equal(attend(q, kp, vp, table, lens), want)
+
+
+def test_bad_page_table_entries_are_skipped():
+    lens, page = [100, 64], 16
+    kp, vp, table, _ = P.pool(2, 2, 128, page, 7, BF)
+    table[0, 2], table[0, 5], table[1, 0] = -1, kp.shape[0], 1 << 30
+    q = query(4, 4, 128)
+    mass = torch.zeros(4, 7 * page, device="cuda")
+    before = mass.clone()
+    out = attend(q, kp, vp, table, lens, mass)
+    check_decode(out, q, kp, vp, table, lens, before, mass)
+    table[1] = -7                                          # a sequence with no page at all
+    assert bool((attend(q, kp, vp, table, lens)[2:] == 0).all())
+
+
+def test_lengths_are_clamped_to_the_table():
+    kp, vp, table, _ = P.pool(1, 2, 64, 16, 3, BF)
+    q = query(2, 4, 64)
+    assert torch.equal(attend(q, kp, vp, table, [1 << 30]), attend(q, kp, vp, table, [48]))
+
+
+def test_pages_shared_by_sequences():
+    kp, vp, table, _ = P.pool(3, 2, 128, 16, 10, BF)
+    table[1, :6], table[2, :3] = table[0, :6], table[0, :3]
+    q, lens = query(6, 4, 128), [160, 130, 60]
+    check_decode(attend(q, kp, vp, table, lens), q, kp, vp, table, lens)
+
+
+def test_a_workspace_serves_call_after_call_and_graph_after_graph():
+    kp, vp, table, _ = P.pool(5, 2, 128, 16, 60, BF)
+    pages = B.make_pages(kp, table)
+    ws = B.alloc_paged_workspace(pages, G=4, mass=True)
+    lens = i32([900, 3, 0, 450, 77])
+    mass = torch.zeros(10, pages.cap, device="cuda")
+    q = query(10, 4, 128)
+    want = attend(q, kp, vp, table, lens)
+    for _ in range(3):
+        assert torch.equal(attend(q, kp, vp, table, lens, ws=ws), want)
+        attend(q, kp, vp, table, lens, mass, ws=ws)
+    graphs, outs = [], []
+    for _ in range(2):                                     # two graphs that share the workspace, one after the other
+        g, o = torch.cuda.CUDAGraph(), torch.empty(10, 4, 128, device="cuda")
+        with torch.cuda.graph(g):
+            attend(q, kp, vp, table, lens, ws=ws, out=o)
+        graphs.append(g)
+        outs.append(o)
+    lens.copy_(i32([60, 900, 1, 0, 333]))                  # another batch for the same graphs
+    q.copy_(query(10, 4, 128, seed=5))
+    want = attend(q, kp, vp, table, lens)
+    for g in (graphs[0], graphs[1], graphs[0]):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
+def test_two_calls_at_once_with_their_own_workspaces():
+    kp, vp, table, _ = P.pool(4, 2, 128, 32, 100, BF)
+    lens = i32([3000, 100, 1, 2222])
+    q = query(8, 4, 128)
+    want = attend(q, kp, vp, table, lens)
+    pages = B.make_pages(kp, table)
+    ws = [B.alloc_paged_workspace(pages, G=4) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [attend(q, kp, vp, table, lens, ws=w, stream=s) for _ in range(4) for w, s in zip(ws, streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in got)
+
+
+def test_cache_in_pinned_host_memory():
+    kp, vp, table, _ = P.pool(2, 2, 128, 16, 20, BF, layout="head")
+    q, lens = query(4, 4, 128), [300, 45]
+    want = attend(q, kp, vp, table, lens)
+    got = attend(q, kp.cpu().pin_memory(), vp.cpu().pin_memory(), table, lens)
+    assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("page,H,D,dt,layout", [(16, 2, 128, BF, "token"), (64, 3, 72, FP, "head"), (1, 1, 8, BF, "token")])
+def test_append_writes_the_named_places_only(page, H, D, dt, layout):
+    seqs, per = 4, max(4, 96 // page)
+    kp, vp, table, _ = P.pool(seqs, H, D, page, per, dt, layout=layout, extra=2)
+    k0, v0 = kp.clone(), vp.clone()
+    new, start = [5, 0, 40, 1], [0, 3, 17, per * page - 1]
+    T = sum(new)
+    kv = torch.randn(T + 3, 2 * H, D, device="cuda").to(dt)          # three tokens behind the last sequence
+    B.fathom_paged_append(B.make_pages(kp, table), kp, vp, table, kv[:, :H], kv[:, H:], i32(start), P.cumulated(new))
+    t = 0
+    for s in range(seqs):
+        for i in range(new[s]):
+            p, slot = int(table[s, (start[s] + i) // page]), (start[s] + i) % page
+            k0[p, :, slot], v0[p, :, slot] = kv[t, :H], kv[t, H:]
+            t += 1
+    assert torch.equal(kp, k0) and torch.equal(vp, v0)
+
+
+def test_append_skips_what_has_no_place():
+    kp, vp, table, _ = P.pool(4, 2, 64, 16, 2, BF, extra=1)
+    k0, v0 = kp.clone(), vp.clone()
+    table[1, 0], table[2, 1] = -1, kp.shape[0]
+    new = torch.randn(4, 2, 64, device="cuda").to(BF)
+    B.fathom_paged_append(B.make_pages(kp, table), kp, vp, table, new, new, i32([32, 3, 20, -1]))
+    assert torch.equal(kp, k0) and torch.equal(vp, v0)               # past the end, no page, bad page, before 0
+    B.fathom_paged_append(B.make_pages(kp, table), kp, vp, table, new, new, i32([31, 16, 0, 7]))
+    for s, pos in enumerate([31, 16, 0, 7]):
+        k0[int(table[s, pos // 16]), :, pos % 16] = new[s]
+    assert torch.equal(kp, k0)
+
+
+# ------------------------------------------------------------------ eviction
+def evict_and_check(lens, H, D, page, keep, ns, nr, dt, mass, in_place, layout="token"):
+    seqs, per = len(lens), mass.shape[1] // page
+    dp = -(-keep // page)
+    kp, vp, table, free = P.pool(seqs, H, D, page, per, dt, extra=seqs * dp, layout=layout)
+    dst = table if in_place else free.reshape(seqs, dp).contiguous()
+    k0, v0, m0 = kp.clone(), vp.clone(), mass.clone()
+    out = None if in_place else torch.full((seqs * H, keep + 3), -2.0, device="cuda")
+    pages = B.make_pages(kp, table)
+    kept, new, mo = B.fathom_paged_evict(pages, kp, vp, table, i32(lens), mass, keep, dst, ns, nr, mass_out=out)
+    wk, wv = k0.clone(), v0.clone()
+    wm = m0.clone() if in_place else torch.full_like(mo, -2.0)
+    tt, dd, mm = table.cpu().numpy(), dst.cpu().numpy(), m0.cpu().numpy()
+    want = np.full((seqs * H, keep), -1, np.int32)
+    for u in range(seqs * H):
+        s, h = divmod(u, H)
+        n = min(max(lens[s], 0), per * page)
+        idx = np.array(P.kept_set(mm[u].tolist(), n, keep, ns, nr), np.int64)
+        want[u, : len(idx)] = idx
+        if len(idx) == 0:
+            continue
+        j = np.arange(len(idx))
+        a, b = tt[s][idx // page], dd[s][j // page]
+        a, b, i, j = (torch.from_numpy(np.asarray(x, np.int64)).cuda() for x in (a, b, idx % page, j % page))
+        wk[b, h, j], wv[b, h, j] = k0[a, h, i], v0[a, h, i]
+        wm[u, : len(idx)] = m0[u, torch.from_numpy(idx).cuda()]
+    np.testing.assert_array_equal(kept.cpu().numpy(), want)
+    assert new.tolist() == [min(min(max(n, 0), per * page), keep) for n in lens]
+    assert torch.equal(kp.view(torch.int16), wk.view(torch.int16)) and torch.equal(vp, wv)
+    assert torch.equal(torch.nan_to_num(mo, nan=9.0), torch.nan_to_num(wm, nan=9.0))
+
+
+def masses(units, cap, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    m = torch.exp(2 * torch.randn(units, cap, generator=g, device="cuda"))
+    m[torch.rand(m.shape, generator=g, device="cuda") < 0.2] = 0          # ties
+    return m
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("lens,H,D,page,keep,ns,nr,dt", [
+    ([500, 64, 65, 0, 1, 40], 2, 128, 16, 64, 4, 32, BF),
+    ([3000, 2999], 3, 128, 64, 1000, 4, 32, FP),
+    ([700, 701, 130], 1, 72, 32, 129, 0, 0, BF),
+    ([300, 299], 2, 64, 8, 36, 4, 32, FP),           # nothing but the forced tokens
+    ([9, 10, 11], 1, 8, 1, 10, 3, 4, BF),
+    ([1025, 2048, 2047], 2, 128, 16, 2047, 4, 32, BF),
+    ([5000], 1, 128, 64, 1, 1, 0, BF),
+    ([100], 1, 128, 16, 300, 4, 32, BF),             # more room than tokens
+])
+def test_eviction_keeps_and_moves_what_the_plain_form_does(lens, H, D, page, keep, ns, nr, dt, in_place):
+    per = -(-max(max(lens), keep) // page)
+    evict_and_check(lens, H, D, page, keep, ns, nr, dt, masses(len(lens) * H, per * page), in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_many_units_and_the_head_major_layout(in_place):
+    lens = [100 + 13 * i for i in range(40)]
+    evict_and_check(lens, 8, 64, 16, 150, 4, 32, BF, masses(320, 640), in_place, layout="head")
+
+
+@pytest.mark.parametrize("kind", ["equal", "zero", "nan", "inf", "negative", "two values"])
+def test_ties_and_special_masses(kind):
+    m = masses(2, 512, seed=4)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    some = torch.rand(m.shape, generator=g, device="cuda") < 0.3
+    if kind == "equal":
+        m.fill_(0.25)
+    elif kind == "zero":
+        m.zero_()
+        m[some] = -0.0                                # the same value as 0
+    elif kind == "nan":
+        m[some] = float("nan")
+        m[some & (m.roll(1, 1) > 1)] = -float("nan")
+    elif kind == "inf":
+        m[some] = float("inf")
+    elif kind == "negative":
+        m[some] *= -1
+    else:
+        m = some.float()
+    evict_and_check([500, 512], 1, 64, 16, 200, 4, 32, BF, m, False)
+
+
+def test_a_bad_page_moves_nothing():
+    kp, vp, table, free = P.pool(1, 1, 64, 16, 8, BF, extra=4)
+    dst = free.reshape(1, 4).contiguous()
+    table[0, 7], dst[0, 1] = -1, 1 << 20              # the recent tokens' page, and the rows 16 .. 31
+    k0 = kp.clone()
+    mass = masses(1, 128)
+    kept, _, _ = B.fathom_paged_evict(B.make_pages(kp, table), kp, vp, table, i32([128]), mass, 64, dst, 4, 32)
+    want = k0.clone()
+    for j, i in enumerate(kept[0].tolist()):
+        a, b = int(table[0, i // 16]), int(dst[0, j // 16])
+        if 0 <= a < kp.shape[0] and 0 <= b < kp.shape[0]:
+            want[b, 0, j % 16] = k0[a, 0, i % 16]
+    assert torch.equal(kp, want)
+
+
+def test_eviction_in_a_graph_and_on_a_stream():
+    lens, keep = i32([400, 90]), 100
+    kp, vp, table, free = P.pool(2, 2, 128, 16, 32, BF, extra=2 * 7)
+    dst = free.reshape(2, 7).contiguous()
+    pages, mass = B.make_pages(kp, table), masses(4, 512)
+    out = [torch.empty(4, keep, dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda"),
+           torch.zeros(4, 112, device="cuda")]
+
+    def call(stream=None):
+        B.fathom_paged_evict(pages, kp, vp, table, lens, mass, keep, dst, kept_idx=out[0], lens_out=out[1],
+                             mass_out=out[2], stream=stream)
+
+    call()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    mass.copy_(masses(4, 512, seed=3))
+    lens.copy_(i32([101, 512]))
+    g.replay()
+    got = [x.clone() for x in out] + [kp.clone()]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    call(stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, out + [kp]))
+    for u in range(4):
+        n = [101, 512][u // 2]
+        assert out[0][u].tolist() == P.kept_set(mass[u].tolist(), n, keep, 4, 32)
+
+
+# ------------------------------------------------------------------ together
+def test_prompt_append_decode_evict_decode():
+    """A serving loop: packed prompts, their rows into the pages, decode steps that gather mass,
+    an eviction, decode steps over what was kept; every step against the plain forms."""
+    H, G, D, page, keep = 2, 4, 128, 16, 96
+    lq = [150, 33, 260]
+    g = torch.Generator(device="cuda").manual_seed(11)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    kp, vp, table, _ = P.pool(3, H, D, page, 20, BF, fill=float("nan"))
+    pages = B.make_pages(kp, table)
+    ws = B.alloc_paged_workspace(pages, G=G, mass=True)
+    mass = torch.zeros(3 * H, pages.cap, device="cuda")
+    q, k, v = (2 * rnd(sum(lq), H * G, D)).to(BF), rnd(sum(lq), H, D).to(BF), rnd(sum(lq), H, D).to(BF)
+    cu = P.cumulated(lq)
+    out, _ = B.fathom_prefill_attn(q, k, v, cu)
+    o, _, tol, _ = P.prefill(q, k, v, lq, lq, D)
+    assert bool(((out.double() - o).abs() <= tol).all())
+    B.fathom_paged_append(pages, kp, vp, table, k, v, i32([0, 0, 0]), cu)
+    lens = i32(lq)
+
+    def step():
+        B.fathom_paged_append(pages, kp, vp, table, rnd(3, H, D).to(BF), rnd(3, H, D).to(BF), lens)
+        lens.add_(1)
+        qd, before = 2 * rnd(3 * H, G, D), mass.clone()
+        got = B.fathom_paged_attn(pages, qd, kp, vp, table, lens, ws, mass=mass)
+        check_decode(got, qd, kp, vp, table, lens.tolist(), before, mass)
+
+    for _ in range(3):
+        step()
+    want = [P.kept_set(mass[u].tolist(), lens.tolist()[u // H], keep, 4, 32) for u in range(3 * H)]
+    kept, new, _ = B.fathom_paged_evict(pages, kp, vp, table, lens, mass, keep, table)     # in place
+    assert new.tolist() == [96, 36, 96]
+    assert [[i for i in row if i >= 0] for row in kept.tolist()] == want
+    for s, n in enumerate(new.tolist()):      # the places behind the kept tokens start anew
+        mass[s * H:(s + 1) * H, n:] = 0
+    lens.copy_(new)
+    for _ in range(2):
+        step()
+
+
+def test_contiguous_rows_are_pages_and_the_cut_back_rows_scan():
+    """Rows [units][C][D] as pages: paged decode equals the dense decode, and after an eviction
+    in place the rows go on through the bit-plane store, the plan, the scan and the sparse
+    attention."""
+    seqs, H, G, D, C, n, keep, k = 2, 2, 4, 128, 1024, 1000, 512, 256
+    g = torch.Generator(device="cuda").manual_seed(2)
+    kr, vr = (torch.randn(seqs * H, C, D, generator=g, device="cuda").to(BF) for _ in range(2))
+    (kp, table), (vp, _) = B.rows_as_pages(kr, H), B.rows_as_pages(vr, H)
+    pages = B.make_pages(kp, table)
+    q, lens = query(seqs * H, G, D), i32([n, n])
+    mass = torch.zeros(seqs * H, C, device="cuda")
+    ws = B.alloc_paged_workspace(pages, G=G, mass=True)
+    got = B.fathom_paged_attn(pages, q, kp, vp, table, lens, ws, mass=mass)
+    full = B.make_shape(seqs * H, n, D, G, k, n_cap=C)
+    want = B.fathom_dense_attn(full, kr, vr, q, B.alloc_workspace(full, B.WS_DENSE_ATTN))
+    assert bool((B.fathom_rel_err(got, want) <= 2e-5).all())       # both fp32 throughout
+    k0 = kr.clone()
+    kept, _, _ = B.fathom_paged_evict(pages, kp, vp, table, lens, mass, keep, table)
+    assert torch.equal(kr[:, :keep], torch.stack([k0[u, kept[u].long()] for u in range(seqs * H)]))
+    cut = B.make_shape(seqs * H, keep, D, G, k, n_cap=C)
+    planes, scales = B.fathom_quantize_pack(cut, kr)
+    var = kr[:, :keep].float().var(1).contiguous()
+    _, _, runs = B.fathom_plan(cut, q, var, i32([512] * seqs * H))          # every plane of every channel
+    idx, _ = B.fathom_scan_topk(cut, planes, scales, runs, q, B.alloc_workspace(cut, B.WS_SCAN_TOPK))
+    out = B.fathom_sparse_attn(cut, kr, vr, q, idx, B.alloc_workspace(cut, B.WS_SPARSE_ATTN))
+    for u in range(seqs * H):
+        x = q[u].double() @ kr[u, :keep].double().T / math.sqrt(D)
+        for h in range(G):
+            at = idx[u, h].long()
+            w = torch.softmax(x[h, at], 0) @ vr[u, at].double()
+            assert torch.linalg.norm(out[u, h].double() - w) <= 2e-3 * torch.linalg.norm(w)

@@ -1,0 +1,160 @@
+"""Causal attention of packed prompts on the GPU against the plain 64-bit form;
+the tolerances are derived in paged_cases."""
+import math
+
+import pytest
+import torch
+
+from bit_plane_kv_gb300 import binding as B
+
+import paged_cases as P
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float16
+
+
+def inputs(lq, lk, H, Hkv, D, dtype, seed=0, q_scale=2.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q = (q_scale * torch.randn(sum(lq), H, D, generator=g, device="cuda")).to(dtype)
+    k = torch.randn(sum(lk), Hkv, D, generator=g, device="cuda").to(dtype)
+    v = torch.randn(sum(lk), Hkv, D, generator=g, device="cuda").to(dtype)
+    return q, k, v
+
+
+def check(out, lse, q, k, v, lq, lk):
+    o, z, tol, tol_z = P.prefill(q, k, v, lq, lk, q.shape[2])
+    assert torch.isfinite(out).all()
+    far = (out.double() - o).abs()
+    assert bool((far <= tol).all()), f"out: worst {(far / tol.clamp(min=1e-30)).max().item():.3f} of the tolerance"
+    none = torch.isinf(z)
+    assert torch.equal(torch.isinf(lse) & (lse < 0), none)
+    far = (lse.double() - z)[~none].abs()
+    assert bool((far <= tol_z[~none]).all())
+
+
+SAME = [1, 2, 31, 63, 64, 65, 127, 128, 129, 257, 300]
+CASES = {
+    "whole prompts, G 4": (SAME, SAME, 8, 2, 128, BF),
+    "whole prompts, one head, fp16": (SAME, SAME, 1, 1, 128, FP),
+    "G 8, 64 channels": (SAME, SAME, 16, 2, 64, FP),
+    "G 2, 96 channels": (SAME, SAME, 6, 3, 96, BF),
+    "G 3": ([40, 200, 129], [40, 200, 129], 6, 2, 64, BF),
+    "G 6, 72 channels": ([130, 7], [130, 7], 12, 2, 72, FP),
+    "G 16, 8 channels": ([130, 7], [130, 7], 16, 1, 8, BF),
+    "G 7": ([50], [50], 7, 1, 128, BF),
+    "chunks": ([5, 128, 1, 300, 64], [300, 1000, 129, 301, 64], 8, 2, 128, BF),
+    "chunks, fp16": ([1, 17, 250], [700, 513, 256], 4, 4, 128, FP),
+    "empty rows and sequences": ([0, 10, 4, 0, 130, 3], [0, 0, 2, 50, 100, 3], 8, 2, 128, BF),
+    "one token": ([1], [1], 1, 1, 8, FP),
+    "long": ([1500], [1500], 4, 1, 128, BF),
+    "many sequences": ([1 + i % 5 for i in range(100)], [1 + i % 5 + 3 * (i % 7) for i in range(100)], 4, 2, 64, BF),
+}
+
+
+@pytest.mark.parametrize("name", list(CASES))
+def test_prefill_matches_the_plain_form(name):
+    lq, lk, H, Hkv, D, dt = CASES[name]
+    q, k, v = inputs(lq, lk, H, Hkv, D, dt)
+    out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated(lq), P.cumulated(lk), want_lse=True)
+    check(out, lse, q, k, v, lq, lk)
+
+
+def test_whole_prompts_need_one_list_of_lengths_and_no_lse():
+    lq = [70, 200]
+    q, k, v = inputs(lq, lq, 4, 2, 128, BF)
+    out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated(lq))
+    both, _ = B.fathom_prefill_attn(q, k, v, P.cumulated(lq), P.cumulated(lq), want_lse=True)
+    assert lse is None and torch.equal(out, both)
+
+
+@pytest.mark.parametrize("scale", [0.0, 40.0])
+def test_flat_and_sharp_rows(scale):
+    lq = [260, 33]
+    q, k, v = inputs(lq, lq, 4, 2, 128, BF, q_scale=scale)
+    out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated(lq), want_lse=True)
+    check(out, lse, q, k, v, lq, lq)
+
+
+def test_growing_scores_rescale_the_running_sums():
+    """Keys whose scores climb by far more than any power the kernel may defer."""
+    n = 900
+    q, k, v = inputs([n], [n], 2, 1, 128, BF)
+    k = (k.float() * torch.linspace(0.01, 30, n, device="cuda")[:, None, None]).to(BF)
+    out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated([n]), want_lse=True)
+    check(out, lse, q, k, v, [n], [n])
+
+
+def test_strided_slices_and_per_head_rows():
+    lq = [77, 140]
+    T, H, Hkv, D = sum(lq), 8, 2, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    qkv = torch.randn(T, H + 2 * Hkv, D, generator=g, device="cuda").to(BF)
+    q, k, v = qkv[:, :H], qkv[:, H:H + Hkv], qkv[:, H + Hkv:]
+    out_all = torch.full((T, H + 1, D), 7.0, dtype=BF, device="cuda")
+    out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated(lq), out=out_all[:, :H], want_lse=True)
+    check(out, lse, q, k, v, lq, lq)
+    assert bool((out_all[:, H] == 7).all())
+    kr, vr = (x.permute(1, 0, 2).contiguous() for x in (k, v))      # [heads][tokens][D]
+    again, _ = B.fathom_prefill_attn(q, kr.permute(1, 0, 2), vr.permute(1, 0, 2), P.cumulated(lq))
+    assert torch.equal(again, out)
+    qh = q.permute(1, 0, 2).contiguous().permute(1, 0, 2)
+    oh = torch.empty(H, T, D, dtype=BF, device="cuda").permute(1, 0, 2)
+    again, _ = B.fathom_prefill_attn(qh, k, v, P.cumulated(lq), out=oh)
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_of_others_never_reach_a_sequence(bad):
+    """NaN and infinities in the padding behind the last sequence, and in a neighbour."""
+    lq, lk = [100, 40, 60], [150, 40, 61]
+    q, k, v = inputs([100, 40, 60, 50], [150, 40, 61, 90], 8, 2, 128, BF)
+    cq, ck = P.cumulated(lq), P.cumulated(lk)
+    want, _ = B.fathom_prefill_attn(q, k, v, cq, ck)
+    want = want.clone()
+    for x, n in ((q, 140), (k, 190), (v, 190)):
+        x[n:] = bad                                # the third sequence and the padding behind it
+    out = torch.full_like(q, 3.0)
+    B.fathom_prefill_attn(q, k, v, cq, ck, out=out)
+    assert torch.equal(out[:140], want[:140])
+    assert bool((out[200:] == 3).all())            # rows behind the last sequence are left alone
+    k[150:190], v[150:190] = bad, bad              # the second one too
+    B.fathom_prefill_attn(q, k, v, cq, ck, out=out)
+    assert torch.equal(out[:100], want[:100])
+
+
+def test_lengths_are_clamped_to_the_arrays():
+    q, k, v = inputs([50, 50], [50, 50], 4, 2, 128, BF)
+    want, _ = B.fathom_prefill_attn(q, k, v, P.cumulated([50, 50]))
+    cu = torch.tensor([0, 50, 1 << 30], dtype=torch.int32, device="cuda")
+    got, _ = B.fathom_prefill_attn(q, k, v, cu)
+    assert torch.equal(got, want)
+
+
+def test_no_keys_at_all_and_no_queries():
+    q, k, v = inputs([9], [0], 4, 2, 64, FP)
+    out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated([9]), P.cumulated([0]), want_lse=True)
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    q, k, v = inputs([0], [9], 4, 2, 64, FP)
+    out, _ = B.fathom_prefill_attn(q, k, v, P.cumulated([0]), P.cumulated([9]))
+    assert out.shape == (0, 4, 64)
+
+
+def test_same_bits_on_streams_and_in_a_graph():
+    lq, lk = [70, 260, 3], [70, 600, 9]
+    q, k, v = inputs(lq, lk, 8, 2, 128, BF)
+    cq, ck = P.cumulated(lq), P.cumulated(lk)
+    want, _ = B.fathom_prefill_attn(q, k, v, cq, ck)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [B.fathom_prefill_attn(q, k, v, cq, ck, stream=s)[0] for s in streams for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in got)
+    graph, out = torch.cuda.CUDAGraph(), torch.empty_like(q)
+    with torch.cuda.graph(graph):
+        B.fathom_prefill_attn(q, k, v, cq, ck, out=out)
+    q2, _, _ = inputs(lq, lk, 8, 2, 128, BF, seed=9)
+    want2, _ = B.fathom_prefill_attn(q2, k, v, cq, ck)
+    q.copy_(q2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want2)
