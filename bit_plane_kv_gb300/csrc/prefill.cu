@@ -1,88 +1,439 @@
-// prefill.cu -- causal attention of packed prompts (grouped query heads).
+// prefill.cu -- causal attention of packed prompts (grouped query heads), on the
+// fifth generation tensor cores.
+//
+// One CTA takes 256 query rows of one sequence: the query heads that share a KV
+// head are interleaved with the tokens (row = token * Gp + head, Gp the largest
+// power of two in the group), so a K or V tile read once serves all of them and
+// the causal edge is narrow.  The rows form two tiles of 128, worked on in turn:
+// while the tensor cores multiply for one, four warps exponentiate the other's
+// scores (thread = row).  Per tile and 128 keys:
+//   S = Q K^T           both operands in shared memory, S in tensor memory
+//   P = exp2(c S - m)   registers; P back to tensor memory in the rows' type
+//   O = O + P V         P from tensor memory, V from shared memory
+// with c = log2(e) / sqrt(D) and the running maximum m, sum l of a softmax in one
+// pass.  The exponentials of a row are taken against a maximum that may be up to
+// 2^8 too small (m is raised, and O and l rescaled, only beyond that): O, 64 KB
+// of tensor memory, is touched by the row's own thread in a few tiles only.
+// A warp loads Q and a ring of K and V tiles by TMA; one thread issues the matrix
+// instructions.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
-#include "fathom_internal.cuh"
+#include <mutex>
+
+#include "blackwell.cuh"
 
 namespace fathom {
 
 namespace {
 
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ void from_float(float x, __nv_bfloat16 *o) { *o = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_float(float x, __half *o) { *o = __float2half_rn(x); }
+constexpr int kRows = 128;          // rows of a tile
+constexpr int kKeys = 128;          // keys per step
+// Warps 0-3 and 4-7: the two tiles' rows; of the third warpgroup one warp issues the
+// matrix instructions and one the loads.  384 threads x 168 registers at launch =
+// 2 x 128 x 200 + 128 x 104: a row of S, 128 registers, stays in registers.
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kPrefillThreads = 384, kRowRegs = 200, kOtherRegs = 104;
+constexpr uint32_t kPanel = 128 * 128;   // bytes of 128 rows x 64 channels
+constexpr float kLazy = 8.0f;            // log2 of how far the running maximum may lag
 
-// One warp per (query token, head): lane l holds channels l + 32 c; running
-// maximum, sum and weighted values over the keys one at a time.
-template <typename T>
-__global__ void __launch_bounds__(256)
-prefill_row_kernel(fathom_prompts p, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
-                   const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, T *__restrict__ out,
-                   float *__restrict__ lse) {
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= (long long)p.total_q * p.heads) return;
-    const int t = (int)(row / p.heads), h = (int)(row % p.heads);
-    int lo = 0, hi = p.seqs;   // the last sequence that starts at or before t
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cu_q[mid] <= t) lo = mid; else hi = mid;
-    }
-    const int q0 = cu_q[lo], q1 = min(cu_q[lo + 1], p.total_q);
-    if (t < q0 || t >= q1) return;
-    const int k0 = max(cu_k[lo], 0), k1 = min(cu_k[lo + 1], p.total_k);
-    const int seen = min(k1 - k0, t - q0 + 1 + (k1 - k0) - (q1 - q0));
-    const int hk = h / (p.heads / p.kv_heads);
-    const float scale = 1.0f / sqrtf((float)p.D);
-    float qv[4], o[4] = {0, 0, 0, 0}, m = -CUDART_INF_F, l = 0.0f;
+// Tensor memory columns: the two S (and P) tiles, then the two O tiles.
+constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
+
+template <int kPanels>   // 64-channel panels of a row: 1 (D <= 64) or 2
+struct PrefillSmem {
+    static constexpr int kStages = kPanels == 2 ? 5 : 8;
+    static constexpr uint32_t kTile = kPanels * kPanel;
+    alignas(1024) unsigned char q[2][kTile];
+    alignas(1024) unsigned char kv[kStages][kTile];
+    uint64_t q_full, kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2], o_full[2], drained;
+    uint32_t tmem;
+    int seq, tile;
+};
+
+// Set when a bounded wait ran out: the call's results are not valid.
+__device__ unsigned g_prefill_timeout;
+
+struct PrefillArgs {
+    int seqs, heads, kv_heads, D, total_q, total_k, gp, lg_gp, groups, tiles;
+    int64_t out_token, out_head;
+    const int32_t *cu_q, *cu_k;
+    void *out;
+    float *lse;
+};
+
+__device__ __forceinline__ int clamp_to(int x, int hi) { return min(max(x, 0), hi); }
+
+template <int kPanels, int kDtype>
+__global__ void __launch_bounds__(kPrefillThreads, 1)
+prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+               const __grid_constant__ CUtensorMap map_v, const PrefillArgs a) {
+    using Smem = PrefillSmem<kPanels>;
+    constexpr int kStages = Smem::kStages;
+    constexpr uint32_t kTile = Smem::kTile;
+    extern __shared__ unsigned char smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // ---- which sequence and which 256 rows: the last tiles first (they see the most keys)
+    if (warp == 0) {
+        int rank = a.tiles - 1 - (int)(blockIdx.x / a.groups), seq = -1, tile = 0;
+        for (int s0 = 0; s0 < a.seqs && seq < 0; s0 += 32) {
+            int n = 0;
+            if (s0 + lane < a.seqs)
+                n = max(clamp_to(a.cu_q[s0 + lane + 1], a.total_q) - clamp_to(a.cu_q[s0 + lane], a.total_q), 0);
+            n = (int)((((long long)n << a.lg_gp) + 2 * kRows - 1) / (2 * kRows));
+            int upto = n;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int j = lane + 32 * c;
-        qv[c] = j < p.D ? to_float(q[t * p.q_token + h * p.q_head + j]) : 0.0f;
-    }
-    for (int i = 0; i < seen; ++i) {
-        const T *kr = k + (k0 + i) * p.k_token + hk * p.k_head, *vr = v + (k0 + i) * p.v_token + hk * p.v_head;
-        float s = 0.0f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int j = lane + 32 * c;
-            if (j < p.D) s = fmaf(qv[c], to_float(kr[j]), s);
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, rank < upto);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                seq = s0 + l;
+                tile = rank - __shfl_sync(0xffffffffu, upto - n, l);
+            }
+            rank -= __shfl_sync(0xffffffffu, upto, 31);
         }
-#pragma unroll
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= scale;
-        const float mn = fmaxf(m, s);
-        const float f = m == -CUDART_INF_F ? 0.0f : expf(m - mn), w = mn == -CUDART_INF_F ? 0.0f : expf(s - mn);
-        l = l * f + w;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int j = lane + 32 * c;
-            if (j < p.D) o[c] = o[c] * f + w * to_float(vr[j]);
+        if (lane == 0) { sm.seq = seq; sm.tile = tile; }
+    }
+    if (warp == kLoadWarp && lane == 0) {
+        tma_prefetch_map(&map_q);
+        tma_prefetch_map(&map_k);
+        tma_prefetch_map(&map_v);
+        mbar_init(smem_addr(&sm.q_full), 1);
+        mbar_init(smem_addr(&sm.drained), 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_addr(&sm.kv_full[i]), 1);
+            mbar_init(smem_addr(&sm.kv_empty[i]), 1);
         }
-        m = mn;
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(smem_addr(&sm.s_full[w]), 1);
+            mbar_init(smem_addr(&sm.p_full[w]), 4);
+            mbar_init(smem_addr(&sm.o_full[w]), 1);
+        }
+        mbar_init_fence();
     }
+    __syncthreads();
+    if (sm.seq < 0) return;   // the grid counts one tile more per sequence than most need
+
+    // ---- the tile's geometry (the same in every warp)
+    const int group = (int)(blockIdx.x % a.groups), seq = sm.seq;
+    const int q0 = clamp_to(a.cu_q[seq], a.total_q), lq = clamp_to(a.cu_q[seq + 1], a.total_q) - q0;
+    const int k0 = clamp_to(a.cu_k[seq], a.total_k), lk = max(clamp_to(a.cu_k[seq + 1], a.total_k) - k0, 0);
+    const int off = lk - lq;                               // query token t sees keys j <= t + off
+    const int t0 = sm.tile << (8 - a.lg_gp);               // first token; tile w starts at t0 + w * (128 / Gp)
+    const int tw = kRows >> a.lg_gp;
+    int nt[2];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int j = lane + 32 * c;
-        if (j < p.D) from_float(l > 0.0f ? o[c] / l : 0.0f, out + t * p.out_token + h * p.out_head + j);
+    for (int w = 0; w < 2; ++w) {
+        const int first = t0 + w * tw, last = min(first + tw, lq) - 1;
+        const int keys = first <= last ? min(lk, last + off + 1) : 0;
+        nt[w] = keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
     }
-    if (lse && lane == 0) lse[(size_t)t * p.heads + h] = l > 0.0f ? m + logf(l) : -CUDART_INF_F;
+    const int steps = max(nt[0], nt[1]);
+
+    if (warp == kMmaWarp) tmem_alloc(smem_addr(&sm.tmem), kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    bool ok = true;
+
+    if (warp >= 8) {   // two of these four warps only make the warpgroup whole
+    regs_lower<kOtherRegs>();
+    if (warp == kLoadWarp) {
+        if (lane == 0 && steps > 0) {
+            const int hq = group << a.lg_gp, hk = hq / (a.heads / a.kv_heads);
+            const uint32_t qb = smem_addr(&sm.q_full);
+            const int tiles = nt[1] > 0 ? 2 : 1;
+            mbar_expect(qb, tiles * kTile);
+            for (int w = 0; w < tiles; ++w)
+                for (int p = 0; p < kPanels; ++p)
+                    tma_load_3d(smem_addr(sm.q[w]) + p * kPanel, &map_q, qb, 64 * p, hq, q0 + t0 + w * tw);
+            int issued = 0;
+            for (; issued < 2 * steps; ++issued) {   // K_0, V_0, K_1, V_1, ...
+                const int st = issued % kStages, round = issued / kStages;
+                if (round > 0 && !(ok = mbar_wait(smem_addr(&sm.kv_empty[st]), (round - 1) & 1))) break;
+                const uint32_t bar = smem_addr(&sm.kv_full[st]);
+                mbar_expect(bar, kTile);
+                for (int p = 0; p < kPanels; ++p)
+                    tma_load_3d(smem_addr(sm.kv[st]) + p * kPanel, (issued & 1) ? &map_v : &map_k, bar, 64 * p, hk,
+                                k0 + (issued >> 1) * kKeys);
+            }
+            if (!ok) {   // the copies in flight land before the CTA ends
+                mbar_wait(qb, 0);
+                for (int i = max(issued - kStages, 0); i < issued; ++i)
+                    mbar_wait(smem_addr(&sm.kv_full[i % kStages]), (i / kStages) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        constexpr uint32_t type = kDtype == FATHOM_BF16 ? 1u : 0u;
+        const int ksteps = (a.D + 15) / 16;
+        const uint32_t desc_s = mma_desc(type, kRows, kKeys, false), desc_o = mma_desc(type, kRows, ksteps * 16, true);
+        const int tail = lk - (steps - 1) * kKeys;   // live rows of the last V tile
+        auto scores = [&](int w, int st) {
+#pragma unroll 1
+            for (int k = 0; k < ksteps; ++k) {
+                const uint32_t at = (k >> 2) * kPanel + (k & 3) * 32;
+                mma_ss(tmem + kColS + w * 128, smem_desc(smem_addr(sm.q[w]) + at, 0),
+                       smem_desc(smem_addr(sm.kv[st]) + at, 0), desc_s, k > 0);
+            }
+            mma_commit(smem_addr(&sm.s_full[w]));
+        };
+        auto values = [&](int w, int st, int j) {
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+                mma_ts(tmem + kColO + w * 128, tmem + kColS + w * 128 + k * 8,
+                       smem_desc(smem_addr(sm.kv[st]) + k * 16 * 128, kPanel), desc_o, j > 0 || k > 0);
+            mma_commit(smem_addr(&sm.o_full[w]));
+        };
+        if (steps > 0) {
+            ok = warp_wait(smem_addr(&sm.q_full), 0) && warp_wait(smem_addr(&sm.kv_full[0]), 0);
+            if (ok && lane == 0) {
+                tc_fence_after();
+                if (nt[0] > 0) scores(0, 0);
+                if (nt[1] > 0) scores(1, 0);
+                mma_commit(smem_addr(&sm.kv_empty[0]));
+            }
+            for (int j = 0; j < steps && ok; ++j) {
+                const int iv = 2 * j + 1, sv = iv % kStages, ik = 2 * j + 2, sk = ik % kStages;
+                if (!(ok = warp_wait(smem_addr(&sm.kv_full[sv]), (iv / kStages) & 1))) break;
+                if (j == steps - 1 && tail < kKeys) {
+                    // rows behind the sequence's end: their weights are 0, and 0 x NaN would not be
+                    for (int e = tail * 8 + lane; e < kKeys * 8; e += 32)
+                        for (int p = 0; p < kPanels; ++p)
+                            *reinterpret_cast<int4 *>(sm.kv[sv] + p * kPanel + e * 16) = make_int4(0, 0, 0, 0);
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                const bool more = j + 1 < steps;
+                if (more && !(ok = warp_wait(smem_addr(&sm.kv_full[sk]), (ik / kStages) & 1))) break;
+                if (j < nt[0]) {
+                    if (!(ok = warp_wait(smem_addr(&sm.p_full[0]), j & 1))) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        values(0, sv, j);
+                        if (j + 1 < nt[0]) scores(0, sk);
+                    }
+                }
+                if (j < nt[1]) {
+                    if (!(ok = warp_wait(smem_addr(&sm.p_full[1]), j & 1))) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        values(1, sv, j);
+                        mma_commit(smem_addr(&sm.kv_empty[sv]));
+                        if (j + 1 < nt[1]) scores(1, sk);
+                    }
+                } else if (lane == 0) {
+                    mma_commit(smem_addr(&sm.kv_empty[sv]));
+                }
+                if (more && lane == 0) mma_commit(smem_addr(&sm.kv_empty[sk]));
+                __syncwarp();
+            }
+            __syncwarp();
+            if (lane == 0) mma_commit(smem_addr(&sm.drained));
+            __syncwarp();
+            warp_wait(smem_addr(&sm.drained), 0);   // no matrix instruction outlives the tensor memory
+        }
+    }
+    } else {
+        regs_raise<kRowRegs>();
+        const int w = warp >> 2, row = (warp & 3) * 32 + lane;
+        const int token = t0 + w * tw + (row >> a.lg_gp);
+        const int head = (group << a.lg_gp) + (row & (a.gp - 1));
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + kColS + w * 128, to = tmem + lanes + kColO + w * 128;
+        // keys this row sees, and the fewest that a row of this warp sees
+        const int seen = min(lk, token + off + 1);
+        const int seen_min = min(lk, t0 + w * tw + (((warp & 3) * 32) >> a.lg_gp) + off + 1);
+        const float c = 1.4426950408889634f / sqrtf((float)a.D);   // log2(e) / sqrt(D)
+        // fp16 weights are kept 2^7 larger (at most 2^15) so that fewer fall among its subnormals
+        constexpr float kShift = kDtype == FATHOM_F16 ? 7.0f : 0.0f;
+        float m = 0.0f, l = 0.0f;   // m in log2 units
+        for (int j = 0; j < nt[w]; ++j) {
+            if (!(ok = warp_wait(smem_addr(&sm.s_full[w]), j & 1))) break;
+            tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tmem_ld32(ts + 32 * b, s[b]);
+            tmem_wait_ld();
+            if ((j + 1) * kKeys > seen_min) {
+                const int live = seen - j * kKeys;
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (32 * b + i >= live) s[b][i] = 0xff800000u;
+            }
+            float mx[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                mx[b] = __uint_as_float(s[b][0]);
+#pragma unroll
+                for (int i = 1; i < 32; ++i) mx[b] = fmaxf(mx[b], __uint_as_float(s[b][i]));
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+            if (j == 0) {
+                m = top == -CUDART_INF_F ? 0.0f : top;
+            } else {
+                const bool raise = top > m + kLazy;
+                if (__any_sync(0xffffffffu, raise)) {
+                    if (!(ok = warp_wait(smem_addr(&sm.o_full[w]), (j - 1) & 1))) break;
+                    tc_fence_after();
+                    const float f = raise ? exp2_approx(m - top) : 1.0f;
+                    if (raise) m = top;
+                    l *= f;
+#pragma unroll 1
+                    for (int b = 0; b < 2 * kPanels; ++b) {
+                        uint32_t o[32];
+                        tmem_ld32(to + 32 * b, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st32(to + 32 * b, o);
+                    }
+                }
+            }
+            const float2 cc = make_float2(c, c), mm = make_float2(kShift - m, kShift - m);
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float2 x = make_float2(__uint_as_float(s[b][2 * i]), __uint_as_float(s[b][2 * i + 1]));
+                    x = fma2(x, cc, mm);
+                    x.x = exp2_approx(x.x);
+                    x.y = exp2_approx(x.y);
+                    sum[i & 1] = add2(sum[i & 1], x);
+                    pk[i] = pack2<kDtype>(x.x, x.y);
+                }
+                tmem_st16(ts + 16 * b, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[w]));
+            sum[0] = add2(sum[0], sum[1]);
+            l += sum[0].x + sum[0].y;
+        }
+        // ---- O / l, rounded once
+        ok = ok && (nt[w] == 0 || warp_wait(smem_addr(&sm.o_full[w]), (nt[w] - 1) & 1));
+        if (ok) {
+            tc_fence_after();
+            const bool live = token < lq;
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            uint16_t *orow = (uint16_t *)a.out + (int64_t)(q0 + token) * a.out_token + head * a.out_head;
+#pragma unroll 1
+            for (int b = 0; b < 2 * kPanels; ++b) {
+                uint32_t o[32];
+                if (nt[w] > 0) {
+                    tmem_ld32(to + 32 * b, o);
+                    tmem_wait_ld();
+                }
+                uint32_t pk[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    pk[i] = seen > 0 ? pack2<kDtype>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0u;
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (32 * b + 8 * i < a.D)
+                            *reinterpret_cast<uint4 *>(orow + 32 * b + 8 * i) =
+                                make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                }
+            }
+            if (live && a.lse)
+                a.lse[(int64_t)(q0 + token) * a.heads + head] =
+                    seen > 0 ? ((m - kShift) + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+        }
+    }
+    if (!ok) atomicExch(&g_prefill_timeout, 1u);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) tmem_free(tmem, kTmemCols);
+}
+
+// ---------------------------------------------------------------- host
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static std::mutex mu;
+    static EncodeFn fn = nullptr;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!fn) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult res;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &res) != cudaSuccess ||
+            res != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        fn = (EncodeFn)p;
+    }
+    return fn;
+}
+
+// Rows [tokens][heads][D] as tiles of `box_tokens` x `box_heads` rows x 64 channels;
+// channels from D on read as zero.
+bool encode_rows(CUtensorMap *map, int dtype, const void *base, int D, int heads, int tokens, int64_t head_stride,
+                 int64_t token_stride, int box_heads, int box_tokens) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) { set_error("prefill_attn: the driver does not offer cuTensorMapEncodeTiled"); return false; }
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)(tokens > 0 ? tokens : 1)};
+    const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? head_stride : D) * 2,
+                                   (cuuint64_t)(tokens > 1 ? token_stride : D) * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens}, one[3] = {1, 1, 1};
+    const CUresult r = fn(map, dtype == FATHOM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                          3, const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) { set_error("prefill_attn: cuTensorMapEncodeTiled failed (%d)", (int)r); return false; }
+    return true;
 }
 
 }  // namespace
 
 int launch_prefill_attn(const fathom_prompts &p, const void *q, const void *k, const void *v, const int32_t *cu_q,
                         const int32_t *cu_k, void *out, float *lse, cudaStream_t st) {
-    const long long rows = (long long)p.total_q * p.heads;
-    const unsigned grid = (unsigned)((rows + 7) / 8);
-    if (p.dtype == FATHOM_BF16)
-        prefill_row_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p, (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)k,
-                                                                (const __nv_bfloat16 *)v, cu_q, cu_k,
-                                                                (__nv_bfloat16 *)out, lse);
-    else
-        prefill_row_kernel<__half><<<grid, 256, 0, st>>>(p, (const __half *)q, (const __half *)k, (const __half *)v,
-                                                         cu_q, cu_k, (__half *)out, lse);
-    return launch_status("prefill_row_kernel");
+    const int G = p.heads / p.kv_heads;
+    PrefillArgs a;
+    a.seqs = p.seqs; a.heads = p.heads; a.kv_heads = p.kv_heads; a.D = p.D;
+    a.total_q = p.total_q; a.total_k = p.total_k;
+    a.lg_gp = 0;
+    while (a.lg_gp < 7 && G % (2 << a.lg_gp) == 0) ++a.lg_gp;
+    a.gp = 1 << a.lg_gp;
+    a.groups = p.heads / a.gp;
+    a.out_token = p.out_token; a.out_head = p.out_head;
+    a.cu_q = cu_q; a.cu_k = cu_k; a.out = out; a.lse = lse;
+    const long long tiles = ((long long)p.total_q * a.gp + 2 * kRows - 1) / (2 * kRows) + p.seqs;
+    if (tiles * a.groups > 0x7fffffffLL) { set_error("prefill_attn: too many rows for one launch"); return FATHOM_EINVAL; }
+    a.tiles = (int)tiles;
+    CUtensorMap mq, mk, mv;
+    if (p.total_k == 0) k = v = q;   // no key is loaded; the maps only have to be well formed
+    if (!encode_rows(&mq, p.dtype, q, p.D, p.heads, p.total_q, p.q_head, p.q_token, a.gp, kRows / a.gp) ||
+        !encode_rows(&mk, p.dtype, k, p.D, p.kv_heads, p.total_k, p.k_head, p.k_token, 1, kKeys) ||
+        !encode_rows(&mv, p.dtype, v, p.D, p.kv_heads, p.total_k, p.v_head, p.v_token, 1, kKeys))
+        return FATHOM_ECUDA;
+    const unsigned grid = (unsigned)(tiles * a.groups);
+#define FATHOM_PREFILL(PP, DD)                                                                     \
+    do {                                                                                           \
+        const size_t smem = sizeof(PrefillSmem<PP>) + 1024;                                        \
+        ensure_smem(prefill_kernel<PP, DD>, smem);                                                 \
+        prefill_kernel<PP, DD><<<grid, kPrefillThreads, smem, st>>>(mq, mk, mv, a);                \
+    } while (0)
+    if (p.D <= 64) {
+        if (p.dtype == FATHOM_BF16) FATHOM_PREFILL(1, FATHOM_BF16); else FATHOM_PREFILL(1, FATHOM_F16);
+    } else {
+        if (p.dtype == FATHOM_BF16) FATHOM_PREFILL(2, FATHOM_BF16); else FATHOM_PREFILL(2, FATHOM_F16);
+    }
+#undef FATHOM_PREFILL
+    return launch_status("prefill_kernel");
 }
 
 }  // namespace fathom
