@@ -29,13 +29,11 @@ namespace {
 
 constexpr int kRows = 128;          // rows of a tile
 constexpr int kKeys = 128;          // keys per step
-// Warps 0-3 and 4-7: the two tiles' rows; of the third warpgroup one warp issues the
-// matrix instructions and one the loads.  384 threads x 168 registers at launch =
-// 2 x 128 x 200 + 128 x 104: a row of S, 128 registers, stays in registers.
+// Warps 0-3 and 4-7: the two tiles' rows; then one warp issues the matrix
+// instructions and one the loads.
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kPrefillThreads = 384, kRowRegs = 200, kOtherRegs = 104;
+constexpr int kPrefillThreads = 320;
 constexpr uint32_t kPanel = 128 * 128;   // bytes of 128 rows x 64 channels
-constexpr float kLazy = 8.0f;            // log2 of how far the running maximum may lag
 
 // Tensor memory columns: the two S (and P) tiles, then the two O tiles.
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
@@ -64,10 +62,15 @@ struct PrefillArgs {
 
 __device__ __forceinline__ int clamp_to(int x, int hi) { return min(max(x, 0), hi); }
 
-template <int kPanels, int kDtype>
+// kSteps: 16-channel steps of a row (4, 6 or 8; channels from D on are zero in shared
+// memory).  A constant, so that no branch stands between the matrix instructions:
+// with a runtime count the unrolled and guarded instructions were issued with wrong
+// descriptors.
+template <int kSteps, int kDtype>
 __global__ void __launch_bounds__(kPrefillThreads, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                const __grid_constant__ CUtensorMap map_v, const PrefillArgs a) {
+    constexpr int kPanels = (kSteps + 3) / 4;
     using Smem = PrefillSmem<kPanels>;
     constexpr int kStages = Smem::kStages;
     constexpr uint32_t kTile = Smem::kTile;
@@ -126,14 +129,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     const int off = lk - lq;                               // query token t sees keys j <= t + off
     const int t0 = sm.tile << (8 - a.lg_gp);               // first token; tile w starts at t0 + w * (128 / Gp)
     const int tw = kRows >> a.lg_gp;
-    int nt[2];
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
+    auto count = [&](int w) {                              // steps of tile w
         const int first = t0 + w * tw, last = min(first + tw, lq) - 1;
         const int keys = first <= last ? min(lk, last + off + 1) : 0;
-        nt[w] = keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
-    }
-    const int steps = max(nt[0], nt[1]);
+        return keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
+    };
+    const int nt0 = count(0), nt1 = count(1), steps = max(nt0, nt1);
 
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&sm.tmem), kTmemCols);
     tc_fence_before();
@@ -142,13 +143,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     const uint32_t tmem = sm.tmem;
     bool ok = true;
 
-    if (warp >= 8) {   // two of these four warps only make the warpgroup whole
-    regs_lower<kOtherRegs>();
     if (warp == kLoadWarp) {
         if (lane == 0 && steps > 0) {
             const int hq = group << a.lg_gp, hk = hq / (a.heads / a.kv_heads);
             const uint32_t qb = smem_addr(&sm.q_full);
-            const int tiles = nt[1] > 0 ? 2 : 1;
+            const int tiles = nt1 > 0 ? 2 : 1;
             mbar_expect(qb, tiles * kTile);
             for (int w = 0; w < tiles; ++w)
                 for (int p = 0; p < kPanels; ++p)
@@ -172,31 +171,35 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         __syncwarp();
     } else if (warp == kMmaWarp) {
         constexpr uint32_t type = kDtype == FATHOM_BF16 ? 1u : 0u;
-        const int ksteps = (a.D + 15) / 16;
-        const uint32_t desc_s = mma_desc(type, kRows, kKeys, false), desc_o = mma_desc(type, kRows, ksteps * 16, true);
+        const uint32_t desc_s = mma_desc(type, kRows, kKeys, false), desc_o = mma_desc(type, kRows, kSteps * 16, true);
         const int tail = lk - (steps - 1) * kKeys;   // live rows of the last V tile
+        // descriptors of the first 16 channels (keys) of each operand; the others lie at fixed offsets, and
+        // the address field of a descriptor counts 16 bytes
+        const uint64_t desc_q = smem_desc(smem_addr(sm.q[0]), 0);
+        const uint64_t desc_k = smem_desc(smem_addr(sm.kv[0]), 0), desc_v = smem_desc(smem_addr(sm.kv[0]), kPanel);
         auto scores = [&](int w, int st) {
-#pragma unroll 1
-            for (int k = 0; k < ksteps; ++k) {
-                const uint32_t at = (k >> 2) * kPanel + (k & 3) * 32;
-                mma_ss(tmem + kColS + w * 128, smem_desc(smem_addr(sm.q[w]) + at, 0),
-                       smem_desc(smem_addr(sm.kv[st]) + at, 0), desc_s, k > 0);
+            const uint64_t dq = desc_q + w * (kTile >> 4), dk = desc_k + st * (kTile >> 4);
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                const uint32_t at = ((k >> 2) * kPanel + (k & 3) * 32) >> 4;
+                mma_ss(tmem + kColS + w * 128, dq + at, dk + at, desc_s, k > 0);
             }
             mma_commit(smem_addr(&sm.s_full[w]));
         };
         auto values = [&](int w, int st, int j) {
+            const uint64_t dv = desc_v + st * (kTile >> 4);
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k)
-                mma_ts(tmem + kColO + w * 128, tmem + kColS + w * 128 + k * 8,
-                       smem_desc(smem_addr(sm.kv[st]) + k * 16 * 128, kPanel), desc_o, j > 0 || k > 0);
+                mma_ts(tmem + kColO + w * 128, tmem + kColS + w * 128 + k * 8, dv + ((k * 16 * 128) >> 4), desc_o,
+                       k > 0 ? 1u : (uint32_t)(j > 0));
             mma_commit(smem_addr(&sm.o_full[w]));
         };
         if (steps > 0) {
             ok = warp_wait(smem_addr(&sm.q_full), 0) && warp_wait(smem_addr(&sm.kv_full[0]), 0);
             if (ok && lane == 0) {
                 tc_fence_after();
-                if (nt[0] > 0) scores(0, 0);
-                if (nt[1] > 0) scores(1, 0);
+                if (nt0 > 0) scores(0, 0);
+                if (nt1 > 0) scores(1, 0);
                 mma_commit(smem_addr(&sm.kv_empty[0]));
             }
             for (int j = 0; j < steps && ok; ++j) {
@@ -212,21 +215,21 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 }
                 const bool more = j + 1 < steps;
                 if (more && !(ok = warp_wait(smem_addr(&sm.kv_full[sk]), (ik / kStages) & 1))) break;
-                if (j < nt[0]) {
+                if (j < nt0) {
                     if (!(ok = warp_wait(smem_addr(&sm.p_full[0]), j & 1))) break;
                     tc_fence_after();
                     if (lane == 0) {
                         values(0, sv, j);
-                        if (j + 1 < nt[0]) scores(0, sk);
+                        if (j + 1 < nt0) scores(0, sk);
                     }
                 }
-                if (j < nt[1]) {
+                if (j < nt1) {
                     if (!(ok = warp_wait(smem_addr(&sm.p_full[1]), j & 1))) break;
                     tc_fence_after();
                     if (lane == 0) {
                         values(1, sv, j);
                         mma_commit(smem_addr(&sm.kv_empty[sv]));
-                        if (j + 1 < nt[1]) scores(1, sk);
+                        if (j + 1 < nt1) scores(1, sk);
                     }
                 } else if (lane == 0) {
                     mma_commit(smem_addr(&sm.kv_empty[sv]));
@@ -239,10 +242,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             __syncwarp();
             warp_wait(smem_addr(&sm.drained), 0);   // no matrix instruction outlives the tensor memory
         }
-    }
     } else {
-        regs_raise<kRowRegs>();
-        const int w = warp >> 2, row = (warp & 3) * 32 + lane;
+        const int w = warp >> 2, nt = w ? nt1 : nt0, row = (warp & 3) * 32 + lane;
         const int token = t0 + w * tw + (row >> a.lg_gp);
         const int head = (group << a.lg_gp) + (row & (a.gp - 1));
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -253,67 +254,94 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const float c = 1.4426950408889634f / sqrtf((float)a.D);   // log2(e) / sqrt(D)
         // fp16 weights are kept 2^7 larger (at most 2^15) so that fewer fall among its subnormals
         constexpr float kShift = kDtype == FATHOM_F16 ? 7.0f : 0.0f;
-        float m = 0.0f, l = 0.0f;   // m in log2 units
-        for (int j = 0; j < nt[w]; ++j) {
+        // how far (log2) a row's maximum may rise above m before m follows: a bf16 weight is as exact at
+        // 2^32 as at 1, a fp16 weight must stay below 2^16
+        constexpr float kLag = kDtype == FATHOM_F16 ? 8.0f : 32.0f;
+        float m = -CUDART_INF_F, l = 0.0f;   // m in log2 units; -inf: no finite score yet
+        for (int j = 0; j < nt; ++j) {
             if (!(ok = warp_wait(smem_addr(&sm.s_full[w]), j & 1))) break;
             tc_fence_after();
-            uint32_t s[4][32];
+            const bool edge = (j + 1) * kKeys > seen_min;
+            const int live = seen - j * kKeys;
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            uint32_t s[4][32];   // columns 32 b .. 32 b + 31 of S
+            tmem_ld32(ts, s[0]);
+            tmem_ld32(ts + 32, s[1]);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) tmem_ld32(ts + 32 * b, s[b]);
-            tmem_wait_ld();
-            if ((j + 1) * kKeys > seen_min) {
-                const int live = seen - j * kKeys;
+            for (int h = 0; h < 2; ++h) {   // 64 keys at a time
+                float top = -CUDART_INF_F, top2 = -CUDART_INF_F;
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+                for (int b = 2 * h; b < 2 * h + 2; ++b) {
+                    tmem_wait_ld(s[b]);
+                    if (edge) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (32 * b + i >= live) s[b][i] = 0xff800000u;
-            }
-            float mx[4];
+                        for (int i = 0; i < 32; ++i)
+                            if (32 * b + i >= live) s[b][i] = 0xff800000u;
+                    }
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                mx[b] = __uint_as_float(s[b][0]);
-#pragma unroll
-                for (int i = 1; i < 32; ++i) mx[b] = fmaxf(mx[b], __uint_as_float(s[b][i]));
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-            if (j == 0) {
-                m = top == -CUDART_INF_F ? 0.0f : top;
-            } else {
-                const bool raise = top > m + kLazy;
-                if (__any_sync(0xffffffffu, raise)) {
-                    if (!(ok = warp_wait(smem_addr(&sm.o_full[w]), (j - 1) & 1))) break;
-                    tc_fence_after();
-                    const float f = raise ? exp2_approx(m - top) : 1.0f;
-                    if (raise) m = top;
-                    l *= f;
-#pragma unroll 1
-                    for (int b = 0; b < 2 * kPanels; ++b) {
-                        uint32_t o[32];
-                        tmem_ld32(to + 32 * b, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st32(to + 32 * b, o);
+                    for (int i = 0; i < 32; i += 2) {
+                        top = fmaxf(top, __uint_as_float(s[b][i]));
+                        top2 = fmaxf(top2, __uint_as_float(s[b][i + 1]));
                     }
                 }
-            }
-            const float2 cc = make_float2(c, c), mm = make_float2(kShift - m, kShift - m);
-            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                top = fmaxf(top, top2) * c;
+                const bool raise = top > m + kLag;
+                if (__any_sync(0xffffffffu, raise)) {
+                    // m rises by a whole power of two, so that what was computed against the old one is
+                    // scaled exactly: l, O, and the first half's weights of this tile
+                    float f = 1.0f;
+                    if (raise) {
+                        const float up = m == -CUDART_INF_F ? top : m + ceilf(top - m);
+                        f = exp2f(m - up);
+                        m = up;
+                    }
+                    l *= f;
+                    sum[0].x *= f; sum[0].y *= f; sum[1].x *= f; sum[1].y *= f;
+                    if (h == 1) {
+                        tmem_wait_st();
+#pragma unroll 1
+                        for (int b = 0; b < 2; ++b) {
+                            uint32_t o[16];
+                            tmem_ld16(ts + 16 * b, o);
+                            tmem_wait_ld(o);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                uint32_t pk[16];
+                            for (int i = 0; i < 16; ++i) o[i] = scale2<kDtype>(o[i], f);
+                            tmem_st16(ts + 16 * b, o);
+                        }
+                    }
+                    if (j > 0) {
+                        if (!(ok = warp_wait(smem_addr(&sm.o_full[w]), (j - 1) & 1))) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int b = 0; b < kSteps; ++b) {
+                            uint32_t o[16];
+                            tmem_ld16(to + 16 * b, o);
+                            tmem_wait_ld(o);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float2 x = make_float2(__uint_as_float(s[b][2 * i]), __uint_as_float(s[b][2 * i + 1]));
-                    x = fma2(x, cc, mm);
-                    x.x = exp2_approx(x.x);
-                    x.y = exp2_approx(x.y);
-                    sum[i & 1] = add2(sum[i & 1], x);
-                    pk[i] = pack2<kDtype>(x.x, x.y);
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st16(to + 16 * b, o);
+                        }
+                    }
                 }
-                tmem_st16(ts + 16 * b, pk);
+                const float shift = kShift - (m == -CUDART_INF_F ? 0.0f : m);
+                const float2 cc = make_float2(c, c), mm = make_float2(shift, shift);
+#pragma unroll
+                for (int b = 2 * h; b < 2 * h + 2; ++b) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float2 x = make_float2(__uint_as_float(s[b][2 * i]), __uint_as_float(s[b][2 * i + 1]));
+                        x = fma2(x, cc, mm);
+                        x.x = exp2_approx(x.x);
+                        x.y = exp2_approx(x.y);
+                        sum[i & 1] = add2(sum[i & 1], x);
+                        pk[i] = pack2<kDtype>(x.x, x.y);
+                    }
+                    tmem_st16(ts + 16 * b, pk);
+                    if (h == 0) tmem_ld32(ts + 64 + 32 * b, s[2 + b]);
+                }
             }
+            if (!ok) break;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -322,18 +350,18 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             l += sum[0].x + sum[0].y;
         }
         // ---- O / l, rounded once
-        ok = ok && (nt[w] == 0 || warp_wait(smem_addr(&sm.o_full[w]), (nt[w] - 1) & 1));
+        ok = ok && (nt == 0 || warp_wait(smem_addr(&sm.o_full[w]), (nt - 1) & 1));
         if (ok) {
             tc_fence_after();
             const bool live = token < lq;
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
             uint16_t *orow = (uint16_t *)a.out + (int64_t)(q0 + token) * a.out_token + head * a.out_head;
 #pragma unroll 1
-            for (int b = 0; b < 2 * kPanels; ++b) {
+            for (int b = 0; b < kSteps / 2; ++b) {
                 uint32_t o[32];
-                if (nt[w] > 0) {
+                if (nt > 0) {
                     tmem_ld32(to + 32 * b, o);
-                    tmem_wait_ld();
+                    tmem_wait_ld(o);
                 }
                 uint32_t pk[16];
 #pragma unroll
@@ -421,17 +449,16 @@ int launch_prefill_attn(const fathom_prompts &p, const void *q, const void *k, c
         !encode_rows(&mv, p.dtype, v, p.D, p.kv_heads, p.total_k, p.v_head, p.v_token, 1, kKeys))
         return FATHOM_ECUDA;
     const unsigned grid = (unsigned)(tiles * a.groups);
-#define FATHOM_PREFILL(PP, DD)                                                                     \
+#define FATHOM_PREFILL(SS, DD)                                                                     \
     do {                                                                                           \
-        const size_t smem = sizeof(PrefillSmem<PP>) + 1024;                                        \
-        ensure_smem(prefill_kernel<PP, DD>, smem);                                                 \
-        prefill_kernel<PP, DD><<<grid, kPrefillThreads, smem, st>>>(mq, mk, mv, a);                \
+        const size_t smem = sizeof(PrefillSmem<(SS + 3) / 4>) + 1024;                              \
+        ensure_smem(prefill_kernel<SS, DD>, smem);                                                 \
+        prefill_kernel<SS, DD><<<grid, kPrefillThreads, smem, st>>>(mq, mk, mv, a);                \
     } while (0)
-    if (p.D <= 64) {
-        if (p.dtype == FATHOM_BF16) FATHOM_PREFILL(1, FATHOM_BF16); else FATHOM_PREFILL(1, FATHOM_F16);
-    } else {
-        if (p.dtype == FATHOM_BF16) FATHOM_PREFILL(2, FATHOM_BF16); else FATHOM_PREFILL(2, FATHOM_F16);
-    }
+    const bool bf = p.dtype == FATHOM_BF16;
+    if (p.D <= 64) { if (bf) FATHOM_PREFILL(4, FATHOM_BF16); else FATHOM_PREFILL(4, FATHOM_F16); }
+    else if (p.D <= 96) { if (bf) FATHOM_PREFILL(6, FATHOM_BF16); else FATHOM_PREFILL(6, FATHOM_F16); }
+    else { if (bf) FATHOM_PREFILL(8, FATHOM_BF16); else FATHOM_PREFILL(8, FATHOM_F16); }
 #undef FATHOM_PREFILL
     return launch_status("prefill_kernel");
 }
