@@ -76,7 +76,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     constexpr uint32_t kTile = Smem::kTile;
     extern __shared__ unsigned char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     // ---- which sequence and which 256 rows: the last tiles first (they see the most keys)
     if (warp == 0) {
@@ -140,11 +140,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sm.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
     bool ok = true;
 
     if (warp == kLoadWarp) {
-        if (lane == 0 && steps > 0) {
+        if (steps > 0 && elect_one()) {
             const int hq = group << a.lg_gp, hk = hq / (a.heads / a.kv_heads);
             const uint32_t qb = smem_addr(&sm.q_full);
             const int tiles = nt1 > 0 ? 2 : 1;
@@ -196,7 +196,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         };
         if (steps > 0) {
             ok = warp_wait(smem_addr(&sm.q_full), 0) && warp_wait(smem_addr(&sm.kv_full[0]), 0);
-            if (ok && lane == 0) {
+            if (ok && elect_one()) {
                 tc_fence_after();
                 if (nt0 > 0) scores(0, 0);
                 if (nt1 > 0) scores(1, 0);
@@ -218,7 +218,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 if (j < nt0) {
                     if (!(ok = warp_wait(smem_addr(&sm.p_full[0]), j & 1))) break;
                     tc_fence_after();
-                    if (lane == 0) {
+                    if (elect_one()) {
                         values(0, sv, j);
                         if (j + 1 < nt0) scores(0, sk);
                     }
@@ -226,19 +226,19 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 if (j < nt1) {
                     if (!(ok = warp_wait(smem_addr(&sm.p_full[1]), j & 1))) break;
                     tc_fence_after();
-                    if (lane == 0) {
+                    if (elect_one()) {
                         values(1, sv, j);
                         mma_commit(smem_addr(&sm.kv_empty[sv]));
                         if (j + 1 < nt1) scores(1, sk);
                     }
-                } else if (lane == 0) {
+                } else if (elect_one()) {
                     mma_commit(smem_addr(&sm.kv_empty[sv]));
                 }
-                if (more && lane == 0) mma_commit(smem_addr(&sm.kv_empty[sk]));
+                if (more && elect_one()) mma_commit(smem_addr(&sm.kv_empty[sk]));
                 __syncwarp();
             }
             __syncwarp();
-            if (lane == 0) mma_commit(smem_addr(&sm.drained));
+            if (elect_one()) mma_commit(smem_addr(&sm.drained));
             __syncwarp();
             warp_wait(smem_addr(&sm.drained), 0);   // no matrix instruction outlives the tensor memory
         }
