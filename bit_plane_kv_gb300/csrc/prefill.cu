@@ -29,7 +29,8 @@ namespace {
 
 constexpr int kRows = 128;          // rows of a tile
 constexpr int kKeys = 128;          // keys per step
-// Warps 0-3 and 4-7: the two tiles' rows; then one warp issues the matrix
+// Warps 0-3 and 4-7: the two tiles' rows (a warp reaches the 32 lanes of tensor
+// memory that its number modulo 4 names); then one warp issues the matrix
 // instructions and one the loads.
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
 constexpr int kPrefillThreads = 320;
@@ -152,15 +153,16 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             for (int w = 0; w < tiles; ++w)
                 for (int p = 0; p < kPanels; ++p)
                     tma_load_3d(smem_addr(sm.q[w]) + p * kPanel, &map_q, qb, 64 * p, hq, q0 + t0 + w * tw);
-            int issued = 0;
+            int issued = 0, st = 0;
+            uint32_t turn = 1;   // parity of the stage's last release; true at once in the first turn
             for (; issued < 2 * steps; ++issued) {   // K_0, V_0, K_1, V_1, ...
-                const int st = issued % kStages, round = issued / kStages;
-                if (round > 0 && !(ok = mbar_wait(smem_addr(&sm.kv_empty[st]), (round - 1) & 1))) break;
+                if (!(ok = mbar_wait(smem_addr(&sm.kv_empty[st]), turn))) break;
                 const uint32_t bar = smem_addr(&sm.kv_full[st]);
                 mbar_expect(bar, kTile);
                 for (int p = 0; p < kPanels; ++p)
                     tma_load_3d(smem_addr(sm.kv[st]) + p * kPanel, (issued & 1) ? &map_v : &map_k, bar, 64 * p, hk,
                                 k0 + (issued >> 1) * kKeys);
+                if (++st == kStages) { st = 0; turn ^= 1; }
             }
             if (!ok) {   // the copies in flight land before the CTA ends
                 mbar_wait(qb, 0);
@@ -195,17 +197,25 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             mma_commit(smem_addr(&sm.o_full[w]));
         };
         if (steps > 0) {
-            ok = warp_wait(smem_addr(&sm.q_full), 0) && warp_wait(smem_addr(&sm.kv_full[0]), 0);
+            // the ring's stages in turn: K_0, V_0, K_1, V_1, ...
+            const uint32_t full = smem_addr(sm.kv_full), empty = smem_addr(sm.kv_empty);
+            const uint32_t p_full = smem_addr(sm.p_full);
+            int sv = 1, sk = 0;
+            uint32_t pv = 0, pk = 0;   // parities of the stages' turns
+            ok = warp_wait(smem_addr(&sm.q_full), 0) && warp_wait(full, 0);
             if (ok && elect_one()) {
                 tc_fence_after();
                 if (nt0 > 0) scores(0, 0);
                 if (nt1 > 0) scores(1, 0);
-                mma_commit(smem_addr(&sm.kv_empty[0]));
+                mma_commit(empty);
             }
             for (int j = 0; j < steps && ok; ++j) {
-                const int iv = 2 * j + 1, sv = iv % kStages, ik = 2 * j + 2, sk = ik % kStages;
-                if (!(ok = warp_wait(smem_addr(&sm.kv_full[sv]), (iv / kStages) & 1))) break;
-                if (j == steps - 1 && tail < kKeys) {
+                sk = sv + 1;
+                pk = pv;
+                if (sk == kStages) { sk = 0; pk ^= 1; }
+                const bool more = j + 1 < steps;
+                if (!(ok = warp_wait(full + 8 * sv, pv) && (!more || warp_wait(full + 8 * sk, pk)))) break;
+                if (!more && tail < kKeys) {
                     // rows behind the sequence's end: their weights are 0, and 0 x NaN would not be
                     for (int e = tail * 8 + lane; e < kKeys * 8; e += 32)
                         for (int p = 0; p < kPanels; ++p)
@@ -213,10 +223,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     fence_async_smem();
                     __syncwarp();
                 }
-                const bool more = j + 1 < steps;
-                if (more && !(ok = warp_wait(smem_addr(&sm.kv_full[sk]), (ik / kStages) & 1))) break;
                 if (j < nt0) {
-                    if (!(ok = warp_wait(smem_addr(&sm.p_full[0]), j & 1))) break;
+                    if (!(ok = warp_wait(p_full, j & 1))) break;
                     tc_fence_after();
                     if (elect_one()) {
                         values(0, sv, j);
@@ -224,18 +232,21 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     }
                 }
                 if (j < nt1) {
-                    if (!(ok = warp_wait(smem_addr(&sm.p_full[1]), j & 1))) break;
+                    if (!(ok = warp_wait(p_full + 8, j & 1))) break;
                     tc_fence_after();
                     if (elect_one()) {
                         values(1, sv, j);
-                        mma_commit(smem_addr(&sm.kv_empty[sv]));
+                        mma_commit(empty + 8 * sv);
                         if (j + 1 < nt1) scores(1, sk);
+                        if (more) mma_commit(empty + 8 * sk);
                     }
                 } else if (elect_one()) {
-                    mma_commit(smem_addr(&sm.kv_empty[sv]));
+                    mma_commit(empty + 8 * sv);
+                    if (more) mma_commit(empty + 8 * sk);
                 }
-                if (more && elect_one()) mma_commit(smem_addr(&sm.kv_empty[sk]));
-                __syncwarp();
+                sv = sk + 1;
+                pv = pk;
+                if (sv == kStages) { sv = 0; pv ^= 1; }
             }
             __syncwarp();
             if (elect_one()) mma_commit(smem_addr(&sm.drained));
