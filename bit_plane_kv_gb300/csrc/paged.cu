@@ -2,6 +2,8 @@
 // new token per sequence.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "fathom_internal.cuh"
 
 namespace fathom {
@@ -48,75 +50,492 @@ paged_append_kernel(fathom_pages p, int lg, int4 *__restrict__ kp, int4 *__restr
 }
 
 // ---------------------------------------------------------------- decode
-__device__ __forceinline__ float row_value(const __nv_bfloat16 *x) { return __bfloat162float(*x); }
-__device__ __forceinline__ float row_value(const __half *x) { return __half2float(*x); }
+// One new token per sequence over its cache: o_h = sum_i softmax_i(q_h . k_i / sqrt(D)) v_i.
+// Bound by the cache's bytes, each K and V row read once for the G heads of a unit.
+//
+// The 64-token tiles (128 for D <= 64) of all units, in unit order, are dealt out to
+// the CTAs in equal contiguous shares, whatever the sequences' lengths; a unit that
+// several CTAs share is joined by the last of them to arrive at the unit's ticket.
+// In a tile each warp takes its own 16 tokens, in 16-byte asynchronous copies to a
+// ring of its own, so that warps wait for their own copies only.
+//
+// Products run on the tensor cores without rounding the fp32 operands: q and the
+// softmax weights are sums of three pieces of the rows' type (8 or 11 bits each), and
+// the 16 rows of a matrix operand hold them side by side -- for G <= 4, row 4 i + h is
+// piece i of head h; for G <= 8, rows h and 8 + h are the first two pieces and a
+// second instruction adds the third -- so a K or V fragment is read from shared
+// memory once for all heads and pieces.
 
-// One CTA per (unit, query head): warp w takes tokens w, w + 8, ..., lane l
-// channels l + 32 c; the warps' running states are merged at the end.
+constexpr int kDecWarps = 4, kDecThreads = 32 * kDecWarps, kDecStages = 3;
+
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi, __nv_bfloat16) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi, __half) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_pair(uint32_t v, __nv_bfloat16) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+__device__ __forceinline__ float2 unpack_pair(uint32_t v, __half) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+// Two values as three pairs of pieces, x = piece[0] + piece[1] + piece[2] up to 2^-24 |x|.
 template <typename T>
-__global__ void __launch_bounds__(256)
-paged_attn_kernel(fathom_pages p, int lg, int G, const float *__restrict__ q, const T *__restrict__ kp,
-                  const T *__restrict__ vp, const int32_t *__restrict__ table, const int32_t *__restrict__ lens,
-                  float *__restrict__ out, float *__restrict__ logits, float *__restrict__ norm) {
-    __shared__ float sm[8], sl[8], so[8][FATHOM_MAX_D];
-    const int u = blockIdx.x / G, g = blockIdx.x % G, s = u / p.kv_heads, h = u % p.kv_heads;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n = min(max(lens[s], 0), p.max_pages << lg);
-    const float scale = 1.0f / sqrtf((float)p.D);
-    const size_t row = (size_t)u * G + g;
-    float qv[4], o[4] = {0, 0, 0, 0}, m = -CUDART_INF_F, l = 0.0f;
+__device__ __forceinline__ void split3(float x, float y, uint32_t (&piece)[3]) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) qv[c] = lane + 32 * c < p.D ? q[row * p.D + lane + 32 * c] : 0.0f;
-    for (int i = warp; i < n; i += 8) {
-        const int page = table[(size_t)s * p.max_pages + (i >> lg)];
-        const bool ok = page >= 0 && page < p.num_pages;
-        float x = 0.0f;
-        const int64_t at = ok ? page * p.page_stride + h * p.head_stride + (i & (p.page_tokens - 1)) * p.token_stride : 0;
-        if (ok)
-            for (int c = 0; c < 4; ++c)
-                if (lane + 32 * c < p.D) x = fmaf(qv[c], row_value(kp + at + lane + 32 * c), x);
-#pragma unroll
-        for (int e = 16; e; e >>= 1) x += __shfl_xor_sync(0xffffffffu, x, e);
-        x = ok ? x * scale : -CUDART_INF_F;
-        if (logits && lane == 0) logits[row * (p.max_pages << lg) + i] = x;
-        const float mn = fmaxf(m, x);
-        const float f = m == -CUDART_INF_F ? 0.0f : expf(m - mn), w = mn == -CUDART_INF_F ? 0.0f : expf(x - mn);
-        l = l * f + w;
-        for (int c = 0; c < 4; ++c) o[c] = o[c] * f + (ok && lane + 32 * c < p.D ? w * row_value(vp + at + lane + 32 * c) : 0.0f);
-        m = mn;
+    for (int i = 0; i < 3; ++i) {
+        piece[i] = pack_pair(x, y, T());
+        const float2 r = unpack_pair(piece[i], T());
+        x -= r.x;
+        y -= r.y;
     }
-    if (lane == 0) { sm[warp] = m; sl[warp] = l; }
-    for (int c = 0; c < 4; ++c) so[warp][lane + 32 * c] = o[c];
-    __syncthreads();
-    float M = -CUDART_INF_F, L = 0.0f, O = 0.0f;
-    for (int w = 0; w < 8; ++w) M = fmaxf(M, sm[w]);
-    for (int w = 0; w < 8; ++w) {
-        const float f = sm[w] == -CUDART_INF_F ? 0.0f : expf(sm[w] - M);
-        L += f * sl[w];
-        if (threadIdx.x < FATHOM_MAX_D) O += f * so[w][threadIdx.x];
-    }
-    if (threadIdx.x < p.D) out[row * p.D + threadIdx.x] = L > 0.0f ? O / L : 0.0f;
-    if (norm && threadIdx.x == 0) norm[row] = L > 0.0f ? M + logf(L) : 0.0f;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
+struct DecArgs {
+    fathom_pages p;
+    int lg, G, cap;
+    const float *q;
+    const void *kp, *vp;
+    const int32_t *table, *lens;
+    float *out, *part, *lse, *logits;
+    unsigned *ticket;
+};
+
+// 16-token rows of a warp's stage: K, then V; 16-byte piece c of row t lies at piece
+// c ^ (t & 7), which keeps ldmatrix free of bank conflicts.
+template <int kD>
+struct DecSmem {
+    static constexpr int kSub = kD == 128 ? 1 : 2;   // 16-token parts of a warp's share of a tile
+    static constexpr int kTile = 16 * kSub * kDecWarps;
+    static constexpr int kRowBytes = kD * 2;
+    alignas(128) unsigned char ring[kDecWarps][kDecStages][kSub][2][16 * kRowBytes];
+    float o[kDecWarps][FATHOM_MAX_G][kD];
+    float m[kDecWarps][FATHOM_MAX_G], l[kDecWarps][FATHOM_MAX_G];
+    unsigned live[kDecWarps][kDecStages][kSub];   // which of the 16 tokens there are
+    long long sum[kDecWarps], first_tile, first_seq_tile;
+    int seq, last;
+};
+
+// Position in the order (sequence, head, tile); `tiles` of the sequence.
+struct DecCursor {
+    int seq, head, tile, tiles, n;
+};
+
+template <typename T, int kD, int kTwo, bool kMass>   // kTwo: G > 4
+__global__ void __launch_bounds__(kDecThreads, 2)
+paged_attn_kernel(const DecArgs a) {
+    pdl_enter();
+    using Smem = DecSmem<kD>;
+    constexpr int kSub = Smem::kSub, kTile = Smem::kTile, kRowBytes = Smem::kRowBytes;
+    constexpr int kNT = kD / 8, kKS = kD / 16, kPieces = kD / 8;
+    extern __shared__ __align__(128) unsigned char dec_smem[];
+    Smem &sm = *reinterpret_cast<Smem *>(dec_smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
+    const fathom_pages &p = a.p;
+    const int D = p.D, H = p.kv_heads, G = a.G;
+    auto length = [&](int s) { return min(max(a.lens[s], 0), a.cap); };
+    auto tiles_of = [&](int n) { return (n + kTile - 1) / kTile; };
+
+    // ---- all tiles, and this CTA's share of them
+    long long mine = 0;
+    for (int s = tid; s < p.seqs; s += kDecThreads) mine += tiles_of(length(s));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) sm.sum[warp] = mine;
+    __syncthreads();
+    long long W = 0;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) W += sm.sum[w];
+    W *= H;
+    const long long NC = min((long long)gridDim.x, W);
+    // units of empty sequences
+    for (int u = blockIdx.x; u < p.seqs * H; u += gridDim.x)
+        if (length(u / H) == 0)
+            for (int e = tid; e < G * D; e += kDecThreads) a.out[(size_t)u * G * D + e] = 0.0f;
+    const long long cta = blockIdx.x;
+    if (cta >= NC) return;
+    const long long w0 = cta * W / NC, w1 = (cta + 1) * W / NC;
+    if (warp == 0) {   // the sequence of tile w0
+        long long before = 0;
+        for (int s0 = 0; s0 < p.seqs; s0 += 32) {
+            const long long x = s0 + lane < p.seqs ? (long long)tiles_of(length(s0 + lane)) * H : 0;
+            long long upto = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, before + upto > w0);
+            if (hit) {
+                const int f = __ffs(hit) - 1;
+                if (lane == f) { sm.seq = s0 + f; sm.first_seq_tile = before + upto - x; }
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, upto, 31);
+        }
+    }
+    __syncthreads();
+    DecCursor at;   // the tile being computed
+    at.seq = sm.seq;
+    at.n = length(at.seq);
+    at.tiles = tiles_of(at.n);
+    {
+        const long long in = w0 - sm.first_seq_tile;
+        at.head = (int)(in / at.tiles);
+        at.tile = (int)(in % at.tiles);
+    }
+    auto advance = [&](DecCursor &x) {   // true when the unit changes
+        if (++x.tile < x.tiles) return false;
+        x.tile = 0;
+        if (++x.head == H) {
+            x.head = 0;
+            do {
+                if (++x.seq >= p.seqs) { x.n = 0; x.tiles = 1; break; }
+                x.n = length(x.seq);
+                x.tiles = tiles_of(x.n);
+            } while (x.tiles == 0);
+        }
+        return true;
+    };
+
+    // ---- loads: lane t < 16 looks up the page of token t, one tile ahead of its copies
+    const char *kb = (const char *)a.kp, *vb = (const char *)a.vp;
+    DecCursor ld = at;
+    int pid[kSub];
+    auto lookup = [&]() {
+#pragma unroll
+        for (int b = 0; b < kSub; ++b) {
+            const int i = ld.tile * kTile + (warp * kSub + b) * 16 + (lane & 15);
+            int page = -1;
+            if (ld.seq < p.seqs && i < ld.n) {
+                page = __ldg(a.table + (size_t)ld.seq * p.max_pages + (i >> a.lg));
+                if (page >= p.num_pages) page = -1;
+            }
+            pid[b] = page;
+        }
+    };
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm.ring[warp]);
+    constexpr uint32_t kHalf = 16 * kRowBytes, kStageBytes = kSub * 2 * kHalf;
+    const int col = lane % kPieces, row0 = lane / kPieces;   // this lane's 16-byte piece, its first row
+    constexpr int kRowsPer = 32 / kPieces;
+    auto issue = [&](int st) {   // the copies of the tile at `ld`, whose pages are in pid
+#pragma unroll
+        for (int b = 0; b < kSub; ++b) {
+            const unsigned ok = __ballot_sync(0xffffffffu, pid[b] >= 0) & 0xffffu;
+            if (lane == 0) sm.live[warp][st][b] = ok;
+#pragma unroll
+            for (int i = 0; i < 16 / kRowsPer; ++i) {
+                const int t = row0 + i * kRowsPer;
+                const int page = __shfl_sync(0xffffffffu, pid[b], t);
+                const int slot = (ld.tile * kTile + (warp * kSub + b) * 16 + t) & (p.page_tokens - 1);
+                const bool live = page >= 0 && col * 8 < D;
+                const int64_t off = live ? 2 * (page * p.page_stride + ld.head * p.head_stride + slot * p.token_stride) + col * 16 : 0;
+                const uint32_t dst = ring + st * kStageBytes + b * 2 * kHalf + t * kRowBytes + ((col ^ (t & 7)) << 4);
+                const int bytes = live ? 16 : 0;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(kb + off), "r"(bytes) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + kHalf), "l"(vb + off), "r"(bytes) : "memory");
+            }
+        }
+    };
+    const int count = (int)(w1 - w0);
+    lookup();
+#pragma unroll
+    for (int st = 0; st < kDecStages - 1; ++st) {
+        if (st < count) {
+            issue(st);
+            advance(ld);
+            lookup();
+        }
+        cp_async_commit();
+    }
+
+    const int head = kTwo ? r : (r & 3);   // this lane's head in score and output fragments
+    const float to_log2 = 1.4426950408889634f / sqrtf((float)D);
+    uint32_t qa[kKS][4], qb[kTwo ? kKS : 1][2];
+    float unscale = 1.0f, m = -CUDART_INF_F, l = 0.0f, o[kNT][4];
+    // fp16 weights are kept 2^12 larger, so that their pieces stay clear of the subnormals
+    constexpr float kUp = sizeof(T) == 2 && std::is_same<T, __half>::value ? 12.0f : 0.0f;
+    bool fresh = true;
+    long long unit_w0 = w0 - at.tile;   // index of the unit's first tile
+
+    for (int i = 0; i < count; ++i) {
+        if (fresh) {   // a new unit: its queries in pieces, empty sums
+            fresh = false;
+            const float *qr = a.q + ((size_t)(at.seq * H + at.head) * G + head) * D;
+            float2 x[kKS][2];
+            float big = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int k = ks * 16 + 2 * c + 8 * e;
+                    x[ks][e] = head < G && k < D ? make_float2(__ldg(qr + k), __ldg(qr + k + 1)) : make_float2(0.0f, 0.0f);
+                    x[ks][e].x *= to_log2;
+                    x[ks][e].y *= to_log2;
+                    big = fmaxf(big, fmaxf(fabsf(x[ks][e].x), fabsf(x[ks][e].y)));
+                }
+            unscale = 1.0f;
+            if (std::is_same<T, __half>::value) {   // a power of two that brings the largest to about 2^12
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                if (big > 0.0f && big < CUDART_INF_F) {
+                    const int e = min(max(ilogbf(big) - 12, -126), 126);
+                    unscale = ldexpf(1.0f, e);
+                    const float up = ldexpf(1.0f, -e);
+#pragma unroll
+                    for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) { x[ks][f].x *= up; x[ks][f].y *= up; }
+                }
+            }
+#pragma unroll
+            for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t pc[3];
+                    split3<T>(x[ks][e].x, x[ks][e].y, pc);
+                    if (kTwo) {
+                        qa[ks][2 * e] = pc[0];
+                        qa[ks][2 * e + 1] = pc[1];
+                        qb[kTwo ? ks : 0][e] = pc[2];
+                    } else {
+                        qa[ks][2 * e] = r < 4 ? pc[0] : pc[1];
+                        qa[ks][2 * e + 1] = r < 4 ? pc[2] : 0u;
+                    }
+                }
+            m = -CUDART_INF_F;
+            l = 0.0f;
+#pragma unroll
+            for (int j = 0; j < kNT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+        }
+        const int st = i % kDecStages;
+        {   // the copies two tiles ahead, into the stage that was read last
+            if (i + kDecStages - 1 < count) {
+                issue((i + kDecStages - 1) % kDecStages);
+                advance(ld);
+                lookup();
+            }
+            cp_async_commit();
+            cp_async_wait<kDecStages - 1>();
+            __syncwarp();
+        }
+#pragma unroll
+        for (int b = 0; b < kSub; ++b) {
+            const uint32_t kt = ring + st * kStageBytes + b * 2 * kHalf, vt = kt + kHalf;
+            const unsigned ok = sm.live[warp][st][b];
+            // scores of 16 tokens: columns 2 c, 2 c + 1 of two 8-token products
+            float s[2][4] = {};
+#pragma unroll
+            for (int ks = 0; ks < kKS; ++ks) {
+                // matrices: tokens 0-7 and 8-15 of channels 0-7 and 8-15 of this step
+                const int t = (lane & 7) + ((lane >> 4) << 3), pc = 2 * ks + ((lane >> 3) & 1);
+                uint32_t kf[4];
+                ldmatrix4(kf, kt + t * kRowBytes + ((pc ^ (t & 7)) << 4));
+                mma16816(s[0], qa[ks], kf[0], kf[1], T());
+                mma16816(s[1], qa[ks], kf[2], kf[3], T());
+                if (kTwo) {
+                    const uint32_t third[4] = {qb[kTwo ? ks : 0][0], 0u, qb[kTwo ? ks : 0][1], 0u};
+                    mma16816(s[0], third, kf[0], kf[1], T());
+                    mma16816(s[1], third, kf[2], kf[3], T());
+                }
+            }
+            float x[2][2], top = -CUDART_INF_F;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float v = s[j][e] + s[j][2 + e];
+                    if (!kTwo) v += __shfl_xor_sync(0xffffffffu, v, 16);
+                    v *= unscale;
+                    x[j][e] = (ok >> (8 * j + 2 * c + e)) & 1u ? v : -CUDART_INF_F;
+                    top = fmaxf(top, x[j][e]);
+                }
+            if (kMass) {
+                const int i0 = at.tile * kTile + (warp * kSub + b) * 16 + 2 * c;
+                float *lr = a.logits + ((size_t)(at.seq * H + at.head) * G + head) * a.cap;
+                if (head < G && (kTwo || r < 4)) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (i0 + 8 * j + e < at.n) lr[i0 + 8 * j + e] = x[j][e];
+                }
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            if (__any_sync(0xffffffffu, top > m)) {
+                const float mn = fmaxf(m, top);
+                const float f = m == -CUDART_INF_F ? 0.0f : exp2_fast(m - mn);
+                m = mn;
+                l *= f;
+#pragma unroll
+                for (int j = 0; j < kNT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[j][e] *= f;
+            }
+            const float shift = kUp - (m == -CUDART_INF_F ? 0.0f : m);
+            uint32_t pa[4], pb[4] = {};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float p0 = exp2_fast(x[j][0] + shift), p1 = exp2_fast(x[j][1] + shift);
+                l += p0 + p1;
+                uint32_t pc[3];
+                split3<T>(p0, p1, pc);
+                if (kTwo) {
+                    pa[2 * j] = pc[0];
+                    pa[2 * j + 1] = pc[1];
+                    pb[2 * j] = pc[2];
+                } else {
+                    pa[2 * j] = r < 4 ? pc[0] : pc[1];
+                    pa[2 * j + 1] = r < 4 ? pc[2] : 0u;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kNT; j += 2) {
+                // matrices: tokens 0-7 and 8-15 of channels 8 j .. 8 j + 7 and of the next eight
+                const int t = lane & 15, pc = j + (lane >> 4);
+                uint32_t vf[4];
+                ldmatrix4_trans(vf, vt + t * kRowBytes + ((pc ^ (t & 7)) << 4));
+                mma16816(o[j], pa, vf[0], vf[1], T());
+                mma16816(o[j + 1], pa, vf[2], vf[3], T());
+                if (kTwo) {
+                    mma16816(o[j], pb, vf[0], vf[1], T());
+                    mma16816(o[j + 1], pb, vf[2], vf[3], T());
+                }
+            }
+        }
+        __syncwarp();   // the stage is read before its next copies start
+
+        // ---- end of the unit, or of this CTA's share of it
+        const int unit = at.seq * H + at.head, tiles = at.tiles;
+        const bool turn = advance(at);
+        if (!turn && i + 1 < count) continue;
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        const bool owner = head < G && (kTwo || r < 4);
+        if (owner && c == 0) { sm.m[warp][head] = m; sm.l[warp][head] = l; }
+        __syncthreads();
+        float M = -CUDART_INF_F;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, owner ? sm.m[w][head] : -CUDART_INF_F);
+        const float f = m == -CUDART_INF_F ? 0.0f : exp2_fast(m - M);
+#pragma unroll
+        for (int j = 0; j < kNT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float v = o[j][e] + o[j][2 + e];
+                if (!kTwo) v += __shfl_xor_sync(0xffffffffu, v, 16);
+                if (owner) sm.o[warp][head][8 * j + 2 * c + e] = v * f;
+            }
+        __syncthreads();
+        // the CTA's state of each head: (m, l, o), to `out` when the unit is all here
+        const long long c_first = ((unit_w0 + 1) * NC - 1) / W, c_last = ((unit_w0 + tiles) * NC - 1) / W;
+        const bool whole = c_first == c_last;
+        float *pp = a.part + (size_t)(2 * cta + (w0 < unit_w0 ? 1 : 0)) * G * (D + 2);
+        for (int e = tid; e < G * D; e += kDecThreads) {
+            const int h = e / D, d = e % D;
+            float Mh = -CUDART_INF_F, L = 0.0f, O = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kDecWarps; ++w) Mh = fmaxf(Mh, sm.m[w][h]);
+#pragma unroll
+            for (int w = 0; w < kDecWarps; ++w) {
+                O += sm.o[w][h][d];
+                L += sm.m[w][h] == -CUDART_INF_F ? 0.0f : sm.l[w][h] * exp2_fast(sm.m[w][h] - Mh);
+            }
+            if (whole) a.out[(size_t)unit * G * D + e] = L > 0.0f ? O / L : 0.0f;
+            else pp[h * (D + 2) + 2 + d] = O;
+            if (d == 0) {
+                if (!whole) { pp[h * (D + 2)] = Mh; pp[h * (D + 2) + 1] = L; }
+                else if (kMass) a.lse[(size_t)unit * G + h] = L > 0.0f ? Mh + log2f(L) - kUp : 0.0f;
+            }
+        }
+        if (!whole) {
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) sm.last = atomicAdd(a.ticket + unit, 1u) == (unsigned)(c_last - c_first) ? 1 : 0;
+            __syncthreads();
+            if (sm.last) {   // every share of the unit is there: joined in their order
+                __threadfence();
+                if (tid == 0) a.ticket[unit] = 0u;
+                for (int e = tid; e < G * D; e += kDecThreads) {
+                    const int h = e / D, d = e % D;
+                    float Mh = -CUDART_INF_F, L = 0.0f, O = 0.0f;
+                    for (long long x = c_first; x <= c_last; ++x) {
+                        const float *px = a.part + ((size_t)(2 * x + (x * W / NC < unit_w0 ? 1 : 0)) * G + h) * (D + 2);
+                        const float mx = __ldcg(px), lx = __ldcg(px + 1), ox = __ldcg(px + 2 + d);
+                        const float mn = fmaxf(Mh, mx);
+                        const float f0 = Mh == -CUDART_INF_F ? 0.0f : exp2_fast(Mh - mn);
+                        const float f1 = mx == -CUDART_INF_F ? 0.0f : exp2_fast(mx - mn);
+                        O = O * f0 + ox * f1;
+                        L = L * f0 + lx * f1;
+                        Mh = mn;
+                    }
+                    a.out[(size_t)unit * G * D + e] = L > 0.0f ? O / L : 0.0f;
+                    if (kMass && d == 0) a.lse[(size_t)unit * G + h] = L > 0.0f ? Mh + log2f(L) - kUp : 0.0f;
+                }
+            }
+        }
+        fresh = true;
+        unit_w0 += tiles;
+        __syncthreads();   // the merge buffers are free again
+    }
+    cp_async_wait<0>();
+}
+
+// mass[i] += sum_h 2^(logit_h(i) - lse_h), from the logits that the attention left
 __global__ void __launch_bounds__(256)
-paged_mass_kernel(fathom_pages p, int lg, int G, const int32_t *__restrict__ lens, const float *__restrict__ logits,
-                  const float *__restrict__ norm, float *__restrict__ mass, size_t mass_stride) {
-    const int u = blockIdx.y, cap = p.max_pages << lg, n = min(max(lens[u / p.kv_heads], 0), cap);
+paged_mass_kernel(fathom_pages p, int cap, int G, const int32_t *__restrict__ lens, const float *__restrict__ logits,
+                  const float *__restrict__ lse, float *__restrict__ mass, size_t mass_stride) {
+    pdl_enter();
+    const int u = blockIdx.y, n = min(max(lens[u / p.kv_heads], 0), cap);
     for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
         float w = 0.0f;
-        for (int g = 0; g < G; ++g) w += expf(logits[((size_t)u * G + g) * cap + i] - norm[(size_t)u * G + g]);
+        for (int g = 0; g < G; ++g)
+            w += exp2_fast(__ldcg(logits + ((size_t)u * G + g) * cap + i) - __ldcg(lse + (size_t)u * G + g));
         mass[u * mass_stride + i] += w;
     }
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-template <typename T>
-void launch_attn(const fathom_pages &p, int G, const float *q, const void *kp, const void *vp, const int32_t *table,
-                 const int32_t *lens, float *out, float *logits, float *norm, cudaStream_t st) {
-    paged_attn_kernel<T><<<p.seqs * p.kv_heads * G, 256, 0, st>>>(p, log2_of(p.page_tokens), G, q, (const T *)kp,
-                                                                  (const T *)vp, table, lens, out, logits, norm);
+template <typename T, int kD, int kTwo, bool kMass>
+cudaError_t launch_dec(const DecArgs &a, int ctas, cudaStream_t st) {
+    const size_t smem = sizeof(DecSmem<kD>);
+    ensure_smem(paged_attn_kernel<T, kD, kTwo, kMass>, smem);
+    return launch_pdl(paged_attn_kernel<T, kD, kTwo, kMass>, dim3(ctas), dim3(kDecThreads), smem, st, a);
+}
+template <typename T, int kD>
+cudaError_t launch_dec_form(const DecArgs &a, int ctas, cudaStream_t st) {
+    if (a.G > 4) return a.logits ? launch_dec<T, kD, 1, true>(a, ctas, st) : launch_dec<T, kD, 1, false>(a, ctas, st);
+    return a.logits ? launch_dec<T, kD, 0, true>(a, ctas, st) : launch_dec<T, kD, 0, false>(a, ctas, st);
 }
 
 }  // namespace
@@ -134,12 +553,14 @@ int launch_paged_append(const fathom_pages &p, void *kp, void *vp, const int32_t
 
 PagedWorkspace paged_workspace_layout(const fathom_pages &p, int G, bool mass) {
     PagedWorkspace w;
-    const size_t rows = (size_t)p.seqs * p.kv_heads * G;
-    w.ctas = 0;
+    int sms = device_sm_count();
+    if (sms <= 0) sms = 152;
+    const size_t units = (size_t)p.seqs * p.kv_heads, rows = units * G;
+    w.ctas = 2 * sms;   // resident at once
     w.ticket_off = 0;
-    w.lse_off = align256((size_t)p.seqs * p.kv_heads * sizeof(uint32_t));
-    w.part_off = align256(w.lse_off + rows * sizeof(float));
-    w.logit_off = w.part_off;
+    w.lse_off = align256(units * sizeof(uint32_t));
+    w.part_off = align256(w.lse_off + (mass ? rows * sizeof(float) : 0));
+    w.logit_off = align256(w.part_off + (size_t)w.ctas * 2 * G * (p.D + 2) * sizeof(float));
     w.total = align256(w.logit_off + (mass ? rows * ((size_t)p.max_pages * p.page_tokens) * sizeof(float) : 0));
     return w;
 }
@@ -148,16 +569,29 @@ int launch_paged_attn(const fathom_pages &p, int G, const float *q, const void *
                       const int32_t *table, const int32_t *lens, float *out, float *mass, size_t mass_stride,
                       void *ws, cudaStream_t st) {
     const PagedWorkspace w = paged_workspace_layout(p, G, mass != nullptr);
-    float *logits = mass ? (float *)((char *)ws + w.logit_off) : nullptr;
-    float *norm = mass ? (float *)((char *)ws + w.lse_off) : nullptr;
-    if (p.dtype == FATHOM_BF16) launch_attn<__nv_bfloat16>(p, G, q, kp, vp, table, lens, out, logits, norm, st);
-    else launch_attn<__half>(p, G, q, kp, vp, table, lens, out, logits, norm, st);
-    int rc = launch_status("paged_attn_kernel");
-    if (rc || !mass) return rc;
-    const int cap = p.max_pages * p.page_tokens;
-    const dim3 grid(cap / 256 / 4 + 1, p.seqs * p.kv_heads);
-    paged_mass_kernel<<<grid, 256, 0, st>>>(p, log2_of(p.page_tokens), G, lens, logits, norm, mass, mass_stride);
-    return launch_status("paged_mass_kernel");
+    DecArgs a;
+    a.p = p;
+    a.lg = log2_of(p.page_tokens);
+    a.G = G;
+    a.cap = p.max_pages * p.page_tokens;
+    a.q = q; a.kp = kp; a.vp = vp; a.table = table; a.lens = lens; a.out = out;
+    a.ticket = (unsigned *)((char *)ws + w.ticket_off);
+    a.part = (float *)((char *)ws + w.part_off);
+    a.lse = mass ? (float *)((char *)ws + w.lse_off) : nullptr;
+    a.logits = mass ? (float *)((char *)ws + w.logit_off) : nullptr;
+    cudaError_t e;
+    if (p.dtype == FATHOM_BF16)
+        e = p.D <= 64 ? launch_dec_form<__nv_bfloat16, 64>(a, w.ctas, st) : launch_dec_form<__nv_bfloat16, 128>(a, w.ctas, st);
+    else
+        e = p.D <= 64 ? launch_dec_form<__half, 64>(a, w.ctas, st) : launch_dec_form<__half, 128>(a, w.ctas, st);
+    if (e != cudaSuccess) { set_error("paged_attn_kernel: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }
+    if (mass) {
+        const int units = p.seqs * p.kv_heads, want = (a.cap + 1023) / 1024, most = (w.ctas * 16 + units - 1) / units;
+        e = launch_pdl(paged_mass_kernel, dim3(want < most ? want : most, units), dim3(256), 0, st, p, a.cap, G, lens,
+                       (const float *)a.logits, (const float *)a.lse, mass, mass_stride);
+        if (e != cudaSuccess) { set_error("paged_mass_kernel: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }
+    }
+    return launch_status("paged_attn");
 }
 
 }  // namespace fathom
