@@ -601,24 +601,30 @@ def fathom_sparse_attn(shape: Shape, k_rows, v_rows, q, topk_idx, workspace, out
 _ROW_TYPES = {torch.bfloat16: BF16, torch.float16: F16}
 
 
-@contextlib.contextmanager
-def _on(stream, *tensors):
-    """The tensors' device made current (one device: the library launches on the
-    current one) and, when a stream is given, that stream: outputs allocated inside
-    belong to the stream that writes them."""
-    devices = {t.device for t in tensors if t is not None and t.is_cuda}
-    if len(devices) > 1:
-        raise ValueError(f"tensors on several devices: {sorted(map(str, devices))}")
-    with contextlib.ExitStack() as stack:
-        if devices:
-            device = devices.pop()
-            if stream is not None and stream.device != device:
-                raise ValueError(f"stream on {stream.device}, tensors on {device}")
-            if device.index != torch.cuda.current_device():
-                stack.enter_context(torch.cuda.device(device))
-        if stream is not None:
-            stack.enter_context(torch.cuda.stream(stream))
-        yield
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(stream, tensors):
+    """(context, stream handle) of a call on these tensors: their device is made current
+    (one device: the library launches on the current one) and, when a stream is given,
+    that stream, so that outputs allocated inside belong to the stream that writes them."""
+    device = -1
+    for t in tensors:
+        d = t.get_device() if t is not None else -1
+        if d != device and d >= 0:
+            if device >= 0:
+                raise ValueError(f"tensors on several devices: cuda:{device} and cuda:{d}")
+            device = d
+    if stream is None:
+        if device < 0:
+            return contextlib.nullcontext(), _stream(None)
+        if device == torch.cuda.current_device():
+            return contextlib.nullcontext(), _raw_stream(device) if _raw_stream else _stream(None)
+        with torch.cuda.device(device):
+            return torch.cuda.device(device), _stream(None)
+    if device >= 0 and stream.device_index != device:
+        raise ValueError(f"stream on cuda:{stream.device_index}, tensors on cuda:{device}")
+    return torch.cuda.stream(stream), _stream(stream)
 
 
 def _check_strided(t, name, dtypes, shape, pinned=False):
@@ -642,6 +648,12 @@ def _on_device(t) -> bool:
     return t.is_cuda
 
 
+def _ok(t, dtype, shape):
+    """A contiguous CUDA tensor of this type and these sizes (the common case, decided in
+    one expression; anything else goes through the checks that name what is wrong)."""
+    return t is not None and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
+
+
 def fathom_prefill_attn(q, k, v, cu_q, cu_k=None, out=None, lse=None, want_lse=False, stream=None):
     """Causal attention of packed prompts (or of their next chunks): q [Tq][heads][D],
     k, v [Tk][kv_heads][D] bf16 or fp16, any strides with the last axis contiguous;
@@ -649,31 +661,35 @@ def fathom_prefill_attn(q, k, v, cu_q, cu_k=None, out=None, lse=None, want_lse=F
     of q's type, lse [Tq][heads] fp32 or None; rows behind cu_q[-1] are not written)."""
     if q is None or q.dim() != 3:
         raise ValueError("q: expected [tokens][heads][D]")
-    Tq, H, D = q.shape
-    _check_strided(q, "q", tuple(_ROW_TYPES), (Tq, H, D))
     if k is None or k.dim() != 3:
         raise ValueError("k: expected [tokens][kv_heads][D]")
-    Tk, Hkv = k.shape[0], k.shape[1]
-    _check_strided(k, "k", (q.dtype,), (Tk, Hkv, D))
-    _check_strided(v, "v", (q.dtype,), (Tk, Hkv, D))
-    cu_k = cu_q if cu_k is None else cu_k
+    Tq, H, D = q.shape
+    Tk, Hkv, _ = k.shape
+    dt = q.dtype
+    _check_strided(q, "q", _ROW_TYPES, (Tq, H, D))
+    _check_strided(k, "k", (dt,), (Tk, Hkv, D))
+    _check_strided(v, "v", (dt,), (Tk, Hkv, D))
+    if cu_k is None:
+        cu_k = cu_q
     _check(cu_q, "cu_q", (torch.int32,))
-    _check(cu_k, "cu_k", (torch.int32,), tuple(cu_q.shape))
     if cu_q.dim() != 1 or cu_q.shape[0] < 2:
         raise ValueError(f"cu_q: shape {tuple(cu_q.shape)} is not [seqs + 1]")
+    if not _ok(cu_k, torch.int32, cu_q.shape):
+        _check(cu_k, "cu_k", (torch.int32,), tuple(cu_q.shape))
     if out is not None:
-        _check_strided(out, "out", (q.dtype,), (Tq, H, D))
+        _check_strided(out, "out", (dt,), (Tq, H, D))
     if lse is not None:
         _check(lse, "lse", (torch.float32,), (Tq, H))
-    with _on(stream, q, k, v, cu_q, cu_k, out, lse):
+    context, handle = _on(stream, (q, k, v, cu_q, cu_k, out, lse))
+    with context:
         if out is None:
-            out = torch.empty(Tq, H, D, dtype=q.dtype, device=q.device)
+            out = torch.empty((Tq, H, D), dtype=dt, device=q.device)
         if lse is None and want_lse:
-            lse = torch.empty(Tq, H, dtype=torch.float32, device=q.device)
-        p = Prompts(cu_q.shape[0] - 1, H, Hkv, D, _ROW_TYPES[q.dtype], Tq, Tk, q.stride(0), q.stride(1), k.stride(0),
-                    k.stride(1), v.stride(0), v.stride(1), out.stride(0), out.stride(1))
-        _call("fathom_prefill_attn", ctypes.byref(p), _p(q), _p(k), _p(v), _p(cu_q), _p(cu_k), _p(out), _p(lse),
-              _stream(stream))
+            lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
+        (qt, qh, _), (kt, kh, _), (vt, vh, _), (ot, oh, _) = q.stride(), k.stride(), v.stride(), out.stride()
+        p = Prompts(cu_q.shape[0] - 1, H, Hkv, D, _ROW_TYPES[dt], Tq, Tk, qt, qh, kt, kh, vt, vh, ot, oh)
+        _call("fathom_prefill_attn", p, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
+              out.data_ptr(), lse.data_ptr() if lse is not None else None, handle)
     return out, lse
 
 
@@ -708,15 +724,20 @@ def rows_as_pages(rows, kv_heads, page_tokens=64, device=None):
 
 
 def _check_cache(pages, k_pages, v_pages, page_table):
-    dtype = torch.bfloat16 if pages.dtype == BF16 else torch.float16
-    shape = (pages.num_pages, pages.kv_heads, pages.page_tokens, pages.D)
+    """-> (type of the rows, sequences, KV heads, D, tokens a table row can name)."""
+    seqs, H, D, dt, P, n, per = (pages.seqs, pages.kv_heads, pages.D, pages.dtype, pages.page_tokens, pages.num_pages,
+                                 pages.max_pages)
+    dtype = torch.bfloat16 if dt == BF16 else torch.float16
+    shape, stride = (n, H, P, D), (pages.page_stride, pages.head_stride, pages.token_stride, 1)
     for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if t is not None and t.dtype is dtype and t.shape == shape and t.stride() == stride and t.is_cuda:
+            continue
         _check_strided(t, name, (dtype,), shape, pinned=True)
-        st = t.stride()
-        if any(a > 1 and x != y for a, x, y in zip(shape, st, (pages.page_stride, pages.head_stride,
-                                                               pages.token_stride))):
-            raise ValueError(f"{name}: strides {st[:3]} are not those of pages")
-    _check(page_table, "page_table", (torch.int32,), (pages.seqs, pages.max_pages))
+        if any(a > 1 and x != y for a, x, y in zip(shape, t.stride(), stride)):
+            raise ValueError(f"{name}: strides {t.stride()[:3]} are not those of pages")
+    if not _ok(page_table, torch.int32, (seqs, per)):
+        _check(page_table, "page_table", (torch.int32,), (seqs, per))
+    return dtype, seqs, H, D, per * P
 
 
 def paged_workspace_size(pages: Pages, G: int, mass=False) -> int:
@@ -735,22 +756,27 @@ def fathom_paged_append(pages: Pages, k_pages, v_pages, page_table, k_new, v_new
     """Write new rows k_new, v_new [T][kv_heads][D] (strided alike, the last axis contiguous)
     into the cache, in place: token i of sequence s at position start[s] + i.  start [seqs]
     int32; cu_new [seqs + 1] int32, or None: one token per sequence."""
-    _check_cache(pages, k_pages, v_pages, page_table)
+    dtype, seqs, H, D, _ = _check_cache(pages, k_pages, v_pages, page_table)
     if k_new is None or k_new.dim() != 3:
         raise ValueError("k_new: expected [tokens][kv_heads][D]")
     T = k_new.shape[0]
-    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-        _check_strided(t, name, (k_pages.dtype,), (T, pages.kv_heads, pages.D))
-    if any(a > 1 and x != y for a, x, y in zip(k_new.shape[:2], k_new.stride(), v_new.stride())):
+    _check_strided(k_new, "k_new", (dtype,), (T, H, D))
+    _check_strided(v_new, "v_new", (dtype,), (T, H, D))
+    stride = k_new.stride()
+    if stride != v_new.stride() and any(a > 1 and x != y for a, x, y in zip((T, H), stride, v_new.stride())):
         raise ValueError("v_new: strides differ from k_new's")
-    _check(start, "start", (torch.int32,), (pages.seqs,))
+    if not _ok(start, torch.int32, (seqs,)):
+        _check(start, "start", (torch.int32,), (seqs,))
     if cu_new is not None:
-        _check(cu_new, "cu_new", (torch.int32,), (pages.seqs + 1,))
-    elif T != pages.seqs:
-        raise ValueError(f"k_new: {T} tokens for {pages.seqs} sequences without cu_new")
-    with _on(stream, k_pages, v_pages, page_table, k_new, v_new, start, cu_new):
-        _call("fathom_paged_append", ctypes.byref(pages), _p(k_pages), _p(v_pages), _p(page_table), _p(k_new),
-              _p(v_new), T, k_new.stride(0), k_new.stride(1), _p(start), _p(cu_new), _stream(stream))
+        if not _ok(cu_new, torch.int32, (seqs + 1,)):
+            _check(cu_new, "cu_new", (torch.int32,), (seqs + 1,))
+    elif T != seqs:
+        raise ValueError(f"k_new: {T} tokens for {seqs} sequences without cu_new")
+    context, handle = _on(stream, (k_pages, v_pages, page_table, k_new, v_new, start, cu_new))
+    with context:
+        _call("fathom_paged_append", pages, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+              k_new.data_ptr(), v_new.data_ptr(), T, stride[0], stride[1], start.data_ptr(),
+              cu_new.data_ptr() if cu_new is not None else None, handle)
     return k_pages, v_pages
 
 
@@ -759,23 +785,27 @@ def fathom_paged_attn(pages: Pages, q, k_pages, v_pages, page_table, lens, works
     """Decode attention over the cache: q [units][G][D] fp32, lens [seqs] int32 -> out
     [units][G][D] fp32.  mass [units][M] fp32, M >= pages.cap: each token's attention
     weights, summed over the G heads, are added to it (workspace allocated with mass)."""
-    _check_cache(pages, k_pages, v_pages, page_table)
+    _, seqs, H, D, cap = _check_cache(pages, k_pages, v_pages, page_table)
     if q is None or q.dim() != 3:
         raise ValueError("q: expected [units][G][D]")
     G = q.shape[1]
-    _check(q, "q", (torch.float32,), (pages.units, G, pages.D))
-    _check(lens, "lens", (torch.int32,), (pages.seqs,))
+    shape = (seqs * H, G, D)
+    if not _ok(q, torch.float32, shape):
+        _check(q, "q", (torch.float32,), shape)
+    if not _ok(lens, torch.int32, (seqs,)):
+        _check(lens, "lens", (torch.int32,), (seqs,))
     _check(workspace, "workspace", (torch.uint8,))
-    if out is not None:
-        _check(out, "out", (torch.float32,), (pages.units, G, pages.D))
+    if out is not None and not _ok(out, torch.float32, shape):
+        _check(out, "out", (torch.float32,), shape)
     if mass is not None:
-        _check_mass(mass, "mass", pages.units, pages.cap)
-    with _on(stream, q, k_pages, v_pages, page_table, lens, workspace, out, mass):
+        _check_mass(mass, "mass", seqs * H, cap)
+    context, handle = _on(stream, (q, k_pages, v_pages, page_table, lens, workspace, out, mass))
+    with context:
         if out is None:
-            out = torch.empty(pages.units, G, pages.D, dtype=torch.float32, device=q.device)
-        _call("fathom_paged_attn", ctypes.byref(pages), G, _p(q), _p(k_pages), _p(v_pages), _p(page_table), _p(lens),
-              _p(out), _p(mass), mass.shape[1] if mass is not None else 0, _p(workspace), workspace.numel(),
-              _stream(stream))
+            out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        _call("fathom_paged_attn", pages, G, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+              page_table.data_ptr(), lens.data_ptr(), out.data_ptr(), mass.data_ptr() if mass is not None else None,
+              mass.shape[1] if mass is not None else 0, workspace.data_ptr(), workspace.numel(), handle)
     return out
 
 
@@ -791,28 +821,31 @@ def fathom_paged_evict(pages: Pages, k_pages, v_pages, page_table, lens, mass, k
     to the pages of dst_table [seqs][pages] (page_table itself: in place).  -> (kept_idx
     [units][keep] int32, ascending and then -1, lens_out [seqs] int32, mass_out
     [units][M] fp32; mass_out None: mass itself, in place)."""
-    _check_cache(pages, k_pages, v_pages, page_table)
-    keep = int(keep)
-    _check(lens, "lens", (torch.int32,), (pages.seqs,))
-    _check_mass(mass, "mass", pages.units, pages.cap)
+    _, seqs, H, _, cap = _check_cache(pages, k_pages, v_pages, page_table)
+    keep, units = int(keep), seqs * H
+    if not _ok(lens, torch.int32, (seqs,)):
+        _check(lens, "lens", (torch.int32,), (seqs,))
+    _check_mass(mass, "mass", units, cap)
     _check(dst_table, "dst_table", (torch.int32,))
-    if dst_table.dim() != 2 or dst_table.shape[0] != pages.seqs:
-        raise ValueError(f"dst_table: shape {tuple(dst_table.shape)} is not [{pages.seqs}][pages]")
+    if dst_table.dim() != 2 or dst_table.shape[0] != seqs:
+        raise ValueError(f"dst_table: shape {tuple(dst_table.shape)} is not [{seqs}][pages]")
     if mass_out is None:
         mass_out = mass
-    _check_mass(mass_out, "mass_out", pages.units, keep)
+    _check_mass(mass_out, "mass_out", units, keep)
     if kept_idx is not None:
-        _check(kept_idx, "kept_idx", (torch.int32,), (pages.units, keep))
+        _check(kept_idx, "kept_idx", (torch.int32,), (units, keep))
     if lens_out is not None:
-        _check(lens_out, "lens_out", (torch.int32,), (pages.seqs,))
-    with _on(stream, k_pages, v_pages, page_table, lens, mass, dst_table, kept_idx, lens_out, mass_out):
+        _check(lens_out, "lens_out", (torch.int32,), (seqs,))
+    context, handle = _on(stream, (k_pages, v_pages, page_table, lens, mass, dst_table, kept_idx, lens_out, mass_out))
+    with context:
         if kept_idx is None:
-            kept_idx = torch.empty(pages.units, keep, dtype=torch.int32, device=mass.device)
+            kept_idx = torch.empty((units, keep), dtype=torch.int32, device=mass.device)
         if lens_out is None:
-            lens_out = torch.empty(pages.seqs, dtype=torch.int32, device=mass.device)
-        _call("fathom_paged_evict", ctypes.byref(pages), _p(k_pages), _p(v_pages), _p(page_table), _p(lens), _p(mass),
-              mass.shape[1], keep, int(n_sink), int(n_recent), _p(dst_table), dst_table.shape[1], _p(kept_idx),
-              _p(lens_out), _p(mass_out), mass_out.shape[1], _stream(stream))
+            lens_out = torch.empty(seqs, dtype=torch.int32, device=mass.device)
+        _call("fathom_paged_evict", pages, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+              lens.data_ptr(), mass.data_ptr(), mass.shape[1], keep, int(n_sink), int(n_recent), dst_table.data_ptr(),
+              dst_table.shape[1], kept_idx.data_ptr(), lens_out.data_ptr(), mass_out.data_ptr(), mass_out.shape[1],
+              handle)
     return kept_idx, lens_out, mass_out
 
 

@@ -271,7 +271,7 @@ int launch_paged_append(const fathom_pages &p, void *kp, void *vp, const int32_t
 // normaliser.
 struct PagedWorkspace {
     int ctas;
-    size_t ticket_off, lse_off, part_off, logit_off, total;
+    size_t ticket_off, lse_off, part_off, ml_off, logit_off, total;
 };
 PagedWorkspace paged_workspace_layout(const fathom_pages &p, int G, bool mass);
 int launch_paged_attn(const fathom_pages &p, int G, const float *q, const void *kp, const void *vp,

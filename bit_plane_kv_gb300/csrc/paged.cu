@@ -125,8 +125,13 @@ struct DecArgs {
     const float *q;
     const void *kp, *vp;
     const int32_t *table, *lens;
-    float *out, *part, *lse, *logits;
+    float *out, *part_o, *part_ml, *lse, *logits;   // shares: [CTA][2][G][D] and [CTA][2][G][2] = (m, l)
     unsigned *ticket;
+};
+
+// Join of a unit's shares, 32 at a time; in the place of DecSmem::o.
+struct JoinSmem {
+    float weight[FATHOM_MAX_G][32], m[FATHOM_MAX_G], l[FATHOM_MAX_G], f[FATHOM_MAX_G];
 };
 
 // 16-token rows of a warp's stage: K, then V; 16-byte piece c of row t lies at piece
@@ -136,13 +141,20 @@ struct DecSmem {
     static constexpr int kSub = kD == 128 ? 1 : 2;   // 16-token parts of a warp's share of a tile
     static constexpr int kTile = 16 * kSub * kDecWarps;
     static constexpr int kRowBytes = kD * 2;
+    static_assert(sizeof(JoinSmem) <= sizeof(float) * kDecWarps * FATHOM_MAX_G * kD, "the join reuses o");
     alignas(128) unsigned char ring[kDecWarps][kDecStages][kSub][2][16 * kRowBytes];
     float o[kDecWarps][FATHOM_MAX_G][kD];
     float m[kDecWarps][FATHOM_MAX_G], l[kDecWarps][FATHOM_MAX_G];
     unsigned live[kDecWarps][kDecStages][kSub];   // which of the 16 tokens there are
-    long long sum[kDecWarps], first_tile, first_seq_tile;
+    long long sum[kDecWarps], first_seq_tile;
     int seq, last;
 };
+
+// Division of numbers that mostly fit 32 bits, and the first tile of CTA c's share.
+__device__ __forceinline__ long long div64(long long x, long long y) {
+    return (unsigned long long)(x | y) >> 32 ? x / y : (long long)((unsigned)x / (unsigned)y);
+}
+__device__ __forceinline__ long long share(long long c, long long W, long long NC) { return div64(c * W, NC); }
 
 // Position in the order (sequence, head, tile); `tiles` of the sequence.
 struct DecCursor {
@@ -182,7 +194,7 @@ paged_attn_kernel(const DecArgs a) {
             for (int e = tid; e < G * D; e += kDecThreads) a.out[(size_t)u * G * D + e] = 0.0f;
     const long long cta = blockIdx.x;
     if (cta >= NC) return;
-    const long long w0 = cta * W / NC, w1 = (cta + 1) * W / NC;
+    const long long w0 = share(cta, W, NC), w1 = share(cta + 1, W, NC);
     if (warp == 0) {   // the sequence of tile w0
         long long before = 0;
         for (int s0 = 0; s0 < p.seqs; s0 += 32) {
@@ -457,9 +469,9 @@ paged_attn_kernel(const DecArgs a) {
             }
         __syncthreads();
         // the CTA's state of each head: (m, l, o), to `out` when the unit is all here
-        const long long c_first = ((unit_w0 + 1) * NC - 1) / W, c_last = ((unit_w0 + tiles) * NC - 1) / W;
+        const long long c_first = div64((unit_w0 + 1) * NC - 1, W), c_last = div64((unit_w0 + tiles) * NC - 1, W);
         const bool whole = c_first == c_last;
-        float *pp = a.part + (size_t)(2 * cta + (w0 < unit_w0 ? 1 : 0)) * G * (D + 2);
+        const size_t slot = 2 * cta + (w0 < unit_w0 ? 1 : 0);
         for (int e = tid; e < G * D; e += kDecThreads) {
             const int h = e / D, d = e % D;
             float Mh = -CUDART_INF_F, L = 0.0f, O = 0.0f;
@@ -471,9 +483,9 @@ paged_attn_kernel(const DecArgs a) {
                 L += sm.m[w][h] == -CUDART_INF_F ? 0.0f : sm.l[w][h] * exp2_fast(sm.m[w][h] - Mh);
             }
             if (whole) a.out[(size_t)unit * G * D + e] = L > 0.0f ? O / L : 0.0f;
-            else pp[h * (D + 2) + 2 + d] = O;
+            else a.part_o[slot * G * D + e] = O;
             if (d == 0) {
-                if (!whole) { pp[h * (D + 2)] = Mh; pp[h * (D + 2) + 1] = L; }
+                if (!whole) *reinterpret_cast<float2 *>(a.part_ml + (slot * G + h) * 2) = make_float2(Mh, L);
                 else if (kMass) a.lse[(size_t)unit * G + h] = L > 0.0f ? Mh + log2f(L) - kUp : 0.0f;
             }
         }
@@ -482,24 +494,70 @@ paged_attn_kernel(const DecArgs a) {
             __syncthreads();
             if (tid == 0) sm.last = atomicAdd(a.ticket + unit, 1u) == (unsigned)(c_last - c_first) ? 1 : 0;
             __syncthreads();
-            if (sm.last) {   // every share of the unit is there: joined in their order
+            if (sm.last) {   // every share of the unit is there: joined in their order, 32 at a time
                 __threadfence();
                 if (tid == 0) a.ticket[unit] = 0u;
-                for (int e = tid; e < G * D; e += kDecThreads) {
-                    const int h = e / D, d = e % D;
-                    float Mh = -CUDART_INF_F, L = 0.0f, O = 0.0f;
-                    for (long long x = c_first; x <= c_last; ++x) {
-                        const float *px = a.part + ((size_t)(2 * x + (x * W / NC < unit_w0 ? 1 : 0)) * G + h) * (D + 2);
-                        const float mx = __ldcg(px), lx = __ldcg(px + 1), ox = __ldcg(px + 2 + d);
-                        const float mn = fmaxf(Mh, mx);
-                        const float f0 = Mh == -CUDART_INF_F ? 0.0f : exp2_fast(Mh - mn);
-                        const float f1 = mx == -CUDART_INF_F ? 0.0f : exp2_fast(mx - mn);
-                        O = O * f0 + ox * f1;
-                        L = L * f0 + lx * f1;
-                        Mh = mn;
+                JoinSmem &jn = *reinterpret_cast<JoinSmem *>(sm.o);
+                if (tid < G) { jn.m[tid] = -CUDART_INF_F; jn.l[tid] = 0.0f; }
+                constexpr int kVecs = FATHOM_MAX_G * kD / 4 / kDecThreads;   // four channels at a time
+                float4 acc[kVecs];
+#pragma unroll
+                for (int k = 0; k < kVecs; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                const int before = share(c_first, W, NC) < unit_w0;   // only the first share can be a CTA's second
+                auto slot_of = [&](long long x) { return (size_t)(2 * x + (x == c_first ? before : 0)); };
+                for (long long x0 = c_first; x0 <= c_last; x0 += 32) {
+                    const int nx = (int)min(c_last - x0 + 1, 32LL);
+                    __syncthreads();
+                    for (int h = warp; h < G; h += kDecWarps) {
+                        float2 ml = make_float2(-CUDART_INF_F, 0.0f);
+                        if (lane < nx) ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + (slot_of(x0 + lane) * G + h) * 2));
+                        float mx = ml.x;
+#pragma unroll
+                        for (int o2 = 16; o2; o2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
+                        const float old = jn.m[h], mn = fmaxf(old, mx);
+                        const float wt = ml.x == -CUDART_INF_F ? 0.0f : exp2_fast(ml.x - mn);
+                        float ls = ml.y * wt;
+#pragma unroll
+                        for (int o2 = 16; o2; o2 >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o2);
+                        jn.weight[h][lane] = wt;
+                        __syncwarp();
+                        if (lane == 0) {
+                            const float fo = old == -CUDART_INF_F ? 0.0f : exp2_fast(old - mn);
+                            jn.f[h] = fo;
+                            jn.l[h] = jn.l[h] * fo + ls;
+                            jn.m[h] = mn;
+                        }
                     }
-                    a.out[(size_t)unit * G * D + e] = L > 0.0f ? O / L : 0.0f;
-                    if (kMass && d == 0) a.lse[(size_t)unit * G + h] = L > 0.0f ? Mh + log2f(L) - kUp : 0.0f;
+                    __syncthreads();
+#pragma unroll
+                    for (int k = 0; k < kVecs; ++k) {
+                        const int e = 4 * (tid + k * kDecThreads);
+                        if (e < G * D) {
+                            const int h = e / D;   // D is a multiple of 8: the four lie in one head
+                            const float fo = jn.f[h];
+                            acc[k].x *= fo; acc[k].y *= fo; acc[k].z *= fo; acc[k].w *= fo;
+#pragma unroll 8
+                            for (int x = 0; x < nx; ++x) {
+                                const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot_of(x0 + x) * G * D + e));
+                                const float wt = jn.weight[h][x];
+                                acc[k].x = fmaf(v.x, wt, acc[k].x);
+                                acc[k].y = fmaf(v.y, wt, acc[k].y);
+                                acc[k].z = fmaf(v.z, wt, acc[k].z);
+                                acc[k].w = fmaf(v.w, wt, acc[k].w);
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kVecs; ++k) {
+                    const int e = 4 * (tid + k * kDecThreads);
+                    if (e < G * D) {
+                        const int h = e / D;
+                        const float L = jn.l[h], inv = L > 0.0f ? 1.0f / L : 0.0f;
+                        float *ou = a.out + (size_t)unit * G * D + e;
+                        ou[0] = acc[k].x * inv; ou[1] = acc[k].y * inv; ou[2] = acc[k].z * inv; ou[3] = acc[k].w * inv;
+                        if (kMass && e % D == 0) a.lse[(size_t)unit * G + h] = L > 0.0f ? jn.m[h] + log2f(L) - kUp : 0.0f;
+                    }
                 }
             }
         }
@@ -529,6 +587,7 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 template <typename T, int kD, int kTwo, bool kMass>
 cudaError_t launch_dec(const DecArgs &a, int ctas, cudaStream_t st) {
     const size_t smem = sizeof(DecSmem<kD>);
+    static_assert(2 * (sizeof(DecSmem<kD>) + 1024) <= 228 * 1024, "two CTAs share an SM");
     ensure_smem(paged_attn_kernel<T, kD, kTwo, kMass>, smem);
     return launch_pdl(paged_attn_kernel<T, kD, kTwo, kMass>, dim3(ctas), dim3(kDecThreads), smem, st, a);
 }
@@ -560,7 +619,8 @@ PagedWorkspace paged_workspace_layout(const fathom_pages &p, int G, bool mass) {
     w.ticket_off = 0;
     w.lse_off = align256(units * sizeof(uint32_t));
     w.part_off = align256(w.lse_off + (mass ? rows * sizeof(float) : 0));
-    w.logit_off = align256(w.part_off + (size_t)w.ctas * 2 * G * (p.D + 2) * sizeof(float));
+    w.ml_off = align256(w.part_off + (size_t)w.ctas * 2 * G * p.D * sizeof(float));
+    w.logit_off = align256(w.ml_off + (size_t)w.ctas * 2 * G * 2 * sizeof(float));
     w.total = align256(w.logit_off + (mass ? rows * ((size_t)p.max_pages * p.page_tokens) * sizeof(float) : 0));
     return w;
 }
@@ -576,7 +636,8 @@ int launch_paged_attn(const fathom_pages &p, int G, const float *q, const void *
     a.cap = p.max_pages * p.page_tokens;
     a.q = q; a.kp = kp; a.vp = vp; a.table = table; a.lens = lens; a.out = out;
     a.ticket = (unsigned *)((char *)ws + w.ticket_off);
-    a.part = (float *)((char *)ws + w.part_off);
+    a.part_o = (float *)((char *)ws + w.part_off);
+    a.part_ml = (float *)((char *)ws + w.ml_off);
     a.lse = mass ? (float *)((char *)ws + w.lse_off) : nullptr;
     a.logits = mass ? (float *)((char *)ws + w.logit_off) : nullptr;
     cudaError_t e;
