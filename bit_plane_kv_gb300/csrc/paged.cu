@@ -53,7 +53,7 @@ paged_append_kernel(fathom_pages p, int lg, int4 *__restrict__ kp, int4 *__restr
 // One new token per sequence over its cache: o_h = sum_i softmax_i(q_h . k_i / sqrt(D)) v_i.
 // Bound by the cache's bytes, each K and V row read once for the G heads of a unit.
 //
-// The 64-token tiles (128 for D <= 64) of all units, in unit order, are dealt out to
+// The 64-token tiles of all units, in unit order, are dealt out to
 // the CTAs in equal contiguous shares, whatever the sequences' lengths; a unit that
 // several CTAs share is joined by the last of them to arrive at the unit's ticket.
 // In a tile each warp takes its own 16 tokens, in 16-byte asynchronous copies to a
@@ -66,7 +66,10 @@ paged_append_kernel(fathom_pages p, int lg, int4 *__restrict__ kp, int4 *__restr
 // second instruction adds the third -- so a K or V fragment is read from shared
 // memory once for all heads and pieces.
 
-constexpr int kDecWarps = 4, kDecThreads = 32 * kDecWarps, kDecStages = 3;
+constexpr int kDecWarps = 4, kDecThreads = 32 * kDecWarps;
+// CTAs resident per SM, and stages of their rings
+__host__ __device__ constexpr int dec_ctas(int d) { return d == 128 ? 2 : 3; }
+__host__ __device__ constexpr int dec_stages(int d) { return d == 128 ? 3 : 4; }
 
 __device__ __forceinline__ uint32_t pack_pair(float lo, float hi, __nv_bfloat16) {
     uint32_t r;
@@ -121,7 +124,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 struct DecArgs {
     fathom_pages p;
-    int lg, G, cap;
+    int lg, G, cap, logit_stride;   // logits [units][G][logit_stride], rows of whole 16 bytes
     const float *q;
     const void *kp, *vp;
     const int32_t *table, *lens;
@@ -138,16 +141,16 @@ struct JoinSmem {
 // c ^ (t & 7), which keeps ldmatrix free of bank conflicts.
 template <int kD>
 struct DecSmem {
-    static constexpr int kSub = kD == 128 ? 1 : 2;   // 16-token parts of a warp's share of a tile
-    static constexpr int kTile = 16 * kSub * kDecWarps;
+    static constexpr int kDecStages = dec_stages(kD);
+    static constexpr int kTile = 16 * kDecWarps;
     static constexpr int kRowBytes = kD * 2;
     static_assert(sizeof(JoinSmem) <= sizeof(float) * kDecWarps * FATHOM_MAX_G * kD, "the join reuses o");
-    alignas(128) unsigned char ring[kDecWarps][kDecStages][kSub][2][16 * kRowBytes];
+    alignas(128) unsigned char ring[kDecWarps][kDecStages][2][16 * kRowBytes];
     float o[kDecWarps][FATHOM_MAX_G][kD];
     float m[kDecWarps][FATHOM_MAX_G], l[kDecWarps][FATHOM_MAX_G];
-    unsigned live[kDecWarps][kDecStages][kSub];   // which of the 16 tokens there are
-    long long sum[kDecWarps], first_seq_tile;
-    int seq, last;
+    unsigned live[kDecWarps][kDecStages];   // which of the 16 tokens there are
+    long long sum[kDecWarps];
+    int last;
 };
 
 // Division of numbers that mostly fit 32 bits, and the first tile of CTA c's share.
@@ -162,11 +165,11 @@ struct DecCursor {
 };
 
 template <typename T, int kD, int kTwo, bool kMass>   // kTwo: G > 4
-__global__ void __launch_bounds__(kDecThreads, 2)
+__global__ void __launch_bounds__(kDecThreads, dec_ctas(kD))
 paged_attn_kernel(const DecArgs a) {
     pdl_enter();
     using Smem = DecSmem<kD>;
-    constexpr int kSub = Smem::kSub, kTile = Smem::kTile, kRowBytes = Smem::kRowBytes;
+    constexpr int kTile = Smem::kTile, kRowBytes = Smem::kRowBytes, kDecStages = Smem::kDecStages;
     constexpr int kNT = kD / 8, kKS = kD / 16, kPieces = kD / 8;
     extern __shared__ __align__(128) unsigned char dec_smem[];
     Smem &sm = *reinterpret_cast<Smem *>(dec_smem);
@@ -176,56 +179,83 @@ paged_attn_kernel(const DecArgs a) {
     auto length = [&](int s) { return min(max(a.lens[s], 0), a.cap); };
     auto tiles_of = [&](int n) { return (n + kTile - 1) / kTile; };
 
-    // ---- all tiles, and this CTA's share of them
-    long long mine = 0;
-    for (int s = tid; s < p.seqs; s += kDecThreads) mine += tiles_of(length(s));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) sm.sum[warp] = mine;
-    __syncthreads();
-    long long W = 0;
-#pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) W += sm.sum[w];
-    W *= H;
-    const long long NC = min((long long)gridDim.x, W);
-    // units of empty sequences
-    for (int u = blockIdx.x; u < p.seqs * H; u += gridDim.x)
-        if (length(u / H) == 0)
-            for (int e = tid; e < G * D; e += kDecThreads) a.out[(size_t)u * G * D + e] = 0.0f;
+    // ---- all tiles, this CTA's share of them, and the sequence it starts in
+    long long W = 0, first = 0, w0 = 0, w1 = 0, NC = 1;   // first: the sequence's first tile
     const long long cta = blockIdx.x;
-    if (cta >= NC) return;
-    const long long w0 = share(cta, W, NC), w1 = share(cta + 1, W, NC);
-    if (warp == 0) {   // the sequence of tile w0
+    int seq0 = 0;
+    auto split = [&](long long sum) {
+        W = sum * H;
+        // every CTA there is when each gets four tiles or more, else fewer CTAs and longer shares, down to
+        // one per SM: a share less to join costs less than a tile more (one 4k sequence: 304 shares of
+        // two tiles 15.6 us, 152 of four 11.6 us)
+        NC = min((long long)gridDim.x, max(1LL, max(W / 4, min(W, (long long)gridDim.x / dec_ctas(kD)))));
+        if (cta < NC) { w0 = share(cta, W, NC); w1 = share(cta + 1, W, NC); }
+    };
+    // inclusive sums over the lanes; the lane whose tiles hold w0, given the sum before them
+    auto scan = [&](long long x) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        return x;
+    };
+    if (p.seqs <= 128) {   // every warp for itself, four sequences per lane, one round of loads
+        int t[4], sum = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            t[e] = 4 * lane + e < p.seqs ? tiles_of(length(4 * lane + e)) : 0;
+            sum += t[e];
+        }
+        const long long upto = scan(sum);
+        split(__shfl_sync(0xffffffffu, upto, 31));
+        const unsigned hit = __ballot_sync(0xffffffffu, upto * H > w0);
+        const int f = hit ? __ffs(hit) - 1 : 0;
+        long long before = (upto - sum) * H;
+        int s = 4 * lane;
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (s == 4 * lane + e && before + (long long)t[e] * H <= w0) { before += (long long)t[e] * H; ++s; }
+        seq0 = __shfl_sync(0xffffffffu, s, f);
+        first = __shfl_sync(0xffffffffu, before, f);
+    } else {
+        long long mine = 0;
+        for (int s = tid; s < p.seqs; s += kDecThreads) mine += tiles_of(length(s));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        if (lane == 0) sm.sum[warp] = mine;
+        __syncthreads();
+        long long sum = 0;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) sum += sm.sum[w];
+        split(sum);
         long long before = 0;
         for (int s0 = 0; s0 < p.seqs; s0 += 32) {
             const long long x = s0 + lane < p.seqs ? (long long)tiles_of(length(s0 + lane)) * H : 0;
-            long long upto = x;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += y;
-            }
+            const long long upto = scan(x);
             const unsigned hit = __ballot_sync(0xffffffffu, before + upto > w0);
             if (hit) {
                 const int f = __ffs(hit) - 1;
-                if (lane == f) { sm.seq = s0 + f; sm.first_seq_tile = before + upto - x; }
+                seq0 = s0 + f;
+                first = __shfl_sync(0xffffffffu, before + upto - x, f);
                 break;
             }
             before += __shfl_sync(0xffffffffu, upto, 31);
         }
     }
-    __syncthreads();
+    // units of empty sequences
+    for (int u = blockIdx.x; u < p.seqs * H; u += gridDim.x)
+        if (length(u / H) == 0)
+            for (int e = tid; e < G * D; e += kDecThreads) a.out[(size_t)u * G * D + e] = 0.0f;
+    if (w0 >= w1) return;
     DecCursor at;   // the tile being computed
-    at.seq = sm.seq;
+    at.seq = seq0;
     at.n = length(at.seq);
     at.tiles = tiles_of(at.n);
-    {
-        const long long in = w0 - sm.first_seq_tile;
-        at.head = (int)(in / at.tiles);
-        at.tile = (int)(in % at.tiles);
-    }
-    auto advance = [&](DecCursor &x) {   // true when the unit changes
-        if (++x.tile < x.tiles) return false;
+    at.head = (int)div64(w0 - first, at.tiles);
+    at.tile = (int)(w0 - first - (long long)at.head * at.tiles);
+    auto advance = [&](DecCursor &x) {   // true when the unit changes; past the last sequence it stays there
+        if (x.seq >= p.seqs || ++x.tile < x.tiles) return false;
         x.tile = 0;
         if (++x.head == H) {
             x.head = 0;
@@ -238,55 +268,56 @@ paged_attn_kernel(const DecArgs a) {
         return true;
     };
 
-    // ---- loads: lane t < 16 looks up the page of token t, one tile ahead of its copies
+    // ---- loads: lane t < 16 looks up the page of token t, ahead of its tile's copies
     const char *kb = (const char *)a.kp, *vb = (const char *)a.vp;
-    DecCursor ld = at;
-    int pid[kSub];
-    auto lookup = [&]() {
-#pragma unroll
-        for (int b = 0; b < kSub; ++b) {
-            const int i = ld.tile * kTile + (warp * kSub + b) * 16 + (lane & 15);
-            int page = -1;
-            if (ld.seq < p.seqs && i < ld.n) {
-                page = __ldg(a.table + (size_t)ld.seq * p.max_pages + (i >> a.lg));
-                if (page >= p.num_pages) page = -1;
-            }
-            pid[b] = page;
+    auto lookup = [&](const DecCursor &x) {
+        const int i = x.tile * kTile + warp * 16 + (lane & 15);
+        int page = -1;
+        if (x.seq < p.seqs && i < x.n) {
+            page = __ldg(a.table + (size_t)x.seq * p.max_pages + (i >> a.lg));
+            if (page >= p.num_pages) page = -1;
         }
+        return page;
     };
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm.ring[warp]);
-    constexpr uint32_t kHalf = 16 * kRowBytes, kStageBytes = kSub * 2 * kHalf;
+    constexpr uint32_t kHalf = 16 * kRowBytes;
     const int col = lane % kPieces, row0 = lane / kPieces;   // this lane's 16-byte piece, its first row
     constexpr int kRowsPer = 32 / kPieces;
-    auto issue = [&](int st) {   // the copies of the tile at `ld`, whose pages are in pid
+    auto issue = [&](int st, const DecCursor &x, int pid) {   // the copies of a tile whose pages are known
+        const unsigned ok = __ballot_sync(0xffffffffu, pid >= 0) & 0xffffu;
+        if (lane == 0) sm.live[warp][st] = ok;
+        const int64_t at_head = x.head * p.head_stride;
 #pragma unroll
-        for (int b = 0; b < kSub; ++b) {
-            const unsigned ok = __ballot_sync(0xffffffffu, pid[b] >= 0) & 0xffffu;
-            if (lane == 0) sm.live[warp][st][b] = ok;
-#pragma unroll
-            for (int i = 0; i < 16 / kRowsPer; ++i) {
-                const int t = row0 + i * kRowsPer;
-                const int page = __shfl_sync(0xffffffffu, pid[b], t);
-                const int slot = (ld.tile * kTile + (warp * kSub + b) * 16 + t) & (p.page_tokens - 1);
-                const bool live = page >= 0 && col * 8 < D;
-                const int64_t off = live ? 2 * (page * p.page_stride + ld.head * p.head_stride + slot * p.token_stride) + col * 16 : 0;
-                const uint32_t dst = ring + st * kStageBytes + b * 2 * kHalf + t * kRowBytes + ((col ^ (t & 7)) << 4);
-                const int bytes = live ? 16 : 0;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(kb + off), "r"(bytes) : "memory");
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + kHalf), "l"(vb + off), "r"(bytes) : "memory");
-            }
+        for (int i = 0; i < 16 / kRowsPer; ++i) {
+            const int t = row0 + i * kRowsPer;
+            const int page = __shfl_sync(0xffffffffu, pid, t);
+            const int slot = (x.tile * kTile + warp * 16 + t) & (p.page_tokens - 1);
+            const bool live = page >= 0 && col * 8 < D;
+            const int64_t off = live ? 2 * (page * p.page_stride + at_head + slot * p.token_stride) + col * 16 : 0;
+            const uint32_t dst = ring + st * 2 * kHalf + t * kRowBytes + ((col ^ (t & 7)) << 4);
+            const int bytes = live ? 16 : 0;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(kb + off), "r"(bytes) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + kHalf), "l"(vb + off), "r"(bytes) : "memory");
         }
     };
     const int count = (int)(w1 - w0);
-    lookup();
+    DecCursor ld = at;
+    int pid;
+    {   // the first stages: every page looked up before the first copy
+        DecCursor cs[kDecStages - 1];
+        int ids[kDecStages - 1];
 #pragma unroll
-    for (int st = 0; st < kDecStages - 1; ++st) {
-        if (st < count) {
-            issue(st);
+        for (int st = 0; st < kDecStages - 1; ++st) {
+            cs[st] = ld;
+            ids[st] = lookup(ld);
             advance(ld);
-            lookup();
         }
-        cp_async_commit();
+        pid = lookup(ld);
+#pragma unroll
+        for (int st = 0; st < kDecStages - 1; ++st) {
+            if (st < count) issue(st, cs[st], ids[st]);
+            cp_async_commit();
+        }
     }
 
     const int head = kTwo ? r : (r & 3);   // this lane's head in score and output fragments
@@ -351,18 +382,17 @@ paged_attn_kernel(const DecArgs a) {
         const int st = i % kDecStages;
         {   // the copies two tiles ahead, into the stage that was read last
             if (i + kDecStages - 1 < count) {
-                issue((i + kDecStages - 1) % kDecStages);
+                issue((i + kDecStages - 1) % kDecStages, ld, pid);
                 advance(ld);
-                lookup();
+                pid = lookup(ld);
             }
             cp_async_commit();
             cp_async_wait<kDecStages - 1>();
             __syncwarp();
         }
-#pragma unroll
-        for (int b = 0; b < kSub; ++b) {
-            const uint32_t kt = ring + st * kStageBytes + b * 2 * kHalf, vt = kt + kHalf;
-            const unsigned ok = sm.live[warp][st][b];
+        {
+            const uint32_t kt = ring + st * 2 * kHalf, vt = kt + kHalf;
+            const unsigned ok = sm.live[warp][st];
             // scores of 16 tokens: columns 2 c, 2 c + 1 of two 8-token products
             float s[2][4] = {};
 #pragma unroll
@@ -391,14 +421,12 @@ paged_attn_kernel(const DecArgs a) {
                     top = fmaxf(top, x[j][e]);
                 }
             if (kMass) {
-                const int i0 = at.tile * kTile + (warp * kSub + b) * 16 + 2 * c;
-                float *lr = a.logits + ((size_t)(at.seq * H + at.head) * G + head) * a.cap;
+                const int i0 = at.tile * kTile + warp * 16 + 2 * c;
+                float *lr = a.logits + ((size_t)(at.seq * H + at.head) * G + head) * a.logit_stride;
                 if (head < G && (kTwo || r < 4)) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (i0 + 8 * j + e < at.n) lr[i0 + 8 * j + e] = x[j][e];
+                        if (i0 + 8 * j < at.n) *reinterpret_cast<float2 *>(lr + i0 + 8 * j) = make_float2(x[j][0], x[j][1]);
                 }
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -472,34 +500,47 @@ paged_attn_kernel(const DecArgs a) {
         const long long c_first = div64((unit_w0 + 1) * NC - 1, W), c_last = div64((unit_w0 + tiles) * NC - 1, W);
         const bool whole = c_first == c_last;
         const size_t slot = 2 * cta + (w0 < unit_w0 ? 1 : 0);
-        for (int e = tid; e < G * D; e += kDecThreads) {
-            const int h = e / D, d = e % D;
-            float Mh = -CUDART_INF_F, L = 0.0f, O = 0.0f;
+        constexpr int kAll = (kTwo ? FATHOM_MAX_G : 4) * kD / 4;   // four channels at a time
+        constexpr int kVecs = (kAll + kDecThreads - 1) / kDecThreads;
 #pragma unroll
-            for (int w = 0; w < kDecWarps; ++w) Mh = fmaxf(Mh, sm.m[w][h]);
+        for (int k = 0; k < kVecs; ++k) {
+            const int e = 4 * (tid + k * kDecThreads);
+            if (e < G * D) {
+                const int h = e / D, d = e - h * D;   // D is a multiple of 8: the four lie in one head
+                float Mh = -CUDART_INF_F, L = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kDecWarps; ++w) {
-                O += sm.o[w][h][d];
-                L += sm.m[w][h] == -CUDART_INF_F ? 0.0f : sm.l[w][h] * exp2_fast(sm.m[w][h] - Mh);
-            }
-            if (whole) a.out[(size_t)unit * G * D + e] = L > 0.0f ? O / L : 0.0f;
-            else a.part_o[slot * G * D + e] = O;
-            if (d == 0) {
-                if (!whole) *reinterpret_cast<float2 *>(a.part_ml + (slot * G + h) * 2) = make_float2(Mh, L);
-                else if (kMass) a.lse[(size_t)unit * G + h] = L > 0.0f ? Mh + log2f(L) - kUp : 0.0f;
+                for (int w = 0; w < kDecWarps; ++w) Mh = fmaxf(Mh, sm.m[w][h]);
+                float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < kDecWarps; ++w) {
+                    const float4 v = *reinterpret_cast<const float4 *>(&sm.o[w][h][d]);
+                    O.x += v.x; O.y += v.y; O.z += v.z; O.w += v.w;
+                    L += sm.m[w][h] == -CUDART_INF_F ? 0.0f : sm.l[w][h] * exp2_fast(sm.m[w][h] - Mh);
+                }
+                if (whole) {
+                    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+                    float *ou = a.out + (size_t)unit * G * D + e;
+                    ou[0] = O.x * inv; ou[1] = O.y * inv; ou[2] = O.z * inv; ou[3] = O.w * inv;
+                    if (kMass && d == 0) a.lse[(size_t)unit * G + h] = L > 0.0f ? Mh + log2f(L) - kUp : 0.0f;
+                } else {
+                    *reinterpret_cast<float4 *>(a.part_o + slot * G * D + e) = O;
+                    if (d == 0) *reinterpret_cast<float2 *>(a.part_ml + (slot * G + h) * 2) = make_float2(Mh, L);
+                }
             }
         }
         if (!whole) {
-            __threadfence();
             __syncthreads();
-            if (tid == 0) sm.last = atomicAdd(a.ticket + unit, 1u) == (unsigned)(c_last - c_first) ? 1 : 0;
+            if (tid == 0) {
+                __threadfence();   // the CTA's state before its ticket
+                sm.last = atomicAdd(a.ticket + unit, 1u) == (unsigned)(c_last - c_first) ? 1 : 0;
+                __threadfence();
+            }
             __syncthreads();
             if (sm.last) {   // every share of the unit is there: joined in their order, 32 at a time
-                __threadfence();
                 if (tid == 0) a.ticket[unit] = 0u;
                 JoinSmem &jn = *reinterpret_cast<JoinSmem *>(sm.o);
                 if (tid < G) { jn.m[tid] = -CUDART_INF_F; jn.l[tid] = 0.0f; }
-                constexpr int kVecs = FATHOM_MAX_G * kD / 4 / kDecThreads;   // four channels at a time
+                constexpr int kBatch = kD == 64 ? 4 : (kTwo ? 6 : 16);
                 float4 acc[kVecs];
 #pragma unroll
                 for (int k = 0; k < kVecs; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -507,6 +548,18 @@ paged_attn_kernel(const DecArgs a) {
                 auto slot_of = [&](long long x) { return (size_t)(2 * x + (x == c_first ? before : 0)); };
                 for (long long x0 = c_first; x0 <= c_last; x0 += 32) {
                     const int nx = (int)min(c_last - x0 + 1, 32LL);
+                    float4 v[kVecs][kBatch];
+                    auto fetch = [&](int x) {   // shares x0 + x and on, kBatch loads in flight per vector
+#pragma unroll
+                        for (int k = 0; k < kVecs; ++k) {
+                            const int e = 4 * (tid + k * kDecThreads);
+#pragma unroll
+                            for (int y = 0; y < kBatch; ++y)
+                                if (e < G * D && x + y < nx)
+                                    v[k][y] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot_of(x0 + x + y) * G * D + e));
+                        }
+                    };
+                    fetch(0);   // under way while the weights are computed
                     __syncthreads();
                     for (int h = warp; h < G; h += kDecWarps) {
                         float2 ml = make_float2(-CUDART_INF_F, 0.0f);
@@ -532,19 +585,24 @@ paged_attn_kernel(const DecArgs a) {
 #pragma unroll
                     for (int k = 0; k < kVecs; ++k) {
                         const int e = 4 * (tid + k * kDecThreads);
-                        if (e < G * D) {
-                            const int h = e / D;   // D is a multiple of 8: the four lie in one head
-                            const float fo = jn.f[h];
-                            acc[k].x *= fo; acc[k].y *= fo; acc[k].z *= fo; acc[k].w *= fo;
-#pragma unroll 8
-                            for (int x = 0; x < nx; ++x) {
-                                const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot_of(x0 + x) * G * D + e));
-                                const float wt = jn.weight[h][x];
-                                acc[k].x = fmaf(v.x, wt, acc[k].x);
-                                acc[k].y = fmaf(v.y, wt, acc[k].y);
-                                acc[k].z = fmaf(v.z, wt, acc[k].z);
-                                acc[k].w = fmaf(v.w, wt, acc[k].w);
-                            }
+                        const float fo = e < G * D ? jn.f[e / D] : 0.0f;
+                        acc[k].x *= fo; acc[k].y *= fo; acc[k].z *= fo; acc[k].w *= fo;
+                    }
+#pragma unroll 1
+                    for (int x = 0; x < nx; x += kBatch) {
+                        if (x) fetch(x);
+#pragma unroll
+                        for (int k = 0; k < kVecs; ++k) {
+                            const int e = 4 * (tid + k * kDecThreads);
+#pragma unroll
+                            for (int y = 0; y < kBatch; ++y)
+                                if (e < G * D && x + y < nx) {
+                                    const float wt = jn.weight[e / D][x + y];
+                                    acc[k].x = fmaf(v[k][y].x, wt, acc[k].x);
+                                    acc[k].y = fmaf(v[k][y].y, wt, acc[k].y);
+                                    acc[k].z = fmaf(v[k][y].z, wt, acc[k].z);
+                                    acc[k].w = fmaf(v[k][y].w, wt, acc[k].w);
+                                }
                         }
                     }
                 }
@@ -568,17 +626,32 @@ paged_attn_kernel(const DecArgs a) {
     cp_async_wait<0>();
 }
 
-// mass[i] += sum_h 2^(logit_h(i) - lse_h), from the logits that the attention left
+// mass[i] += sum_h 2^(logit_h(i) - lse_h), from the logits that the attention left; four
+// tokens per thread.
 __global__ void __launch_bounds__(256)
-paged_mass_kernel(fathom_pages p, int cap, int G, const int32_t *__restrict__ lens, const float *__restrict__ logits,
-                  const float *__restrict__ lse, float *__restrict__ mass, size_t mass_stride) {
+paged_mass_kernel(fathom_pages p, int cap, int stride, int G, const int32_t *__restrict__ lens,
+                  const float *__restrict__ logits, const float *__restrict__ lse, float *__restrict__ mass,
+                  size_t mass_stride) {
     pdl_enter();
     const int u = blockIdx.y, n = min(max(lens[u / p.kv_heads], 0), cap);
-    for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
-        float w = 0.0f;
-        for (int g = 0; g < G; ++g)
-            w += exp2_fast(__ldcg(logits + ((size_t)u * G + g) * cap + i) - __ldcg(lse + (size_t)u * G + g));
-        mass[u * mass_stride + i] += w;
+    float *mr = mass + u * mass_stride;
+    const bool vec = (((uintptr_t)mr) & 15) == 0;
+    for (int i = 4 * (blockIdx.x * 256 + threadIdx.x); i < n; i += 4 * 256 * gridDim.x) {
+        float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int g = 0; g < G; ++g) {
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(logits + ((size_t)u * G + g) * stride + i));
+            const float z = __ldcg(lse + (size_t)u * G + g);
+            w.x += exp2_fast(x.x - z); w.y += exp2_fast(x.y - z); w.z += exp2_fast(x.z - z); w.w += exp2_fast(x.w - z);
+        }
+        if (vec && i + 3 < n) {
+            float4 v = *reinterpret_cast<float4 *>(mr + i);
+            v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+            *reinterpret_cast<float4 *>(mr + i) = v;
+        } else {
+            const float v[4] = {w.x, w.y, w.z, w.w};
+            for (int e = 0; e < 4; ++e)
+                if (i + e < n) mr[i + e] += v[e];
+        }
     }
 }
 
@@ -587,7 +660,7 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 template <typename T, int kD, int kTwo, bool kMass>
 cudaError_t launch_dec(const DecArgs &a, int ctas, cudaStream_t st) {
     const size_t smem = sizeof(DecSmem<kD>);
-    static_assert(2 * (sizeof(DecSmem<kD>) + 1024) <= 228 * 1024, "two CTAs share an SM");
+    static_assert(dec_ctas(kD) * (sizeof(DecSmem<kD>) + 1024) <= 228 * 1024, "resident CTAs");
     ensure_smem(paged_attn_kernel<T, kD, kTwo, kMass>, smem);
     return launch_pdl(paged_attn_kernel<T, kD, kTwo, kMass>, dim3(ctas), dim3(kDecThreads), smem, st, a);
 }
@@ -615,13 +688,13 @@ PagedWorkspace paged_workspace_layout(const fathom_pages &p, int G, bool mass) {
     int sms = device_sm_count();
     if (sms <= 0) sms = 152;
     const size_t units = (size_t)p.seqs * p.kv_heads, rows = units * G;
-    w.ctas = 2 * sms;   // resident at once
+    w.ctas = dec_ctas(p.D <= 64 ? 64 : 128) * sms;   // resident at once
     w.ticket_off = 0;
     w.lse_off = align256(units * sizeof(uint32_t));
     w.part_off = align256(w.lse_off + (mass ? rows * sizeof(float) : 0));
     w.ml_off = align256(w.part_off + (size_t)w.ctas * 2 * G * p.D * sizeof(float));
     w.logit_off = align256(w.ml_off + (size_t)w.ctas * 2 * G * 2 * sizeof(float));
-    w.total = align256(w.logit_off + (mass ? rows * ((size_t)p.max_pages * p.page_tokens) * sizeof(float) : 0));
+    w.total = align256(w.logit_off + (mass ? rows * (((size_t)p.max_pages * p.page_tokens + 3) / 4 * 4) * sizeof(float) : 0));
     return w;
 }
 
@@ -634,6 +707,7 @@ int launch_paged_attn(const fathom_pages &p, int G, const float *q, const void *
     a.lg = log2_of(p.page_tokens);
     a.G = G;
     a.cap = p.max_pages * p.page_tokens;
+    a.logit_stride = (a.cap + 3) / 4 * 4;
     a.q = q; a.kp = kp; a.vp = vp; a.table = table; a.lens = lens; a.out = out;
     a.ticket = (unsigned *)((char *)ws + w.ticket_off);
     a.part_o = (float *)((char *)ws + w.part_off);
@@ -647,9 +721,9 @@ int launch_paged_attn(const fathom_pages &p, int G, const float *q, const void *
         e = p.D <= 64 ? launch_dec_form<__half, 64>(a, w.ctas, st) : launch_dec_form<__half, 128>(a, w.ctas, st);
     if (e != cudaSuccess) { set_error("paged_attn_kernel: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }
     if (mass) {
-        const int units = p.seqs * p.kv_heads, want = (a.cap + 1023) / 1024, most = (w.ctas * 16 + units - 1) / units;
-        e = launch_pdl(paged_mass_kernel, dim3(want < most ? want : most, units), dim3(256), 0, st, p, a.cap, G, lens,
-                       (const float *)a.logits, (const float *)a.lse, mass, mass_stride);
+        const int units = p.seqs * p.kv_heads, want = (a.cap + 1023) / 1024, most = (w.ctas * 8 + units - 1) / units;
+        e = launch_pdl(paged_mass_kernel, dim3(want < most ? want : most, units), dim3(256), 0, st, p, a.cap, a.logit_stride, G,
+                       lens, (const float *)a.logits, (const float *)a.lse, mass, mass_stride);
         if (e != cudaSuccess) { set_error("paged_mass_kernel: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }
     }
     return launch_status("paged_attn");
