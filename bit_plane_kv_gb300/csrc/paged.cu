@@ -283,21 +283,38 @@ paged_attn_kernel(const DecArgs a) {
     constexpr uint32_t kHalf = 16 * kRowBytes;
     const int col = lane % kPieces, row0 = lane / kPieces;   // this lane's 16-byte piece, its first row
     constexpr int kRowsPer = 32 / kPieces;
+    const int64_t step = 2 * kRowsPer * p.token_stride;
     auto issue = [&](int st, const DecCursor &x, int pid) {   // the copies of a tile whose pages are known
         const unsigned ok = __ballot_sync(0xffffffffu, pid >= 0) & 0xffffu;
         if (lane == 0) sm.live[warp][st] = ok;
         const int64_t at_head = x.head * p.head_stride;
+        const int slot0 = (x.tile * kTile + warp * 16) & (p.page_tokens - 1);
+        uint32_t dst = ring + st * 2 * kHalf + row0 * kRowBytes;
+        if (p.page_tokens >= 16) {   // the 16 tokens lie in one page, the live ones first
+            const int page = __shfl_sync(0xffffffffu, pid, 0), n = col * 8 < D ? __popc(ok) : 0;
+            int64_t off = page >= 0 ? 2 * (page * p.page_stride + at_head + (slot0 + row0) * p.token_stride) + col * 16 : 0;
 #pragma unroll
+            for (int i = 0; i < 16 / kRowsPer; ++i) {
+                const int t = row0 + i * kRowsPer, bytes = t < n ? 16 : 0;
+                const uint32_t to = dst + i * kRowsPer * kRowBytes + ((col ^ (t & 7)) << 4);
+                const char *ks = t < n ? kb + off : kb, *vs = t < n ? vb + off : vb;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(ks), "r"(bytes) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + kHalf), "l"(vs), "r"(bytes) : "memory");
+                off += step;
+            }
+            return;
+        }
+#pragma unroll 1
         for (int i = 0; i < 16 / kRowsPer; ++i) {
             const int t = row0 + i * kRowsPer;
             const int page = __shfl_sync(0xffffffffu, pid, t);
-            const int slot = (x.tile * kTile + warp * 16 + t) & (p.page_tokens - 1);
+            const int slot = (slot0 + t) & (p.page_tokens - 1);
             const bool live = page >= 0 && col * 8 < D;
             const int64_t off = live ? 2 * (page * p.page_stride + at_head + slot * p.token_stride) + col * 16 : 0;
-            const uint32_t dst = ring + st * 2 * kHalf + t * kRowBytes + ((col ^ (t & 7)) << 4);
+            const uint32_t to = dst + i * kRowsPer * kRowBytes + ((col ^ (t & 7)) << 4);
             const int bytes = live ? 16 : 0;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(kb + off), "r"(bytes) : "memory");
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + kHalf), "l"(vb + off), "r"(bytes) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(kb + off), "r"(bytes) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + kHalf), "l"(vb + off), "r"(bytes) : "memory");
         }
     };
     const int count = (int)(w1 - w0);
