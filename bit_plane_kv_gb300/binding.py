@@ -102,6 +102,7 @@ SIGNATURES = {
     "fathom_paged_evict": (ctypes.c_int, [ctypes.POINTER(Pages), _vp, _vp, _vp, _vp, _vp, _sz, _i32, _i32, _i32, _vp,
                                           _i32, _vp, _vp, _vp, _sz, _vp]),
     "fathom_paged_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(Pages), _i32, ctypes.c_int]),
+    "fathom_wait_status": (ctypes.c_int, []),
     "fathom_rel_err": (ctypes.c_int, [_i32, _i32, _vp, _vp, _vp, _vp]),
     "fathom_set_overlap": (ctypes.c_int, [_i32, _i32, _vp, _vp, _vp, _vp]),
     "fathom_greedy_budgets": (ctypes.c_int, [_i32, _i32, _vp, _i32, _i32, _i32, _vp]),
@@ -847,6 +848,12 @@ def fathom_paged_evict(pages: Pages, k_pages, v_pages, page_table, lens, mass, k
               dst_table.shape[1], kept_idx.data_ptr(), lens_out.data_ptr(), mass_out.data_ptr(), mass_out.shape[1],
               handle)
     return kept_idx, lens_out, mass_out
+
+
+def fathom_wait_status():
+    """Synchronises the device; raises FathomError (status 4) if a bounded wait of the
+    prompt attention ran out there since the last time it was asked."""
+    _call("fathom_wait_status")
 
 
 def fathom_debug_status(mode=0):

@@ -400,6 +400,20 @@ int fathom_debug_status(int mode, uint64_t *first_failure) {
 #endif
 }
 
+int fathom_wait_status(void) {
+    g_err[0] = 0;
+    const cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) { set_error("wait_status: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }
+    const bool expired = wait_expired_prefill();
+    const int rc = launch_status("wait_status");
+    if (rc) return rc;
+    if (expired) {
+        set_error("wait_status: a bounded wait ran out in fathom_prefill_attn; its results are not valid");
+        return FATHOM_ETIMEOUT;
+    }
+    return FATHOM_OK;
+}
+
 int fathom_calibrate(int32_t units, int32_t m, int32_t D, const float *calib, float *mean_out,
                      float *var_out, void *stream) {
     g_err[0] = 0;

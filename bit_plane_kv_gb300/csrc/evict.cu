@@ -15,7 +15,7 @@ __device__ __forceinline__ uint32_t mass_key(float x) { return x != x ? 0xffffff
 // of 8 bits (each over the keys that agree with the digits found so far); then
 // each warp counts a contiguous part's tokens above and at that key, the counts
 // are scanned, and the kept tokens are written in ascending order.
-__global__ void __launch_bounds__(kSelThreads)
+__global__ void __launch_bounds__(kSelThreads, 2)
 evict_select_kernel(fathom_pages p, const int32_t *__restrict__ lens, const float *__restrict__ mass,
                     size_t mass_stride, int keep, int n_sink, int n_recent, int32_t *__restrict__ kept,
                     int32_t *__restrict__ lens_out) {

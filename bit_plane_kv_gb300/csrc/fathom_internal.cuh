@@ -282,6 +282,8 @@ int launch_paged_evict(const fathom_pages &p, void *kp, void *vp, const int32_t 
                        const int32_t *dst_table, int dst_pages, int32_t *kept, int32_t *lens_out, float *mass_out,
                        size_t mass_out_stride, cudaStream_t st);
 
+bool wait_expired_prefill();   // whether a bounded wait of its kernel ran out; clears the note
+
 int launch_rel_err(int rows, int D, const float *a, const float *ref, double *err, cudaStream_t st);
 int launch_set_overlap(int rows, int k, const int32_t *a, const int32_t *b, int32_t *count, cudaStream_t st);
 int greedy_budgets(int layers, int levels, const double *err, int b_min, int step, int b_mean, int32_t *budgets);

@@ -51,7 +51,7 @@ struct PrefillSmem {
 };
 
 // Set when a bounded wait ran out: the call's results are not valid.
-__device__ unsigned g_prefill_timeout;
+__device__ unsigned g_wait_expired;
 
 struct PrefillArgs {
     int seqs, heads, kv_heads, D, total_q, total_k, gp, lg_gp, groups, tiles;
@@ -391,7 +391,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     seen > 0 ? ((m - kShift) + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
         }
     }
-    if (!ok) atomicExch(&g_prefill_timeout, 1u);
+    if (!ok) atomicExch(&g_wait_expired, 1u);
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) tmem_free(tmem, kTmemCols);
@@ -437,6 +437,14 @@ bool encode_rows(CUtensorMap *map, int dtype, const void *base, int D, int heads
 }
 
 }  // namespace
+
+bool wait_expired_prefill() {
+    unsigned v = 0;
+    const unsigned none = 0;
+    if (cudaMemcpyFromSymbol(&v, g_wait_expired, sizeof v) != cudaSuccess) return false;
+    if (v) cudaMemcpyToSymbol(g_wait_expired, &none, sizeof none);
+    return v != 0;
+}
 
 int launch_prefill_attn(const fathom_prompts &p, const void *q, const void *k, const void *v, const int32_t *cu_q,
                         const int32_t *cu_k, void *out, float *lse, cudaStream_t st) {

@@ -72,7 +72,7 @@ typedef enum {
     FATHOM_EINVAL = 1,   /* bad argument; nothing was enqueued */
     FATHOM_ECUDA = 2,    /* a CUDA call or launch failed */
     FATHOM_ENOMEM = 3,   /* a caller-provided buffer is too small */
-    FATHOM_ETIMEOUT = 4  /* reserved for bounded device waits */
+    FATHOM_ETIMEOUT = 4  /* a bounded device wait ran out (fathom_wait_status) */
 } fathom_status;
 
 typedef enum {
@@ -561,6 +561,15 @@ size_t fathom_paged_workspace_size(const fathom_pages *pages, int32_t G, int mas
 
 /* Workspace bytes a call needs for this shape (0 if the shape is invalid). */
 size_t fathom_workspace_size(const fathom_shape *shape, int which);
+
+/* Bounded device waits: the kernel of fathom_prefill_attn waits for its own
+ * asynchronous copies and matrix instructions, each wait at most two seconds; one
+ * that runs out ends its CTA without writing the rest of its results and is noted.
+ * This call synchronises the calling thread's device and returns FATHOM_ETIMEOUT if
+ * a wait has run out there since the last time it was asked (it then clears the
+ * note), else FATHOM_OK.  None is expected to; a caller that wants to be sure asks
+ * now and then. */
+int fathom_wait_status(void);
 
 /* The calling thread's last error message ("" if none). */
 const char *fathom_last_error(void);

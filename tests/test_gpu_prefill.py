@@ -158,3 +158,9 @@ def test_same_bits_on_streams_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want2)
+
+
+def test_no_bounded_wait_ran_out():
+    q, k, v = inputs([300], [300], 4, 2, 128, BF)
+    B.fathom_prefill_attn(q, k, v, P.cumulated([300]))
+    B.fathom_wait_status()                             # covers every call of this process
