@@ -71,6 +71,24 @@ __device__ __forceinline__ void tma_prefetch_map(const void *map) {
 // Generic-proxy shared-memory writes made visible to the tensor cores and TMA.
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// ---------------------------------------------------------------- work from the launch queue
+// Asks for a CTA of this grid that has not started; the answer, 16 bytes, arrives at
+// `dst` and completes on `bar`.  Not to be asked again after an answer of "none".
+__device__ __forceinline__ void request_cta(uint32_t dst, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 ::"r"(dst), "r"(bar) : "memory");
+}
+// The blockIdx.x of the CTA that an answer hands over, -1 for none.
+__device__ __forceinline__ int granted_cta(uint64_t lo, uint64_t hi) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .b128 h;\nmov.b128 h, {%2, %3};\n"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\nselp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\n"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n}\n"
+        : "=r"(ok), "=r"(x) : "l"(lo), "l"(hi));
+    return ok ? (int)x : -1;
+}
+
 // ---------------------------------------------------------------- tensor memory
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, uint32_t cols) {   // a whole warp
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_slot), "r"(cols) : "memory");

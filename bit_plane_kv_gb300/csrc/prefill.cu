@@ -45,9 +45,10 @@ struct PrefillSmem {
     static constexpr uint32_t kTile = kPanels * kPanel;
     alignas(1024) unsigned char q[2][kTile];
     alignas(1024) unsigned char kv[kStages][kTile];
-    uint64_t q_full, kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2], o_full[2], drained;
+    alignas(16) uint64_t answer[2][2];   // of the requests for the next tile pair
+    uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2], o_full[2];
+    uint64_t work_full[2], work_empty[2], drained;
     uint32_t tmem;
-    int seq, tile;
 };
 
 // Set when a bounded wait ran out: the call's results are not valid.
@@ -79,9 +80,43 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     Smem &sm = *reinterpret_cast<Smem *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
-    // ---- which sequence and which 256 rows: the last tiles first (they see the most keys)
-    if (warp == 0) {
-        int rank = a.tiles - 1 - (int)(blockIdx.x / a.groups), seq = -1, tile = 0;
+    if (warp == kLoadWarp && lane == 0) {
+        tma_prefetch_map(&map_q);
+        tma_prefetch_map(&map_k);
+        tma_prefetch_map(&map_v);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_addr(&sm.kv_full[i]), 1);
+            mbar_init(smem_addr(&sm.kv_empty[i]), 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(smem_addr(&sm.q_full[w]), 1);
+            mbar_init(smem_addr(&sm.q_empty[w]), 1);
+            mbar_init(smem_addr(&sm.s_full[w]), 1);
+            mbar_init(smem_addr(&sm.p_full[w]), 4);
+            mbar_init(smem_addr(&sm.o_full[w]), 1);
+            mbar_init(smem_addr(&sm.work_full[w]), 1);
+            mbar_init(smem_addr(&sm.work_empty[w]), kLoadWarp + 1);   // every warp reads the answer
+        }
+        mbar_init(smem_addr(&sm.drained), 1);
+        mbar_init_fence();
+    }
+    if (warp == kMmaWarp) tmem_alloc(smem_addr(&sm.tmem), kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
+    bool ok = true;
+
+    // ---- a work item (blockIdx.x of a launch): which sequence and which 256 rows, the last tiles first
+    // (they see the most keys), and what they see.  Computed alike by every warp.
+    const int tw = kRows >> a.lg_gp;
+    struct Work {
+        int group, q0, lq, k0, lk, off, t0, nt0, nt1, steps;
+    };
+    auto geometry = [&](int item) {
+        Work g;
+        g.group = item % a.groups;
+        int rank = a.tiles - 1 - item / a.groups, seq = -1, tile = 0;
         for (int s0 = 0; s0 < a.seqs && seq < 0; s0 += 32) {
             int n = 0;
             if (s0 + lane < a.seqs)
@@ -101,80 +136,85 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             }
             rank -= __shfl_sync(0xffffffffu, upto, 31);
         }
-        if (lane == 0) { sm.seq = seq; sm.tile = tile; }
-    }
-    if (warp == kLoadWarp && lane == 0) {
-        tma_prefetch_map(&map_q);
-        tma_prefetch_map(&map_k);
-        tma_prefetch_map(&map_v);
-        mbar_init(smem_addr(&sm.q_full), 1);
-        mbar_init(smem_addr(&sm.drained), 1);
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_addr(&sm.kv_full[i]), 1);
-            mbar_init(smem_addr(&sm.kv_empty[i]), 1);
-        }
-        for (int w = 0; w < 2; ++w) {
-            mbar_init(smem_addr(&sm.s_full[w]), 1);
-            mbar_init(smem_addr(&sm.p_full[w]), 4);
-            mbar_init(smem_addr(&sm.o_full[w]), 1);
-        }
-        mbar_init_fence();
-    }
-    __syncthreads();
-    if (sm.seq < 0) return;   // the grid counts one tile more per sequence than most need
-
-    // ---- the tile's geometry (the same in every warp)
-    const int group = (int)(blockIdx.x % a.groups), seq = sm.seq;
-    const int q0 = clamp_to(a.cu_q[seq], a.total_q), lq = clamp_to(a.cu_q[seq + 1], a.total_q) - q0;
-    const int k0 = clamp_to(a.cu_k[seq], a.total_k), lk = max(clamp_to(a.cu_k[seq + 1], a.total_k) - k0, 0);
-    const int off = lk - lq;                               // query token t sees keys j <= t + off
-    const int t0 = sm.tile << (8 - a.lg_gp);               // first token; tile w starts at t0 + w * (128 / Gp)
-    const int tw = kRows >> a.lg_gp;
-    auto count = [&](int w) {                              // steps of tile w
-        const int first = t0 + w * tw, last = min(first + tw, lq) - 1;
-        const int keys = first <= last ? min(lk, last + off + 1) : 0;
-        return keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
+        g.lq = g.nt0 = g.nt1 = g.steps = g.q0 = g.k0 = g.lk = g.off = g.t0 = 0;
+        if (seq < 0) return g;   // the grid counts one tile more per sequence than most need
+        g.q0 = clamp_to(a.cu_q[seq], a.total_q);
+        g.lq = clamp_to(a.cu_q[seq + 1], a.total_q) - g.q0;
+        g.k0 = clamp_to(a.cu_k[seq], a.total_k);
+        g.lk = max(clamp_to(a.cu_k[seq + 1], a.total_k) - g.k0, 0);
+        g.off = g.lk - g.lq;                               // query token t sees keys j <= t + off
+        g.t0 = tile << (8 - a.lg_gp);                      // first token; tile w starts at t0 + w * (128 / Gp)
+        auto count = [&](int w) {                          // steps of tile w
+            const int first = g.t0 + w * tw, last = min(first + tw, g.lq) - 1;
+            const int keys = first <= last ? min(g.lk, last + g.off + 1) : 0;
+            return keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
+        };
+        g.nt0 = count(0);
+        g.nt1 = count(1);
+        g.steps = max(g.nt0, g.nt1);
+        return g;
     };
-    const int nt0 = count(0), nt1 = count(1), steps = max(nt0, nt1);
-
-    if (warp == kMmaWarp) tmem_alloc(smem_addr(&sm.tmem), kTmemCols);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
-    bool ok = true;
+    // ---- the CTA takes over the work of CTAs that have not started: while one item is worked on, the
+    // load warp asks for the next, and every warp reads the answer when it gets there
+    int round = 0;
+    auto next_item = [&]() {
+        const int slot = round & 1;
+        ok = ok && warp_wait(smem_addr(&sm.work_full[slot]), (round >> 1) & 1);
+        const int item = ok ? granted_cta(sm.answer[slot][0], sm.answer[slot][1]) : -1;
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.work_empty[slot]));
+        ++round;
+        return __shfl_sync(0xffffffffu, item, 0);
+    };
 
     if (warp == kLoadWarp) {
-        if (steps > 0 && elect_one()) {
-            const int hq = group << a.lg_gp, hk = hq / (a.heads / a.kv_heads);
-            const uint32_t qb = smem_addr(&sm.q_full);
-            const int tiles = nt1 > 0 ? 2 : 1;
-            mbar_expect(qb, tiles * kTile);
-            for (int w = 0; w < tiles; ++w)
-                for (int p = 0; p < kPanels; ++p)
-                    tma_load_3d(smem_addr(sm.q[w]) + p * kPanel, &map_q, qb, 64 * p, hq, q0 + t0 + w * tw);
-            int issued = 0, st = 0;
-            uint32_t turn = 1;   // parity of the stage's last release; true at once in the first turn
-            for (; issued < 2 * steps; ++issued) {   // K_0, V_0, K_1, V_1, ...
-                if (!(ok = mbar_wait(smem_addr(&sm.kv_empty[st]), turn))) break;
-                const uint32_t bar = smem_addr(&sm.kv_full[st]);
-                mbar_expect(bar, kTile);
-                for (int p = 0; p < kPanels; ++p)
-                    tma_load_3d(smem_addr(sm.kv[st]) + p * kPanel, (issued & 1) ? &map_v : &map_k, bar, 64 * p, hk,
-                                k0 + (issued >> 1) * kKeys);
-                if (++st == kStages) { st = 0; turn ^= 1; }
+        int st = 0, nq0 = 0, nq1 = 0;   // the ring's next stage; Q tiles loaded so far
+        uint32_t turn = 1;              // parity of the stage's last release; true at once in the first turn
+        for (int item = blockIdx.x; item >= 0 && ok; item = next_item()) {
+            const Work g = geometry(item);
+            const int slot = round & 1;
+            if (elect_one()) {
+                if ((ok = mbar_wait(smem_addr(&sm.work_empty[slot]), ((round >> 1) & 1) ^ 1))) {
+                    mbar_expect(smem_addr(&sm.work_full[slot]), 16);
+                    request_cta(smem_addr(sm.answer[slot]), smem_addr(&sm.work_full[slot]));
+                }
+                const int hq = g.group << a.lg_gp, hk = hq / (a.heads / a.kv_heads);
+                for (int w = 0; w < 2 && ok; ++w) {
+                    if ((w ? g.nt1 : g.nt0) == 0) continue;
+                    if (!(ok = mbar_wait(smem_addr(&sm.q_empty[w]), ((w ? nq1 : nq0) & 1) ^ 1))) break;
+                    const uint32_t bar = smem_addr(&sm.q_full[w]);
+                    mbar_expect(bar, kTile);
+                    for (int p = 0; p < kPanels; ++p)
+                        tma_load_3d(smem_addr(sm.q[w]) + p * kPanel, &map_q, bar, 64 * p, hq, g.q0 + g.t0 + w * tw);
+                }
+                int s = st;
+                uint32_t t = turn;
+                for (int i = 0; i < 2 * g.steps && ok; ++i) {   // K_0, V_0, K_1, V_1, ...
+                    if (!(ok = mbar_wait(smem_addr(&sm.kv_empty[s]), t))) break;
+                    const uint32_t bar = smem_addr(&sm.kv_full[s]);
+                    mbar_expect(bar, kTile);
+                    for (int p = 0; p < kPanels; ++p)
+                        tma_load_3d(smem_addr(sm.kv[s]) + p * kPanel, (i & 1) ? &map_v : &map_k, bar, 64 * p, hk,
+                                    g.k0 + (i >> 1) * kKeys);
+                    if (++s == kStages) { s = 0; t ^= 1; }
+                }
             }
-            if (!ok) {   // the copies in flight land before the CTA ends
-                mbar_wait(qb, 0);
-                for (int i = max(issued - kStages, 0); i < issued; ++i)
-                    mbar_wait(smem_addr(&sm.kv_full[i % kStages]), (i / kStages) & 1);
-            }
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
+            nq0 += g.nt0 > 0;
+            nq1 += g.nt1 > 0;
+            const int end = st + 2 * g.steps;
+            turn ^= (uint32_t)(end / kStages) & 1u;
+            st = end % kStages;
         }
-        __syncwarp();
+        if (!ok) {   // the copies in flight land before the CTA ends
+            const unsigned long long t0 = global_ns();
+            while (global_ns() - t0 < 10000000ull) {}
+        }
     } else if (warp == kMmaWarp) {
         constexpr uint32_t type = kDtype == FATHOM_BF16 ? 1u : 0u;
         const uint32_t desc_s = mma_desc(type, kRows, kKeys, false), desc_o = mma_desc(type, kRows, kSteps * 16, true);
-        const int tail = lk - (steps - 1) * kKeys;   // live rows of the last V tile
         // descriptors of the first 16 channels (keys) of each operand; the others lie at fixed offsets, and
         // the address field of a descriptor counts 16 bytes
         const uint64_t desc_q = smem_desc(smem_addr(sm.q[0]), 0);
@@ -196,24 +236,38 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                        k > 0 ? 1u : (uint32_t)(j > 0));
             mma_commit(smem_addr(&sm.o_full[w]));
         };
-        if (steps > 0) {
-            // the ring's stages in turn: K_0, V_0, K_1, V_1, ...
-            const uint32_t full = smem_addr(sm.kv_full), empty = smem_addr(sm.kv_empty);
-            const uint32_t p_full = smem_addr(sm.p_full);
-            int sv = 1, sk = 0;
-            uint32_t pv = 0, pk = 0;   // parities of the stages' turns
-            ok = warp_wait(smem_addr(&sm.q_full), 0) && warp_wait(full, 0);
-            if (ok && elect_one()) {
+        const uint32_t full = smem_addr(sm.kv_full), empty = smem_addr(sm.kv_empty);
+        const uint32_t q_full = smem_addr(sm.q_full), q_empty = smem_addr(sm.q_empty), p_full = smem_addr(sm.p_full);
+        int cur = 0;                                // the ring's stages in turn: K_0, V_0, K_1, V_1, ...
+        uint32_t pc = 0, pq0 = 0, pq1 = 0, pp0 = 0, pp1 = 0;   // parities of the next wait on each barrier
+        for (int item = blockIdx.x; item >= 0 && ok; item = next_item()) {
+            const Work g = geometry(item);
+            if (g.steps == 0) continue;
+            const int tail = g.lk - (g.steps - 1) * kKeys;   // live rows of the last V tile
+            ok = warp_wait(full + 8 * cur, pc) && (g.nt0 == 0 || warp_wait(q_full, pq0)) &&
+                 (g.nt1 == 0 || warp_wait(q_full + 8, pq1));
+            if (!ok) break;
+            pq0 ^= g.nt0 > 0;
+            pq1 ^= g.nt1 > 0;
+            if (elect_one()) {
                 tc_fence_after();
-                if (nt0 > 0) scores(0, 0);
-                if (nt1 > 0) scores(1, 0);
-                mma_commit(empty);
+                if (g.nt0 > 0) scores(0, cur);
+                if (g.nt0 == 1) mma_commit(q_empty);
+                if (g.nt1 > 0) scores(1, cur);
+                if (g.nt1 == 1) mma_commit(q_empty + 8);
+                mma_commit(empty + 8 * cur);
             }
-            for (int j = 0; j < steps && ok; ++j) {
+            __syncwarp();
+            for (int j = 0; j < g.steps; ++j) {
+                int sv = cur + 1, sk;
+                uint32_t pv = pc, pk;
+                if (sv == kStages) { sv = 0; pv ^= 1; }
                 sk = sv + 1;
                 pk = pv;
                 if (sk == kStages) { sk = 0; pk ^= 1; }
-                const bool more = j + 1 < steps;
+                cur = sk;   // K_{j+1}, or the next item's K_0
+                pc = pk;
+                const bool more = j + 1 < g.steps;
                 if (!(ok = warp_wait(full + 8 * sv, pv) && (!more || warp_wait(full + 8 * sk, pk)))) break;
                 if (!more && tail < kKeys) {
                     // rows behind the sequence's end: their weights are 0, and 0 x NaN would not be
@@ -223,54 +277,62 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     fence_async_smem();
                     __syncwarp();
                 }
-                if (j < nt0) {
-                    if (!(ok = warp_wait(p_full, j & 1))) break;
+                if (j < g.nt0) {
+                    if (!(ok = warp_wait(p_full, pp0))) break;
+                    pp0 ^= 1;
                     tc_fence_after();
                     if (elect_one()) {
                         values(0, sv, j);
-                        if (j + 1 < nt0) scores(0, sk);
+                        if (j + 1 < g.nt0) scores(0, sk);
+                        if (j + 2 == g.nt0) mma_commit(q_empty);
                     }
+                    __syncwarp();
                 }
-                if (j < nt1) {
-                    if (!(ok = warp_wait(p_full + 8, j & 1))) break;
+                if (j < g.nt1) {
+                    if (!(ok = warp_wait(p_full + 8, pp1))) break;
+                    pp1 ^= 1;
                     tc_fence_after();
                     if (elect_one()) {
                         values(1, sv, j);
                         mma_commit(empty + 8 * sv);
-                        if (j + 1 < nt1) scores(1, sk);
+                        if (j + 1 < g.nt1) scores(1, sk);
+                        if (j + 2 == g.nt1) mma_commit(q_empty + 8);
                         if (more) mma_commit(empty + 8 * sk);
                     }
                 } else if (elect_one()) {
                     mma_commit(empty + 8 * sv);
                     if (more) mma_commit(empty + 8 * sk);
                 }
-                sv = sk + 1;
-                pv = pk;
-                if (sv == kStages) { sv = 0; pv ^= 1; }
+                __syncwarp();
             }
-            __syncwarp();
-            if (elect_one()) mma_commit(smem_addr(&sm.drained));
-            __syncwarp();
-            warp_wait(smem_addr(&sm.drained), 0);   // no matrix instruction outlives the tensor memory
         }
+        __syncwarp();
+        if (elect_one()) mma_commit(smem_addr(&sm.drained));
+        __syncwarp();
+        warp_wait(smem_addr(&sm.drained), 0);   // no matrix instruction outlives the tensor memory
     } else {
-        const int w = warp >> 2, nt = w ? nt1 : nt0, row = (warp & 3) * 32 + lane;
-        const int token = t0 + w * tw + (row >> a.lg_gp);
-        const int head = (group << a.lg_gp) + (row & (a.gp - 1));
+        const int w = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + kColS + w * 128, to = tmem + lanes + kColO + w * 128;
-        // keys this row sees, and the fewest that a row of this warp sees
-        const int seen = min(lk, token + off + 1);
-        const int seen_min = min(lk, t0 + w * tw + (((warp & 3) * 32) >> a.lg_gp) + off + 1);
         const float c = 1.4426950408889634f / sqrtf((float)a.D);   // log2(e) / sqrt(D)
         // fp16 weights are kept 2^7 larger (at most 2^15) so that fewer fall among its subnormals
         constexpr float kShift = kDtype == FATHOM_F16 ? 7.0f : 0.0f;
         // how far (log2) a row's maximum may rise above m before m follows: a bf16 weight is as exact at
         // 2^32 as at 1, a fp16 weight must stay below 2^16
         constexpr float kLag = kDtype == FATHOM_F16 ? 8.0f : 32.0f;
+        uint32_t ps = 0, po = 0;   // parities of the next wait for S, and for the last product into O
+        for (int item = blockIdx.x; item >= 0 && ok; item = next_item()) {
+        const Work g = geometry(item);
+        const int nt = w ? g.nt1 : g.nt0, lk = g.lk;
+        const int token = g.t0 + w * tw + (row >> a.lg_gp);
+        const int head = (g.group << a.lg_gp) + (row & (a.gp - 1));
+        // keys this row sees, and the fewest that a row of this warp sees
+        const int seen = min(lk, token + g.off + 1);
+        const int seen_min = min(lk, g.t0 + w * tw + (((warp & 3) * 32) >> a.lg_gp) + g.off + 1);
         float m = -CUDART_INF_F, l = 0.0f;   // m in log2 units; -inf: no finite score yet
         for (int j = 0; j < nt; ++j) {
-            if (!(ok = warp_wait(smem_addr(&sm.s_full[w]), j & 1))) break;
+            if (!(ok = warp_wait(smem_addr(&sm.s_full[w]), ps))) break;
+            ps ^= 1;
             tc_fence_after();
             const bool edge = (j + 1) * kKeys > seen_min;
             const int live = seen - j * kKeys;
@@ -321,7 +383,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         }
                     }
                     if (j > 0) {
-                        if (!(ok = warp_wait(smem_addr(&sm.o_full[w]), (j - 1) & 1))) break;
+                        if (!(ok = warp_wait(smem_addr(&sm.o_full[w]), po ^ 1))) break;   // the product before
                         tc_fence_after();
 #pragma unroll 1
                         for (int b = 0; b < kSteps; ++b) {
@@ -359,14 +421,15 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[w]));
             sum[0] = add2(sum[0], sum[1]);
             l += sum[0].x + sum[0].y;
+            po ^= 1;
         }
         // ---- O / l, rounded once
-        ok = ok && (nt == 0 || warp_wait(smem_addr(&sm.o_full[w]), (nt - 1) & 1));
+        ok = ok && (nt == 0 || warp_wait(smem_addr(&sm.o_full[w]), po ^ 1));
         if (ok) {
             tc_fence_after();
-            const bool live = token < lq;
+            const bool live = token < g.lq;
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            uint16_t *orow = (uint16_t *)a.out + (int64_t)(q0 + token) * a.out_token + head * a.out_head;
+            uint16_t *orow = (uint16_t *)a.out + (int64_t)(g.q0 + token) * a.out_token + head * a.out_head;
 #pragma unroll 1
             for (int b = 0; b < kSteps / 2; ++b) {
                 uint32_t o[32];
@@ -387,8 +450,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 }
             }
             if (live && a.lse)
-                a.lse[(int64_t)(q0 + token) * a.heads + head] =
+                a.lse[(int64_t)(g.q0 + token) * a.heads + head] =
                     seen > 0 ? ((m - kShift) + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+            tc_fence_before();
+        }
         }
     }
     if (!ok) atomicExch(&g_wait_expired, 1u);
