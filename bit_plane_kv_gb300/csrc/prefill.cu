@@ -56,6 +56,7 @@ __device__ unsigned g_wait_expired;
 
 struct PrefillArgs {
     int seqs, heads, kv_heads, D, total_q, total_k, gp, lg_gp, groups, tiles;
+    int wide;   // rows of out start on 32-byte boundaries and are whole 32 bytes
     int64_t out_token, out_head;
     const int32_t *cu_q, *cu_k;
     void *out;
@@ -322,138 +323,145 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         constexpr float kLag = kDtype == FATHOM_F16 ? 8.0f : 32.0f;
         uint32_t ps = 0, po = 0;   // parities of the next wait for S, and for the last product into O
         for (int item = blockIdx.x; item >= 0 && ok; item = next_item()) {
-        const Work g = geometry(item);
-        const int nt = w ? g.nt1 : g.nt0, lk = g.lk;
-        const int token = g.t0 + w * tw + (row >> a.lg_gp);
-        const int head = (g.group << a.lg_gp) + (row & (a.gp - 1));
-        // keys this row sees, and the fewest that a row of this warp sees
-        const int seen = min(lk, token + g.off + 1);
-        const int seen_min = min(lk, g.t0 + w * tw + (((warp & 3) * 32) >> a.lg_gp) + g.off + 1);
-        float m = -CUDART_INF_F, l = 0.0f;   // m in log2 units; -inf: no finite score yet
-        for (int j = 0; j < nt; ++j) {
-            if (!(ok = warp_wait(smem_addr(&sm.s_full[w]), ps))) break;
-            ps ^= 1;
-            tc_fence_after();
-            const bool edge = (j + 1) * kKeys > seen_min;
-            const int live = seen - j * kKeys;
-            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-            uint32_t s[4][32];   // columns 32 b .. 32 b + 31 of S
-            tmem_ld32(ts, s[0]);
-            tmem_ld32(ts + 32, s[1]);
+            const Work g = geometry(item);
+            const int nt = w ? g.nt1 : g.nt0;
+            const int token = g.t0 + w * tw + (row >> a.lg_gp);
+            const int at = token < g.lq ? g.q0 + token : -1;   // row of out; -1: behind the sequence
+            const int head = (g.group << a.lg_gp) + (row & (a.gp - 1));
+            // keys this row sees, and the fewest that a row of this warp sees
+            const int seen = min(g.lk, token + g.off + 1);
+            const int seen_min = min(g.lk, g.t0 + w * tw + (((warp & 3) * 32) >> a.lg_gp) + g.off + 1);
+            float m = -CUDART_INF_F, l = 0.0f;   // m in log2 units; -inf: no finite score yet
+            for (int j = 0; j < nt; ++j) {
+                if (!(ok = warp_wait(smem_addr(&sm.s_full[w]), ps))) break;
+                ps ^= 1;
+                tc_fence_after();
+                const bool edge = (j + 1) * kKeys > seen_min;
+                const int live = seen - j * kKeys;
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                uint32_t s[4][32];   // columns 32 b .. 32 b + 31 of S
+                tmem_ld32(ts, s[0]);
+                tmem_ld32(ts + 32, s[1]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {   // 64 keys at a time
-                float top = -CUDART_INF_F, top2 = -CUDART_INF_F;
+                for (int h = 0; h < 2; ++h) {   // 64 keys at a time
+                    float top = -CUDART_INF_F, top2 = -CUDART_INF_F;
 #pragma unroll
-                for (int b = 2 * h; b < 2 * h + 2; ++b) {
-                    tmem_wait_ld(s[b]);
-                    if (edge) {
+                    for (int b = 2 * h; b < 2 * h + 2; ++b) {
+                        tmem_wait_ld(s[b]);
+                        if (edge) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (32 * b + i >= live) s[b][i] = 0xff800000u;
-                    }
+                            for (int i = 0; i < 32; ++i)
+                                if (32 * b + i >= live) s[b][i] = 0xff800000u;
+                        }
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        top = fmaxf(top, __uint_as_float(s[b][i]));
-                        top2 = fmaxf(top2, __uint_as_float(s[b][i + 1]));
-                    }
-                }
-                top = fmaxf(top, top2) * c;
-                const bool raise = top > m + kLag;
-                if (__any_sync(0xffffffffu, raise)) {
-                    // m rises by a whole power of two, so that what was computed against the old one is
-                    // scaled exactly: l, O, and the first half's weights of this tile
-                    float f = 1.0f;
-                    if (raise) {
-                        const float up = m == -CUDART_INF_F ? top : m + ceilf(top - m);
-                        f = exp2f(m - up);
-                        m = up;
-                    }
-                    l *= f;
-                    sum[0].x *= f; sum[0].y *= f; sum[1].x *= f; sum[1].y *= f;
-                    if (h == 1) {
-                        tmem_wait_st();
-#pragma unroll 1
-                        for (int b = 0; b < 2; ++b) {
-                            uint32_t o[16];
-                            tmem_ld16(ts + 16 * b, o);
-                            tmem_wait_ld(o);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = scale2<kDtype>(o[i], f);
-                            tmem_st16(ts + 16 * b, o);
+                        for (int i = 0; i < 32; i += 2) {
+                            top = fmaxf(top, __uint_as_float(s[b][i]));
+                            top2 = fmaxf(top2, __uint_as_float(s[b][i + 1]));
                         }
                     }
-                    if (j > 0) {
-                        if (!(ok = warp_wait(smem_addr(&sm.o_full[w]), po ^ 1))) break;   // the product before
-                        tc_fence_after();
+                    top = fmaxf(top, top2) * c;
+                    const bool raise = top > m + kLag;
+                    if (__any_sync(0xffffffffu, raise)) {
+                        // m rises by a whole power of two, so that what was computed against the old one is
+                        // scaled exactly: l, O, and the first half's weights of this tile
+                        float f = 1.0f;
+                        if (raise) {
+                            const float up = m == -CUDART_INF_F ? top : m + ceilf(top - m);
+                            f = exp2f(m - up);
+                            m = up;
+                        }
+                        l *= f;
+                        sum[0].x *= f; sum[0].y *= f; sum[1].x *= f; sum[1].y *= f;
+                        if (h == 1) {
+                            tmem_wait_st();
 #pragma unroll 1
-                        for (int b = 0; b < kSteps; ++b) {
-                            uint32_t o[16];
-                            tmem_ld16(to + 16 * b, o);
-                            tmem_wait_ld(o);
+                            for (int b = 0; b < 2; ++b) {
+                                uint32_t o[16];
+                                tmem_ld16(ts + 16 * b, o);
+                                tmem_wait_ld(o);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            tmem_st16(to + 16 * b, o);
+                                for (int i = 0; i < 16; ++i) o[i] = scale2<kDtype>(o[i], f);
+                                tmem_st16(ts + 16 * b, o);
+                            }
+                        }
+                        if (j > 0) {
+                            if (!(ok = warp_wait(smem_addr(&sm.o_full[w]), po ^ 1))) break;   // the product before
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int b = 0; b < kSteps; ++b) {
+                                uint32_t o[16];
+                                tmem_ld16(to + 16 * b, o);
+                                tmem_wait_ld(o);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tmem_st16(to + 16 * b, o);
+                            }
                         }
                     }
-                }
-                const float shift = kShift - (m == -CUDART_INF_F ? 0.0f : m);
-                const float2 cc = make_float2(c, c), mm = make_float2(shift, shift);
+                    const float shift = kShift - (m == -CUDART_INF_F ? 0.0f : m);
+                    const float2 cc = make_float2(c, c), mm = make_float2(shift, shift);
 #pragma unroll
-                for (int b = 2 * h; b < 2 * h + 2; ++b) {
+                    for (int b = 2 * h; b < 2 * h + 2; ++b) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float2 x = make_float2(__uint_as_float(s[b][2 * i]), __uint_as_float(s[b][2 * i + 1]));
+                            x = fma2(x, cc, mm);
+                            x.x = exp2_approx(x.x);
+                            x.y = exp2_approx(x.y);
+                            sum[i & 1] = add2(sum[i & 1], x);
+                            pk[i] = pack2<kDtype>(x.x, x.y);
+                        }
+                        tmem_st16(ts + 16 * b, pk);
+                        if (h == 0) tmem_ld32(ts + 64 + 32 * b, s[2 + b]);
+                    }
+                }
+                if (!ok) break;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[w]));
+                sum[0] = add2(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
+                po ^= 1;
+            }
+            // ---- O / l, rounded once
+            ok = ok && (nt == 0 || warp_wait(smem_addr(&sm.o_full[w]), po ^ 1));
+            if (ok) {
+                tc_fence_after();
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                uint16_t *orow = (uint16_t *)a.out + (int64_t)at * a.out_token + head * a.out_head;
+#pragma unroll 1
+                for (int b = 0; b < kSteps / 2; ++b) {
+                    uint32_t x[32];
+                    if (nt > 0) {
+                        tmem_ld32(to + 32 * b, x);
+                        tmem_wait_ld(x);
+                    }
                     uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float2 x = make_float2(__uint_as_float(s[b][2 * i]), __uint_as_float(s[b][2 * i + 1]));
-                        x = fma2(x, cc, mm);
-                        x.x = exp2_approx(x.x);
-                        x.y = exp2_approx(x.y);
-                        sum[i & 1] = add2(sum[i & 1], x);
-                        pk[i] = pack2<kDtype>(x.x, x.y);
+                    for (int i = 0; i < 16; ++i)
+                        pk[i] = seen > 0 ? pack2<kDtype>(__uint_as_float(x[2 * i]) * inv,
+                                                         __uint_as_float(x[2 * i + 1]) * inv) : 0u;
+                    if (at >= 0) {
+                        if (a.wide) {   // whole sectors: 32 bytes per store
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                if (32 * b + 16 * i < a.D) store32(orow + 32 * b + 16 * i, pk + 8 * i);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (32 * b + 8 * i < a.D)
+                                    *reinterpret_cast<uint4 *>(orow + 32 * b + 8 * i) =
+                                        make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                        }
                     }
-                    tmem_st16(ts + 16 * b, pk);
-                    if (h == 0) tmem_ld32(ts + 64 + 32 * b, s[2 + b]);
                 }
+                if (at >= 0 && a.lse)
+                    a.lse[(int64_t)at * a.heads + head] =
+                        seen > 0 ? ((m - kShift) + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+                tc_fence_before();
             }
-            if (!ok) break;
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[w]));
-            sum[0] = add2(sum[0], sum[1]);
-            l += sum[0].x + sum[0].y;
-            po ^= 1;
-        }
-        // ---- O / l, rounded once
-        ok = ok && (nt == 0 || warp_wait(smem_addr(&sm.o_full[w]), po ^ 1));
-        if (ok) {
-            tc_fence_after();
-            const bool live = token < g.lq;
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            uint16_t *orow = (uint16_t *)a.out + (int64_t)(g.q0 + token) * a.out_token + head * a.out_head;
-#pragma unroll 1
-            for (int b = 0; b < kSteps / 2; ++b) {
-                uint32_t o[32];
-                if (nt > 0) {
-                    tmem_ld32(to + 32 * b, o);
-                    tmem_wait_ld(o);
-                }
-                uint32_t pk[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    pk[i] = seen > 0 ? pack2<kDtype>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0u;
-                if (live) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (32 * b + 8 * i < a.D)
-                            *reinterpret_cast<uint4 *>(orow + 32 * b + 8 * i) =
-                                make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-                }
-            }
-            if (live && a.lse)
-                a.lse[(int64_t)(g.q0 + token) * a.heads + head] =
-                    seen > 0 ? ((m - kShift) + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
-            tc_fence_before();
-        }
         }
     }
     if (!ok) atomicExch(&g_wait_expired, 1u);
@@ -522,6 +530,8 @@ int launch_prefill_attn(const fathom_prompts &p, const void *q, const void *k, c
     a.gp = 1 << a.lg_gp;
     a.groups = p.heads / a.gp;
     a.out_token = p.out_token; a.out_head = p.out_head;
+    a.wide = p.D % 16 == 0 && ((uintptr_t)out & 31) == 0 && (p.total_q == 1 || p.out_token % 16 == 0) &&
+             (p.heads == 1 || p.out_head % 16 == 0);
     a.cu_q = cu_q; a.cu_k = cu_k; a.out = out; a.lse = lse;
     const long long tiles = ((long long)p.total_q * a.gp + 2 * kRows - 1) / (2 * kRows) + p.seqs;
     if (tiles * a.groups > 0x7fffffffLL) { set_error("prefill_attn: too many rows for one launch"); return FATHOM_EINVAL; }
