@@ -56,6 +56,7 @@ __device__ unsigned g_wait_expired;
 
 struct PrefillArgs {
     int seqs, heads, kv_heads, D, total_q, total_k, gp, lg_gp, groups, tiles;
+    int split;  // CTAs that share a work item's keys
     int wide;   // rows of out start on 32-byte boundaries and are whole 32 bytes
     int64_t out_token, out_head;
     const int32_t *cu_q, *cu_k;
@@ -69,7 +70,10 @@ __device__ __forceinline__ int clamp_to(int x, int hi) { return min(max(x, 0), h
 // memory).  A constant, so that no branch stands between the matrix instructions:
 // with a runtime count the unrolled and guarded instructions were issued with wrong
 // descriptors.
-template <int kSteps, int kDtype>
+// kSplit: few rows.  The CTAs of a cluster take the same 256 rows and a share of their
+// keys each; at the end each row's partial results meet, through distributed shared
+// memory, in the CTA that its warp's number names.
+template <int kSteps, int kDtype, bool kSplit>
 __global__ void __launch_bounds__(kPrefillThreads, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                const __grid_constant__ CUtensorMap map_v, const PrefillArgs a) {
@@ -114,10 +118,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     struct Work {
         int group, q0, lq, k0, lk, off, t0, nt0, nt1, steps;
     };
+    const int rank = kSplit ? (int)(blockIdx.x % a.split) : 0;
+    const int first_item = kSplit ? (int)(blockIdx.x / a.split) : (int)blockIdx.x;
     auto geometry = [&](int item) {
         Work g;
         g.group = item % a.groups;
-        int rank = a.tiles - 1 - item / a.groups, seq = -1, tile = 0;
+        int nth = a.tiles - 1 - item / a.groups, seq = -1, tile = 0;
         for (int s0 = 0; s0 < a.seqs && seq < 0; s0 += 32) {
             int n = 0;
             if (s0 + lane < a.seqs)
@@ -129,13 +135,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 const int x = __shfl_up_sync(0xffffffffu, upto, o);
                 if (lane >= o) upto += x;
             }
-            const unsigned hit = __ballot_sync(0xffffffffu, rank < upto);
+            const unsigned hit = __ballot_sync(0xffffffffu, nth < upto);
             if (hit) {
                 const int l = __ffs(hit) - 1;
                 seq = s0 + l;
-                tile = rank - __shfl_sync(0xffffffffu, upto - n, l);
+                tile = nth - __shfl_sync(0xffffffffu, upto - n, l);
             }
-            rank -= __shfl_sync(0xffffffffu, upto, 31);
+            nth -= __shfl_sync(0xffffffffu, upto, 31);
         }
         g.lq = g.nt0 = g.nt1 = g.steps = g.q0 = g.k0 = g.lk = g.off = g.t0 = 0;
         if (seq < 0) return g;   // the grid counts one tile more per sequence than most need
@@ -153,12 +159,22 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         g.nt0 = count(0);
         g.nt1 = count(1);
         g.steps = max(g.nt0, g.nt1);
+        if constexpr (kSplit) {   // this CTA's share of the steps, its keys counted from the first of them
+            const int from = g.steps * rank / a.split, to = g.steps * (rank + 1) / a.split;
+            g.nt0 = min(max(g.nt0 - from, 0), to - from);
+            g.nt1 = min(max(g.nt1 - from, 0), to - from);
+            g.steps = max(g.nt0, g.nt1);
+            g.k0 += from * kKeys;
+            g.lk -= from * kKeys;
+            g.off -= from * kKeys;
+        }
         return g;
     };
     // ---- the CTA takes over the work of CTAs that have not started: while one item is worked on, the
     // load warp asks for the next, and every warp reads the answer when it gets there
     int round = 0;
     auto next_item = [&]() {
+        if (kSplit) return -1;
         const int slot = round & 1;
         ok = ok && warp_wait(smem_addr(&sm.work_full[slot]), (round >> 1) & 1);
         const int item = ok ? granted_cta(sm.answer[slot][0], sm.answer[slot][1]) : -1;
@@ -172,11 +188,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     if (warp == kLoadWarp) {
         int st = 0, nq0 = 0, nq1 = 0;   // the ring's next stage; Q tiles loaded so far
         uint32_t turn = 1;              // parity of the stage's last release; true at once in the first turn
-        for (int item = blockIdx.x; item >= 0 && ok; item = next_item()) {
+        for (int item = first_item; item >= 0 && ok; item = next_item()) {
             const Work g = geometry(item);
             const int slot = round & 1;
             if (elect_one()) {
-                if ((ok = mbar_wait(smem_addr(&sm.work_empty[slot]), ((round >> 1) & 1) ^ 1))) {
+                if (!kSplit && (ok = mbar_wait(smem_addr(&sm.work_empty[slot]), ((round >> 1) & 1) ^ 1))) {
                     mbar_expect(smem_addr(&sm.work_full[slot]), 16);
                     request_cta(smem_addr(sm.answer[slot]), smem_addr(&sm.work_full[slot]));
                 }
@@ -241,7 +257,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const uint32_t q_full = smem_addr(sm.q_full), q_empty = smem_addr(sm.q_empty), p_full = smem_addr(sm.p_full);
         int cur = 0;                                // the ring's stages in turn: K_0, V_0, K_1, V_1, ...
         uint32_t pc = 0, pq0 = 0, pq1 = 0, pp0 = 0, pp1 = 0;   // parities of the next wait on each barrier
-        for (int item = blockIdx.x; item >= 0 && ok; item = next_item()) {
+        for (int item = first_item; item >= 0 && ok; item = next_item()) {
             const Work g = geometry(item);
             if (g.steps == 0) continue;
             const int tail = g.lk - (g.steps - 1) * kKeys;   // live rows of the last V tile
@@ -322,7 +338,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         // 2^32 as at 1, a fp16 weight must stay below 2^16
         constexpr float kLag = kDtype == FATHOM_F16 ? 8.0f : 32.0f;
         uint32_t ps = 0, po = 0;   // parities of the next wait for S, and for the last product into O
-        for (int item = blockIdx.x; item >= 0 && ok; item = next_item()) {
+        for (int item = first_item; item >= 0 && ok; item = next_item()) {
             const Work g = geometry(item);
             const int nt = w ? g.nt1 : g.nt0;
             const int token = g.t0 + w * tw + (row >> a.lg_gp);
@@ -427,23 +443,75 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             }
             // ---- O / l, rounded once
             ok = ok && (nt == 0 || warp_wait(smem_addr(&sm.o_full[w]), po ^ 1));
-            if (ok) {
+            if (ok || kSplit) {
                 tc_fence_after();
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                // kSplit: the other CTAs' (O, m, l) of these rows, [share][channel or m or l][row of the warp]
+                constexpr int kShare = (kSteps * 16 + 2) * 32;
+                static_assert(!kSplit || 7 * kShare * 4 <= (int)sizeof(sm.kv), "shares reuse the ring");
+                const int per = 8 / (kSplit ? a.split : 1), dst = warp / per;   // warps per CTA, and this one's CTA
+                float *shares = reinterpret_cast<float *>(sm.kv) + warp % per * kShare + lane;   // += per * kShare each
+                float own = 1.0f, other[7];
+                if constexpr (kSplit) {
+                    cluster_sync();   // no CTA reads its ring any more
+                    if (rank != dst) {
+                        const uint32_t to_dst = cluster_addr(smem_addr(shares + (rank < dst ? rank : rank - 1) * per * kShare), dst);
+                        if (nt > 0) {
+#pragma unroll 1
+                            for (int b = 0; b < kSteps / 2; ++b) {
+                                uint32_t x[32];
+                                tmem_ld32(to + 32 * b, x);
+                                tmem_wait_ld(x);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) cluster_store(to_dst + (32 * b + i) * 128, __uint_as_float(x[i]));
+                            }
+                        }
+                        cluster_store(to_dst + kSteps * 16 * 128, ok ? m : -CUDART_INF_F);
+                        cluster_store(to_dst + (kSteps * 16 + 1) * 128, l);
+                    }
+                    cluster_sync();   // every share is there
+                    if (rank == dst) {
+                        float top = m;
+#pragma unroll
+                        for (int x = 0; x < 7; ++x) {
+                            other[x] = x < a.split - 1 ? shares[x * per * kShare + kSteps * 16 * 32] : -CUDART_INF_F;
+                            top = fmaxf(top, other[x]);
+                        }
+                        own = m == -CUDART_INF_F ? 0.0f : exp2f(m - top);
+                        l *= own;
+#pragma unroll
+                        for (int x = 0; x < 7; ++x) {
+                            other[x] = other[x] == -CUDART_INF_F ? 0.0f : exp2f(other[x] - top);
+                            if (other[x] != 0.0f) l += other[x] * shares[x * per * kShare + (kSteps * 16 + 1) * 32];
+                        }
+                        m = top;
+                    }
+                }
+                const bool mine = at >= 0 && ok && (!kSplit || rank == dst);
+                const float inv = l > 0.0f ? own / l : 0.0f, inv_other = l > 0.0f ? 1.0f / l : 0.0f;
+                const bool some = kSplit ? own != 0.0f && nt > 0 : seen > 0;   // O holds something for this row
                 uint16_t *orow = (uint16_t *)a.out + (int64_t)at * a.out_token + head * a.out_head;
 #pragma unroll 1
-                for (int b = 0; b < kSteps / 2; ++b) {
+                for (int b = 0; b < (!kSplit || rank == dst ? kSteps / 2 : 0); ++b) {
                     uint32_t x[32];
                     if (nt > 0) {
                         tmem_ld32(to + 32 * b, x);
                         tmem_wait_ld(x);
                     }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float v = some ? __uint_as_float(x[i]) * inv : 0.0f;
+                        if constexpr (kSplit) {
+#pragma unroll
+                            for (int y = 0; y < 7; ++y)
+                                if (other[y] != 0.0f) v = fmaf(shares[y * per * kShare + (32 * b + i) * 32], other[y] * inv_other, v);
+                        }
+                        x[i] = __float_as_uint(v);
+                    }
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        pk[i] = seen > 0 ? pack2<kDtype>(__uint_as_float(x[2 * i]) * inv,
-                                                         __uint_as_float(x[2 * i + 1]) * inv) : 0u;
-                    if (at >= 0) {
+                        pk[i] = pack2<kDtype>(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+                    if (mine) {
                         if (a.wide) {   // whole sectors: 32 bytes per store
 #pragma unroll
                             for (int i = 0; i < 2; ++i)
@@ -457,12 +525,17 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         }
                     }
                 }
-                if (at >= 0 && a.lse)
+                if (mine && a.lse)
                     a.lse[(int64_t)at * a.heads + head] =
-                        seen > 0 ? ((m - kShift) + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+                        (kSplit ? l > 0.0f : seen > 0) ? ((m - kShift) + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
                 tc_fence_before();
             }
         }
+    }
+    if (kSplit && warp >= 8) {   // the rows' warps meet twice; so do these
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
     }
     if (!ok) atomicExch(&g_wait_expired, 1u);
     tc_fence_before();
@@ -511,6 +584,23 @@ bool encode_rows(CUtensorMap *map, int dtype, const void *base, int D, int heads
 
 }  // namespace
 
+template <typename F, typename... Args>
+static cudaError_t launch_cluster(F *kernel, unsigned grid, int cluster, size_t smem, cudaStream_t st,
+                                  const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kPrefillThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 bool wait_expired_prefill() {
     unsigned v = 0;
     const unsigned none = 0;
@@ -542,18 +632,31 @@ int launch_prefill_attn(const fathom_prompts &p, const void *q, const void *k, c
         !encode_rows(&mk, p.dtype, k, p.D, p.kv_heads, p.total_k, p.k_head, p.k_token, 1, kKeys) ||
         !encode_rows(&mv, p.dtype, v, p.D, p.kv_heads, p.total_k, p.v_head, p.v_token, 1, kKeys))
         return FATHOM_ECUDA;
-    const unsigned grid = (unsigned)(tiles * a.groups);
+    // With fewer work items than half the SMs, clusters of 2, 4 or 8 CTAs share an item's keys, as long as
+    // each gets a few steps
+    int sms = device_sm_count();
+    if (sms <= 0) sms = 152;
+    a.split = 1;
+    while (a.split < 8 && tiles * a.groups * 2 * a.split <= sms && p.total_k >= 4 * kKeys * 2 * a.split) a.split *= 2;
+    const unsigned grid = (unsigned)(tiles * a.groups * a.split);
 #define FATHOM_PREFILL(SS, DD)                                                                     \
     do {                                                                                           \
         const size_t smem = sizeof(PrefillSmem<(SS + 3) / 4>) + 1024;                              \
-        ensure_smem(prefill_kernel<SS, DD>, smem);                                                 \
-        prefill_kernel<SS, DD><<<grid, kPrefillThreads, smem, st>>>(mq, mk, mv, a);                \
+        if (a.split > 1) {                                                                         \
+            ensure_smem(prefill_kernel<SS, DD, true>, smem);                                       \
+            e = launch_cluster(prefill_kernel<SS, DD, true>, grid, a.split, smem, st, mq, mk, mv, a); \
+        } else {                                                                                   \
+            ensure_smem(prefill_kernel<SS, DD, false>, smem);                                      \
+            prefill_kernel<SS, DD, false><<<grid, kPrefillThreads, smem, st>>>(mq, mk, mv, a);     \
+        }                                                                                          \
     } while (0)
+    cudaError_t e = cudaSuccess;
     const bool bf = p.dtype == FATHOM_BF16;
     if (p.D <= 64) { if (bf) FATHOM_PREFILL(4, FATHOM_BF16); else FATHOM_PREFILL(4, FATHOM_F16); }
     else if (p.D <= 96) { if (bf) FATHOM_PREFILL(6, FATHOM_BF16); else FATHOM_PREFILL(6, FATHOM_F16); }
     else { if (bf) FATHOM_PREFILL(8, FATHOM_BF16); else FATHOM_PREFILL(8, FATHOM_F16); }
 #undef FATHOM_PREFILL
+    if (e != cudaSuccess) { set_error("prefill_kernel: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }
     return launch_status("prefill_kernel");
 }
 

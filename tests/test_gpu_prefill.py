@@ -48,6 +48,14 @@ CASES = {
     "one token": ([1], [1], 1, 1, 8, FP),
     "long": ([1500], [1500], 4, 1, 128, BF),
     "many sequences": ([1 + i % 5 for i in range(100)], [1 + i % 5 + 3 * (i % 7) for i in range(100)], 4, 2, 64, BF),
+    # few rows and many keys: clusters of CTAs share the keys (2, 4 and 8 of them; shares that a row does not reach)
+    "few rows, 8 shares": ([3, 1, 40], [5000, 9, 41], 2, 1, 128, BF),
+    "few rows, 8 shares, fp16": ([1, 16], [300, 6000], 8, 2, 128, FP),
+    "few rows, 4 shares": ([7], [3000], 8, 4, 96, FP),
+    "few rows, 4 shares, whole prompt": ([2100], [2100], 2, 2, 64, BF),
+    "few rows, 2 shares": ([130, 3], [1500, 2], 4, 1, 64, FP),
+    "few rows, odd channels": ([5], [4500], 3, 1, 72, BF),
+    "few rows, some see nothing": ([60, 9], [50, 5000], 4, 1, 128, BF),
 }
 
 
@@ -82,6 +90,19 @@ def test_growing_scores_rescale_the_running_sums():
     k = (k.float() * torch.linspace(0.01, 30, n, device="cuda")[:, None, None]).to(BF)
     out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated([n]), want_lse=True)
     check(out, lse, q, k, v, [n], [n])
+
+
+@pytest.mark.parametrize("rising", [False, True])
+def test_shares_of_unequal_weight_are_joined(rising):
+    """The keys' scores climb or fall from one CTA's share of them to the next."""
+    n = 5000
+    q, k, v = inputs([4], [n], 2, 1, 128, BF)
+    ramp = torch.linspace(0.01, 30, n, device="cuda")[:, None, None]
+    k = (k.float() * (ramp if rising else ramp.flip(0))).to(BF)
+    out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated([4]), P.cumulated([n]), want_lse=True)
+    check(out, lse, q, k, v, [4], [n])
+    again, _ = B.fathom_prefill_attn(q, k, v, P.cumulated([4]), P.cumulated([n]))
+    assert torch.equal(out, again)
 
 
 def test_strided_slices_and_per_head_rows():
