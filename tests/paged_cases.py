@@ -66,8 +66,8 @@ def prefill(q, k, v, lq, lk, D):
 def rows_of(pages, table, n, h):
     """The first n rows of head h that one row of a page table names (bad entries: None)."""
     P = pages.shape[2]
-    keep = [i for i in range(n) if 0 <= int(table[i // P]) < pages.shape[0]]
     t = table.tolist()
+    keep = [i for i in range(n) if 0 <= t[i // P] < pages.shape[0]]
     idx = torch.tensor([t[i // P] for i in keep], dtype=torch.long, device=pages.device)
     slot = torch.tensor([i % P for i in keep], dtype=torch.long, device=pages.device)
     return pages[idx, h, slot], keep

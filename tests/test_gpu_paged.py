@@ -166,6 +166,32 @@ def test_a_workspace_serves_call_after_call_and_graph_after_graph():
     assert all(torch.equal(o, want) for o in outs)
 
 
+@pytest.mark.parametrize("lens,H,G,D,dt", [
+    ([30000, 17, 0, 22001], 4, 4, 128, BF),                # long shares of few sequences
+    ([2000 + 13 * i for i in range(150)], 2, 8, 64, FP),   # more than 128 sequences
+])
+def test_the_same_bits_every_time(lens, H, G, D, dt):
+    kp, vp, table, _ = P.pool(len(lens), H, D, 64, -(-max(lens) // 64), dt)
+    q = query(len(lens) * H, G, D)
+    pages = B.make_pages(kp, table)
+    ws = B.alloc_paged_workspace(pages, G=G, mass=True)
+    mass = torch.zeros(len(lens) * H, pages.cap, device="cuda")
+    before = mass.clone()
+    out = attend(q, kp, vp, table, lens, mass, ws=ws)
+    check_decode(out, q, kp, vp, table, lens, before, mass)
+    for _ in range(5):
+        again = torch.zeros_like(mass)
+        assert torch.equal(attend(q, kp, vp, table, lens, again, ws=ws), out)
+        assert torch.equal(again, mass)
+
+
+def test_thousands_of_sequences():
+    lens = [(7 * i) % 61 for i in range(1500)]
+    kp, vp, table, _ = P.pool(1500, 1, 64, 16, 4, BF)
+    q = query(1500, 2, 64)
+    check_decode(attend(q, kp, vp, table, lens), q, kp, vp, table, lens)
+
+
 def test_two_calls_at_once_with_their_own_workspaces():
     kp, vp, table, _ = P.pool(4, 2, 128, 32, 100, BF)
     lens = i32([3000, 100, 1, 2222])
