@@ -39,15 +39,28 @@ constexpr uint32_t kPanel = 128 * 128;   // bytes of 128 rows x 64 channels
 // Tensor memory columns: the two S (and P) tiles, then the two O tiles.
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 
+// A work item: 256 rows of a sequence and what they see.
+struct alignas(16) Work {
+    int group;      // of gp query heads
+    int q0, lq;     // the sequence's first query row, its query tokens
+    int k0, lk;     // its first key row, its key tokens
+    int off;        // query token t sees keys j <= t + off
+    int t0;         // first token; tile w starts at t0 + w * (128 / gp)
+    int nt0, nt1;   // steps of 128 keys of the two tiles
+    int steps;      // the larger; -1: no more work
+};
+
 template <int kPanels>   // 64-channel panels of a row: 1 (D <= 64) or 2
 struct PrefillSmem {
-    static constexpr int kStages = kPanels == 2 ? 5 : 8;
+    static constexpr int kStages = kPanels == 2 ? 4 : 8;
     static constexpr uint32_t kTile = kPanels * kPanel;
     alignas(1024) unsigned char q[2][kTile];
     alignas(1024) unsigned char kv[kStages][kTile];
-    alignas(16) uint64_t answer[2][2];   // of the requests for the next tile pair
+    alignas(128) unsigned char out[8][32 * 128];   // a warp's rows of O, 64 channels, on their way out
+    alignas(16) uint64_t answer[2];   // to the request for another CTA's work
+    Work work[2];                     // the item being worked on and the next
     uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2], o_full[2];
-    uint64_t work_full[2], work_empty[2], drained;
+    uint64_t work_full[2], work_empty[2], answered, drained;
     uint32_t tmem;
 };
 
@@ -57,7 +70,6 @@ __device__ unsigned g_wait_expired;
 struct PrefillArgs {
     int seqs, heads, kv_heads, D, total_q, total_k, gp, lg_gp, groups, tiles;
     int split;  // CTAs that share a work item's keys
-    int wide;   // rows of out start on 32-byte boundaries and are whole 32 bytes
     int64_t out_token, out_head;
     const int32_t *cu_q, *cu_k;
     void *out;
@@ -100,8 +112,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             mbar_init(smem_addr(&sm.p_full[w]), 4);
             mbar_init(smem_addr(&sm.o_full[w]), 1);
             mbar_init(smem_addr(&sm.work_full[w]), 1);
-            mbar_init(smem_addr(&sm.work_empty[w]), kLoadWarp + 1);   // every warp reads the answer
+            mbar_init(smem_addr(&sm.work_empty[w]), kLoadWarp);   // every other warp reads it
         }
+        mbar_init(smem_addr(&sm.answered), 1);
         mbar_init(smem_addr(&sm.drained), 1);
         mbar_init_fence();
     }
@@ -112,12 +125,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
     bool ok = true;
 
-    // ---- a work item (blockIdx.x of a launch): which sequence and which 256 rows, the last tiles first
-    // (they see the most keys), and what they see.  Computed alike by every warp.
+    // ---- the work item of a blockIdx.x: which sequence and which 256 rows, the last tiles first (they see
+    // the most keys); a whole warp
     const int tw = kRows >> a.lg_gp;
-    struct Work {
-        int group, q0, lq, k0, lk, off, t0, nt0, nt1, steps;
-    };
     const int rank = kSplit ? (int)(blockIdx.x % a.split) : 0;
     const int first_item = kSplit ? (int)(blockIdx.x / a.split) : (int)blockIdx.x;
     auto geometry = [&](int item) {
@@ -149,8 +159,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         g.lq = clamp_to(a.cu_q[seq + 1], a.total_q) - g.q0;
         g.k0 = clamp_to(a.cu_k[seq], a.total_k);
         g.lk = max(clamp_to(a.cu_k[seq + 1], a.total_k) - g.k0, 0);
-        g.off = g.lk - g.lq;                               // query token t sees keys j <= t + off
-        g.t0 = tile << (8 - a.lg_gp);                      // first token; tile w starts at t0 + w * (128 / Gp)
+        g.off = g.lk - g.lq;
+        g.t0 = tile << (8 - a.lg_gp);
         auto count = [&](int w) {                          // steps of tile w
             const int first = g.t0 + w * tw, last = min(first + tw, g.lq) - 1;
             const int keys = first <= last ? min(g.lk, last + g.off + 1) : 0;
@@ -170,31 +180,43 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         }
         return g;
     };
-    // ---- the CTA takes over the work of CTAs that have not started: while one item is worked on, the
-    // load warp asks for the next, and every warp reads the answer when it gets there
+    // ---- the CTA takes over the work of CTAs that have not started: while the loads of one item run, the
+    // load warp asks for the next, works out its geometry and leaves it for the other warps
     int round = 0;
-    auto next_item = [&]() {
-        if (kSplit) return -1;
+    auto get_work = [&](Work &g) {
         const int slot = round & 1;
         ok = ok && warp_wait(smem_addr(&sm.work_full[slot]), (round >> 1) & 1);
-        const int item = ok ? granted_cta(sm.answer[slot][0], sm.answer[slot][1]) : -1;
-        fence_async_smem();
-        __syncwarp();
+        // every field from one lane: the compiler then knows that the warp branches as one (without that the
+        // loops below ran 9 % slower)
+        const int *f = &sm.work[slot].group;
+        auto field = [&](int i) { return __shfl_sync(0xffffffffu, f[i], 0); };
+        g.group = field(0); g.q0 = field(1); g.lq = field(2); g.k0 = field(3); g.lk = field(4);
+        g.off = field(5); g.t0 = field(6); g.nt0 = field(7); g.nt1 = field(8); g.steps = field(9);
         if (lane == 0) mbar_arrive(smem_addr(&sm.work_empty[slot]));
         ++round;
-        return __shfl_sync(0xffffffffu, item, 0);
+        return ok && g.steps >= 0;
     };
 
     if (warp == kLoadWarp) {
         int st = 0, nq0 = 0, nq1 = 0;   // the ring's next stage; Q tiles loaded so far
         uint32_t turn = 1;              // parity of the stage's last release; true at once in the first turn
-        for (int item = first_item; item >= 0 && ok; item = next_item()) {
-            const Work g = geometry(item);
+        auto publish = [&](const Work &g) {
             const int slot = round & 1;
+            ok = ok && warp_wait(smem_addr(&sm.work_empty[slot]), ((round >> 1) & 1) ^ 1);
+            if (lane == 0 && ok) {
+                sm.work[slot] = g;
+                mbar_arrive(smem_addr(&sm.work_full[slot]));
+            }
+            __syncwarp();
+            ++round;
+        };
+        Work g = geometry(first_item);
+        publish(g);
+        for (int asked = 0; ok && g.steps >= 0; ++asked) {
             if (elect_one()) {
-                if (!kSplit && (ok = mbar_wait(smem_addr(&sm.work_empty[slot]), ((round >> 1) & 1) ^ 1))) {
-                    mbar_expect(smem_addr(&sm.work_full[slot]), 16);
-                    request_cta(smem_addr(sm.answer[slot]), smem_addr(&sm.work_full[slot]));
+                if (!kSplit) {
+                    mbar_expect(smem_addr(&sm.answered), 16);
+                    request_cta(smem_addr(sm.answer), smem_addr(&sm.answered));
                 }
                 const int hq = g.group << a.lg_gp, hk = hq / (a.heads / a.kv_heads);
                 for (int w = 0; w < 2 && ok; ++w) {
@@ -224,6 +246,16 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             const int end = st + 2 * g.steps;
             turn ^= (uint32_t)(end / kStages) & 1u;
             st = end % kStages;
+            int item = -1;
+            if (!kSplit && ok) {
+                ok = warp_wait(smem_addr(&sm.answered), asked & 1);
+                if (ok) item = granted_cta(sm.answer[0], sm.answer[1]);
+                fence_async_smem();   // the answer is read before the next one is asked for
+                __syncwarp();
+            }
+            if (item >= 0) g = geometry(item);
+            else g.steps = -1;
+            publish(g);
         }
         if (!ok) {   // the copies in flight land before the CTA ends
             const unsigned long long t0 = global_ns();
@@ -257,8 +289,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const uint32_t q_full = smem_addr(sm.q_full), q_empty = smem_addr(sm.q_empty), p_full = smem_addr(sm.p_full);
         int cur = 0;                                // the ring's stages in turn: K_0, V_0, K_1, V_1, ...
         uint32_t pc = 0, pq0 = 0, pq1 = 0, pp0 = 0, pp1 = 0;   // parities of the next wait on each barrier
-        for (int item = first_item; item >= 0 && ok; item = next_item()) {
-            const Work g = geometry(item);
+        for (Work g; get_work(g);) {
             if (g.steps == 0) continue;
             const int tail = g.lk - (g.steps - 1) * kKeys;   // live rows of the last V tile
             ok = warp_wait(full + 8 * cur, pc) && (g.nt0 == 0 || warp_wait(q_full, pq0)) &&
@@ -338,8 +369,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         // 2^32 as at 1, a fp16 weight must stay below 2^16
         constexpr float kLag = kDtype == FATHOM_F16 ? 8.0f : 32.0f;
         uint32_t ps = 0, po = 0;   // parities of the next wait for S, and for the last product into O
-        for (int item = first_item; item >= 0 && ok; item = next_item()) {
-            const Work g = geometry(item);
+        for (Work g; get_work(g);) {
             const int nt = w ? g.nt1 : g.nt0;
             const int token = g.t0 + w * tw + (row >> a.lg_gp);
             const int at = token < g.lq ? g.q0 + token : -1;   // row of out; -1: behind the sequence
@@ -489,7 +519,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 const bool mine = at >= 0 && ok && (!kSplit || rank == dst);
                 const float inv = l > 0.0f ? own / l : 0.0f, inv_other = l > 0.0f ? 1.0f / l : 0.0f;
                 const bool some = kSplit ? own != 0.0f && nt > 0 : seen > 0;   // O holds something for this row
-                uint16_t *orow = (uint16_t *)a.out + (int64_t)at * a.out_token + head * a.out_head;
+                const int row_at = mine ? at : -1;
+                unsigned char *stage = sm.out[warp];
+                // 64 channels at a time through shared memory, so that a store writes four whole lines and
+                // not 32 pieces of as many rows
 #pragma unroll 1
                 for (int b = 0; b < (!kSplit || rank == dst ? kSteps / 2 : 0); ++b) {
                     uint32_t x[32];
@@ -507,22 +540,28 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         }
                         x[i] = __float_as_uint(v);
                     }
-                    uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        pk[i] = pack2<kDtype>(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-                    if (mine) {
-                        if (a.wide) {   // whole sectors: 32 bytes per store
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t pk[4];
 #pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                if (32 * b + 16 * i < a.D) store32(orow + 32 * b + 16 * i, pk + 8 * i);
-                        } else {
+                        for (int e = 0; e < 4; ++e)
+                            pk[e] = pack2<kDtype>(__uint_as_float(x[8 * i + 2 * e]), __uint_as_float(x[8 * i + 2 * e + 1]));
+                        *reinterpret_cast<uint4 *>(stage + lane * 128 + (((4 * (b & 1) + i) ^ (lane & 7)) << 4)) =
+                            make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+                    if ((b & 1) || b + 1 == kSteps / 2) {
+                        __syncwarp();
+                        const int ch = lane & 7, col = 64 * (b >> 1) + 8 * ch;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (32 * b + 8 * i < a.D)
-                                    *reinterpret_cast<uint4 *>(orow + 32 * b + 8 * i) =
-                                        make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                        for (int i = 0; i < 8; ++i) {
+                            const int rr = 4 * i + (lane >> 3);
+                            const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
+                            const int t = __shfl_sync(0xffffffffu, row_at, rr);
+                            const int h = (g.group << a.lg_gp) + (((warp & 3) * 32 + rr) & (a.gp - 1));
+                            if (t >= 0 && col < a.D)
+                                *reinterpret_cast<uint4 *>((uint16_t *)a.out + (int64_t)t * a.out_token + h * a.out_head + col) = v;
                         }
+                        __syncwarp();
                     }
                 }
                 if (mine && a.lse)
@@ -620,8 +659,6 @@ int launch_prefill_attn(const fathom_prompts &p, const void *q, const void *k, c
     a.gp = 1 << a.lg_gp;
     a.groups = p.heads / a.gp;
     a.out_token = p.out_token; a.out_head = p.out_head;
-    a.wide = p.D % 16 == 0 && ((uintptr_t)out & 31) == 0 && (p.total_q == 1 || p.out_token % 16 == 0) &&
-             (p.heads == 1 || p.out_head % 16 == 0);
     a.cu_q = cu_q; a.cu_k = cu_k; a.out = out; a.lse = lse;
     const long long tiles = ((long long)p.total_q * a.gp + 2 * kRows - 1) / (2 * kRows) + p.seqs;
     if (tiles * a.groups > 0x7fffffffLL) { set_error("prefill_attn: too many rows for one launch"); return FATHOM_EINVAL; }
