@@ -667,9 +667,14 @@ def fathom_prefill_attn(q, k, v, cu_q, cu_k=None, out=None, lse=None, want_lse=F
     Tq, H, D = q.shape
     Tk, Hkv, _ = k.shape
     dt = q.dtype
-    _check_strided(q, "q", _ROW_TYPES, (Tq, H, D))
-    _check_strided(k, "k", (dt,), (Tk, Hkv, D))
-    _check_strided(v, "v", (dt,), (Tk, Hkv, D))
+    (qt, qh, qc), (kt, kh, kc) = q.stride(), k.stride()
+    if not (dt in _ROW_TYPES and qc == 1 and q.is_cuda):
+        _check_strided(q, "q", _ROW_TYPES, (Tq, H, D))
+    if not (k.dtype is dt and k.shape[2] == D and kc == 1 and k.is_cuda):
+        _check_strided(k, "k", (dt,), (Tk, Hkv, D))
+    if v is None or not (v.dtype is dt and v.shape == (Tk, Hkv, D) and v.stride(2) == 1 and v.is_cuda):
+        _check_strided(v, "v", (dt,), (Tk, Hkv, D))
+    vt, vh, _ = v.stride()
     if cu_k is None:
         cu_k = cu_q
     _check(cu_q, "cu_q", (torch.int32,))
@@ -687,7 +692,7 @@ def fathom_prefill_attn(q, k, v, cu_q, cu_k=None, out=None, lse=None, want_lse=F
             out = torch.empty((Tq, H, D), dtype=dt, device=q.device)
         if lse is None and want_lse:
             lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
-        (qt, qh, _), (kt, kh, _), (vt, vh, _), (ot, oh, _) = q.stride(), k.stride(), v.stride(), out.stride()
+        ot, oh, _ = out.stride()
         p = Prompts(cu_q.shape[0] - 1, H, Hkv, D, _ROW_TYPES[dt], Tq, Tk, qt, qh, kt, kh, vt, vh, ot, oh)
         _call("fathom_prefill_attn", p, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
               out.data_ptr(), lse.data_ptr() if lse is not None else None, handle)

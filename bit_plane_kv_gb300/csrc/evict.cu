@@ -1,5 +1,11 @@
 // evict.cu -- eviction from a paged KV cache by accumulated attention weight:
 // the kept set of every unit, then its rows and mass moved together.
+// Measured, 128 channels, bf16: 256 units of up to 16k tokens cut back to 4096 each
+// 27 us (the kept sets) + 205 us (the move: 1.0 GB in rows of 256 bytes, 2 KB apart,
+// 4.9 TB/s); 8 units of 8192 tokens cut to 2048 14 + 17 us (latency: a chunk's three
+// dependent lookups and its copy).  For the move, twice the loads in flight from a
+// pipelined loop (220 us) and bulk copies through shared memory (210 us; 76 us for the
+// 8 units) were no faster; fewer resident threads were slower (128 per CTA: 330 us).
 #include "fathom_internal.cuh"
 
 namespace fathom {

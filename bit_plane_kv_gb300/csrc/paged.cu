@@ -66,6 +66,14 @@ paged_append_kernel(fathom_pages p, int lg, int4 *__restrict__ kp, int4 *__restr
 // piece i of head h; for G <= 8, rows h and 8 + h are the first two pieces and a
 // second instruction adds the third -- so a K or V fragment is read from shared
 // memory once for all heads and pieces.
+//
+// Measured, 128 channels, bf16, 4 heads per unit: 32 sequences of up to 32k tokens
+// (2.3 GB) 358 us, 6.4 TB/s, the copy rate 6.8; one sequence of 4096 tokens 15 us, of
+// which the data take 3 (start and page numbers 2.5 us, the first data 1, two or four
+// tiles 2, merge and ticket 2, the join 4: dependent accesses of about a microsecond
+// each); 61 sequences of up to 3001 tokens, 64 channels, 8 heads, fp16: 34 us.
+// Shares that CTAs take from a counter as they finish, instead of equal ones, gained
+// nothing (359 us): CTAs finish a fifth apart, but DRAM is busy until the end.
 
 constexpr int kDecWarps = 4, kDecThreads = 32 * kDecWarps;
 // CTAs resident per SM, and stages of their rings

@@ -14,12 +14,27 @@
 // pass.  The exponentials of a row are taken against a maximum that may be up to
 // 2^8 too small (m is raised, and O and l rescaled, only beyond that): O, 64 KB
 // of tensor memory, is touched by the row's own thread in a few tiles only.
-// A warp loads Q and a ring of K and V tiles by TMA; one thread issues the matrix
-// instructions.
+// A warp loads Q and a ring of K and V tiles by TMA; one elected lane of another
+// issues the matrix instructions; CTAs stay and take over the work of those that have
+// not started, so that one item's epilogue runs beside the next one's loads and
+// products.  With fewer items than half the SMs, clusters share an item's keys.
+//
+// Bound: a tile's chain S -> softmax -> P V, S of the next keys (P takes the place of
+// S in tensor memory, which S, P and O of two tiles fill, so the next S waits for it):
+// about 2700 clocks per 128 keys and two tiles where the products alone take 2050.
+// Measured, 32 query heads on 8 KV heads, 128 channels, bf16: one prompt of 16384
+// tokens 1369 us (2.2 TFLOP, 1.61 PFLOP/s; 1.90 measured for library products), 12
+// prompts of up to 2048 tokens 165 us (1.11 PFLOP/s), 16 tokens against 8192 27 us.
+// What the steps gave on the 16k prompt: one thread per row with a full pass for the
+// maximum 2029 us; matrix instructions behind an elected lane instead of lane 0
+// 1883 -> 1445 us (their issue, not their execution, had been the bound); CTAs that
+// take over work 1445 -> 1370 us, and 237 -> 182 us for the packed prompts; whole-line
+// stores 173 -> 165 us there.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "blackwell.cuh"
 
@@ -48,6 +63,7 @@ struct alignas(16) Work {
     int t0;         // first token; tile w starts at t0 + w * (128 / gp)
     int nt0, nt1;   // steps of 128 keys of the two tiles
     int steps;      // the larger; -1: no more work
+    int half;       // bit w: tile w's last step has 64 keys or fewer and is worked on as half a step
 };
 
 template <int kPanels>   // 64-channel panels of a row: 1 (D <= 64) or 2
@@ -153,7 +169,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             }
             nth -= __shfl_sync(0xffffffffu, upto, 31);
         }
-        g.lq = g.nt0 = g.nt1 = g.steps = g.q0 = g.k0 = g.lk = g.off = g.t0 = 0;
+        g.lq = g.nt0 = g.nt1 = g.steps = g.q0 = g.k0 = g.lk = g.off = g.t0 = g.half = 0;
         if (seq < 0) return g;   // the grid counts one tile more per sequence than most need
         g.q0 = clamp_to(a.cu_q[seq], a.total_q);
         g.lq = clamp_to(a.cu_q[seq + 1], a.total_q) - g.q0;
@@ -161,16 +177,19 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         g.lk = max(clamp_to(a.cu_k[seq + 1], a.total_k) - g.k0, 0);
         g.off = g.lk - g.lq;
         g.t0 = tile << (8 - a.lg_gp);
-        auto count = [&](int w) {                          // steps of tile w
-            const int first = g.t0 + w * tw, last = min(first + tw, g.lq) - 1;
-            const int keys = first <= last ? min(g.lk, last + g.off + 1) : 0;
-            return keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
+        auto keys = [&](int w) {                           // that some row of tile w sees
+            const int start = g.t0 + w * tw, last = min(start + tw, g.lq) - 1;
+            return start <= last ? max(min(g.lk, last + g.off + 1), 0) : 0;
         };
-        g.nt0 = count(0);
-        g.nt1 = count(1);
+        const int keys0 = keys(0), keys1 = keys(1);
+        g.nt0 = (keys0 + kKeys - 1) / kKeys;
+        g.nt1 = (keys1 + kKeys - 1) / kKeys;
+        g.half = (keys0 > 0 && (keys0 - 1) % kKeys < kKeys / 2 ? 1 : 0) | (keys1 > 0 && (keys1 - 1) % kKeys < kKeys / 2 ? 2 : 0);
         g.steps = max(g.nt0, g.nt1);
         if constexpr (kSplit) {   // this CTA's share of the steps, its keys counted from the first of them
             const int from = g.steps * rank / a.split, to = g.steps * (rank + 1) / a.split;
+            if (g.nt0 > to) g.half &= ~1;
+            if (g.nt1 > to) g.half &= ~2;
             g.nt0 = min(max(g.nt0 - from, 0), to - from);
             g.nt1 = min(max(g.nt1 - from, 0), to - from);
             g.steps = max(g.nt0, g.nt1);
@@ -191,7 +210,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const int *f = &sm.work[slot].group;
         auto field = [&](int i) { return __shfl_sync(0xffffffffu, f[i], 0); };
         g.group = field(0); g.q0 = field(1); g.lq = field(2); g.k0 = field(3); g.lk = field(4);
-        g.off = field(5); g.t0 = field(6); g.nt0 = field(7); g.nt1 = field(8); g.steps = field(9);
+        g.off = field(5); g.t0 = field(6); g.nt0 = field(7); g.nt1 = field(8); g.steps = field(9); g.half = field(10);
         if (lane == 0) mbar_arrive(smem_addr(&sm.work_empty[slot]));
         ++round;
         return ok && g.steps >= 0;
@@ -263,26 +282,41 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         }
     } else if (warp == kMmaWarp) {
         constexpr uint32_t type = kDtype == FATHOM_BF16 ? 1u : 0u;
-        const uint32_t desc_s = mma_desc(type, kRows, kKeys, false), desc_o = mma_desc(type, kRows, kSteps * 16, true);
+        const uint32_t desc_s = mma_desc(type, kRows, kKeys, false), desc_h = mma_desc(type, kRows, kKeys / 2, false);
+        const uint32_t desc_o = mma_desc(type, kRows, kSteps * 16, true);
         // descriptors of the first 16 channels (keys) of each operand; the others lie at fixed offsets, and
         // the address field of a descriptor counts 16 bytes
         const uint64_t desc_q = smem_desc(smem_addr(sm.q[0]), 0);
         const uint64_t desc_k = smem_desc(smem_addr(sm.kv[0]), 0), desc_v = smem_desc(smem_addr(sm.kv[0]), kPanel);
-        auto scores = [&](int w, int st) {
+        // S of tile w against the K tile of a stage, all of its keys or the first 64
+        auto scores = [&](int w, int st, bool half) {
             const uint64_t dq = desc_q + w * (kTile >> 4), dk = desc_k + st * (kTile >> 4);
+            if (half) {
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                const uint32_t at = ((k >> 2) * kPanel + (k & 3) * 32) >> 4;
-                mma_ss(tmem + kColS + w * 128, dq + at, dk + at, desc_s, k > 0);
+                for (int k = 0; k < kSteps; ++k) {
+                    const uint32_t at = ((k >> 2) * kPanel + (k & 3) * 32) >> 4;
+                    mma_ss(tmem + kColS + w * 128, dq + at, dk + at, desc_h, k > 0);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    const uint32_t at = ((k >> 2) * kPanel + (k & 3) * 32) >> 4;
+                    mma_ss(tmem + kColS + w * 128, dq + at, dk + at, desc_s, k > 0);
+                }
             }
             mma_commit(smem_addr(&sm.s_full[w]));
         };
-        auto values = [&](int w, int st, int j) {
+        auto values = [&](int w, int st, bool first, bool half) {
             const uint64_t dv = desc_v + st * (kTile >> 4);
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
+            for (int k = 0; k < kKeys / 32; ++k)
                 mma_ts(tmem + kColO + w * 128, tmem + kColS + w * 128 + k * 8, dv + ((k * 16 * 128) >> 4), desc_o,
-                       k > 0 ? 1u : (uint32_t)(j > 0));
+                       k > 0 ? 1u : (uint32_t)!first);
+            if (!half) {
+#pragma unroll
+                for (int k = kKeys / 32; k < kKeys / 16; ++k)
+                    mma_ts(tmem + kColO + w * 128, tmem + kColS + w * 128 + k * 8, dv + ((k * 16 * 128) >> 4), desc_o, 1u);
+            }
             mma_commit(smem_addr(&sm.o_full[w]));
         };
         const uint32_t full = smem_addr(sm.kv_full), empty = smem_addr(sm.kv_empty);
@@ -299,9 +333,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             pq1 ^= g.nt1 > 0;
             if (elect_one()) {
                 tc_fence_after();
-                if (g.nt0 > 0) scores(0, cur);
+                if (g.nt0 > 0) scores(0, cur, g.nt0 == 1 && (g.half & 1));
                 if (g.nt0 == 1) mma_commit(q_empty);
-                if (g.nt1 > 0) scores(1, cur);
+                if (g.nt1 > 0) scores(1, cur, g.nt1 == 1 && (g.half & 2));
                 if (g.nt1 == 1) mma_commit(q_empty + 8);
                 mma_commit(empty + 8 * cur);
             }
@@ -330,8 +364,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     pp0 ^= 1;
                     tc_fence_after();
                     if (elect_one()) {
-                        values(0, sv, j);
-                        if (j + 1 < g.nt0) scores(0, sk);
+                        values(0, sv, j == 0, j + 1 == g.nt0 && (g.half & 1));
+                        if (j + 1 < g.nt0) scores(0, sk, j + 2 == g.nt0 && (g.half & 1));
                         if (j + 2 == g.nt0) mma_commit(q_empty);
                     }
                     __syncwarp();
@@ -341,9 +375,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     pp1 ^= 1;
                     tc_fence_after();
                     if (elect_one()) {
-                        values(1, sv, j);
+                        values(1, sv, j == 0, j + 1 == g.nt1 && (g.half & 2));
                         mma_commit(empty + 8 * sv);
-                        if (j + 1 < g.nt1) scores(1, sk);
+                        if (j + 1 < g.nt1) scores(1, sk, j + 2 == g.nt1 && (g.half & 2));
                         if (j + 2 == g.nt1) mma_commit(q_empty + 8);
                         if (more) mma_commit(empty + 8 * sk);
                     }
@@ -378,8 +412,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             const int seen = min(g.lk, token + g.off + 1);
             const int seen_min = min(g.lk, g.t0 + w * tw + (((warp & 3) * 32) >> a.lg_gp) + g.off + 1);
             float m = -CUDART_INF_F, l = 0.0f;   // m in log2 units; -inf: no finite score yet
-            for (int j = 0; j < nt; ++j) {
-                if (!(ok = warp_wait(smem_addr(&sm.s_full[w]), ps))) break;
+            auto step = [&](int j, auto halves) {   // 128 keys, or the first 64 of the last ones
+                constexpr int kHalves = decltype(halves)::value;
+                if (!(ok = warp_wait(smem_addr(&sm.s_full[w]), ps))) return;
                 ps ^= 1;
                 tc_fence_after();
                 const bool edge = (j + 1) * kKeys > seen_min;
@@ -389,7 +424,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 tmem_ld32(ts, s[0]);
                 tmem_ld32(ts + 32, s[1]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {   // 64 keys at a time
+                for (int h = 0; h < kHalves; ++h) {   // 64 keys at a time
                     float top = -CUDART_INF_F, top2 = -CUDART_INF_F;
 #pragma unroll
                     for (int b = 2 * h; b < 2 * h + 2; ++b) {
@@ -431,7 +466,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                             }
                         }
                         if (j > 0) {
-                            if (!(ok = warp_wait(smem_addr(&sm.o_full[w]), po ^ 1))) break;   // the product before
+                            if (!(ok = warp_wait(smem_addr(&sm.o_full[w]), po ^ 1))) return;   // the product before
                             tc_fence_after();
 #pragma unroll 1
                             for (int b = 0; b < kSteps; ++b) {
@@ -459,10 +494,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                             pk[i] = pack2<kDtype>(x.x, x.y);
                         }
                         tmem_st16(ts + 16 * b, pk);
-                        if (h == 0) tmem_ld32(ts + 64 + 32 * b, s[2 + b]);
+                        if (h == 0 && kHalves == 2) tmem_ld32(ts + 64 + 32 * b, s[2 + b]);
                     }
                 }
-                if (!ok) break;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -470,7 +504,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
                 po ^= 1;
-            }
+            };
+            const int full = nt - (g.half >> w & 1);
+            for (int j = 0; j < full && ok; ++j) step(j, std::integral_constant<int, 2>());
+            if (full < nt && ok) step(full, std::integral_constant<int, 1>());
             // ---- O / l, rounded once
             ok = ok && (nt == 0 || warp_wait(smem_addr(&sm.o_full[w]), po ^ 1));
             if (ok || kSplit) {
