@@ -158,8 +158,8 @@ struct DecSmem {
     float o[kDecWarps][FATHOM_MAX_G][kD];
     float m[kDecWarps][FATHOM_MAX_G], l[kDecWarps][FATHOM_MAX_G];
     unsigned live[kDecWarps][kDecStages];   // which of the 16 tokens there are
-    long long sum[kDecWarps];
-    int last;
+    long long sum[kDecWarps], before;
+    int part, last;
 };
 
 // Division of numbers that mostly fit 32 bits, and the first tile of CTA c's share.
@@ -228,28 +228,35 @@ paged_attn_kernel(const DecArgs a) {
         seq0 = __shfl_sync(0xffffffffu, s, f);
         first = __shfl_sync(0xffffffffu, before, f);
     } else {
+        // every thread the sum of a contiguous part; the part that holds w0 is searched by every warp
+        const int per = (p.seqs + kDecThreads - 1) / kDecThreads;
         long long mine = 0;
-        for (int s = tid; s < p.seqs; s += kDecThreads) mine += tiles_of(length(s));
-#pragma unroll
-        for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-        if (lane == 0) sm.sum[warp] = mine;
+        for (int s = tid * per; s < min((tid + 1) * per, p.seqs); ++s) mine += tiles_of(length(s));
+        const long long upto = scan(mine);
+        if (lane == 31) sm.sum[warp] = upto;
         __syncthreads();
-        long long sum = 0;
+        long long sum = 0, before = upto - mine;
 #pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) sum += sm.sum[w];
+        for (int w = 0; w < kDecWarps; ++w) {
+            if (w < warp) before += sm.sum[w];
+            sum += sm.sum[w];
+        }
         split(sum);
-        long long before = 0;
-        for (int s0 = 0; s0 < p.seqs; s0 += 32) {
-            const long long x = s0 + lane < p.seqs ? (long long)tiles_of(length(s0 + lane)) * H : 0;
-            const long long upto = scan(x);
-            const unsigned hit = __ballot_sync(0xffffffffu, before + upto > w0);
-            if (hit) {
-                const int f = __ffs(hit) - 1;
-                seq0 = s0 + f;
-                first = __shfl_sync(0xffffffffu, before + upto - x, f);
-                break;
+        if (before * H <= w0 && w0 < (before + mine) * H) { sm.part = tid; sm.before = before; }
+        __syncthreads();
+        if (w0 < w1) {
+            before = sm.before;
+            for (int s0 = sm.part * per;; s0 += 32) {
+                const long long x = s0 + lane < p.seqs ? tiles_of(length(s0 + lane)) : 0, end = before + scan(x);
+                const unsigned hit = __ballot_sync(0xffffffffu, end * H > w0);
+                if (hit || s0 >= p.seqs) {
+                    const int f = hit ? __ffs(hit) - 1 : 0;
+                    seq0 = min(s0 + f, p.seqs - 1);
+                    first = __shfl_sync(0xffffffffu, (end - x) * H, f);
+                    break;
+                }
+                before = __shfl_sync(0xffffffffu, end, 31);
             }
-            before += __shfl_sync(0xffffffffu, upto, 31);
         }
     }
     // units of empty sequences

@@ -146,28 +146,39 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     const int tw = kRows >> a.lg_gp;
     const int rank = kSplit ? (int)(blockIdx.x % a.split) : 0;
     const int first_item = kSplit ? (int)(blockIdx.x / a.split) : (int)blockIdx.x;
+    int seen_s0 = 0, seen_before = 0;   // the 32 sequences that held the last item, and the tile pairs before them
     auto geometry = [&](int item) {
         Work g;
         g.group = item % a.groups;
-        int nth = a.tiles - 1 - item / a.groups, seq = -1, tile = 0;
-        for (int s0 = 0; s0 < a.seqs && seq < 0; s0 += 32) {
+        const int nth = a.tiles - 1 - item / a.groups;
+        int seq = -1, tile = 0;
+        auto pairs = [&](int s0) {   // of 256-row pairs of tiles: this lane's sequence's
             int n = 0;
             if (s0 + lane < a.seqs)
                 n = max(clamp_to(a.cu_q[s0 + lane + 1], a.total_q) - clamp_to(a.cu_q[s0 + lane], a.total_q), 0);
-            n = (int)((((long long)n << a.lg_gp) + 2 * kRows - 1) / (2 * kRows));
-            int upto = n;
+            return (int)((((long long)n << a.lg_gp) + 2 * kRows - 1) / (2 * kRows));
+        };
+        // items come in falling order: the search starts where the last one ended
+        while (nth < seen_before && seen_s0 > 0) {
+            seen_s0 -= 32;
+            seen_before -= __reduce_add_sync(0xffffffffu, pairs(seen_s0));
+        }
+        for (; seen_s0 < a.seqs; seen_s0 += 32) {
+            const int n = pairs(seen_s0);
+            int upto = seen_before + n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, upto, o);
+                const int x = __shfl_up_sync(0xffffffffu, upto - seen_before, o);
                 if (lane >= o) upto += x;
             }
             const unsigned hit = __ballot_sync(0xffffffffu, nth < upto);
             if (hit) {
                 const int l = __ffs(hit) - 1;
-                seq = s0 + l;
+                seq = seen_s0 + l;
                 tile = nth - __shfl_sync(0xffffffffu, upto - n, l);
+                break;
             }
-            nth -= __shfl_sync(0xffffffffu, upto, 31);
+            seen_before = __shfl_sync(0xffffffffu, upto, 31);
         }
         g.lq = g.nt0 = g.nt1 = g.steps = g.q0 = g.k0 = g.lk = g.off = g.t0 = g.half = 0;
         if (seq < 0) return g;   // the grid counts one tile more per sequence than most need

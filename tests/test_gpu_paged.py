@@ -206,6 +206,24 @@ def test_two_calls_at_once_with_their_own_workspaces():
     assert all(torch.equal(x, want) for x in got)
 
 
+def test_pages_beyond_32_bit_offsets():
+    """Four pages 2^30 elements apart: append, attention and eviction past 2^32 bytes."""
+    H, D, page, step = 1, 64, 64, 1 << 30
+    pools = [torch.empty(3 * step + H * page * D, dtype=BF, device="cuda").as_strided((4, H, page, D), (step, page * D, D, 1))
+             for _ in range(2)]
+    table = i32([[3, 1, 2, 0]])
+    pages = B.make_pages(pools[0], table)
+    new = torch.randn(200, 2, D, device="cuda").to(BF)
+    B.fathom_paged_append(pages, *pools, table, new[:, :1], new[:, 1:], i32([0]), P.cumulated([200]))
+    q = query(1, 4, D)
+    check_decode(attend(q, *pools, table, [200]), q, *pools, table, [200])
+    m = masses(1, 256)
+    kept, _, _ = B.fathom_paged_evict(pages, *pools, table, i32([200]), m, 70, table, 4, 32)     # in place
+    at = kept[0].long()
+    assert torch.equal(torch.cat([pools[0][3, 0], pools[0][1, 0, :6]]), new[at, 0])
+    assert torch.equal(torch.cat([pools[1][3, 0], pools[1][1, 0, :6]]), new[at, 1])
+
+
 def test_cache_in_pinned_host_memory():
     kp, vp, table, _ = P.pool(2, 2, 128, 16, 20, BF, layout="head")
     q, lens = query(4, 4, 128), [300, 45]

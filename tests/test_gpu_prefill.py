@@ -1,6 +1,9 @@
 """Causal attention of packed prompts on the GPU against the plain 64-bit form;
 the tolerances are derived in paged_cases."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -47,6 +50,8 @@ CASES = {
     "empty rows and sequences": ([0, 10, 4, 0, 130, 3], [0, 0, 2, 50, 100, 3], 8, 2, 128, BF),
     "one token": ([1], [1], 1, 1, 8, FP),
     "long": ([1500], [1500], 4, 1, 128, BF),
+    "128 heads on one": ([3, 130], [3, 140], 128, 1, 64, BF),
+    "160 heads on one": ([9], [70], 160, 1, 72, FP),
     "many sequences": ([1 + i % 5 for i in range(100)], [1 + i % 5 + 3 * (i % 7) for i in range(100)], 4, 2, 64, BF),
     # few rows and many keys: clusters of CTAs share the keys (2, 4 and 8 of them; shares that a row does not reach)
     "few rows, 8 shares": ([3, 1, 40], [5000, 9, 41], 2, 1, 128, BF),
@@ -65,6 +70,27 @@ def test_prefill_matches_the_plain_form(name):
     q, k, v = inputs(lq, lk, H, Hkv, D, dt)
     out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated(lq), P.cumulated(lk), want_lse=True)
     check(out, lse, q, k, v, lq, lk)
+
+
+def test_thousands_of_sequences():
+    """Two-row sequences between longer ones: the search for a tile's sequence goes over many of them."""
+    lq = [2 + 70 * (i % 97 == 0) for i in range(1500)]
+    q, k, v = inputs(lq, lq, 2, 1, 64, BF)
+    out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated(lq), want_lse=True)
+    check(out, lse, q, k, v, lq, lq)
+
+
+def test_rows_beyond_32_bit_offsets():
+    """Strides that put the later tokens past 2^32 bytes, of the inputs and of the result."""
+    n, H, D, step = 300, 2, 64, 1 << 23
+    g = torch.Generator(device="cuda").manual_seed(1)
+    big = torch.empty(n * step, dtype=BF, device="cuda").as_strided((n, 4, 2, D), (step, 2 * D, D, 1))
+    rows = torch.randn(n, 3, 2, D, generator=g, device="cuda").to(BF)
+    big[:, :3].copy_(rows)
+    q, k, v = big[:, 0], big[:, 1], big[:, 2]
+    out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated([100, 200]), out=big[:, 3], want_lse=True)
+    check(out.contiguous(), lse, rows[:, 0].contiguous(), rows[:, 1].contiguous(), rows[:, 2].contiguous(), [100, 200],
+          [100, 200])
 
 
 def test_whole_prompts_need_one_list_of_lengths_and_no_lse():
@@ -185,3 +211,43 @@ def test_no_bounded_wait_ran_out():
     q, k, v = inputs([300], [300], 4, 2, 128, BF)
     B.fathom_prefill_attn(q, k, v, P.cumulated([300]))
     B.fathom_wait_status()                             # covers every call of this process
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Every call, captured by a process that has not made it before, and replayed."""
+    code = """
+import sys
+sys.path.insert(0, %r); sys.path.insert(0, %r)
+import torch
+from bit_plane_kv_gb300 import binding as B
+import paged_cases as P
+kp, vp, table, free = P.pool(2, 2, 128, 16, 8, torch.bfloat16, extra=8)
+pages = B.make_pages(kp, table)
+ws = B.alloc_paged_workspace(pages, G=4, mass=True)
+q, new = torch.randn(4, 4, 128, device="cuda"), torch.randn(2, 2, 128, device="cuda").bfloat16()
+lens, start = torch.full((2,), 100, dtype=torch.int32, device="cuda"), torch.full((2,), 99, dtype=torch.int32, device="cuda")
+mass, dst = torch.zeros(4, 128, device="cuda"), free.reshape(2, 4).contiguous()
+p = torch.randn(40, 8, 128, device="cuda").bfloat16()
+cu = P.cumulated([7, 33])
+
+def calls():
+    a, _ = B.fathom_prefill_attn(p, p[:, :2], p[:, 2:4], cu)
+    B.fathom_paged_append(pages, kp, vp, table, new, new, start)
+    b = B.fathom_paged_attn(pages, q, kp, vp, table, lens, ws, mass=mass)
+    c, _, d = B.fathom_paged_evict(pages, kp, vp, table, lens, mass, 60, dst, mass_out=torch.zeros(4, 64, device="cuda"))
+    return a, b, c, d
+
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = calls()
+g.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in got]
+mass.zero_()
+want = calls()
+torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(got, want))
+print("same")
+""" % (os.path.dirname(os.path.dirname(os.path.abspath(__file__))), os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stdout + r.stderr[-2000:]
