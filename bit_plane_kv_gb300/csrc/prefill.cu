@@ -63,6 +63,7 @@ struct alignas(16) Work {
     int t0;         // first token; tile w starts at t0 + w * (128 / gp)
     int nt0, nt1;   // steps of 128 keys of the two tiles
     int steps;      // the larger; -1: no more work
+    int from;       // keys of the sequence before k0 (kSplit: the shares of other CTAs)
     int half;       // bit w: tile w's last step has 64 keys or fewer and is worked on as half a step
 };
 
@@ -86,11 +87,78 @@ __device__ unsigned g_wait_expired;
 struct PrefillArgs {
     int seqs, heads, kv_heads, D, total_q, total_k, gp, lg_gp, groups, tiles;
     int split;  // CTAs that share a work item's keys
-    int64_t out_token, out_head;
+    int64_t out_token, out_head, q_token, q_head, k_token, k_head, v_token, v_head;
     const int32_t *cu_q, *cu_k;
+    const uint16_t *q, *k, *v;   // for rows that are computed again (below)
     void *out;
     float *lse;
 };
+
+// ---------------------------------------------------------------- rows behind a query
+// P V runs over whole tiles, so a value row that a query does not see enters its sums
+// with the weight 0, and 0 x NaN is NaN.  A row whose result is not finite is therefore
+// looked at again: where a value row behind it, near enough to have been in one of its
+// tiles, holds a NaN or an infinity in a channel that the rows it sees just before do
+// not, the row is computed anew, key by key, by its own thread.
+struct PlainRow {
+    const uint16_t *q, *k, *v;   // the query row, and the sequence's first key and value row
+    int64_t k_token, v_token;
+    int D, seen, lk;
+    uint16_t *out;
+};
+
+template <int kDtype>
+__device__ __forceinline__ float wide(uint16_t x) {
+    return kDtype == FATHOM_BF16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x));
+}
+
+// Channels with a NaN or an infinity in value rows j0 .. j1 - 1.
+template <int kDtype>
+__device__ void odd_channels(const PlainRow &p, int j0, int j1, uint32_t (&odd)[FATHOM_MAX_D / 32]) {
+    constexpr uint32_t kTop = kDtype == FATHOM_BF16 ? 0x7f80u : 0x7c00u;   // the exponent of NaN and infinity
+    for (int i = 0; i < FATHOM_MAX_D / 32; ++i) odd[i] = 0;
+    for (int j = j0; j < j1; ++j)
+        for (int c = 0; c < p.D; c += 8) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p.v + j * p.v_token + c);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            for (int e = 0; e < 8; ++e)
+                if ((w[e / 2] >> (e % 2 * 16) & kTop) == kTop) odd[c / 32] |= 1u << (c % 32 + e);
+        }
+}
+
+template <int kDtype>
+__device__ __noinline__ bool tainted(const PlainRow &p) {
+    uint32_t behind[FATHOM_MAX_D / 32], before[FATHOM_MAX_D / 32];
+    odd_channels<kDtype>(p, p.seen, min(p.lk, p.seen + 2 * kKeys), behind);
+    uint32_t any = 0;
+    for (uint32_t x : behind) any |= x;
+    if (!any) return false;
+    odd_channels<kDtype>(p, max(p.seen - kKeys, 0), p.seen, before);
+    any = 0;
+    for (int i = 0; i < FATHOM_MAX_D / 32; ++i) any |= behind[i] & ~before[i];
+    return any != 0;
+}
+
+// The row from the formula, in fp32; returns its log-sum-exp.
+template <int kDtype>
+__device__ __noinline__ float plain_row(const PlainRow &p) {
+    const float scale = 1.0f / sqrtf((float)p.D);
+    float m = -CUDART_INF_F, l = 0.0f, o[FATHOM_MAX_D];
+    auto score = [&](int j) {
+        float s = 0.0f;
+        for (int c = 0; c < p.D; ++c) s = fmaf(wide<kDtype>(p.q[c]), wide<kDtype>(p.k[j * p.k_token + c]), s);
+        return s * scale;
+    };
+    for (int j = 0; j < p.seen; ++j) m = fmaxf(m, score(j));
+    for (int c = 0; c < p.D; ++c) o[c] = 0.0f;
+    for (int j = 0; j < p.seen; ++j) {
+        const float w = expf(score(j) - m);
+        l += w;
+        for (int c = 0; c < p.D; ++c) o[c] = fmaf(w, wide<kDtype>(p.v[j * p.v_token + c]), o[c]);
+    }
+    for (int c = 0; c < p.D; ++c) p.out[c] = (uint16_t)pack2<kDtype>(o[c] / l, 0.0f);
+    return m + logf(l);
+}
 
 __device__ __forceinline__ int clamp_to(int x, int hi) { return min(max(x, 0), hi); }
 
@@ -180,7 +248,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             }
             seen_before = __shfl_sync(0xffffffffu, upto, 31);
         }
-        g.lq = g.nt0 = g.nt1 = g.steps = g.q0 = g.k0 = g.lk = g.off = g.t0 = g.half = 0;
+        g.lq = g.nt0 = g.nt1 = g.steps = g.q0 = g.k0 = g.lk = g.off = g.t0 = g.from = g.half = 0;
         if (seq < 0) return g;   // the grid counts one tile more per sequence than most need
         g.q0 = clamp_to(a.cu_q[seq], a.total_q);
         g.lq = clamp_to(a.cu_q[seq + 1], a.total_q) - g.q0;
@@ -204,6 +272,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             g.nt0 = min(max(g.nt0 - from, 0), to - from);
             g.nt1 = min(max(g.nt1 - from, 0), to - from);
             g.steps = max(g.nt0, g.nt1);
+            g.from = from * kKeys;
             g.k0 += from * kKeys;
             g.lk -= from * kKeys;
             g.off -= from * kKeys;
@@ -221,7 +290,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const int *f = &sm.work[slot].group;
         auto field = [&](int i) { return __shfl_sync(0xffffffffu, f[i], 0); };
         g.group = field(0); g.q0 = field(1); g.lq = field(2); g.k0 = field(3); g.lk = field(4);
-        g.off = field(5); g.t0 = field(6); g.nt0 = field(7); g.nt1 = field(8); g.steps = field(9); g.half = field(10);
+        g.off = field(5); g.t0 = field(6); g.nt0 = field(7); g.nt1 = field(8); g.steps = field(9);
+        g.from = field(10); g.half = field(11);
         if (lane == 0) mbar_arrive(smem_addr(&sm.work_empty[slot]));
         ++round;
         return ok && g.steps >= 0;
@@ -568,6 +638,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 const float inv = l > 0.0f ? own / l : 0.0f, inv_other = l > 0.0f ? 1.0f / l : 0.0f;
                 const bool some = kSplit ? own != 0.0f && nt > 0 : seen > 0;   // O holds something for this row
                 const int row_at = mine ? at : -1;
+                float2 odd = make_float2(0.0f, 0.0f);   // 0 as long as the row is finite
                 unsigned char *stage = sm.out[warp];
                 // 64 channels at a time through shared memory, so that a store writes four whole lines and
                 // not 32 pieces of as many rows
@@ -588,6 +659,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         }
                         x[i] = __float_as_uint(v);
                     }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        odd = fma2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                                   make_float2(0.0f, 0.0f), odd);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t pk[4];
@@ -612,9 +687,21 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         __syncwarp();
                     }
                 }
+                float again = 0.0f;
+                bool odd_row = mine && !(odd.x + odd.y == 0.0f);
+                if (odd_row) {
+                    const int hk = head / (a.heads / a.kv_heads);
+                    const int64_t first = g.k0 - g.from;
+                    const PlainRow p = {a.q + (int64_t)at * a.q_token + head * a.q_head, a.k + first * a.k_token + hk * a.k_head,
+                                        a.v + first * a.v_token + hk * a.v_head, a.k_token, a.v_token, a.D, seen + g.from,
+                                        g.lk + g.from, (uint16_t *)a.out + (int64_t)at * a.out_token + head * a.out_head};
+                    odd_row = p.seen > 0 && tainted<kDtype>(p);
+                    if (odd_row) again = plain_row<kDtype>(p);
+                }
+                __syncwarp();
                 if (mine && a.lse)
                     a.lse[(int64_t)at * a.heads + head] =
-                        (kSplit ? l > 0.0f : seen > 0) ? ((m - kShift) + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+                        odd_row ? again : (kSplit ? l > 0.0f : seen > 0) ? ((m - kShift) + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
                 tc_fence_before();
             }
         }
@@ -707,6 +794,9 @@ int launch_prefill_attn(const fathom_prompts &p, const void *q, const void *k, c
     a.gp = 1 << a.lg_gp;
     a.groups = p.heads / a.gp;
     a.out_token = p.out_token; a.out_head = p.out_head;
+    a.q_token = p.q_token; a.q_head = p.q_head; a.k_token = p.k_token; a.k_head = p.k_head;
+    a.v_token = p.v_token; a.v_head = p.v_head;
+    a.q = (const uint16_t *)q; a.k = (const uint16_t *)k; a.v = (const uint16_t *)v;
     a.cu_q = cu_q; a.cu_k = cu_k; a.out = out; a.lse = lse;
     const long long tiles = ((long long)p.total_q * a.gp + 2 * kRows - 1) / (2 * kRows) + p.seqs;
     if (tiles * a.groups > 0x7fffffffLL) { set_error("prefill_attn: too many rows for one launch"); return FATHOM_EINVAL; }

@@ -24,8 +24,9 @@
  *   synchronisation, no host read of device results.  Results are valid once
  *   the stream reaches them.  The kernels of fathom_plan, fathom_plan_fixed,
  *   fathom_scan_topk, fathom_scan, fathom_select, fathom_exact_topk, fathom_sparse_attn,
- *   fathom_sparse_attn_planes and fathom_sparse_attn_noalloc are launched with
- *   programmatic stream serialisation: each may be scheduled while the work before it on
+ *   fathom_sparse_attn_planes, fathom_sparse_attn_noalloc, fathom_paged_attn and
+ *   fathom_paged_evict are launched with programmatic stream serialisation: each may
+ *   be scheduled while the work before it on
  *   the stream is finishing, but it waits for that work to complete before
  *   it reads or writes memory, so the stream order is unchanged.
  * - Every call returns a fathom_status.  Argument errors return FATHOM_EINVAL
@@ -489,9 +490,9 @@ int fathom_sparse_attn_noalloc(const fathom_shape *shape, const uint16_t *k_rows
  *   cu_q, cu_k [seqs + 1] int32, ascending from 0 (device); values are clamped
  *   to [0, total], and rows of out behind cu_q[seqs] are left as they were
  *   lse_opt NULL, or [total_q][heads] fp32 (out)
- * Rows behind a sequence's end (padding, other sequences) never reach its
- * outputs, whatever they hold; a NaN or infinity in a value row j of the
- * sequence itself may reach every query of it. */
+ * Key and value rows that a query does not see (later tokens, other sequences,
+ * padding) never reach its outputs, whatever they hold, NaN and infinities
+ * included. */
 int fathom_prefill_attn(const fathom_prompts *prompts, const void *q, const void *k, const void *v,
                         const int32_t *cu_q, const int32_t *cu_k, void *out, float *lse_opt, void *stream);
 

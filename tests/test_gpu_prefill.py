@@ -169,6 +169,35 @@ def test_rows_of_others_never_reach_a_sequence(bad):
     assert torch.equal(out[:100], want[:100])
 
 
+@pytest.mark.parametrize("lq,lk,H,Hkv,D,dt", [([300], [300], 4, 1, 128, BF), ([130], [200], 2, 2, 64, FP),
+                                              ([5], [5000], 4, 2, 96, BF), ([40, 260], [40, 260], 3, 1, 72, FP)])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_rows_behind_a_query_never_reach_it(lq, lk, H, Hkv, D, dt, what):
+    """NaN and infinities in keys and values of the sequence itself: only the queries that see them change,
+    and of those, for a value, only its channel."""
+    q, k, v = inputs(lq, lk, H, Hkv, D, dt)
+    o, z, tol, tol_z = P.prefill(q, k, v, lq, lk, D)
+    ends = torch.tensor([sum(lk[: i + 1]) for i in range(len(lk))])
+    first_q = sum(lq[:-1])
+    bad = [(int(ends[-1]) - 3, 0, float("nan")), (int(ends[-1]) - 70, D - 1, float("inf"))]     # of the last sequence
+    for row, channel, x in bad:
+        (k if what == "k" else v)[row, 0, channel] = x
+    out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated(lq), P.cumulated(lk), want_lse=True)
+    # the first query that sees each of them
+    sees = [max(first_q, first_q + lq[-1] - (int(ends[-1]) - row)) for row, _, _ in bad]
+    clean = torch.ones_like(out, dtype=torch.bool)
+    for t, (_, channel, _) in zip(sees, bad):
+        hit = slice(0, H // Hkv)                                       # the query heads of KV head 0
+        if what == "k":
+            clean[t:, hit] = False
+        else:
+            assert not torch.isfinite(out[t:, hit, channel]).any()
+            clean[t:, hit, channel] = False
+    assert bool(((out.double() - o).abs() <= tol)[clean].all())
+    rows = clean.any(2)
+    assert bool(((lse.double() - z).abs() <= tol_z)[rows].all())
+
+
 def test_lengths_are_clamped_to_the_arrays():
     q, k, v = inputs([50, 50], [50, 50], 4, 2, 128, BF)
     want, _ = B.fathom_prefill_attn(q, k, v, P.cumulated([50, 50]))
