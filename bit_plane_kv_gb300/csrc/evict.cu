@@ -1,11 +1,11 @@
 // evict.cu -- eviction from a paged KV cache by accumulated attention weight:
 // the kept set of every unit, then its rows and mass moved together.
 // Measured, 128 channels, bf16: 256 units of up to 16k tokens cut back to 4096 each
-// 27 us (the kept sets) + 205 us (the move: 1.0 GB in rows of 256 bytes, 2 KB apart,
-// 4.9 TB/s); 8 units of 8192 tokens cut to 2048 14 + 17 us (latency: a chunk's three
-// dependent lookups and its copy).  For the move, twice the loads in flight from a
-// pipelined loop (220 us) and bulk copies through shared memory (210 us; 76 us for the
-// 8 units) were no faster; fewer resident threads were slower (128 per CTA: 330 us).
+// 26 us (the kept sets) + 167 us (the move to other pages: 1.0 GB in rows of 256 bytes,
+// 2 KB apart, 6.0 TB/s); 8 units of 8192 tokens cut to 2048 14 + 7 us.  In place the
+// move takes 205 and 17 us: it has an order to keep.  Tried for that order: twice the
+// loads in flight from a pipelined loop (220 us), bulk copies through shared memory
+// (210 us; 76 us for the 8 units).
 #include "fathom_internal.cuh"
 
 namespace fathom {
@@ -108,16 +108,18 @@ evict_select_kernel(fathom_pages p, const int32_t *__restrict__ lens, const floa
     }
 }
 
-// Moves kept rows in ascending order.  CTA (x, u): x < 2 slices, channels of
-// slice x / 2 of unit u's K (x even) or V rows; x == 2 slices, the unit's mass.
-// Row j goes to position j and comes from position kept[j] >= j, so in place a
-// write can only hit a source of the same or an earlier row: the CTA loads a
-// chunk of rows, meets at the barrier and then stores the chunk, and the next
-// chunk's loads, which lie behind every row stored so far, are issued before.
+// CTA (x, u), the last x: unit u's mass.  The others: its rows, in one of two ways.
+//
+// To other pages (no destination page is the source page of the same place): the x-th,
+// (x + CTAs)-th, ... chunk of rows, K and V together, in any order.
+//
+// In place: channels of slice x / 2 of K (x even) or V, x < 2 slices, chunk after chunk.
+// Row j goes to position j and comes from position kept[j] >= j, so a write can only
+// hit a source of the same or an earlier row: the CTA loads a chunk of rows, meets at
+// the barrier and then stores the chunk.
 constexpr int kMoveThreads = 256, kMoveUnroll = 8;
 
-
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kMoveThreads, 4)
 evict_move_kernel(fathom_pages p, int lg, int slices, int4 *kp, int4 *vp, const int32_t *__restrict__ table,
                   const int32_t *__restrict__ lens, int keep, const int32_t *__restrict__ dst_table, int dst_pages,
                   const int32_t *kept, const float *mass, size_t mass_stride, float *mass_out, size_t out_stride) {
@@ -125,7 +127,7 @@ evict_move_kernel(fathom_pages p, int lg, int slices, int4 *kp, int4 *vp, const 
     const int u = blockIdx.y, s = u / p.kv_heads, h = u % p.kv_heads, tid = threadIdx.x;
     const int n = min(min(max(lens[s], 0), p.max_pages << lg), keep);
     const int32_t *kr = kept + (size_t)u * keep;
-    if ((int)blockIdx.x == 2 * slices) {
+    if (blockIdx.x == gridDim.x - 1) {
         const float *mr = mass + u * mass_stride;
         float *mo = mass_out + u * out_stride;
         for (int j0 = 0; j0 < n; j0 += kMoveThreads * kMoveUnroll) {
@@ -144,33 +146,66 @@ evict_move_kernel(fathom_pages p, int lg, int slices, int4 *kp, int4 *vp, const 
         }
         return;
     }
+    const int32_t *ta = table + (size_t)s * p.max_pages, *tb = dst_table + (size_t)s * dst_pages;
+    const int64_t head = h * p.head_stride;
+    const int pieces = p.D / 8;   // 16-byte pieces of a row
+    // where row j of the kept ones lies and goes, in pieces; false: nowhere, or it is there already
+    auto place = [&](int j, int i, int64_t &src, int64_t &dst) {
+        const int a = ta[i >> lg], b = tb[j >> lg];
+        if (a < 0 || a >= p.num_pages || b < 0 || b >= p.num_pages) return false;
+        src = (a * p.page_stride + head + (i & (p.page_tokens - 1)) * p.token_stride) / 8;
+        dst = (b * p.page_stride + head + (j & (p.page_tokens - 1)) * p.token_stride) / 8;
+        return src != dst;
+    };
+    bool same = false;
+    for (int q = tid; q < min(p.max_pages, (n + p.page_tokens - 1) >> lg); q += kMoveThreads) same |= ta[q] == tb[q];
+    if (!__syncthreads_or(same)) {
+        constexpr int kRowsUnroll = kMoveUnroll / 2;
+        const int R = kMoveThreads / pieces, r = tid / pieces, c = tid % pieces;   // rows per step
+        const int chunk = R * kRowsUnroll;
+        if (r >= R) return;
+        for (int j0 = blockIdx.x * chunk; j0 < n; j0 += chunk * (gridDim.x - 1)) {
+            int4 x[kRowsUnroll], y[kRowsUnroll];
+            int64_t to[kRowsUnroll];
+            int i[kRowsUnroll];
+#pragma unroll
+            for (int e = 0; e < kRowsUnroll; ++e) {
+                const int j = j0 + e * R + r;
+                i[e] = j < n ? kr[j] : -1;
+            }
+#pragma unroll
+            for (int e = 0; e < kRowsUnroll; ++e) {
+                int64_t src;
+                if (i[e] < 0 || !place(j0 + e * R + r, i[e], src, to[e])) { to[e] = -1; continue; }
+                x[e] = kp[src + c];
+                y[e] = vp[src + c];
+            }
+#pragma unroll
+            for (int e = 0; e < kRowsUnroll; ++e)
+                if (to[e] >= 0) { kp[to[e] + c] = x[e]; vp[to[e] + c] = y[e]; }
+        }
+        return;
+    }
+    if ((int)blockIdx.x >= 2 * slices) return;
     int4 *rows = (blockIdx.x & 1) ? vp : kp;
-    const int pieces = p.D / 8, per = (pieces + slices - 1) / slices;   // 16-byte pieces of a row, and per slice
+    const int per = (pieces + slices - 1) / slices;   // pieces of a slice
     const int c0 = (blockIdx.x >> 1) * per, pc = min(per, pieces - c0);
     if (pc <= 0) return;
-    const int R = kMoveThreads / pc, r = tid / pc, c = c0 + tid % pc;   // rows per step
-    const int64_t head = h * p.head_stride;
+    const int R = kMoveThreads / pc, r = tid / pc, c = c0 + tid % pc;
     for (int j0 = 0; j0 < n; j0 += R * kMoveUnroll) {
         int4 x[kMoveUnroll];
         int64_t to[kMoveUnroll];
 #pragma unroll
         for (int e = 0; e < kMoveUnroll; ++e) {
             const int j = j0 + e * R + r;
-            to[e] = -1;
-            if (r < R && j < n) {
-                const int i = kr[j];
-                const int a = table[(size_t)s * p.max_pages + (i >> lg)], b = dst_table[(size_t)s * dst_pages + (j >> lg)];
-                if (a >= 0 && a < p.num_pages && b >= 0 && b < p.num_pages) {
-                    const int64_t src = (a * p.page_stride + head + (i & (p.page_tokens - 1)) * p.token_stride) / 8 + c;
-                    const int64_t dst = (b * p.page_stride + head + (j & (p.page_tokens - 1)) * p.token_stride) / 8 + c;
-                    if (src != dst) { x[e] = rows[src]; to[e] = dst; }
-                }
-            }
+            int64_t src;
+            if (r >= R || j >= n || !place(j, kr[j], src, to[e])) { to[e] = -1; continue; }
+            x[e] = rows[src + c];
         }
         __syncthreads();
 #pragma unroll
         for (int e = 0; e < kMoveUnroll; ++e)
-            if (to[e] >= 0) rows[to[e]] = x[e];
+            if (to[e] >= 0) rows[to[e] + c] = x[e];
     }
 }
 
@@ -188,9 +223,14 @@ int launch_paged_evict(const fathom_pages &p, void *kp, void *vp, const int32_t 
     if (e != cudaSuccess) { set_error("evict_select_kernel: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }
     int sms = device_sm_count();
     if (sms <= 0) sms = 152;
-    int slices = 1;   // of a row, 32 bytes at least, until the CTAs fill the device
+    int slices = 1;   // of a row, 32 bytes at least, until the CTAs fill the device (in place)
     while (2 * slices <= p.D / 16 && 2LL * units * slices < 2LL * sms) slices *= 2;
-    e = launch_pdl(evict_move_kernel, dim3(2 * slices + 1, units), dim3(kMoveThreads), 0, st, p, lg, slices,
+    // CTAs per unit: those, or more until two waves of four per SM have work (to other pages)
+    const int chunk = kMoveThreads / (p.D / 8) * (kMoveUnroll / 2), chunks = (keep + chunk - 1) / chunk;
+    int ctas = (8 * sms + units - 1) / units;
+    ctas = ctas > chunks ? chunks : ctas;
+    ctas = ctas < 2 * slices ? 2 * slices : ctas;
+    e = launch_pdl(evict_move_kernel, dim3(ctas + 1, units), dim3(kMoveThreads), 0, st, p, lg, slices,
                    (int4 *)kp, (int4 *)vp, table, lens, keep, dst_table, dst_pages, (const int32_t *)kept, mass,
                    mass_stride, mass_out, mass_out_stride);
     if (e != cudaSuccess) { set_error("evict_move_kernel: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }

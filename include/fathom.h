@@ -540,9 +540,10 @@ int fathom_paged_attn(const fathom_pages *pages, int32_t G, const float *q, cons
  * sequence of at most `keep` tokens keeps them all.  The units of a sequence
  * keep different tokens.
  *   mass [units][mass_stride] fp32, mass_stride >= max_pages * page_tokens
- *   dst_table [seqs][dst_pages] int32, dst_pages * page_tokens >= keep: either pages
- *   that no table row names, or page_table itself (in place: the rows move down
- *   within the sequence's own pages); no page may belong to two sequences
+ *   dst_table [seqs][dst_pages] int32, dst_pages * page_tokens >= keep: for each
+ *   sequence either pages that no table row names, or the first pages of its row of
+ *   page_table (in place: the rows move down within the sequence's own pages;
+ *   page_table itself will do); no page may belong to two sequences
  *   kept_idx [units][keep] int32 (out): the kept tokens, ascending, then -1
  *   lens_out [seqs] int32 (out, not lens): min(lens[s], keep)
  *   mass_out [units][mass_out_stride] fp32 (out), mass_out_stride >= keep: may be

@@ -269,7 +269,9 @@ def evict_and_check(lens, H, D, page, keep, ns, nr, dt, mass, in_place, layout="
     seqs, per = len(lens), mass.shape[1] // page
     dp = -(-keep // page)
     kp, vp, table, free = P.pool(seqs, H, D, page, per, dt, extra=seqs * dp, layout=layout)
-    dst = table if in_place else free.reshape(seqs, dp).contiguous()
+    dst = free.reshape(seqs, dp).contiguous()
+    if in_place:      # the table itself, or a copy of as much of it as the kept rows need
+        dst = table if in_place is True else table[:, :dp].contiguous()
     k0, v0, m0 = kp.clone(), vp.clone(), mass.clone()
     out = None if in_place else torch.full((seqs * H, keep + 3), -2.0, device="cuda")
     pages = B.make_pages(kp, table)
@@ -303,7 +305,7 @@ def masses(units, cap, seed=0):
     return m
 
 
-@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("in_place", [False, True, "a copy of the table"])
 @pytest.mark.parametrize("lens,H,D,page,keep,ns,nr,dt", [
     ([500, 64, 65, 0, 1, 40], 2, 128, 16, 64, 4, 32, BF),
     ([3000, 2999], 3, 128, 64, 1000, 4, 32, FP),
@@ -319,7 +321,7 @@ def test_eviction_keeps_and_moves_what_the_plain_form_does(lens, H, D, page, kee
     evict_and_check(lens, H, D, page, keep, ns, nr, dt, masses(len(lens) * H, per * page), in_place)
 
 
-@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("in_place", [False, True, "a copy of the table"])
 def test_many_units_and_the_head_major_layout(in_place):
     lens = [100 + 13 * i for i in range(40)]
     evict_and_check(lens, 8, 64, 16, 150, 4, 32, BF, masses(320, 640), in_place, layout="head")
