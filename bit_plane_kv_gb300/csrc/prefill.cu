@@ -143,20 +143,26 @@ __device__ __noinline__ bool tainted(const PlainRow &p) {
 template <int kDtype>
 __device__ __noinline__ float plain_row(const PlainRow &p) {
     const float scale = 1.0f / sqrtf((float)p.D);
-    float m = -CUDART_INF_F, l = 0.0f, o[FATHOM_MAX_D];
+    float m = -CUDART_INF_F, l = 0.0f;
     auto score = [&](int j) {
         float s = 0.0f;
         for (int c = 0; c < p.D; ++c) s = fmaf(wide<kDtype>(p.q[c]), wide<kDtype>(p.k[j * p.k_token + c]), s);
         return s * scale;
     };
     for (int j = 0; j < p.seen; ++j) m = fmaxf(m, score(j));
-    for (int c = 0; c < p.D; ++c) o[c] = 0.0f;
-    for (int j = 0; j < p.seen; ++j) {
-        const float w = expf(score(j) - m);
-        l += w;
-        for (int c = 0; c < p.D; ++c) o[c] = fmaf(w, wide<kDtype>(p.v[j * p.v_token + c]), o[c]);
+    for (int j = 0; j < p.seen; ++j) l += expf(score(j) - m);
+    for (int c0 = 0; c0 < p.D; c0 += 16) {   // 16 channels at a time, in registers
+        float o[16] = {};
+        for (int j = 0; j < p.seen; ++j) {
+            const float w = expf(score(j) - m);
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                if (c0 + c < p.D) o[c] = fmaf(w, wide<kDtype>(p.v[j * p.v_token + c0 + c]), o[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            if (c0 + c < p.D) p.out[c0 + c] = (uint16_t)pack2<kDtype>(o[c] / l, 0.0f);
     }
-    for (int c = 0; c < p.D; ++c) p.out[c] = (uint16_t)pack2<kDtype>(o[c] / l, 0.0f);
     return m + logf(l);
 }
 
