@@ -375,7 +375,7 @@ extern "C" {
 
 const char *fathom_last_error(void) { return g_err; }
 
-const char *fathom_version(void) { return "fathom-gb300 0.2 (sm_103a)"; }
+const char *fathom_version(void) { return "fathom-gb300 0.3 (sm_103a)"; }
 
 int fathom_debug_status(int mode, uint64_t *first_failure) {
     g_err[0] = 0;
