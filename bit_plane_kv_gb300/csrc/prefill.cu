@@ -96,10 +96,10 @@ struct PrefillArgs {
 
 // ---------------------------------------------------------------- rows behind a query
 // P V runs over whole tiles, so a value row that a query does not see enters its sums
-// with the weight 0, and 0 x NaN is NaN.  A row whose result is not finite is therefore
-// looked at again: where a value row behind it, near enough to have been in one of its
-// tiles, holds a NaN or an infinity in a channel that the rows it sees just before do
-// not, the row is computed anew, key by key, by its own thread.
+// with the weight 0, and 0 x NaN and 0 x infinity are NaN.  A row whose result is not
+// finite is therefore looked at again: where a value row behind it, near enough to have
+// been in one of its tiles, holds a NaN or an infinity in a channel in which no row that
+// it sees just before holds a NaN, the row is computed anew by its warp.
 struct PlainRow {
     const uint16_t *q, *k, *v;   // the query row, and the sequence's first key and value row
     int64_t k_token, v_token;
@@ -112,58 +112,108 @@ __device__ __forceinline__ float wide(uint16_t x) {
     return kDtype == FATHOM_BF16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x));
 }
 
-// Channels with a NaN or an infinity in value rows j0 .. j1 - 1.
-template <int kDtype>
+// Channels with a NaN (or, kInf, an infinity) in value rows j0 .. j1 - 1.
+template <int kDtype, bool kInf>
 __device__ void odd_channels(const PlainRow &p, int j0, int j1, uint32_t (&odd)[FATHOM_MAX_D / 32]) {
-    constexpr uint32_t kTop = kDtype == FATHOM_BF16 ? 0x7f80u : 0x7c00u;   // the exponent of NaN and infinity
+    constexpr uint32_t kTop = kDtype == FATHOM_BF16 ? 0x7f80u : 0x7c00u;   // infinity; a NaN is larger
     for (int i = 0; i < FATHOM_MAX_D / 32; ++i) odd[i] = 0;
     for (int j = j0; j < j1; ++j)
         for (int c = 0; c < p.D; c += 8) {
             const uint4 v = *reinterpret_cast<const uint4 *>(p.v + j * p.v_token + c);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            for (int e = 0; e < 8; ++e)
-                if ((w[e / 2] >> (e % 2 * 16) & kTop) == kTop) odd[c / 32] |= 1u << (c % 32 + e);
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t x = w[e / 2] >> (e % 2 * 16) & 0x7fffu;
+                if (kInf ? x >= kTop : x > kTop) odd[c / 32] |= 1u << (c % 32 + e);
+            }
         }
 }
 
 template <int kDtype>
-__device__ __noinline__ bool tainted(const PlainRow &p) {
+__device__ bool tainted(const PlainRow &p) {
     uint32_t behind[FATHOM_MAX_D / 32], before[FATHOM_MAX_D / 32];
-    odd_channels<kDtype>(p, p.seen, min(p.lk, p.seen + 2 * kKeys), behind);
+    odd_channels<kDtype, true>(p, p.seen, min(p.lk, p.seen + 2 * kKeys), behind);
     uint32_t any = 0;
     for (uint32_t x : behind) any |= x;
     if (!any) return false;
-    odd_channels<kDtype>(p, max(p.seen - kKeys, 0), p.seen, before);
+    odd_channels<kDtype, false>(p, max(p.seen - kKeys, 0), p.seen, before);
     any = 0;
     for (int i = 0; i < FATHOM_MAX_D / 32; ++i) any |= behind[i] & ~before[i];
     return any != 0;
 }
 
-// The row from the formula, in fp32; returns its log-sum-exp.
+// The row from the formula, in fp32, by a whole warp: 32 keys at a time, a key's score
+// per lane, then four channels per lane.  Returns the row's log-sum-exp.
 template <int kDtype>
-__device__ __noinline__ float plain_row(const PlainRow &p) {
+__device__ float plain_row(const PlainRow &p, int lane) {
     const float scale = 1.0f / sqrtf((float)p.D);
-    float m = -CUDART_INF_F, l = 0.0f;
-    auto score = [&](int j) {
-        float s = 0.0f;
-        for (int c = 0; c < p.D; ++c) s = fmaf(wide<kDtype>(p.q[c]), wide<kDtype>(p.k[j * p.k_token + c]), s);
-        return s * scale;
-    };
-    for (int j = 0; j < p.seen; ++j) m = fmaxf(m, score(j));
-    for (int j = 0; j < p.seen; ++j) l += expf(score(j) - m);
-    for (int c0 = 0; c0 < p.D; c0 += 16) {   // 16 channels at a time, in registers
-        float o[16] = {};
-        for (int j = 0; j < p.seen; ++j) {
-            const float w = expf(score(j) - m);
+    float m = -CUDART_INF_F, l = 0.0f, o[4] = {};
+    for (int j0 = 0; j0 < p.seen; j0 += 32) {
+        const int n = min(p.seen - j0, 32);
+        float s = -CUDART_INF_F;
+        if (lane < n) {
+            const uint16_t *k = p.k + (j0 + lane) * p.k_token;
+            s = 0.0f;
+            for (int c = 0; c < p.D; c += 8) {
+                const uint4 a = *reinterpret_cast<const uint4 *>(p.q + c), b = *reinterpret_cast<const uint4 *>(k + c);
+                const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-                if (c0 + c < p.D) o[c] = fmaf(w, wide<kDtype>(p.v[j * p.v_token + c0 + c]), o[c]);
+                for (int e = 0; e < 4; ++e) {
+                    s = fmaf(wide<kDtype>((uint16_t)x[e]), wide<kDtype>((uint16_t)y[e]), s);
+                    s = fmaf(wide<kDtype>((uint16_t)(x[e] >> 16)), wide<kDtype>((uint16_t)(y[e] >> 16)), s);
+                }
+            }
+            s *= scale;
         }
+        float top = s;
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
-            if (c0 + c < p.D) p.out[c0 + c] = (uint16_t)pack2<kDtype>(o[c] / l, 0.0f);
+        for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+        top = fmaxf(top, m);
+        const float base = top == -CUDART_INF_F ? 0.0f : top, f = expf(m - base);
+        m = top;
+        const float w = expf(s - base);
+        float sum = w;
+#pragma unroll
+        for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+        l = fmaf(l, f, sum);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] *= f;
+        for (int e = 0; e < n; ++e) {
+            const float we = __shfl_sync(0xffffffffu, w, e);
+            if (4 * lane < p.D) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(p.v + (j0 + e) * p.v_token + 4 * lane);
+                o[0] = fmaf(we, wide<kDtype>((uint16_t)x.x), o[0]);
+                o[1] = fmaf(we, wide<kDtype>((uint16_t)(x.x >> 16)), o[1]);
+                o[2] = fmaf(we, wide<kDtype>((uint16_t)x.y), o[2]);
+                o[3] = fmaf(we, wide<kDtype>((uint16_t)(x.y >> 16)), o[3]);
+            }
+        }
     }
+    if (4 * lane < p.D)
+        *reinterpret_cast<uint2 *>(p.out + 4 * lane) =
+            make_uint2(pack2<kDtype>(o[0] / l, o[1] / l), pack2<kDtype>(o[2] / l, o[3] / l));
     return m + logf(l);
+}
+
+// The warp's rows (lane: row `at` of out, `head`, `seen` keys of the sequence's lk, which
+// start at k0; odd: not finite) looked at again; returns the lane's log-sum-exp.
+template <int kDtype>
+__device__ __noinline__ float odd_rows(const PrefillArgs &a, int k0, int lk, int at, int head, int seen, bool odd,
+                                       float lse) {
+    const int lane = threadIdx.x & 31;
+    auto row = [&](int t, int h, int n) {
+        const int hk = h / (a.heads / a.kv_heads);
+        return PlainRow{a.q + (int64_t)t * a.q_token + h * a.q_head, a.k + (int64_t)k0 * a.k_token + hk * a.k_head,
+                        a.v + (int64_t)k0 * a.v_token + hk * a.v_head, a.k_token, a.v_token, a.D, n, lk,
+                        (uint16_t *)a.out + (int64_t)t * a.out_token + h * a.out_head};
+    };
+    odd = odd && seen > 0 && tainted<kDtype>(row(at, head, seen));
+    for (unsigned todo = __ballot_sync(0xffffffffu, odd); todo; todo &= todo - 1) {
+        const int src = __ffs(todo) - 1;
+        const float z = plain_row<kDtype>(row(__shfl_sync(0xffffffffu, at, src), __shfl_sync(0xffffffffu, head, src),
+                                              __shfl_sync(0xffffffffu, seen, src)), lane);
+        if (lane == src) lse = z;
+    }
+    return lse;
 }
 
 __device__ __forceinline__ int clamp_to(int x, int hi) { return min(max(x, 0), hi); }
@@ -178,7 +228,7 @@ __device__ __forceinline__ int clamp_to(int x, int hi) { return min(max(x, 0), h
 template <int kSteps, int kDtype, bool kSplit>
 __global__ void __launch_bounds__(kPrefillThreads, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-               const __grid_constant__ CUtensorMap map_v, const PrefillArgs a) {
+               const __grid_constant__ CUtensorMap map_v, const __grid_constant__ PrefillArgs a) {
     constexpr int kPanels = (kSteps + 3) / 4;
     using Smem = PrefillSmem<kPanels>;
     constexpr int kStages = Smem::kStages;
@@ -693,21 +743,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         __syncwarp();
                     }
                 }
-                float again = 0.0f;
-                bool odd_row = mine && !(odd.x + odd.y == 0.0f);
-                if (odd_row) {
-                    const int hk = head / (a.heads / a.kv_heads);
-                    const int64_t first = g.k0 - g.from;
-                    const PlainRow p = {a.q + (int64_t)at * a.q_token + head * a.q_head, a.k + first * a.k_token + hk * a.k_head,
-                                        a.v + first * a.v_token + hk * a.v_head, a.k_token, a.v_token, a.D, seen + g.from,
-                                        g.lk + g.from, (uint16_t *)a.out + (int64_t)at * a.out_token + head * a.out_head};
-                    odd_row = p.seen > 0 && tainted<kDtype>(p);
-                    if (odd_row) again = plain_row<kDtype>(p);
-                }
+                float lse = (kSplit ? l > 0.0f : seen > 0) ? ((m - kShift) + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+                const bool odd_row = mine && !(odd.x + odd.y == 0.0f);
+                if (__any_sync(0xffffffffu, odd_row))
+                    lse = odd_rows<kDtype>(a, g.k0 - g.from, g.lk + g.from, at, head, seen + g.from, odd_row, lse);
                 __syncwarp();
-                if (mine && a.lse)
-                    a.lse[(int64_t)at * a.heads + head] =
-                        odd_row ? again : (kSplit ? l > 0.0f : seen > 0) ? ((m - kShift) + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+                if (mine && a.lse) a.lse[(int64_t)at * a.heads + head] = lse;
                 tc_fence_before();
             }
         }

@@ -198,6 +198,36 @@ def test_rows_behind_a_query_never_reach_it(lq, lk, H, Hkv, D, dt, what):
     assert bool(((lse.double() - z).abs() <= tol_z)[rows].all())
 
 
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_infinite_values_seen_and_unseen(dt):
+    """A channel that is infinite in every value row: infinite for every query, and never NaN from the rows
+    behind; the other channels are the formula's."""
+    lq, H, Hkv, D = [7, 200, 130], 4, 2, 128
+    q, k, v = inputs(lq, lq, H, Hkv, D, dt, q_scale=0.5)    # weights far from underflow
+    o, z, tol, tol_z = P.prefill(q, k, v, lq, lq, D)
+    v[:, 1, 5], v[:, 1, 64] = float("inf"), float("-inf")
+    out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated(lq), want_lse=True)
+    assert bool((out[:, 2:, 5] == float("inf")).all()) and bool((out[:, 2:, 64] == float("-inf")).all())
+    clean = torch.ones_like(out, dtype=torch.bool)
+    clean[:, 2:, 5] = clean[:, 2:, 64] = False
+    assert bool(((out.double() - o).abs() <= tol)[clean].all())
+    assert bool(((lse.double() - z).abs() <= tol_z).all())
+
+
+@pytest.mark.parametrize("lq", [200, 16])
+def test_an_odd_value_at_the_end_of_a_long_sequence(lq):
+    """The next tokens of a sequence of 100 003, the last of whose values is NaN: the others do not see it."""
+    lk, H, Hkv, D = 100003, 4, 1, 128
+    q, k, v = inputs([lq], [lk], H, Hkv, D, BF)
+    o, z, tol, tol_z = P.prefill(q, k, v, [lq], [lk], D)
+    v[-1, 0, 17] = float("nan")
+    out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated([lq]), P.cumulated([lk]), want_lse=True)
+    assert bool(torch.isnan(out[-1, :, 17]).all())
+    assert bool(((out.double() - o).abs() <= tol)[:-1].all())
+    assert bool(((lse.double() - z).abs() <= tol_z).all())
+    B.fathom_wait_status()
+
+
 def test_lengths_are_clamped_to_the_arrays():
     q, k, v = inputs([50, 50], [50, 50], 4, 2, 128, BF)
     want, _ = B.fathom_prefill_attn(q, k, v, P.cumulated([50, 50]))
