@@ -548,13 +548,13 @@ paged_attn_kernel(const DecArgs a) {
                 for (int w = 0; w < kDecWarps; ++w) {
                     const float4 v = *reinterpret_cast<const float4 *>(&sm.o[w][h][d]);
                     O.x += v.x; O.y += v.y; O.z += v.z; O.w += v.w;
-                    L += sm.m[w][h] == -CUDART_INF_F ? 0.0f : sm.l[w][h] * exp2_fast(sm.m[w][h] - Mh);
+                    L += sm.l[w][h] * (sm.m[w][h] == -CUDART_INF_F ? 0.0f : exp2_fast(sm.m[w][h] - Mh));   // a NaN stays
                 }
                 if (whole) {
                     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
                     float *ou = a.out + (size_t)unit * G * D + e;
                     ou[0] = O.x * inv; ou[1] = O.y * inv; ou[2] = O.z * inv; ou[3] = O.w * inv;
-                    if (kMass && d == 0) a.lse[(size_t)unit * G + h] = L > 0.0f ? Mh + log2f(L) - kUp : 0.0f;
+                    if (kMass && d == 0) a.lse[(size_t)unit * G + h] = L == 0.0f ? 0.0f : Mh + log2f(L) - kUp;
                 } else {
                     *reinterpret_cast<float4 *>(a.part_o + slot * G * D + e) = O;
                     if (d == 0) *reinterpret_cast<float2 *>(a.part_ml + (slot * G + h) * 2) = make_float2(Mh, L);
@@ -647,7 +647,7 @@ paged_attn_kernel(const DecArgs a) {
                         const float L = jn.l[h], inv = L > 0.0f ? 1.0f / L : 0.0f;
                         float *ou = a.out + (size_t)unit * G * D + e;
                         ou[0] = acc[k].x * inv; ou[1] = acc[k].y * inv; ou[2] = acc[k].z * inv; ou[3] = acc[k].w * inv;
-                        if (kMass && e % D == 0) a.lse[(size_t)unit * G + h] = L > 0.0f ? jn.m[h] + log2f(L) - kUp : 0.0f;
+                        if (kMass && e % D == 0) a.lse[(size_t)unit * G + h] = L == 0.0f ? 0.0f : jn.m[h] + log2f(L) - kUp;
                     }
                 }
             }

@@ -340,7 +340,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     int round = 0;
     auto get_work = [&](Work &g) {
         const int slot = round & 1;
-        ok = ok && warp_wait(smem_addr(&sm.work_full[slot]), (round >> 1) & 1);
+        // a tile without keys waits here while the other goes over all of them (2^28 keys: about 3 s)
+        ok = ok && warp_wait(smem_addr(&sm.work_full[slot]), (round >> 1) & 1, 5 * kWaitLimitNs);
         // every field from one lane: the compiler then knows that the warp branches as one (without that the
         // loops below ran 9 % slower)
         const int *f = &sm.work[slot].group;

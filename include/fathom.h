@@ -519,6 +519,9 @@ int fathom_paged_append(const fathom_pages *pages, void *k_pages, void *v_pages,
  * fp32 queries and results as in every decode call; q and the softmax weights
  * enter the tensor cores as sums of pieces of the rows' type, so nothing is
  * rounded to 16 bits.  No atomics on values: the same inputs give the same bits.
+ * Queries and the rows attended to are meant to be finite: a NaN in a unit's query
+ * or keys makes its head's (all its heads') outputs and its mass NaN, one in a value
+ * its channel; an infinity may do the same.  Other units never depend on them.
  *   G query heads per KV head, 1 .. 8
  *   q [units][G][D] fp32, k_pages, v_pages (device or pinned host), page_table,
  *   lens [seqs] int32 (clamped to [0, max_pages * page_tokens]), out [units][G][D]
@@ -565,8 +568,8 @@ size_t fathom_paged_workspace_size(const fathom_pages *pages, int32_t G, int mas
 size_t fathom_workspace_size(const fathom_shape *shape, int which);
 
 /* Bounded device waits: the kernel of fathom_prefill_attn waits for its own
- * asynchronous copies and matrix instructions, each wait at most two seconds; one
- * that runs out ends its CTA without writing the rest of its results and is noted.
+ * asynchronous copies and matrix instructions, each wait at most two seconds (ten
+ * for the next piece of work); one that runs out ends its CTA without writing the rest of its results and is noted.
  * This call synchronises the calling thread's device and returns FATHOM_ETIMEOUT if
  * a wait has run out there since the last time it was asked (it then clears the
  * note), else FATHOM_OK.  None is expected to; a caller that wants to be sure asks

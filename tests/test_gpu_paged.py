@@ -113,6 +113,36 @@ def test_rows_behind_the_length_and_unnamed_pages_are_never_read(bad):
     assert torch.equal(attend(q, kp, vp, table, lens), want)
 
 
+@pytest.mark.parametrize("lens", [[70, 300, 5], [20, 40000, 1]])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("what", ["q", "k", "v"])
+def test_what_is_not_finite_stays_in_its_unit(what, bad, lens):
+    """A NaN or an infinity that a unit does attend to: its own results only, and never finite ones where
+    a NaN took part (also where a warp's 16 tokens are all NaN)."""
+    H, G, D, page = 2, 4, 128, 64
+    kp, vp, table, _ = P.pool(3, H, D, page, (max(lens) + page - 1) // page, BF)
+    q = query(6, G, D)
+    mass = torch.zeros(6, table.shape[1] * page, device="cuda")
+    want = attend(q, kp, vp, table, lens, mass=mass)
+    unit, seq, head = 3, 1, 1
+    if what == "q":
+        q[unit, 2, 9] = bad
+    else:
+        (kp if what == "k" else vp)[table[seq, 0], head, :16, 9] = bad
+    mass2 = torch.zeros_like(mass)
+    out = attend(q, kp, vp, table, lens, mass=mass2)
+    others = [u for u in range(6) if u != unit]
+    assert torch.equal(out[others], want[others]) and torch.equal(mass2[others], mass[others])
+    if what == "v":
+        rest = [c for c in range(D) if c != 9]
+        assert torch.equal(out[unit][:, rest], want[unit][:, rest]) and torch.equal(mass2, mass)
+        assert not torch.isfinite(out[unit, :, 9]).any()
+    elif math.isnan(bad):
+        heads = [2] if what == "q" else list(range(G))
+        assert torch.isnan(out[unit, heads]).all() and torch.isnan(mass2[unit, : lens[seq]]).all()
+        assert bool((mass2[unit, lens[seq]:] == 0).all())
+
+
 def test_bad_page_table_entries_are_skipped():
     lens, page = [100, 64], 16
     kp, vp, table, _ = P.pool(2, 2, 128, page, 7, BF)
