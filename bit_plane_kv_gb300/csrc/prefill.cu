@@ -23,8 +23,8 @@
 // S in tensor memory, which S, P and O of two tiles fill, so the next S waits for it):
 // about 2700 clocks per 128 keys and two tiles where the products alone take 2050.
 // Measured, 32 query heads on 8 KV heads, 128 channels, bf16: one prompt of 16384
-// tokens 1369 us (2.2 TFLOP, 1.61 PFLOP/s; 1.90 measured for library products), 12
-// prompts of up to 2048 tokens 165 us (1.11 PFLOP/s), 16 tokens against 8192 27 us.
+// tokens 1342 us (2.2 TFLOP, 1.64 PFLOP/s; 1.90 measured for library products), 12
+// prompts of up to 2048 tokens 164 us (1.12 PFLOP/s), 16 tokens against 8192 27 us.
 // What the steps gave on the 16k prompt: one thread per row with a full pass for the
 // maximum 2029 us; matrix instructions behind an elected lane instead of lane 0
 // 1883 -> 1445 us (their issue, not their execution, had been the bound); CTAs that
@@ -33,6 +33,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <mutex>
 #include <type_traits>
 
@@ -60,10 +61,11 @@ struct alignas(16) Work {
     int q0, lq;     // the sequence's first query row, its query tokens
     int k0, lk;     // its first key row, its key tokens
     int off;        // query token t sees keys j <= t + off
-    int t0;         // first token; tile w starts at t0 + w * (128 / gp)
+    int t0;         // first token; tile w starts at t0 + (w ^ flip) * (128 / gp)
     int nt0, nt1;   // steps of 128 keys of the two tiles
     int steps;      // the larger; -1: no more work
     int from;       // keys of the sequence before k0 (kSplit: the shares of other CTAs)
+    int flip;       // rows for one tile only: whether tile 1 takes them
     int half;       // bit w: tile w's last step has 64 keys or fewer and is worked on as half a step
 };
 
@@ -270,17 +272,26 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     const int tw = kRows >> a.lg_gp;
     const int rank = kSplit ? (int)(blockIdx.x % a.split) : 0;
     const int first_item = kSplit ? (int)(blockIdx.x / a.split) : (int)blockIdx.x;
+    int turns = 0;   // items of one tile so far
     int seen_s0 = 0, seen_before = 0;   // the 32 sequences that held the last item, and the tile pairs before them
+    int held_s0 = -1, q0 = 0, lq = 0, k0 = 0, lk = 0;   // the 32 sequences at hand, one per lane
     auto geometry = [&](int item) {
         Work g;
         g.group = item % a.groups;
         const int nth = a.tiles - 1 - item / a.groups;
         int seq = -1, tile = 0;
         auto pairs = [&](int s0) {   // of 256-row pairs of tiles: this lane's sequence's
-            int n = 0;
-            if (s0 + lane < a.seqs)
-                n = max(clamp_to(a.cu_q[s0 + lane + 1], a.total_q) - clamp_to(a.cu_q[s0 + lane], a.total_q), 0);
-            return (int)((((long long)n << a.lg_gp) + 2 * kRows - 1) / (2 * kRows));
+            if (s0 != held_s0) {
+                held_s0 = s0;
+                q0 = lq = k0 = lk = 0;
+                if (s0 + lane < a.seqs) {
+                    q0 = clamp_to(a.cu_q[s0 + lane], a.total_q);
+                    lq = max(clamp_to(a.cu_q[s0 + lane + 1], a.total_q) - q0, 0);
+                    k0 = clamp_to(a.cu_k[s0 + lane], a.total_k);
+                    lk = max(clamp_to(a.cu_k[s0 + lane + 1], a.total_k) - k0, 0);
+                }
+            }
+            return (int)((((long long)lq << a.lg_gp) + 2 * kRows - 1) / (2 * kRows));
         };
         // items come in falling order: the search starts where the last one ended
         while (nth < seen_before && seen_s0 > 0) {
@@ -298,22 +309,25 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             const unsigned hit = __ballot_sync(0xffffffffu, nth < upto);
             if (hit) {
                 const int l = __ffs(hit) - 1;
-                seq = seen_s0 + l;
+                seq = l;
                 tile = nth - __shfl_sync(0xffffffffu, upto - n, l);
                 break;
             }
             seen_before = __shfl_sync(0xffffffffu, upto, 31);
         }
-        g.lq = g.nt0 = g.nt1 = g.steps = g.q0 = g.k0 = g.lk = g.off = g.t0 = g.from = g.half = 0;
-        if (seq < 0) return g;   // the grid counts one tile more per sequence than most need
-        g.q0 = clamp_to(a.cu_q[seq], a.total_q);
-        g.lq = clamp_to(a.cu_q[seq + 1], a.total_q) - g.q0;
-        g.k0 = clamp_to(a.cu_k[seq], a.total_k);
-        g.lk = max(clamp_to(a.cu_k[seq + 1], a.total_k) - g.k0, 0);
+        g.lq = g.nt0 = g.nt1 = g.steps = g.q0 = g.k0 = g.lk = g.off = g.t0 = g.from = g.flip = g.half = 0;
+        if (seq < 0) return g;   // the grid counts up to a tile pair per sequence more than needed
+        g.q0 = __shfl_sync(0xffffffffu, q0, seq);
+        g.lq = __shfl_sync(0xffffffffu, lq, seq);
+        g.k0 = __shfl_sync(0xffffffffu, k0, seq);
+        g.lk = __shfl_sync(0xffffffffu, lk, seq);
         g.off = g.lk - g.lq;
         g.t0 = tile << (8 - a.lg_gp);
+        // rows for one tile only go to either in turn, so that its epilogue runs beside the other's products
+        // (1000 prompts of 16 tokens, 32 heads on 8: 213 -> 133 us)
+        g.flip = !kSplit && g.lq - g.t0 <= tw ? turns++ & 1 : 0;
         auto keys = [&](int w) {                           // that some row of tile w sees
-            const int start = g.t0 + w * tw, last = min(start + tw, g.lq) - 1;
+            const int start = g.t0 + (w ^ g.flip) * tw, last = min(start + tw, g.lq) - 1;
             return start <= last ? max(min(g.lk, last + g.off + 1), 0) : 0;
         };
         const int keys0 = keys(0), keys1 = keys(1);
@@ -348,7 +362,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         auto field = [&](int i) { return __shfl_sync(0xffffffffu, f[i], 0); };
         g.group = field(0); g.q0 = field(1); g.lq = field(2); g.k0 = field(3); g.lk = field(4);
         g.off = field(5); g.t0 = field(6); g.nt0 = field(7); g.nt1 = field(8); g.steps = field(9);
-        g.from = field(10); g.half = field(11);
+        g.from = field(10); g.flip = field(11); g.half = field(12);
         if (lane == 0) mbar_arrive(smem_addr(&sm.work_empty[slot]));
         ++round;
         return ok && g.steps >= 0;
@@ -382,7 +396,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     const uint32_t bar = smem_addr(&sm.q_full[w]);
                     mbar_expect(bar, kTile);
                     for (int p = 0; p < kPanels; ++p)
-                        tma_load_3d(smem_addr(sm.q[w]) + p * kPanel, &map_q, bar, 64 * p, hq, g.q0 + g.t0 + w * tw);
+                        tma_load_3d(smem_addr(sm.q[w]) + p * kPanel, &map_q, bar, 64 * p, hq, g.q0 + g.t0 + (w ^ g.flip) * tw);
                 }
                 int s = st;
                 uint32_t t = turn;
@@ -542,13 +556,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         constexpr float kLag = kDtype == FATHOM_F16 ? 8.0f : 32.0f;
         uint32_t ps = 0, po = 0;   // parities of the next wait for S, and for the last product into O
         for (Work g; get_work(g);) {
+            if (!kSplit && g.t0 + (w ^ g.flip) * tw >= g.lq) continue;   // no rows
             const int nt = w ? g.nt1 : g.nt0;
-            const int token = g.t0 + w * tw + (row >> a.lg_gp);
+            const int token = g.t0 + (w ^ g.flip) * tw + (row >> a.lg_gp);
             const int at = token < g.lq ? g.q0 + token : -1;   // row of out; -1: behind the sequence
             const int head = (g.group << a.lg_gp) + (row & (a.gp - 1));
             // keys this row sees, and the fewest that a row of this warp sees
             const int seen = min(g.lk, token + g.off + 1);
-            const int seen_min = min(g.lk, g.t0 + w * tw + (((warp & 3) * 32) >> a.lg_gp) + g.off + 1);
+            const int seen_min = min(g.lk, g.t0 + (w ^ g.flip) * tw + (((warp & 3) * 32) >> a.lg_gp) + g.off + 1);
             float m = -CUDART_INF_F, l = 0.0f;   // m in log2 units; -inf: no finite score yet
             auto step = [&](int j, auto halves) {   // 128 keys, or the first 64 of the last ones
                 constexpr int kHalves = decltype(halves)::value;
@@ -806,20 +821,43 @@ bool encode_rows(CUtensorMap *map, int dtype, const void *base, int D, int heads
 
 }  // namespace
 
-template <typename F, typename... Args>
-static cudaError_t launch_cluster(F *kernel, unsigned grid, int cluster, size_t smem, cudaStream_t st,
-                                  const Args &...args) {
+static cudaLaunchConfig_t cluster_config(cudaLaunchAttribute *attr, unsigned grid, int cluster, size_t smem) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kPrefillThreads);
     cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = (unsigned)cluster;
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    return cfg;
+}
+
+// Clusters of that many CTAs that the current device holds at once (8 CTAs: 15, not 19 as by
+// the number of SMs, for a cluster lies within a GPC); asked once
+// per device (every form of the kernel takes a whole SM).
+template <typename F>
+static int resident_clusters(F *kernel, int cluster, size_t smem) {
+    constexpr int kDevices = 16;
+    static std::atomic<int> known[kDevices][9];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const bool keep = dev < kDevices;
+    if (keep && (n = known[dev][cluster].load(std::memory_order_relaxed)) != 0) return n - 1;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = cluster_config(&attr, (unsigned)cluster, cluster, smem);
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) { cudaGetLastError(); return 0; }
+    if (keep) known[dev][cluster].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+template <typename F, typename... Args>
+static cudaError_t launch_cluster(F *kernel, unsigned grid, int cluster, size_t smem, cudaStream_t st,
+                                  const Args &...args) {
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = cluster_config(&attr, grid, cluster, smem);
+    cfg.stream = st;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -846,7 +884,8 @@ int launch_prefill_attn(const fathom_prompts &p, const void *q, const void *k, c
     a.v_token = p.v_token; a.v_head = p.v_head;
     a.q = (const uint16_t *)q; a.k = (const uint16_t *)k; a.v = (const uint16_t *)v;
     a.cu_q = cu_q; a.cu_k = cu_k; a.out = out; a.lse = lse;
-    const long long tiles = ((long long)p.total_q * a.gp + 2 * kRows - 1) / (2 * kRows) + p.seqs;
+    // pairs of tiles, at most: exact for one sequence
+    const long long tiles = ((long long)p.total_q * a.gp + (2LL * kRows - 1) * p.seqs) / (2 * kRows);
     if (tiles * a.groups > 0x7fffffffLL) { set_error("prefill_attn: too many rows for one launch"); return FATHOM_EINVAL; }
     a.tiles = (int)tiles;
     CUtensorMap mq, mk, mv;
@@ -855,18 +894,21 @@ int launch_prefill_attn(const fathom_prompts &p, const void *q, const void *k, c
         !encode_rows(&mk, p.dtype, k, p.D, p.kv_heads, p.total_k, p.k_head, p.k_token, 1, kKeys) ||
         !encode_rows(&mv, p.dtype, v, p.D, p.kv_heads, p.total_k, p.v_head, p.v_token, 1, kKeys))
         return FATHOM_ECUDA;
-    // With fewer work items than half the SMs, clusters of 2, 4 or 8 CTAs share an item's keys, as long as
-    // each gets a few steps
-    int sms = device_sm_count();
-    if (sms <= 0) sms = 152;
-    a.split = 1;
-    while (a.split < 8 && tiles * a.groups * 2 * a.split <= sms && p.total_k >= 4 * kKeys * 2 * a.split) a.split *= 2;
-    const unsigned grid = (unsigned)(tiles * a.groups * a.split);
+    // With few work items, clusters of 2, 4 or 8 CTAs share an item's keys, as long as each gets a few
+    // steps and all clusters are resident at once
+    const long long items = tiles * a.groups;
 #define FATHOM_PREFILL(SS, DD)                                                                     \
     do {                                                                                           \
         const size_t smem = sizeof(PrefillSmem<(SS + 3) / 4>) + 1024;                              \
-        if (a.split > 1) {                                                                         \
+        a.split = 1;                                                                               \
+        if (items <= 76 && p.total_k >= 8 * kKeys) {                                               \
             ensure_smem(prefill_kernel<SS, DD, true>, smem);                                       \
+            while (a.split < 8 && p.total_k >= 4 * kKeys * 2 * a.split &&                          \
+                   items <= resident_clusters(prefill_kernel<SS, DD, true>, 2 * a.split, smem))    \
+                a.split *= 2;                                                                      \
+        }                                                                                          \
+        const unsigned grid = (unsigned)(items * a.split);                                         \
+        if (a.split > 1) {                                                                         \
             e = launch_cluster(prefill_kernel<SS, DD, true>, grid, a.split, smem, st, mq, mk, mv, a); \
         } else {                                                                                   \
             ensure_smem(prefill_kernel<SS, DD, false>, smem);                                      \
