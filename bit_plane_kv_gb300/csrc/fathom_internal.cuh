@@ -267,7 +267,7 @@ int launch_paged_append(const fathom_pages &p, void *kp, void *vp, const int32_t
                         const void *vn, int total, int64_t new_token, int64_t new_head, const int32_t *start,
                         const int32_t *cu_new, cudaStream_t st);
 // Scratch of the paged decode attention: partial softmax states (two per CTA), a
-// ticket per unit and, with the mass, every token's logits and each row's
+// ticket per unit and per group of shares and, with the mass, every token's logits and each row's
 // normaliser.
 struct PagedWorkspace {
     int ctas;

@@ -138,7 +138,7 @@ struct DecArgs {
     const void *kp, *vp;
     const int32_t *table, *lens;
     float *out, *part_o, *part_ml, *lse, *logits;   // shares: [CTA][2][G][D] and [CTA][2][G][2] = (m, l)
-    unsigned *ticket;
+    unsigned *ticket, *group_ticket;   // of a unit's shares; of a group of them, at its first share's place
 };
 
 // Join of a unit's shares, 32 at a time; in the place of DecSmem::o.
@@ -562,25 +562,40 @@ paged_attn_kernel(const DecArgs a) {
             }
         }
         if (!whole) {
-            __syncthreads();
-            if (tid == 0) {
-                __threadfence();   // the CTA's state before its ticket
-                sm.last = atomicAdd(a.ticket + unit, 1u) == (unsigned)(c_last - c_first) ? 1 : 0;
-                __threadfence();
+            // The last share to arrive joins them, in their order.  Of more than 32 shares, groups of
+            // kGroup are joined first, each by its last share and into its first one's place, so that no
+            // CTA reads hundreds (one unit of 131072 tokens, 8 heads, 304 shares: 121 -> 33 us)
+            constexpr int kGroup = 16;
+            const int before = share(c_first, W, NC) < unit_w0;   // only the first share can be a CTA's second
+            auto slot_of = [&](long long x) { return (size_t)(2 * x + (x == c_first ? before : 0)); };
+            const int shares = (int)(c_last - c_first) + 1;
+            long long x_first = c_first;   // what is joined: shares x_first, x_first + every, ...
+            int every = 1, n = shares;
+            unsigned *ticket = a.ticket + unit;
+            bool final = shares <= 32;
+            if (!final) {
+                x_first += (cta - c_first) / kGroup * kGroup;
+                n = (int)min((long long)kGroup, c_last - x_first + 1);
+                ticket = a.group_ticket + slot_of(x_first);
             }
-            __syncthreads();
-            if (sm.last) {   // every share of the unit is there: joined in their order, 32 at a time
-                if (tid == 0) a.ticket[unit] = 0u;
+            for (;;) {
+                __syncthreads();
+                if (tid == 0) {
+                    __threadfence();   // the CTA's state before its ticket
+                    sm.last = atomicAdd(ticket, 1u) == (unsigned)(n - 1) ? 1 : 0;
+                    __threadfence();
+                }
+                __syncthreads();
+                if (!sm.last) break;
+                if (tid == 0) *ticket = 0u;
                 JoinSmem &jn = *reinterpret_cast<JoinSmem *>(sm.o);
                 if (tid < G) { jn.m[tid] = -CUDART_INF_F; jn.l[tid] = 0.0f; }
-                constexpr int kBatch = kD == 64 ? 4 : (kTwo ? 6 : 16);
+                constexpr int kBatch = kD == 64 ? 8 : (kTwo ? 6 : 16);
                 float4 acc[kVecs];
 #pragma unroll
                 for (int k = 0; k < kVecs; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                const int before = share(c_first, W, NC) < unit_w0;   // only the first share can be a CTA's second
-                auto slot_of = [&](long long x) { return (size_t)(2 * x + (x == c_first ? before : 0)); };
-                for (long long x0 = c_first; x0 <= c_last; x0 += 32) {
-                    const int nx = (int)min(c_last - x0 + 1, 32LL);
+                for (int x0 = 0; x0 < n; x0 += 32) {
+                    const int nx = min(n - x0, 32);
                     float4 v[kVecs][kBatch];
                     auto fetch = [&](int x) {   // shares x0 + x and on, kBatch loads in flight per vector
 #pragma unroll
@@ -589,14 +604,27 @@ paged_attn_kernel(const DecArgs a) {
 #pragma unroll
                             for (int y = 0; y < kBatch; ++y)
                                 if (e < G * D && x + y < nx)
-                                    v[k][y] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot_of(x0 + x + y) * G * D + e));
+                                    v[k][y] = __ldcg(reinterpret_cast<const float4 *>(
+                                        a.part_o + slot_of(x_first + (x0 + x + y) * every) * G * D + e));
                         }
                     };
+                    constexpr int kHeads = kTwo ? 2 : 1;   // of a warp
+                    float2 mls[kHeads];
+#pragma unroll
+                    for (int i = 0; i < kHeads; ++i) {
+                        const int h = warp + i * kDecWarps;
+                        mls[i] = make_float2(-CUDART_INF_F, 0.0f);
+                        if (lane < nx && h < G)
+                            mls[i] = __ldcg(reinterpret_cast<const float2 *>(
+                                a.part_ml + (slot_of(x_first + (x0 + lane) * every) * G + h) * 2));
+                    }
                     fetch(0);   // under way while the weights are computed
                     __syncthreads();
-                    for (int h = warp; h < G; h += kDecWarps) {
-                        float2 ml = make_float2(-CUDART_INF_F, 0.0f);
-                        if (lane < nx) ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + (slot_of(x0 + lane) * G + h) * 2));
+#pragma unroll
+                    for (int i = 0; i < kHeads; ++i) {
+                        const int h = warp + i * kDecWarps;
+                        if (h >= G) break;
+                        const float2 ml = mls[i];
                         float mx = ml.x;
 #pragma unroll
                         for (int o2 = 16; o2; o2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
@@ -642,14 +670,26 @@ paged_attn_kernel(const DecArgs a) {
 #pragma unroll
                 for (int k = 0; k < kVecs; ++k) {
                     const int e = 4 * (tid + k * kDecThreads);
-                    if (e < G * D) {
-                        const int h = e / D;
-                        const float L = jn.l[h], inv = L > 0.0f ? 1.0f / L : 0.0f;
+                    if (e >= G * D) continue;
+                    const int h = e / D;
+                    const float L = jn.l[h];
+                    if (final) {
+                        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
                         float *ou = a.out + (size_t)unit * G * D + e;
                         ou[0] = acc[k].x * inv; ou[1] = acc[k].y * inv; ou[2] = acc[k].z * inv; ou[3] = acc[k].w * inv;
                         if (kMass && e % D == 0) a.lse[(size_t)unit * G + h] = L == 0.0f ? 0.0f : jn.m[h] + log2f(L) - kUp;
+                    } else {
+                        const size_t to = slot_of(x_first);
+                        *reinterpret_cast<float4 *>(a.part_o + to * G * D + e) = acc[k];
+                        if (e % D == 0) *reinterpret_cast<float2 *>(a.part_ml + (to * G + h) * 2) = make_float2(jn.m[h], L);
                     }
                 }
+                if (final) break;
+                x_first = c_first;
+                every = kGroup;
+                n = (shares + kGroup - 1) / kGroup;
+                ticket = a.ticket + unit;
+                final = true;
             }
         }
         fresh = true;
@@ -723,7 +763,7 @@ PagedWorkspace paged_workspace_layout(const fathom_pages &p, int G, bool mass) {
     const size_t units = (size_t)p.seqs * p.kv_heads, rows = units * G;
     w.ctas = dec_ctas(p.D <= 64 ? 64 : 128) * sms;   // resident at once
     w.ticket_off = 0;
-    w.lse_off = align256(units * sizeof(uint32_t));
+    w.lse_off = align256((units + 2 * (size_t)w.ctas) * sizeof(uint32_t));
     w.part_off = align256(w.lse_off + (mass ? rows * sizeof(float) : 0));
     w.ml_off = align256(w.part_off + (size_t)w.ctas * 2 * G * p.D * sizeof(float));
     w.logit_off = align256(w.ml_off + (size_t)w.ctas * 2 * G * 2 * sizeof(float));
@@ -743,6 +783,7 @@ int launch_paged_attn(const fathom_pages &p, int G, const float *q, const void *
     a.logit_stride = (a.cap + 3) / 4 * 4;
     a.q = q; a.kp = kp; a.vp = vp; a.table = table; a.lens = lens; a.out = out;
     a.ticket = (unsigned *)((char *)ws + w.ticket_off);
+    a.group_ticket = a.ticket + (size_t)p.seqs * p.kv_heads;
     a.part_o = (float *)((char *)ws + w.part_off);
     a.part_ml = (float *)((char *)ws + w.ml_off);
     a.lse = mass ? (float *)((char *)ws + w.lse_off) : nullptr;

@@ -56,6 +56,9 @@ DECODE = {
     "G 5, 72 channels": ([300, 4], 2, 5, 72, 16, BF, "token"),
     "G 6, page 256": ([300, 4, 256, 257], 1, 6, 128, 256, FP, "head"),
     "G 7": ([100, 33], 1, 7, 64, 8, BF, "token"),
+    "one unit of many shares": ([40000], 1, 8, 128, 64, BF, "token"),
+    "one unit of many shares, 64 channels": ([51000], 1, 4, 64, 64, FP, "token"),
+    "few units of many shares": ([30000, 5, 0, 21000], 1, 4, 128, 16, BF, "head"),
     "one token": ([1], 1, 1, 8, 16, BF, "token"),
     "all idle": ([0, 0, 0], 2, 4, 128, 16, BF, "token"),
     "long and short": ([9000, 3, 0, 700], 2, 4, 128, 64, BF, "token"),
@@ -198,6 +201,7 @@ def test_a_workspace_serves_call_after_call_and_graph_after_graph():
 
 @pytest.mark.parametrize("lens,H,G,D,dt", [
     ([30000, 17, 0, 22001], 4, 4, 128, BF),                # long shares of few sequences
+    ([50000, 17], 1, 8, 128, BF),                          # more shares than are joined at once
     ([2000 + 13 * i for i in range(150)], 2, 8, 64, FP),   # more than 128 sequences
 ])
 def test_the_same_bits_every_time(lens, H, G, D, dt):
