@@ -1,6 +1,6 @@
 // blackwell.cuh -- thin wrappers of the sm_103a instructions the prompt attention
 // uses: mbarriers with bounded waits, TMA tile loads, tensor memory and the fifth
-// generation tensor cores.
+// generation tensor cores; and of clusters and their distributed shared memory.
 #pragma once
 
 #include "fathom_internal.cuh"
@@ -99,6 +99,11 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
+}
+__device__ __forceinline__ uint2 cluster_load2(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
 }
 __device__ __forceinline__ void cluster_store(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");

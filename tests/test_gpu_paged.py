@@ -349,6 +349,9 @@ def masses(units, cap, seed=0):
     ([1025, 2048, 2047], 2, 128, 16, 2047, 4, 32, BF),
     ([5000], 1, 128, 64, 1, 1, 0, BF),
     ([100], 1, 128, 16, 300, 4, 32, BF),             # more room than tokens
+    ([9001, 4000], 1, 72, 16, 3500, 4, 32, FP),      # teams of CTAs over several chunks
+    ([40000], 2, 64, 64, 20011, 4, 32, BF),          # clusters of CTAs choose
+    ([200000], 1, 8, 64, 1000, 4, 32, BF),           # more tokens than a cluster holds
 ])
 def test_eviction_keeps_and_moves_what_the_plain_form_does(lens, H, D, page, keep, ns, nr, dt, in_place):
     per = -(-max(max(lens), keep) // page)
