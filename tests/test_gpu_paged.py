@@ -1,6 +1,9 @@
 """The paged cache on the GPU (append, decode attention with attention mass,
 eviction) against plain 64-bit forms; the tolerances are derived in paged_cases."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -429,6 +432,51 @@ def test_eviction_in_a_graph_and_on_a_stream():
     for u in range(4):
         n = [101, 512][u // 2]
         assert out[0][u].tolist() == P.kept_set(mass[u].tolist(), n, keep, 4, 32)
+
+
+def test_calls_by_clusters_captured_by_a_process_that_has_not_made_them():
+    """Few rows against many keys, one unit of many shares, an eviction of long sequences in place: captured as a
+    process's first calls, replayed twice, and the same as eager calls."""
+    code = """
+import sys
+sys.path.insert(0, %r); sys.path.insert(0, %r)
+import torch
+from bit_plane_kv_gb300 import binding as B
+import paged_cases as P
+n = 30000
+kp, vp, table, _ = P.pool(1, 1, 128, 64, 469, torch.bfloat16)
+k0, v0 = kp.clone(), vp.clone()
+pages = B.make_pages(kp, table)
+ws = B.alloc_paged_workspace(pages, G=8, mass=True)
+q, lens = torch.randn(1, 8, 128, device="cuda"), torch.full((1,), n, dtype=torch.int32, device="cuda")
+mass, part = torch.zeros(1, 469 * 64, device="cuda"), torch.zeros(1, 5000, device="cuda")
+p = torch.randn(9000, 3, 128, device="cuda").bfloat16()
+cq, ck = P.cumulated([20]), P.cumulated([9000])
+
+def calls():
+    kp.copy_(k0), vp.copy_(v0), mass.zero_()
+    a, _ = B.fathom_prefill_attn(p[:20, :1], p[:, 1:2], p[:, 2:], cq, ck)
+    b = B.fathom_paged_attn(pages, q, kp, vp, table, lens, ws, mass=mass)
+    c, d, e = B.fathom_paged_evict(pages, kp, vp, table, lens, mass, 5000, table, mass_out=part)
+    return a, b, c, d, e, mass, kp, vp
+
+g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.graph(g):
+    got = calls()
+g.replay()
+g.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in got]
+with torch.cuda.stream(side):
+    want = calls()
+torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(got, want))
+assert want[2][0].tolist() == P.kept_set(mass[0].tolist(), n, 5000, 4, 32)
+B.fathom_wait_status()
+print("same")
+""" % (os.path.dirname(os.path.dirname(os.path.abspath(__file__))), os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stdout + r.stderr[-2000:]
 
 
 # ------------------------------------------------------------------ together
