@@ -897,11 +897,12 @@ int launch_prefill_attn(const fathom_prompts &p, const void *q, const void *k, c
     // With few work items, clusters of 2, 4 or 8 CTAs share an item's keys, as long as each gets a few
     // steps and all clusters are resident at once
     const long long items = tiles * a.groups;
+    const bool few = 2 * items <= device_sm_count() && p.total_k >= 8 * kKeys;
 #define FATHOM_PREFILL(SS, DD)                                                                     \
     do {                                                                                           \
         const size_t smem = sizeof(PrefillSmem<(SS + 3) / 4>) + 1024;                              \
         a.split = 1;                                                                               \
-        if (items <= 76 && p.total_k >= 8 * kKeys) {                                               \
+        if (few) {                                                                                 \
             ensure_smem(prefill_kernel<SS, DD, true>, smem);                                       \
             while (a.split < 8 && p.total_k >= 4 * kKeys * 2 * a.split &&                          \
                    items <= resident_clusters(prefill_kernel<SS, DD, true>, 2 * a.split, smem))    \
