@@ -12,8 +12,8 @@
 //   O = O + P V         P from tensor memory, V from shared memory
 // with c = log2(e) / sqrt(D) and the running maximum m, sum l of a softmax in one
 // pass.  The exponentials of a row are taken against a maximum that may be up to
-// 2^8 too small (m is raised, and O and l rescaled, only beyond that): O, 64 KB
-// of tensor memory, is touched by the row's own thread in a few tiles only.
+// 2^32 (bf16) or 2^8 (fp16) too small (m is raised, and O and l rescaled, only beyond
+// that): O, 64 KB of tensor memory, is touched by the row's own thread in a few tiles only.
 // A warp loads Q and a ring of K and V tiles by TMA; one elected lane of another
 // issues the matrix instructions; CTAs stay and take over the work of those that have
 // not started, so that one item's epilogue runs beside the next one's loads and
@@ -835,8 +835,8 @@ static cudaLaunchConfig_t cluster_config(cudaLaunchAttribute *attr, unsigned gri
 }
 
 // Clusters of that many CTAs that the current device holds at once (8 CTAs: 15, not 19 as by
-// the number of SMs, for a cluster lies within a GPC); asked once
-// per device (every form of the kernel takes a whole SM).
+// the number of SMs, for a cluster lies within a GPC); asked once per device, as every form
+// of the kernel takes a whole SM.
 template <typename F>
 static int resident_clusters(F *kernel, int cluster, size_t smem) {
     constexpr int kDevices = 16;
