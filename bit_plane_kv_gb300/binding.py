@@ -751,7 +751,8 @@ def paged_workspace_size(pages: Pages, G: int, mass=False) -> int:
 
 
 def alloc_paged_workspace(pages: Pages, G=4, mass=False, device="cuda") -> torch.Tensor:
-    """Workspace of fathom_paged_attn (mass: also large enough for calls with it)."""
+    """Workspace of fathom_paged_attn (mass: also large enough for calls with it).  One that is large enough for
+    several calls of different sizes serves them in any order."""
     nbytes = paged_workspace_size(pages, G, mass)
     if nbytes == 0:
         raise FathomError("fathom_paged_workspace_size", 1, lib().fathom_last_error().decode())

@@ -266,9 +266,9 @@ int launch_prefill_attn(const fathom_prompts &p, const void *q, const void *k, c
 int launch_paged_append(const fathom_pages &p, void *kp, void *vp, const int32_t *table, const void *kn,
                         const void *vn, int total, int64_t new_token, int64_t new_head, const int32_t *start,
                         const int32_t *cu_new, cudaStream_t st);
-// Scratch of the paged decode attention: partial softmax states (two per CTA), a
-// ticket per unit and per group of shares and, with the mass, every token's logits and each row's
-// normaliser.
+// Scratch of the paged decode attention: tickets, for units and for groups of shares, a fixed
+// number of them; then partial softmax states (two per CTA) and, with the mass, every token's
+// logits and each row's normaliser.
 struct PagedWorkspace {
     int ctas;
     size_t ticket_off, lse_off, part_off, ml_off, logit_off, total;

@@ -78,6 +78,7 @@ paged_append_kernel(fathom_pages p, int lg, int4 *__restrict__ kp, int4 *__restr
 constexpr int kDecWarps = 4, kDecThreads = 32 * kDecWarps;
 // CTAs resident per SM, and stages of their rings
 __host__ __device__ constexpr int dec_ctas(int d) { return d == 128 ? 2 : 3; }
+constexpr int kMaxDecCtas = 3;   // the larger
 __host__ __device__ constexpr int dec_stages(int d) { return d == 128 ? 3 : 4; }
 
 __device__ __forceinline__ uint32_t pack_pair(float lo, float hi, __nv_bfloat16) {
@@ -138,7 +139,7 @@ struct DecArgs {
     const void *kp, *vp;
     const int32_t *table, *lens;
     float *out, *part_o, *part_ml, *lse, *logits;   // shares: [CTA][2][G][D] and [CTA][2][G][2] = (m, l)
-    unsigned *ticket, *group_ticket;   // of a unit's shares; of a group of them, at its first share's place
+    unsigned *ticket, *group_ticket;   // of a unit's shares, and of a group of them; at the first share's place
 };
 
 // Join of a unit's shares, 32 at a time; in the place of DecSmem::o.
@@ -571,7 +572,7 @@ paged_attn_kernel(const DecArgs a) {
             const int shares = (int)(c_last - c_first) + 1;
             long long x_first = c_first;   // what is joined: shares x_first, x_first + every, ...
             int every = 1, n = shares;
-            unsigned *ticket = a.ticket + unit;
+            unsigned *ticket = a.ticket + slot_of(c_first);
             bool final = shares <= 32;
             if (!final) {
                 x_first += (cta - c_first) / kGroup * kGroup;
@@ -688,7 +689,7 @@ paged_attn_kernel(const DecArgs a) {
                 x_first = c_first;
                 every = kGroup;
                 n = (shares + kGroup - 1) / kGroup;
-                ticket = a.ticket + unit;
+                ticket = a.ticket + slot_of(c_first);
                 final = true;
             }
         }
@@ -730,6 +731,10 @@ paged_mass_kernel(fathom_pages p, int cap, int stride, int G, const int32_t *__r
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Places of partial results, two per CTA: as many tickets of units, and of groups of shares.  A place names its
+// unit: the unit's first share lies there, and no other unit's does.
+size_t paged_tickets(int sms) { return 2 * (size_t)kMaxDecCtas * sms; }
+
 template <typename T, int kD, int kTwo, bool kMass>
 cudaError_t launch_dec(const DecArgs &a, int ctas, cudaStream_t st) {
     const size_t smem = sizeof(DecSmem<kD>);
@@ -762,8 +767,11 @@ PagedWorkspace paged_workspace_layout(const fathom_pages &p, int G, bool mass) {
     if (sms <= 0) sms = 152;
     const size_t units = (size_t)p.seqs * p.kv_heads, rows = units * G;
     w.ctas = dec_ctas(p.D <= 64 ? 64 : 128) * sms;   // resident at once
+    // Tickets, which are zero between calls, take the same bytes whatever the call's sizes: a buffer made for the
+    // largest of several calls serves them all.  (A ticket per unit, with the data behind the last one, put a
+    // smaller call's partial results into a larger one's tickets.)
     w.ticket_off = 0;
-    w.lse_off = align256((units + 2 * (size_t)w.ctas) * sizeof(uint32_t));
+    w.lse_off = align256(2 * paged_tickets(sms) * sizeof(uint32_t));
     w.part_off = align256(w.lse_off + (mass ? rows * sizeof(float) : 0));
     w.ml_off = align256(w.part_off + (size_t)w.ctas * 2 * G * p.D * sizeof(float));
     w.logit_off = align256(w.ml_off + (size_t)w.ctas * 2 * G * 2 * sizeof(float));
@@ -783,7 +791,7 @@ int launch_paged_attn(const fathom_pages &p, int G, const float *q, const void *
     a.logit_stride = (a.cap + 3) / 4 * 4;
     a.q = q; a.kp = kp; a.vp = vp; a.table = table; a.lens = lens; a.out = out;
     a.ticket = (unsigned *)((char *)ws + w.ticket_off);
-    a.group_ticket = a.ticket + (size_t)p.seqs * p.kv_heads;
+    a.group_ticket = a.ticket + (w.lse_off - w.ticket_off) / sizeof(unsigned) / 2;
     a.part_o = (float *)((char *)ws + w.part_off);
     a.part_ml = (float *)((char *)ws + w.ml_off);
     a.lse = mass ? (float *)((char *)ws + w.lse_off) : nullptr;

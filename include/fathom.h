@@ -528,7 +528,10 @@ int fathom_paged_append(const fathom_pages *pages, void *k_pages, void *v_pages,
  *   fp32 (out), mass_opt NULL or [units][mass_stride] fp32 (in and out;
  *   mass_stride >= max_pages * page_tokens); device
  *   workspace: at least fathom_paged_workspace_size(pages, G, mass) bytes, same
- *   rules as fathom_scan_topk's. */
+ *   rules as fathom_scan_topk's; a buffer that is large enough for several calls of
+ *   different sizes (batches, layouts, D, G, with and without mass) serves them in
+ *   any order.  With mass it holds a logit for every token that the page table can
+ *   name: units * G * max_pages * page_tokens * 4 bytes, whatever lens says. */
 int fathom_paged_attn(const fathom_pages *pages, int32_t G, const float *q, const void *k_pages,
                       const void *v_pages, const int32_t *page_table, const int32_t *lens, float *out,
                       float *mass_opt, size_t mass_stride, void *workspace, size_t workspace_bytes,

@@ -202,6 +202,33 @@ def test_a_workspace_serves_call_after_call_and_graph_after_graph():
     assert all(torch.equal(o, want) for o in outs)
 
 
+def test_a_workspace_serves_calls_of_different_sizes_in_turn():
+    """A serving loop's batch changes from step to step: one buffer, made for the largest call, gives what a fresh
+    one gives (every output filled with NaN before)."""
+    calls = [                                              # (lengths, KV heads, G, D, type, with mass)
+        ([700 + i % 90 for i in range(256)], 4, 4, 128, BF, False),    # most units shared by two CTAs
+        ([3000], 8, 4, 128, BF, False),
+        ([60000], 1, 8, 64, FP, True),                                # joined in groups
+        ([900 - i for i in range(300)], 2, 8, 64, FP, True),
+        ([50000], 1, 4, 128, BF, True),
+        ([1, 40, 9000], 2, 2, 72, BF, False),
+    ]
+    made = []
+    for lens, H, G, D, dt, with_mass in calls:
+        kp, vp, table, _ = P.pool(len(lens), H, D, 64, -(-max(lens) // 64), dt)
+        q, pages = query(len(lens) * H, G, D), B.make_pages(kp, table)
+        mass = torch.zeros(len(lens) * H, pages.cap, device="cuda") if with_mass else None
+        want = attend(q, kp, vp, table, lens, mass)
+        made.append((q, kp, vp, table, i32(lens), want, mass, B.paged_workspace_size(pages, G, with_mass)))
+    ws = torch.zeros(max(m[-1] for m in made), dtype=torch.uint8, device="cuda")
+    for i in (0, 1, 0, 2, 0, 3, 4, 3, 1, 5, 4, 2, 2, 0, 5, 3):
+        q, kp, vp, table, lens, want, mass, _ = made[i]
+        again = None if mass is None else torch.zeros_like(mass)
+        out = attend(q, kp, vp, table, lens, again, ws=ws, out=torch.full_like(want, math.nan))
+        assert torch.equal(out, want), f"call {i}"
+        assert mass is None or torch.equal(again, mass), f"call {i}"
+
+
 @pytest.mark.parametrize("lens,H,G,D,dt", [
     ([30000, 17, 0, 22001], 4, 4, 128, BF),                # long shares of few sequences
     ([50000, 17], 1, 8, 128, BF),                          # more shares than are joined at once
