@@ -38,13 +38,12 @@
 #include <type_traits>
 
 #include "blackwell.cuh"
+#include "prefill_work.cuh"
 
 namespace fathom {
 
 namespace {
 
-constexpr int kRows = 128;          // rows of a tile
-constexpr int kKeys = 128;          // keys per step
 // Warps 0-3 and 4-7: the two tiles' rows (a warp reaches the 32 lanes of tensor
 // memory that its number modulo 4 names); then one warp issues the matrix
 // instructions and one the loads.
@@ -54,20 +53,6 @@ constexpr uint32_t kPanel = 128 * 128;   // bytes of 128 rows x 64 channels
 
 // Tensor memory columns: the two S (and P) tiles, then the two O tiles.
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
-
-// A work item: 256 rows of a sequence and what they see.
-struct alignas(16) Work {
-    int group;      // of gp query heads
-    int q0, lq;     // the sequence's first query row, its query tokens
-    int k0, lk;     // its first key row, its key tokens
-    int off;        // query token t sees keys j <= t + off
-    int t0;         // first token; tile w starts at t0 + (w ^ flip) * (128 / gp)
-    int nt0, nt1;   // steps of 128 keys of the two tiles
-    int steps;      // the larger; -1: no more work
-    int from;       // keys of the sequence before k0 (kSplit: the shares of other CTAs)
-    int flip;       // rows for one tile only: whether tile 1 takes them
-    int half;       // bit w: tile w's last step has 64 keys or fewer and is worked on as half a step
-};
 
 template <int kPanels>   // 64-channel panels of a row: 1 (D <= 64) or 2
 struct PrefillSmem {
@@ -326,27 +311,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         // rows for one tile only go to either in turn, so that its epilogue runs beside the other's products
         // (1000 prompts of 16 tokens, 32 heads on 8: 213 -> 133 us)
         g.flip = !kSplit && g.lq - g.t0 <= tw ? turns++ & 1 : 0;
-        auto keys = [&](int w) {                           // that some row of tile w sees
-            const int start = g.t0 + (w ^ g.flip) * tw, last = min(start + tw, g.lq) - 1;
-            return start <= last ? max(min(g.lk, last + g.off + 1), 0) : 0;
-        };
-        const int keys0 = keys(0), keys1 = keys(1);
-        g.nt0 = (keys0 + kKeys - 1) / kKeys;
-        g.nt1 = (keys1 + kKeys - 1) / kKeys;
-        g.half = (keys0 > 0 && (keys0 - 1) % kKeys < kKeys / 2 ? 1 : 0) | (keys1 > 0 && (keys1 - 1) % kKeys < kKeys / 2 ? 2 : 0);
-        g.steps = max(g.nt0, g.nt1);
-        if constexpr (kSplit) {   // this CTA's share of the steps, its keys counted from the first of them
-            const int from = g.steps * rank / a.split, to = g.steps * (rank + 1) / a.split;
-            if (g.nt0 > to) g.half &= ~1;
-            if (g.nt1 > to) g.half &= ~2;
-            g.nt0 = min(max(g.nt0 - from, 0), to - from);
-            g.nt1 = min(max(g.nt1 - from, 0), to - from);
-            g.steps = max(g.nt0, g.nt1);
-            g.from = from * kKeys;
-            g.k0 += from * kKeys;
-            g.lk -= from * kKeys;
-            g.off -= from * kKeys;
-        }
+        work_steps(g, tw);
+        if constexpr (kSplit) work_share(g, rank, a.split);
         return g;
     };
     // ---- the CTA takes over the work of CTAs that have not started: while the loads of one item run, the
@@ -658,7 +624,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 l += sum[0].x + sum[0].y;
                 po ^= 1;
             };
-            const int full = nt - (g.half >> w & 1);
+            const int full = nt - (nt > 0 ? g.half >> w & 1 : 0);
             for (int j = 0; j < full && ok; ++j) step(j, std::integral_constant<int, 2>());
             if (full < nt && ok) step(full, std::integral_constant<int, 1>());
             // ---- O / l, rounded once

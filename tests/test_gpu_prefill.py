@@ -72,6 +72,16 @@ def test_prefill_matches_the_plain_form(name):
     check(out, lse, q, k, v, lq, lk)
 
 
+@pytest.mark.parametrize("lq,lk,H", [([2048], [2080], 1), ([3000], [3001], 3), ([1500, 1500], [1540, 1540], 1)])
+def test_shares_that_a_tile_does_not_reach(lq, lk, H):
+    """Few rows, one per token, after a prefix: some CTA's share of the keys has no step for the first tile, whose
+    last step elsewhere is half a step.  No wait runs out."""
+    q, k, v = inputs(lq, lk, H, H, 64, BF)
+    out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated(lq), P.cumulated(lk), want_lse=True)
+    check(out, lse, q, k, v, lq, lk)
+    B.fathom_wait_status()
+
+
 def test_thousands_of_sequences():
     """Two-row sequences between longer ones: the search for a tile's sequence goes over many of them."""
     lq = [2 + 70 * (i % 97 == 0) for i in range(1500)]
