@@ -652,7 +652,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                             }
                         }
                         cluster_store(to_dst + kSteps * 16 * 128, ok ? m : -CUDART_INF_F);
-                        cluster_store(to_dst + (kSteps * 16 + 1) * 128, l);
+                        cluster_store(to_dst + (kSteps * 16 + 1) * 128, ok ? l : 0.0f);
                     }
                     cluster_sync();   // every share is there
                     if (rank == dst) {
@@ -662,18 +662,23 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                             other[x] = x < a.split - 1 ? shares[x * per * kShare + kSteps * 16 * 32] : -CUDART_INF_F;
                             top = fmaxf(top, other[x]);
                         }
+                        // a share holds nothing when its l is 0; one whose scores are all NaN has m = -inf too, and
+                        // its l, which is NaN, has to stay
                         own = m == -CUDART_INF_F ? 0.0f : exp2f(m - top);
                         l *= own;
 #pragma unroll
                         for (int x = 0; x < 7; ++x) {
+                            const float part = x < a.split - 1 ? shares[x * per * kShare + (kSteps * 16 + 1) * 32] : 0.0f;
                             other[x] = other[x] == -CUDART_INF_F ? 0.0f : exp2f(other[x] - top);
-                            if (other[x] != 0.0f) l += other[x] * shares[x * per * kShare + (kSteps * 16 + 1) * 32];
+                            if (part != 0.0f) l += other[x] * part;
                         }
                         m = top;
                     }
                 }
                 const bool mine = at >= 0 && ok && (!kSplit || rank == dst);
-                const float inv = l > 0.0f ? own / l : 0.0f, inv_other = l > 0.0f ? 1.0f / l : 0.0f;
+                // of a row that sees no key 0, of one with a NaN among its scores NaN
+                const float inv_other = l == 0.0f ? 0.0f : 1.0f / l, inv = kSplit ? own * inv_other : inv_other;
+                const float none = l == l ? 0.0f : l;
                 const bool some = kSplit ? own != 0.0f && nt > 0 : seen > 0;   // O holds something for this row
                 const int row_at = mine ? at : -1;
                 float2 odd = make_float2(0.0f, 0.0f);   // 0 as long as the row is finite
@@ -689,7 +694,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     }
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        float v = some ? __uint_as_float(x[i]) * inv : 0.0f;
+                        float v = some ? __uint_as_float(x[i]) * inv : none;
                         if constexpr (kSplit) {
 #pragma unroll
                             for (int y = 0; y < 7; ++y)
@@ -725,7 +730,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         __syncwarp();
                     }
                 }
-                float lse = (kSplit ? l > 0.0f : seen > 0) ? ((m - kShift) + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+                float lse = l == 0.0f ? -CUDART_INF_F : ((m - kShift) + log2f(l)) * 0.6931471805599453f;
                 const bool odd_row = mine && !(odd.x + odd.y == 0.0f);
                 if (__any_sync(0xffffffffu, odd_row))
                     lse = odd_rows<kDtype>(a, g.k0 - g.from, g.lk + g.from, at, head, seen + g.from, odd_row, lse);

@@ -238,6 +238,40 @@ def test_an_odd_value_at_the_end_of_a_long_sequence(lq):
     B.fathom_wait_status()
 
 
+FEW_OR_MANY = {           # (new tokens, tokens, heads, KV heads, channels, type): the CTAs that share an item's keys
+    "2 shares": (130, 1500, 4, 1, 64, FP),
+    "4 shares": (7, 3000, 8, 4, 96, BF),
+    "8 shares": (5, 5000, 4, 2, 128, BF),
+    "8 shares, fp16": (3, 6000, 2, 1, 128, FP),
+    "one CTA": (2600, 2600, 8, 8, 64, BF),
+}
+
+
+@pytest.mark.parametrize("name", list(FEW_OR_MANY))
+@pytest.mark.parametrize("what", ["a query", "one key", "the first keys", "a share's keys", "the last keys"])
+def test_a_nan_that_a_query_sees_reaches_its_results(name, what):
+    """NaN in out and lse of every row that sees it, by however many CTAs its keys are shared; other rows as they were."""
+    lq, lk, H, Hkv, D, dt = FEW_OR_MANY[name]
+    q, k, v = inputs([lq], [lk], H, Hkv, D, dt)
+    o, z, tol, tol_z = P.prefill(q, k, v, [lq], [lk], D)
+    nan = torch.zeros(lq, H, dtype=torch.bool, device="cuda")
+    G = H // Hkv
+    if what == "a query":
+        q[lq // 2, H - 1, 3] = math.nan
+        nan[lq // 2, H - 1] = True
+    else:
+        steps = -(-lk // 128)
+        first, last = {"one key": (lk - 2, lk - 1), "the first keys": (0, 700), "a share's keys": (steps // 8 * 128, 2 * steps // 8 * 128),
+                       "the last keys": (7 * steps // 8 * 128, lk)}[what]
+        k[first:last, Hkv - 1, D - 1] = math.nan
+        sees = torch.arange(lq, device="cuda") + lk - lq >= first
+        nan[:, (Hkv - 1) * G:] = sees[:, None]
+    out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated([lq]), P.cumulated([lk]), want_lse=True)
+    assert bool(torch.isnan(out[nan]).all()) and bool(torch.isnan(lse[nan]).all())
+    assert bool(((out.double() - o).abs() <= tol)[~nan].all())
+    assert bool(((lse.double() - z).abs() <= tol_z)[~nan].all())
+
+
 def test_lengths_are_clamped_to_the_arrays():
     q, k, v = inputs([50, 50], [50, 50], 4, 2, 128, BF)
     want, _ = B.fathom_prefill_attn(q, k, v, P.cumulated([50, 50]))
