@@ -521,8 +521,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         // 2^32 as at 1, a fp16 weight must stay below 2^16
         constexpr float kLag = kDtype == FATHOM_F16 ? 8.0f : 32.0f;
         uint32_t ps = 0, po = 0;   // parities of the next wait for S, and for the last product into O
-        for (Work g; get_work(g);) {
-            if (!kSplit && g.t0 + (w ^ g.flip) * tw >= g.lq) continue;   // no rows
+        auto rows = [&](const Work &g, auto meet) {
+            if (!kSplit && g.t0 + (w ^ g.flip) * tw >= g.lq) return;   // no rows
             const int nt = w ? g.nt1 : g.nt0;
             const int token = g.t0 + (w ^ g.flip) * tw + (row >> a.lg_gp);
             const int at = token < g.lq ? g.q0 + token : -1;   // row of out; -1: behind the sequence
@@ -635,10 +635,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 constexpr int kShare = (kSteps * 16 + 2) * 32;
                 static_assert(!kSplit || 7 * kShare * 4 <= (int)sizeof(sm.kv), "shares reuse the ring");
                 const int per = 8 / (kSplit ? a.split : 1), dst = warp / per;   // warps per CTA, and this one's CTA
-                float *shares = reinterpret_cast<float *>(sm.kv) + warp % per * kShare + lane;   // += per * kShare each
-                float own = 1.0f, other[7];
+                [[maybe_unused]] float *shares = reinterpret_cast<float *>(sm.kv) + warp % per * kShare + lane;   // += per * kShare each
+                float own = 1.0f;
+                [[maybe_unused]] float other[7];
                 if constexpr (kSplit) {
-                    cluster_sync();   // no CTA reads its ring any more
+                    meet();   // no CTA reads its ring any more
                     if (rank != dst) {
                         const uint32_t to_dst = cluster_addr(smem_addr(shares + (rank < dst ? rank : rank - 1) * per * kShare), dst);
                         if (nt > 0) {
@@ -654,7 +655,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         cluster_store(to_dst + kSteps * 16 * 128, ok ? m : -CUDART_INF_F);
                         cluster_store(to_dst + (kSteps * 16 + 1) * 128, ok ? l : 0.0f);
                     }
-                    cluster_sync();   // every share is there
+                    meet();   // every share is there
                     if (rank == dst) {
                         float top = m;
 #pragma unroll
@@ -738,7 +739,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 if (mine && a.lse) a.lse[(int64_t)at * a.heads + head] = lse;
                 tc_fence_before();
             }
-        }
+        };
+        work_items(get_work, rows, [] { __syncwarp(); cluster_sync(); }, kSplit ? 2 : 0);
     }
     if (kSplit && warp >= 8) {   // the rows' warps meet twice; so do these
         __syncwarp();

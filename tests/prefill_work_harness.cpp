@@ -15,3 +15,14 @@ extern "C" void prefill_work(int lq, int lk, int tw, int t0, int flip, int rank,
     const int f[] = {g.nt0, g.nt1, g.steps, g.half, g.from, g.k0, g.lk, g.off};
     for (int i = 0; i < 8; ++i) out[i] = f[i];
 }
+
+// Cluster barriers that a row warp passes when its wait for work brings `items` items (0: it ran out at once).
+extern "C" int prefill_meetings(int items, int meetings) {
+    int passed = 0;
+    fathom::work_items([&](fathom::Work &) { return items-- > 0; },
+                       [&](const fathom::Work &, auto meet) {
+                           for (int i = 0; i < meetings; ++i) meet();
+                       },
+                       [&] { ++passed; }, meetings);
+    return passed;
+}

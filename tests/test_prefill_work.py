@@ -20,12 +20,13 @@ def work(tmp_path_factory):
     out = str(tmp_path_factory.mktemp("work") / "libwork.so")
     subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", CSRC,
                     os.path.join(HERE, "prefill_work_harness.cpp"), "-o", out], check=True)
-    f = ctypes.CDLL(out).prefill_work
+    lib = ctypes.CDLL(out)
 
     def get(*args):
         buf = (ctypes.c_int * len(FIELDS))()
-        f(*args, buf)
+        lib.prefill_work(*args, buf)
         return dict(zip(FIELDS, buf))
+    get.meetings = lib.prefill_meetings
     return get
 
 
@@ -78,3 +79,10 @@ def test_shares_cover_every_step_once_and_half_a_step_only_where_it_is(work, spl
                 assert half == (last_here and whole["half"] >> w & 1), (item, rank, w)
         for w in (0, 1):
             assert steps[w] == list(range(whole[f"nt{w}"])), item
+
+
+def test_a_row_warp_passes_every_cluster_barrier_with_and_without_its_item(work):
+    """The cluster's other warps wait there without a limit."""
+    assert work.meetings(1, 2) == 2
+    assert work.meetings(0, 2) == 2
+    assert work.meetings(0, 0) == work.meetings(5, 0) == 0       # no cluster
