@@ -12,8 +12,8 @@
 //   O = O + P V         P from tensor memory, V from shared memory
 // with c = log2(e) / sqrt(D) and the running maximum m, sum l of a softmax in one
 // pass.  The exponentials of a row are taken against a maximum that may be up to
-// 2^32 (bf16) or 2^8 (fp16) too small (m is raised, and O and l rescaled, only beyond
-// that): O, 64 KB of tensor memory, is touched by the row's own thread in a few tiles only.
+// 2^8 too small (m is raised, and O and l rescaled, only beyond that): O, 64 KB of
+// tensor memory, is touched by the row's own thread in a few tiles only.
 // A warp loads Q and a ring of K and V tiles by TMA; one elected lane of another
 // issues the matrix instructions; CTAs stay and take over the work of those that have
 // not started, so that one item's epilogue runs beside the next one's loads and
@@ -515,11 +515,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + kColS + w * 128, to = tmem + lanes + kColO + w * 128;
         const float c = 1.4426950408889634f / sqrtf((float)a.D);   // log2(e) / sqrt(D)
-        // fp16 weights are kept 2^7 larger (at most 2^15) so that fewer fall among its subnormals
-        constexpr float kShift = kDtype == FATHOM_F16 ? 7.0f : 0.0f;
-        // how far (log2) a row's maximum may rise above m before m follows: a bf16 weight is as exact at
-        // 2^32 as at 1, a fp16 weight must stay below 2^16
-        constexpr float kLag = kDtype == FATHOM_F16 ? 8.0f : 32.0f;
+        // How far (log2) a row's maximum may rise above m before m follows, and the power of two by which all
+        // weights are scaled.  A bf16 weight is as exact at any scale, and at most 1 here: O overflows only where
+        // the sum of the values themselves does (weights of up to 2^32, with a lag of 32, made an average of values
+        // of 2^100 infinite; ordinary scores do not rise by 2^8 above those of the first 64 keys).  fp16 weights are
+        // kept larger, at most 2^15, so that fewer fall among the subnormals.
+        constexpr float kLag = 8.0f, kShift = kDtype == FATHOM_F16 ? 7.0f : -8.0f;
         uint32_t ps = 0, po = 0;   // parities of the next wait for S, and for the last product into O
         auto rows = [&](const Work &g, auto meet) {
             if (!kSplit && g.t0 + (w ^ g.flip) * tw >= g.lq) return;   // no rows

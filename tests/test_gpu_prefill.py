@@ -238,6 +238,20 @@ def test_an_odd_value_at_the_end_of_a_long_sequence(lq):
     B.fathom_wait_status()
 
 
+@pytest.mark.parametrize("lq,lk", [(900, 900), (4, 5000)])
+@pytest.mark.parametrize("rising", [False, True])
+@pytest.mark.parametrize("power", [-120, -90, 100, 112])
+def test_values_near_the_ends_of_bf16(lq, lk, rising, power):
+    """Values of up to 4 x 2^112, of which fp32 holds the sum of 5000, and of no less than 2^-124, in whatever order
+    the scores come."""
+    q, k, v = inputs([lq], [lk], 2, 1, 128, BF)
+    ramp = torch.linspace(0.01, 6, lk, device="cuda")[:, None, None]
+    k = (k.float() * (ramp if rising else ramp.flip(0))).to(BF)
+    v = (v.sign() * v.abs().clamp(1 / 16, 4) * 2.0 ** power).to(BF)
+    out, lse = B.fathom_prefill_attn(q, k, v, P.cumulated([lq]), P.cumulated([lk]), want_lse=True)
+    check(out, lse, q, k, v, [lq], [lk])
+
+
 FEW_OR_MANY = {           # (new tokens, tokens, heads, KV heads, channels, type): the CTAs that share an item's keys
     "2 shares": (130, 1500, 4, 1, 64, FP),
     "4 shares": (7, 3000, 8, 4, 96, BF),
