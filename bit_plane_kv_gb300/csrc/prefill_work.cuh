@@ -60,18 +60,19 @@ FATHOM_WORK_HD void work_share(Work &g, int rank, int split) {
     g.off -= from * kKeys;
 }
 
-// A row warp's items, as long as next(g) brings one.  item(g, meet) calls `meet` at its cluster
-// barriers, `meetings` in all: a warp whose wait for its item ran out passes those that are left all
-// the same, for the cluster's other warps wait for it there without a limit.
-template <typename Next, typename Item, typename Sync>
-FATHOM_WORK_HD void work_items(Next next, Item item, Sync sync, int meetings) {
-    int left = meetings;
-    auto meet = [&] {
+// The cluster barriers that a row warp passes, `left` of them still to come.  A warp whose wait for its
+// item ran out passes the rest all the same: the cluster's other warps wait for it there without a limit.
+struct Meetings {
+    int left;
+    template <typename Sync>
+    FATHOM_WORK_HD void meet(Sync sync) {
         sync();
         --left;
-    };
-    for (Work g; next(g);) item(g, meet);
-    while (left > 0) meet();
-}
+    }
+    template <typename Sync>
+    FATHOM_WORK_HD void rest(Sync sync) {
+        while (left > 0) meet(sync);
+    }
+};
 
 }  // namespace fathom

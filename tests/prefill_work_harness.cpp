@@ -16,13 +16,12 @@ extern "C" void prefill_work(int lq, int lk, int tw, int t0, int flip, int rank,
     for (int i = 0; i < 8; ++i) out[i] = f[i];
 }
 
-// Cluster barriers that a row warp passes when its wait for work brings `items` items (0: it ran out at once).
-extern "C" int prefill_meetings(int items, int meetings) {
+// Cluster barriers that a warp passes, of `meetings`, when its item took it past `met` of them.
+extern "C" int prefill_meetings(int meetings, int met) {
     int passed = 0;
-    fathom::work_items([&](fathom::Work &) { return items-- > 0; },
-                       [&](const fathom::Work &, auto meet) {
-                           for (int i = 0; i < meetings; ++i) meet();
-                       },
-                       [&] { ++passed; }, meetings);
+    auto sync = [&] { ++passed; };
+    fathom::Meetings cluster{meetings};
+    for (int i = 0; i < met; ++i) cluster.meet(sync);
+    cluster.rest(sync);
     return passed;
 }
