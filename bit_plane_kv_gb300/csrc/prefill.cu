@@ -54,6 +54,8 @@ constexpr uint32_t kPanel = 128 * 128;   // bytes of 128 rows x 64 channels
 // Tensor memory columns: the two S (and P) tiles, then the two O tiles.
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 
+constexpr int kAgain = 16;   // places for items to be worked on again; a CTA turns to them when 8 are left
+
 template <int kPanels>   // 64-channel panels of a row: 1 (D <= 64) or 2
 struct PrefillSmem {
     static constexpr int kStages = kPanels == 2 ? 4 : 8;
@@ -62,9 +64,13 @@ struct PrefillSmem {
     alignas(1024) unsigned char kv[kStages][kTile];
     alignas(128) unsigned char out[8][32 * 128];   // a warp's rows of O, 64 channels, on their way out
     alignas(16) uint64_t answer[2];   // to the request for another CTA's work
-    Work work[2];                     // the item being worked on and the next
+    Work work[4];                     // the item being worked on, the next, and two before
     uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2], o_full[2];
-    uint64_t work_full[2], work_empty[2], answered, drained;
+    uint64_t work_full[2], work_empty[2], cleaned[2], answered, drained;
+    Work again[kAgain];               // items that have to be worked on again
+    int agains;                       // how many
+    int noted[4];                     // which of the items in work are among them
+    uint32_t odd[2];                  // kSplit: values that a tile's products read were set to 0
     uint32_t tmem;
 };
 
@@ -74,133 +80,121 @@ __device__ unsigned g_wait_expired;
 struct PrefillArgs {
     int seqs, heads, kv_heads, D, total_q, total_k, gp, lg_gp, groups, tiles;
     int split;  // CTAs that share a work item's keys
-    int64_t out_token, out_head, q_token, q_head, k_token, k_head, v_token, v_head;
+    int64_t out_token, out_head, v_token, v_head;
     const int32_t *cu_q, *cu_k;
-    const uint16_t *q, *k, *v;   // for rows that are computed again (below)
+    const uint16_t *v;   // for values that are put back (below)
     void *out;
     float *lse;
 };
 
 // ---------------------------------------------------------------- rows behind a query
 // P V runs over whole tiles, so a value row that a query does not see enters its sums
-// with the weight 0, and 0 x NaN and 0 x infinity are NaN.  A row whose result is not
-// finite is therefore looked at again: where a value row behind it, near enough to have
-// been in one of its tiles, holds a NaN or an infinity in a channel in which no row that
-// it sees just before holds a NaN, the row is computed anew by its warp.
-struct PlainRow {
-    const uint16_t *q, *k, *v;   // the query row, and the sequence's first key and value row
-    int64_t k_token, v_token;
-    int D, seen, lk;
-    uint16_t *out;
-};
+// with the weight 0, and 0 x NaN and 0 x infinity are NaN.  An item with a result that is not
+// finite is therefore worked on again, once: what is not finite among the value rows from the first one on that
+// some of its queries does not see, a few hundred at most, counts as 0 then (copy_rows), and
+// the rows that do see such a value get it back at their end (put_back).  Every other result
+// is, bit for bit, the one for zeros in their place, and it takes the same time whatever the number of
+// keys before.  With few rows (kSplit) that is done the first time (clean_rows).
+// (Tried: the values gone over always, by the warp that issues the products or by one or two
+// warps of their own, in shared memory or ahead of time in device memory: packed prompts 4
+// to 9 % slower.  The test of the results and the notes of what to do again cost 2 %.)
 
+// acc + 0 x, two values at once: NaN from the first x that is not finite on.
 template <int kDtype>
-__device__ __forceinline__ float wide(uint16_t x) {
-    return kDtype == FATHOM_BF16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x));
+__device__ __forceinline__ uint32_t add_zero_times(uint32_t x, uint32_t acc) {
+    if constexpr (kDtype == FATHOM_BF16) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+    else asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+    return acc;
 }
-
-// Channels with a NaN (or, kInf, an infinity) in value rows j0 .. j1 - 1.
-template <int kDtype, bool kInf>
-__device__ void odd_channels(const PlainRow &p, int j0, int j1, uint32_t (&odd)[FATHOM_MAX_D / 32]) {
+// The two values, 0 in the place of one that is not finite.
+template <int kDtype>
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t x) {
     constexpr uint32_t kTop = kDtype == FATHOM_BF16 ? 0x7f80u : 0x7c00u;   // infinity; a NaN is larger
-    for (int i = 0; i < FATHOM_MAX_D / 32; ++i) odd[i] = 0;
-    for (int j = j0; j < j1; ++j)
-        for (int c = 0; c < p.D; c += 8) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(p.v + j * p.v_token + c);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t x = w[e / 2] >> (e % 2 * 16) & 0x7fffu;
-                if (kInf ? x >= kTop : x > kTop) odd[c / 32] |= 1u << (c % 32 + e);
-            }
-        }
+    return ((x & 0x7fffu) < kTop ? x & 0xffffu : 0u) | ((x >> 16 & 0x7fffu) < kTop ? x & 0xffff0000u : 0u);
 }
 
-template <int kDtype>
-__device__ bool tainted(const PlainRow &p) {
-    uint32_t behind[FATHOM_MAX_D / 32], before[FATHOM_MAX_D / 32];
-    odd_channels<kDtype, true>(p, p.seen, min(p.lk, p.seen + 2 * kKeys), behind);
-    uint32_t any = 0;
-    for (uint32_t x : behind) any |= x;
-    if (!any) return false;
-    odd_channels<kDtype, false>(p, max(p.seen - kKeys, 0), p.seen, before);
-    any = 0;
-    for (int i = 0; i < FATHOM_MAX_D / 32; ++i) any |= behind[i] & ~before[i];
-    return any != 0;
-}
-
-// The row from the formula, in fp32, by a whole warp: 32 keys at a time, a key's score
-// per lane, then four channels per lane.  Returns the row's log-sum-exp.
-template <int kDtype>
-__device__ float plain_row(const PlainRow &p, int lane) {
-    const float scale = 1.0f / sqrtf((float)p.D);
-    float m = -CUDART_INF_F, l = 0.0f, o[4] = {};
-    for (int j0 = 0; j0 < p.seen; j0 += 32) {
-        const int n = min(p.seen - j0, 32);
-        float s = -CUDART_INF_F;
-        if (lane < n) {
-            const uint16_t *k = p.k + (j0 + lane) * p.k_token;
-            s = 0.0f;
-            for (int c = 0; c < p.D; c += 8) {
-                const uint4 a = *reinterpret_cast<const uint4 *>(p.q + c), b = *reinterpret_cast<const uint4 *>(k + c);
-                const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s = fmaf(wide<kDtype>((uint16_t)x[e]), wide<kDtype>((uint16_t)y[e]), s);
-                    s = fmaf(wide<kDtype>((uint16_t)(x[e] >> 16)), wide<kDtype>((uint16_t)(y[e] >> 16)), s);
-                }
-            }
-            s *= scale;
-        }
-        float top = s;
-#pragma unroll
-        for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-        top = fmaxf(top, m);
-        const float base = top == -CUDART_INF_F ? 0.0f : top, f = expf(m - base);
-        m = top;
-        const float w = expf(s - base);
-        float sum = w;
-#pragma unroll
-        for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-        l = fmaf(l, f, sum);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] *= f;
-        for (int e = 0; e < n; ++e) {
-            const float we = __shfl_sync(0xffffffffu, w, e);
-            if (4 * lane < p.D) {
-                const uint2 x = *reinterpret_cast<const uint2 *>(p.v + (j0 + e) * p.v_token + 4 * lane);
-                o[0] = fmaf(we, wide<kDtype>((uint16_t)x.x), o[0]);
-                o[1] = fmaf(we, wide<kDtype>((uint16_t)(x.x >> 16)), o[1]);
-                o[2] = fmaf(we, wide<kDtype>((uint16_t)x.y), o[2]);
-                o[3] = fmaf(we, wide<kDtype>((uint16_t)(x.y >> 16)), o[3]);
-            }
-        }
-    }
-    if (4 * lane < p.D)
-        *reinterpret_cast<uint2 *>(p.out + 4 * lane) =
-            make_uint2(pack2<kDtype>(o[0] / l, o[1] / l), pack2<kDtype>(o[2] / l, o[3] / l));
-    return m + logf(l);
-}
-
-// The warp's rows (lane: row `at` of out, `head`, `seen` keys of the sequence's lk, which
-// start at k0; odd: not finite) looked at again; returns the lane's log-sum-exp.
-template <int kDtype>
-__device__ __noinline__ float odd_rows(const PrefillArgs &a, int k0, int lk, int at, int head, int seen, bool odd,
-                                       float lse) {
+// Rows r0 .. r1 - 1 of a V tile in shared memory (kPanels panels of 128 bytes per row), by a
+// warp: whether there was something that is not finite; it is 0 now.  (Not inlined: that made the
+// loop around it, the one that issues the products, 10 % slower.)
+template <int kPanels, int kDtype>
+__device__ __noinline__ bool clean_rows(unsigned char *tile, int r0, int r1) {
     const int lane = threadIdx.x & 31;
-    auto row = [&](int t, int h, int n) {
-        const int hk = h / (a.heads / a.kv_heads);
-        return PlainRow{a.q + (int64_t)t * a.q_token + h * a.q_head, a.k + (int64_t)k0 * a.k_token + hk * a.k_head,
-                        a.v + (int64_t)k0 * a.v_token + hk * a.v_head, a.k_token, a.v_token, a.D, n, lk,
-                        (uint16_t *)a.out + (int64_t)t * a.out_token + h * a.out_head};
-    };
-    odd = odd && seen > 0 && tainted<kDtype>(row(at, head, seen));
-    for (unsigned todo = __ballot_sync(0xffffffffu, odd); todo; todo &= todo - 1) {
-        const int src = __ffs(todo) - 1;
-        const float z = plain_row<kDtype>(row(__shfl_sync(0xffffffffu, at, src), __shfl_sync(0xffffffffu, head, src),
-                                              __shfl_sync(0xffffffffu, seen, src)), lane);
-        if (lane == src) lse = z;
+    uint32_t acc[4] = {};
+#pragma unroll 4
+    for (int e = r0 * 8 + lane; e < r1 * 8; e += 32)
+#pragma unroll
+        for (int p = 0; p < kPanels; ++p) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(tile + p * kPanel + e * 16);
+            acc[0] = add_zero_times<kDtype>(x.x, acc[0]);
+            acc[1] = add_zero_times<kDtype>(x.y, acc[1]);
+            acc[2] = add_zero_times<kDtype>(x.z, acc[2]);
+            acc[3] = add_zero_times<kDtype>(x.w, acc[3]);
+        }
+    if (!__any_sync(0xffffffffu, ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0)) return false;
+    for (int e = r0 * 8 + lane; e < r1 * 8; e += 32)
+        for (int p = 0; p < kPanels; ++p) {
+            uint4 &x = *reinterpret_cast<uint4 *>(tile + p * kPanel + e * 16);
+            x = make_uint4(finite_or_zero<kDtype>(x.x), finite_or_zero<kDtype>(x.y), finite_or_zero<kDtype>(x.z),
+                           finite_or_zero<kDtype>(x.w));
+        }
+    fence_async_smem();
+    __syncwarp();
+    return true;
+}
+
+// A V tile, as TMA leaves it, from the rows at `v` by a warp, but rows from `first` on with 0 in the place of what
+// is not finite, and 0 from row `end` on.
+template <int kPanels, int kDtype>
+__device__ __noinline__ void copy_rows(unsigned char *tile, const uint16_t *v, int64_t v_token, int D, int first, int end) {
+    constexpr int kPieces = 8 * kPanels;   // of 16 bytes, per row
+#pragma unroll 8
+    for (int e = threadIdx.x & 31; e < kKeys * kPieces; e += 32) {
+        const int r = e / kPieces, c = e % kPieces;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < end && c * 8 < D) x = *reinterpret_cast<const uint4 *>(v + r * v_token + c * 8);
+        if (r >= first)
+            x = make_uint4(finite_or_zero<kDtype>(x.x), finite_or_zero<kDtype>(x.y), finite_or_zero<kDtype>(x.z),
+                           finite_or_zero<kDtype>(x.w));
+        *reinterpret_cast<uint4 *>(tile + c / 8 * kPanel + r * 128 + ((c % 8 ^ (r & 7)) << 4)) = x;
     }
-    return lse;
+    fence_async_smem();
+    __syncwarp();
+}
+
+template <int kDtype>
+__device__ __forceinline__ float wide(uint32_t x) {
+    return kDtype == FATHOM_BF16 ? __uint_as_float(x << 16) : __half2float(__ushort_as_half((unsigned short)x));
+}
+
+// The values that are not finite among the rows that a query sees from the item's first unseen one on, added
+// to its result: rows r0 .. r1 - 1 of an item (as of a Work that has all its keys), by a warp, four channels per lane.
+template <int kDtype>
+__device__ __noinline__ void put_back(const PrefillArgs &a, int group, int q0, int lq, int k0, int lk, int t0, int r0, int r1) {
+    const int c = 4 * (threadIdx.x & 31), head0 = group << a.lg_gp;
+    __syncwarp();   // the rows of out are there
+    if (c < a.D) {
+        const uint16_t *v = a.v + (int64_t)k0 * a.v_token + head0 / (a.heads / a.kv_heads) * a.v_head + c;
+        float sum[4] = {};   // 0, or not finite
+        for (int r = r0, j = max(t0 + lk - lq + 1, 0); r < r1; ++r) {
+            const int t = t0 + (r >> a.lg_gp), seen = min(lk, t + lk - lq + 1);
+            if (t >= lq) break;
+            for (; j < seen; ++j) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(v + j * a.v_token);
+                const float y[4] = {wide<kDtype>(x.x & 0xffffu), wide<kDtype>(x.x >> 16), wide<kDtype>(x.y & 0xffffu),
+                                    wide<kDtype>(x.y >> 16)};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!(fabsf(y[i]) < CUDART_INF_F)) sum[i] += y[i];
+            }
+            if (sum[0] == 0.0f && sum[1] == 0.0f && sum[2] == 0.0f && sum[3] == 0.0f) continue;
+            uint2 &o = *reinterpret_cast<uint2 *>((uint16_t *)a.out + (int64_t)(q0 + t) * a.out_token +
+                                                  (head0 + (r & (a.gp - 1))) * a.out_head + c);
+            const uint2 x = o;
+            o = make_uint2(pack2<kDtype>(wide<kDtype>(x.x & 0xffffu) + sum[0], wide<kDtype>(x.x >> 16) + sum[1]),
+                           pack2<kDtype>(wide<kDtype>(x.y & 0xffffu) + sum[2], wide<kDtype>(x.y >> 16) + sum[3]));
+        }
+    }
+    __syncwarp();
 }
 
 __device__ __forceinline__ int clamp_to(int x, int hi) { return min(max(x, 0), hi); }
@@ -238,9 +232,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             mbar_init(smem_addr(&sm.s_full[w]), 1);
             mbar_init(smem_addr(&sm.p_full[w]), 4);
             mbar_init(smem_addr(&sm.o_full[w]), 1);
+            mbar_init(smem_addr(&sm.cleaned[w]), 1);
             mbar_init(smem_addr(&sm.work_full[w]), 1);
             mbar_init(smem_addr(&sm.work_empty[w]), kLoadWarp);   // every other warp reads it
         }
+        for (int i = 0; i < 4; ++i) sm.noted[i] = 0;
+        sm.agains = 0;
         mbar_init(smem_addr(&sm.answered), 1);
         mbar_init(smem_addr(&sm.drained), 1);
         mbar_init_fence();
@@ -300,7 +297,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             }
             seen_before = __shfl_sync(0xffffffffu, upto, 31);
         }
-        g.lq = g.nt0 = g.nt1 = g.steps = g.q0 = g.k0 = g.lk = g.off = g.t0 = g.from = g.flip = g.half = 0;
+        g.lq = g.nt0 = g.nt1 = g.steps = g.q0 = g.k0 = g.lk = g.off = g.t0 = g.from = g.flip = g.half = g.again = 0;
         if (seq < 0) return g;   // the grid counts up to a tile pair per sequence more than needed
         g.q0 = __shfl_sync(0xffffffffu, q0, seq);
         g.lq = __shfl_sync(0xffffffffu, lq, seq);
@@ -317,14 +314,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     };
     // ---- the CTA takes over the work of CTAs that have not started: while the loads of one item run, the
     // load warp asks for the next, works out its geometry and leaves it for the other warps
-    int round = 0;
+    int round = 0;   // items published (read) so far
     auto get_work = [&](Work &g) {
         const int slot = round & 1;
         // a tile without keys waits here while the other goes over all of them (2^28 keys: about 3 s)
         ok = ok && warp_wait(smem_addr(&sm.work_full[slot]), (round >> 1) & 1, 5 * kWaitLimitNs);
         // every field from one lane: the compiler then knows that the warp branches as one (without that the
         // loops below ran 9 % slower)
-        const int *f = &sm.work[slot].group;
+        const int *f = &sm.work[round & 3].group;
         auto field = [&](int i) { return __shfl_sync(0xffffffffu, f[i], 0); };
         g.group = field(0); g.q0 = field(1); g.lq = field(2); g.k0 = field(3); g.lk = field(4);
         g.off = field(5); g.t0 = field(6); g.nt0 = field(7); g.nt1 = field(8); g.steps = field(9);
@@ -341,59 +338,122 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             const int slot = round & 1;
             ok = ok && warp_wait(smem_addr(&sm.work_empty[slot]), ((round >> 1) & 1) ^ 1);
             if (lane == 0 && ok) {
-                sm.work[slot] = g;
+                sm.work[round & 3] = g;
                 mbar_arrive(smem_addr(&sm.work_full[slot]));
             }
             __syncwarp();
             ++round;
         };
-        Work g = geometry(first_item);
-        publish(g);
-        for (int asked = 0; ok && g.steps >= 0; ++asked) {
-            if (elect_one()) {
-                if (!kSplit) {
-                    mbar_expect(smem_addr(&sm.answered), 16);
-                    request_cta(smem_addr(sm.answer), smem_addr(&sm.answered));
-                }
-                const int hq = g.group << a.lg_gp, hk = hq / (a.heads / a.kv_heads);
-                for (int w = 0; w < 2 && ok; ++w) {
-                    if ((w ? g.nt1 : g.nt0) == 0) continue;
-                    if (!(ok = mbar_wait(smem_addr(&sm.q_empty[w]), ((w ? nq1 : nq0) & 1) ^ 1))) break;
-                    const uint32_t bar = smem_addr(&sm.q_full[w]);
-                    mbar_expect(bar, kTile);
-                    for (int p = 0; p < kPanels; ++p)
-                        tma_load_3d(smem_addr(sm.q[w]) + p * kPanel, &map_q, bar, 64 * p, hq, g.q0 + g.t0 + (w ^ g.flip) * tw);
-                }
-                int s = st;
-                uint32_t t = turn;
-                for (int i = 0; i < 2 * g.steps && ok; ++i) {   // K_0, V_0, K_1, V_1, ...
-                    if (!(ok = mbar_wait(smem_addr(&sm.kv_empty[s]), t))) break;
-                    const uint32_t bar = smem_addr(&sm.kv_full[s]);
-                    mbar_expect(bar, kTile);
-                    for (int p = 0; p < kPanels; ++p)
-                        tma_load_3d(smem_addr(sm.kv[s]) + p * kPanel, (i & 1) ? &map_v : &map_k, bar, 64 * p, hk,
-                                    g.k0 + (i >> 1) * kKeys);
-                    if (++s == kStages) { s = 0; t ^= 1; }
-                }
-            }
-            __syncwarp();
-            ok = __all_sync(0xffffffffu, ok);
+        auto loaded = [&](const Work &g) {
             nq0 += g.nt0 > 0;
             nq1 += g.nt1 > 0;
             const int end = st + 2 * g.steps;
             turn ^= (uint32_t)(end / kStages) & 1u;
             st = end % kStages;
-            int item = -1;
-            if (!kSplit && ok) {
-                ok = warp_wait(smem_addr(&sm.answered), asked & 1);
-                if (ok) item = granted_cta(sm.answer[0], sm.answer[1]);
-                fence_async_smem();   // the answer is read before the next one is asked for
-                __syncwarp();
+        };
+        // Until all warps have read an item without rows: they are done with all others then.
+        auto all_done = [&] {
+            Work none = {};
+            publish(none);
+            ok = ok && warp_wait(smem_addr(&sm.work_empty[(round - 1) & 1]), ((round - 1) >> 1) & 1, 5 * kWaitLimitNs);
+        };
+        // The items noted so far, all over again: by the whole warp, and V tiles with rows behind a query not by TMA.
+        auto work_again = [&] {
+            const int n = __shfl_sync(0xffffffffu, sm.agains, 0);
+            for (int i = 0; i < 2 * n && ok; ++i) {
+                if (i == n) all_done();
+                const Work r = sm.again[i % n];
+                if (i >= n) {
+                    put_back<kDtype>(a, r.group, r.q0, r.lq, r.k0, r.lk, r.t0, 0, 2 * kRows);
+                    continue;
+                }
+                publish(r);
+                const int hq = r.group << a.lg_gp, hk = hq / (a.heads / a.kv_heads);
+                auto load = [&](uint32_t bar, unsigned char *to, const void *map, int head, int row) {
+                    if (lane == 0) {
+                        mbar_expect(bar, kTile);
+                        for (int p = 0; p < kPanels; ++p) tma_load_3d(smem_addr(to) + p * kPanel, map, bar, 64 * p, head, row);
+                    }
+                    __syncwarp();
+                };
+                for (int w = 0; w < 2 && ok; ++w) {
+                    if ((w ? r.nt1 : r.nt0) == 0) continue;
+                    if (!(ok = warp_wait(smem_addr(&sm.q_empty[w]), ((w ? nq1 : nq0) & 1) ^ 1))) break;
+                    load(smem_addr(&sm.q_full[w]), sm.q[w], &map_q, hq, r.q0 + r.t0 + (w ^ r.flip) * tw);
+                }
+                int s = st;
+                uint32_t t = turn;
+                for (int x = 0; x < 2 * r.steps && ok; ++x) {
+                    if (!(ok = warp_wait(smem_addr(&sm.kv_empty[s]), t))) break;
+                    const int j = x >> 1;
+                    if ((x & 1) && j >= work_first_edge(r)) {
+                        copy_rows<kPanels, kDtype>(sm.kv[s], a.v + (int64_t)(r.k0 + j * kKeys) * a.v_token + hk * a.v_head,
+                                                   a.v_token, a.D, work_first_unseen(r) - j * kKeys, r.lk - j * kKeys);
+                        if (lane == 0) mbar_arrive(smem_addr(&sm.kv_full[s]));
+                    } else {
+                        load(smem_addr(&sm.kv_full[s]), sm.kv[s], (x & 1) ? &map_v : &map_k, hk, r.k0 + j * kKeys);
+                    }
+                    if (++s == kStages) { s = 0; t ^= 1; }
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                loaded(r);
             }
-            if (item >= 0) g = geometry(item);
-            else g.steps = -1;
-            publish(g);
+            __syncwarp();
+            if (lane == 0) sm.agains = 0;
+            __syncwarp();
+        };
+        Work g = geometry(first_item);
+        int asked = 0;
+        for (bool more = true; ok && more;) {
+            do {
+                publish(g);
+                if (!ok) break;
+                if (elect_one()) {
+                    if (!kSplit) {
+                        mbar_expect(smem_addr(&sm.answered), 16);
+                        request_cta(smem_addr(sm.answer), smem_addr(&sm.answered));
+                    }
+                    const int hq = g.group << a.lg_gp, hk = hq / (a.heads / a.kv_heads);
+                    for (int w = 0; w < 2 && ok; ++w) {
+                        if ((w ? g.nt1 : g.nt0) == 0) continue;
+                        if (!(ok = mbar_wait(smem_addr(&sm.q_empty[w]), ((w ? nq1 : nq0) & 1) ^ 1))) break;
+                        const uint32_t bar = smem_addr(&sm.q_full[w]);
+                        mbar_expect(bar, kTile);
+                        for (int p = 0; p < kPanels; ++p)
+                            tma_load_3d(smem_addr(sm.q[w]) + p * kPanel, &map_q, bar, 64 * p, hq, g.q0 + g.t0 + (w ^ g.flip) * tw);
+                    }
+                    int s = st;
+                    uint32_t t = turn;
+                    for (int i = 0; i < 2 * g.steps && ok; ++i) {   // K_0, V_0, K_1, V_1, ...
+                        if (!(ok = mbar_wait(smem_addr(&sm.kv_empty[s]), t))) break;
+                        const uint32_t bar = smem_addr(&sm.kv_full[s]);
+                        mbar_expect(bar, kTile);
+                        for (int p = 0; p < kPanels; ++p)
+                            tma_load_3d(smem_addr(sm.kv[s]) + p * kPanel, (i & 1) ? &map_v : &map_k, bar, 64 * p, hk,
+                                        g.k0 + (i >> 1) * kKeys);
+                        if (++s == kStages) { s = 0; t ^= 1; }
+                    }
+                }
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, ok);
+                loaded(g);
+                int item = -1;
+                if (!kSplit && ok) {
+                    ok = warp_wait(smem_addr(&sm.answered), asked++ & 1);
+                    if (ok) item = granted_cta(sm.answer[0], sm.answer[1]);
+                    fence_async_smem();   // the answer is read before the next one is asked for
+                    __syncwarp();
+                }
+                more = item >= 0;
+                if (more) g = geometry(item);
+            } while (ok && more && (kSplit || __shfl_sync(0xffffffffu, sm.agains, 0) < kAgain - 8));
+            if (!kSplit && ok) {
+                all_done();
+                work_again();
+            }
         }
+        g.steps = -1;
+        publish(g);
         if (!ok) {   // the copies in flight land before the CTA ends
             const unsigned long long t0 = global_ns();
             while (global_ns() - t0 < 10000000ull) {}
@@ -441,12 +501,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const uint32_t q_full = smem_addr(sm.q_full), q_empty = smem_addr(sm.q_empty), p_full = smem_addr(sm.p_full);
         int cur = 0;                                // the ring's stages in turn: K_0, V_0, K_1, V_1, ...
         uint32_t pc = 0, pq0 = 0, pq1 = 0, pp0 = 0, pp1 = 0;   // parities of the next wait on each barrier
-        for (Work g; get_work(g);) {
-            if (g.steps == 0) continue;
+        auto products = [&](const Work &g) {   // of an item
             const int tail = g.lk - (g.steps - 1) * kKeys;   // live rows of the last V tile
+            [[maybe_unused]] uint32_t odd = 0;
             ok = warp_wait(full + 8 * cur, pc) && (g.nt0 == 0 || warp_wait(q_full, pq0)) &&
                  (g.nt1 == 0 || warp_wait(q_full + 8, pq1));
-            if (!ok) break;
+            if (!ok) return;
             pq0 ^= g.nt0 > 0;
             pq1 ^= g.nt1 > 0;
             if (elect_one()) {
@@ -469,6 +529,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 pc = pk;
                 const bool more = j + 1 < g.steps;
                 if (!(ok = warp_wait(full + 8 * sv, pv) && (!more || warp_wait(full + 8 * sk, pk)))) break;
+                if constexpr (kSplit) {
+                    if (j >= work_first_edge(g)) {
+                        const EdgeRows e = work_edge(g, j);
+                        odd |= clean_rows<kPanels, kDtype>(sm.kv[sv], e.r0, e.r1);
+                    }
+                }
                 if (!more && tail < kKeys) {
                     // rows behind the sequence's end: their weights are 0, and 0 x NaN would not be
                     for (int e = tail * 8 + lane; e < kKeys * 8; e += 32)
@@ -485,6 +551,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         values(0, sv, j == 0, j + 1 == g.nt0 && (g.half & 1));
                         if (j + 1 < g.nt0) scores(0, sk, j + 2 == g.nt0 && (g.half & 1));
                         if (j + 2 == g.nt0) mma_commit(q_empty);
+                        if (kSplit && j + 1 == g.nt0) {
+                            sm.odd[0] = odd;
+                            mbar_arrive(smem_addr(&sm.cleaned[0]));
+                        }
                     }
                     __syncwarp();
                 }
@@ -497,6 +567,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         mma_commit(empty + 8 * sv);
                         if (j + 1 < g.nt1) scores(1, sk, j + 2 == g.nt1 && (g.half & 2));
                         if (j + 2 == g.nt1) mma_commit(q_empty + 8);
+                        if (kSplit && j + 1 == g.nt1) {
+                            sm.odd[1] = odd;
+                            mbar_arrive(smem_addr(&sm.cleaned[1]));
+                        }
                         if (more) mma_commit(empty + 8 * sk);
                     }
                 } else if (elect_one()) {
@@ -505,6 +579,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 }
                 __syncwarp();
             }
+        };
+        for (Work g; ok && get_work(g);) {
+            if (g.steps == 0) continue;
+            products(g);
         }
         __syncwarp();
         if (elect_one()) mma_commit(smem_addr(&sm.drained));
@@ -526,7 +604,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         // (a plain loop here: with the items' code in a function of its own, tiles without rows held up the other
         // tile: 1000 prompts of 16 tokens 132 -> 191 us)
         for (Work g; get_work(g);) {
-            if (!kSplit && g.t0 + (w ^ g.flip) * tw >= g.lq) continue;   // no rows
+            // no rows (anything before this `continue` makes packed prompts 10 % slower)
+            if (!kSplit && g.t0 + (w ^ g.flip) * tw >= g.lq) continue;
             const int nt = w ? g.nt1 : g.nt0;
             const int token = g.t0 + (w ^ g.flip) * tw + (row >> a.lg_gp);
             const int at = token < g.lq ? g.q0 + token : -1;   // row of out; -1: behind the sequence
@@ -633,10 +712,15 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             if (full < nt && ok) step(full, std::integral_constant<int, 1>());
             // ---- O / l, rounded once
             ok = ok && (nt == 0 || warp_wait(smem_addr(&sm.o_full[w]), po ^ 1));
+            [[maybe_unused]] bool cleaned = false;   // kSplit: values that these rows' products read were set to 0
+            if (kSplit && nt > 0) {
+                ok = ok && warp_wait(smem_addr(&sm.cleaned[w]), 0);
+                cleaned = ok && sm.odd[w];
+            }
             if (ok || kSplit) {
                 tc_fence_after();
-                // kSplit: the other CTAs' (O, m, l) of these rows, [share][channel or m or l][row of the warp]
-                constexpr int kShare = (kSteps * 16 + 2) * 32;
+                // kSplit: the other CTAs' (O, m, l, cleaned) of these rows, [share][channel, then those][row of the warp]
+                constexpr int kShare = (kSteps * 16 + 3) * 32;
                 static_assert(!kSplit || 7 * kShare * 4 <= (int)sizeof(sm.kv), "shares reuse the ring");
                 const int per = 8 / (kSplit ? a.split : 1), dst = warp / per;   // warps per CTA, and this one's CTA
                 [[maybe_unused]] float *shares = reinterpret_cast<float *>(sm.kv) + warp % per * kShare + lane;   // += per * kShare each
@@ -658,6 +742,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         }
                         cluster_store(to_dst + kSteps * 16 * 128, ok ? m : -CUDART_INF_F);
                         cluster_store(to_dst + (kSteps * 16 + 1) * 128, ok ? l : 0.0f);
+                        cluster_store(to_dst + (kSteps * 16 + 2) * 128, cleaned ? 1.0f : 0.0f);
                     }
                     cluster.meet(cluster_sync);   // every share is there
                     if (rank == dst) {
@@ -676,6 +761,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                             const float part = x < a.split - 1 ? shares[x * per * kShare + (kSteps * 16 + 1) * 32] : 0.0f;
                             other[x] = other[x] == -CUDART_INF_F ? 0.0f : exp2f(other[x] - top);
                             if (part != 0.0f) l += other[x] * part;
+                            if (x < a.split - 1) cleaned |= shares[x * per * kShare + (kSteps * 16 + 2) * 32] != 0.0f;
                         }
                         m = top;
                     }
@@ -708,7 +794,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         x[i] = __float_as_uint(v);
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
+                    for (int i = 0; i < (kSplit ? 0 : 16); ++i)
                         odd = fma2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
                                    make_float2(0.0f, 0.0f), odd);
 #pragma unroll
@@ -735,12 +821,21 @@ prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         __syncwarp();
                     }
                 }
-                float lse = l == 0.0f ? -CUDART_INF_F : ((m - kShift) + log2f(l)) * 0.6931471805599453f;
-                const bool odd_row = mine && !(odd.x + odd.y == 0.0f);
-                if (__any_sync(0xffffffffu, odd_row))
-                    lse = odd_rows<kDtype>(a, g.k0 - g.from, g.lk + g.from, at, head, seen + g.from, odd_row, lse);
-                __syncwarp();
+                const float lse = l == 0.0f ? -CUDART_INF_F : ((m - kShift) + log2f(l)) * 0.6931471805599453f;
                 if (mine && a.lse) a.lse[(int64_t)at * a.heads + head] = lse;
+                if constexpr (kSplit) {
+                    if (__any_sync(0xffffffffu, cleaned && ok && rank == dst))
+                        put_back<kDtype>(a, g.group, g.q0, g.lq, g.k0 - g.from, g.lk + g.from, g.t0, 32 * warp, 32 * warp + 32);
+                } else if (__any_sync(0xffffffffu, mine && !(odd.x + odd.y == 0.0f))) {
+                    // noted once, by the first warp of the item that comes here
+                    const int at = (round - 1) & 3;
+                    if (lane == 0 && !sm.work[at].again && atomicExch(&sm.noted[at], round) != round) {
+                        Work &r = sm.again[atomicAdd(&sm.agains, 1)];
+                        r = sm.work[at];
+                        r.again = 1;
+                    }
+                    __syncwarp();
+                }
                 tc_fence_before();
             }
         }
@@ -858,9 +953,8 @@ int launch_prefill_attn(const fathom_prompts &p, const void *q, const void *k, c
     a.gp = 1 << a.lg_gp;
     a.groups = p.heads / a.gp;
     a.out_token = p.out_token; a.out_head = p.out_head;
-    a.q_token = p.q_token; a.q_head = p.q_head; a.k_token = p.k_token; a.k_head = p.k_head;
     a.v_token = p.v_token; a.v_head = p.v_head;
-    a.q = (const uint16_t *)q; a.k = (const uint16_t *)k; a.v = (const uint16_t *)v;
+    a.v = (const uint16_t *)v;
     a.cu_q = cu_q; a.cu_k = cu_k; a.out = out; a.lse = lse;
     // pairs of tiles, at most: exact for one sequence
     const long long tiles = ((long long)p.total_q * a.gp + (2LL * kRows - 1) * p.seqs) / (2 * kRows);

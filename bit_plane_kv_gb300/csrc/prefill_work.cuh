@@ -25,6 +25,7 @@ struct alignas(16) Work {
     int from;       // keys of the sequence before k0 (shares of a cluster: those of other CTAs)
     int flip;       // rows for one tile only: whether tile 1 takes them
     int half;       // bit w: tile w's last step has 64 keys or fewer and is worked on as half a step
+    int again;      // worked on a second time, values that are not finite counting as 0
 };
 
 FATHOM_WORK_HD int work_min(int a, int b) { return a < b ? a : b; }
@@ -58,6 +59,26 @@ FATHOM_WORK_HD void work_share(Work &g, int rank, int split) {
     g.k0 += from * kKeys;
     g.lk -= from * kKeys;
     g.off -= from * kKeys;
+}
+
+// The item's first key that some query of it does not see.
+FATHOM_WORK_HD int work_first_unseen(const Work &g) { return work_max(g.t0 + g.off + 1, 0); }
+
+// The first step that reads value rows which some query of it does not see.
+FATHOM_WORK_HD int work_first_edge(const Work &g) { return work_first_unseen(g) / kKeys; }
+
+// Those rows of such a step (j * 128 and on): r0 .. r1 - 1 of the sequence, and r1 .. r2 - 1 behind its end.
+struct EdgeRows {
+    int r0, r1, r2;
+};
+FATHOM_WORK_HD EdgeRows work_edge(const Work &g, int j) {
+    const bool half0 = j >= g.nt0 || (j + 1 == g.nt0 && (g.half & 1));
+    const bool half1 = j >= g.nt1 || (j + 1 == g.nt1 && (g.half & 2));
+    EdgeRows e;
+    e.r2 = half0 && half1 ? kKeys / 2 : kKeys;
+    e.r0 = work_min(work_max(work_first_unseen(g) - j * kKeys, 0), e.r2);
+    e.r1 = work_min(work_max(g.lk - j * kKeys, e.r0), e.r2);
+    return e;
 }
 
 // The cluster barriers that a row warp passes, `left` of them still to come.  A warp whose wait for its

@@ -16,6 +16,25 @@ extern "C" void prefill_work(int lq, int lk, int tw, int t0, int flip, int rank,
     for (int i = 0; i < 8; ++i) out[i] = f[i];
 }
 
+// The steps of that share that read value rows which some query does not see: out[4 n ..] = step, r0, r1, r2; how many.
+extern "C" int prefill_edges(int lq, int lk, int tw, int t0, int flip, int rank, int split, int *out) {
+    fathom::Work g = {};
+    g.lq = lq;
+    g.lk = lk;
+    g.off = lk - lq;
+    g.t0 = t0;
+    g.flip = flip;
+    fathom::work_steps(g, tw);
+    if (split > 1) fathom::work_share(g, rank, split);
+    int n = 0;
+    for (int j = fathom::work_first_edge(g); j < g.steps; ++j, ++n) {
+        const fathom::EdgeRows e = fathom::work_edge(g, j);
+        const int f[] = {j, e.r0, e.r1, e.r2};
+        for (int i = 0; i < 4; ++i) out[4 * n + i] = f[i];
+    }
+    return n;
+}
+
 // Cluster barriers that a warp passes, of `meetings`, when its item took it past `met` of them.
 extern "C" int prefill_meetings(int meetings, int met) {
     int passed = 0;

@@ -238,6 +238,80 @@ def test_an_odd_value_at_the_end_of_a_long_sequence(lq):
     B.fathom_wait_status()
 
 
+ODD = {                   # (new tokens, tokens, heads, KV heads, channels, type)
+    "tiles of 32 tokens": ([300, 77], [300, 500], 8, 2, 128, BF),
+    "one row per token, fp16": ([513, 40], [700, 40], 2, 2, 64, FP),
+    "tiles of one token": ([9], [70], 160, 1, 72, FP),
+    "single tiles in turn": ([1 + i % 30 for i in range(200)], [1 + i % 30 + i % 7 for i in range(200)], 8, 8, 96, BF),
+    "more items than are noted at once": ([1 + i % 16 for i in range(1500)], [1 + i % 16 + i % 3 for i in range(1500)], 4, 4,
+                                          64, BF),
+    "queries that see nothing": ([200, 60], [90, 300], 4, 2, 128, BF),
+    "2 shares": ([300], [1500], 4, 1, 64, BF),
+    "4 shares": ([129, 7], [3000, 9], 3, 3, 128, FP),
+    "8 shares": ([16, 130], [300, 6000], 4, 1, 96, BF),
+}
+
+
+@pytest.mark.parametrize("name", list(ODD))
+@pytest.mark.parametrize("count", [1, 7, 60])
+def test_values_that_are_not_finite_reach_the_queries_that_see_them(name, count):
+    """A query that sees such values has their sum in the channel; every other result is, bit for bit, the one for
+    zeros in their place."""
+    lq, lk, H, Hkv, D, dt = ODD[name]
+    count = max(count, 3 * len(lq) * (count == 60))          # in most sequences, where there are many
+    q, k, v = inputs(lq, lk, H, Hkv, D, dt, q_scale=0.25)    # weights far from underflow
+    g = torch.Generator().manual_seed(count)
+    seq = torch.randint(len(lk), (count,), generator=g).tolist()
+    first_k, first_q = [sum(lk[:s]) for s in range(len(lk))], [sum(lq[:s]) for s in range(len(lq))]
+    sums = torch.zeros(sum(lq), H, D, device="cuda")
+    for i, s in enumerate(seq):
+        # near the end, where some queries see the key and some do not
+        key = lk[s] - 1 - int(torch.randint(min(lk[s], 2 * lq[s]), (1,), generator=g))
+        h, c = int(torch.randint(Hkv, (1,), generator=g)), int(torch.randint(D, (1,), generator=g))
+        bad = (math.nan, math.inf, -math.inf)[i % 3]
+        v[first_k[s] + key, h, c] = bad
+    for s in set(seq):
+        for h in range(Hkv):
+            odd = v[first_k[s]:first_k[s] + lk[s], h].float()
+            odd = torch.where(torch.isfinite(odd), 0.0, odd).cumsum(0)       # of the keys up to each one
+            sees = torch.arange(lq[s], device="cuda") + lk[s] - lq[s]
+            part = torch.where((sees >= 0)[:, None], odd[sees.clamp(min=0)], 0.0)
+            sums[first_q[s]:first_q[s] + lq[s], h * (H // Hkv):(h + 1) * (H // Hkv)] = part[:, None]
+    zeros = torch.where(torch.isfinite(v), v, torch.zeros_like(v))
+    cq, ck = P.cumulated(lq), P.cumulated(lk)
+    want, lse = B.fathom_prefill_attn(q, k, zeros, cq, ck, want_lse=True)
+    check(want, lse, q, k, zeros, lq, lk)
+    out, lse2 = B.fathom_prefill_attn(q, k, v, cq, ck, want_lse=True)
+    want = want.float() + sums
+    assert not torch.isfinite(want).all()
+    assert torch.equal(torch.nan_to_num(out.float(), nan=7e30), torch.nan_to_num(want, nan=7e30))
+    assert torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("lq,lk,H", [(20000, 600000, 2), (10000, 300000, 8)])
+def test_odd_values_of_a_long_sequence_with_more_work_than_the_device_holds(lq, lk, H):
+    """Rows next to such values cost no more than others, however many keys they see: no wait of the work that
+    follows runs out."""
+    D = 64
+    q, k, v = inputs([lq], [lk], H, H, D, BF, q_scale=0.25)
+    cq, ck = P.cumulated([lq]), P.cumulated([lk])
+    rows = [lk - 1, lk - 7000, lk - lq + 130]
+    v[rows, 0] = 0.0
+    want, lse = B.fathom_prefill_attn(q, k, v, cq, ck, want_lse=True)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    for row, bad in zip(rows, (math.nan, math.inf, -math.inf)):
+        v[row, 0] = bad
+    start.record()
+    out, lse2 = B.fathom_prefill_attn(q, k, v, cq, ck, want_lse=True)
+    end.record()
+    B.fathom_wait_status()
+    assert start.elapsed_time(end) < 1000
+    seen = [row - (lk - lq) for row in rows]                 # the first query that sees each
+    assert torch.equal(out[:, 1:], want[:, 1:]) and torch.equal(lse, lse2)
+    assert torch.equal(out[:seen[2], 0], want[:seen[2], 0])
+    assert bool((out[seen[2]:seen[1], 0] == -math.inf).all()) and bool(torch.isnan(out[seen[1]:, 0]).all())
+
+
 @pytest.mark.parametrize("lq,lk", [(900, 900), (4, 5000)])
 @pytest.mark.parametrize("rising", [False, True])
 @pytest.mark.parametrize("power", [-120, -90, 100, 112])

@@ -27,6 +27,12 @@ def work(tmp_path_factory):
         lib.prefill_work(*args, buf)
         return dict(zip(FIELDS, buf))
     get.meetings = lib.prefill_meetings
+
+    def edges(*args):
+        buf = (ctypes.c_int * 64)()
+        n = lib.prefill_edges(*args, buf)
+        return {buf[4 * i]: tuple(buf[4 * i + 1:4 * i + 4]) for i in range(n)}
+    get.edges = edges
     return get
 
 
@@ -79,6 +85,27 @@ def test_shares_cover_every_step_once_and_half_a_step_only_where_it_is(work, spl
                 assert half == (last_here and whole["half"] >> w & 1), (item, rank, w)
         for w in (0, 1):
             assert steps[w] == list(range(whole[f"nt{w}"])), item
+
+
+@pytest.mark.parametrize("split", [1, 2, 8])
+def test_value_rows_that_a_query_does_not_see_are_looked_over(work, split):
+    """Every row that a tile's products read and that some query of the item does not see, those behind the
+    sequence's end apart; in the steps between the first of them and the last they lie without a gap."""
+    for n, item in enumerate(_items()):
+        if split > 1 and n % 5:
+            continue
+        lq, lk, tw, t0, flip = item
+        fewest = max(0, t0 + lk - lq + 1)                       # keys that the item's first query sees
+        for rank in range(split):
+            g, edges = work(*item, rank, split), work.edges(*item, rank, split)
+            for j in range(g["steps"]):
+                key0 = g["from_"] + 128 * j
+                used = max(64 if g["half"] >> w & 1 and j + 1 == g[f"nt{w}"] else 128 for w in (0, 1) if j < g[f"nt{w}"])
+                r0, r1, r2 = edges.get(j, (used, used, used))
+                assert 0 <= r0 <= r1 <= r2 == used, (item, rank, j)
+                assert r0 == min(max(0, fewest - key0), used)
+                assert r1 == min(max(lk - key0, r0), used)
+                assert j + 1 == g["steps"] or r1 == r2 == 128
 
 
 def test_a_row_warp_passes_every_cluster_barrier_with_and_without_its_item(work):
