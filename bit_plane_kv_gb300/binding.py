@@ -655,6 +655,13 @@ def _ok(t, dtype, shape):
     return t is not None and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
 
 
+def _fit32(**counts):
+    """The library's counts are 32-bit, and ctypes would cut a larger one off without a word."""
+    for name, x in counts.items():
+        if not -(1 << 31) <= x < 1 << 31:
+            raise ValueError(f"{name}: {x} does not fit 32 bits")
+
+
 def fathom_prefill_attn(q, k, v, cu_q, cu_k=None, out=None, lse=None, want_lse=False, stream=None):
     """Causal attention of packed prompts (or of their next chunks): q [Tq][heads][D],
     k, v [Tk][kv_heads][D] bf16 or fp16, any strides with the last axis contiguous;
@@ -667,6 +674,8 @@ def fathom_prefill_attn(q, k, v, cu_q, cu_k=None, out=None, lse=None, want_lse=F
     Tq, H, D = q.shape
     Tk, Hkv, _ = k.shape
     dt = q.dtype
+    if Tq >> 31 or Tk >> 31:
+        _fit32(query_tokens=Tq, key_tokens=Tk)
     (qt, qh, qc), (kt, kh, kc) = q.stride(), k.stride()
     if not (dt in _ROW_TYPES and qc == 1 and q.is_cuda):
         _check_strided(q, "q", _ROW_TYPES, (Tq, H, D))
@@ -708,6 +717,7 @@ def make_pages(k_pages, page_table) -> Pages:
     if k_pages.dtype not in _ROW_TYPES:
         raise TypeError(f"k_pages: dtype {k_pages.dtype} not in {tuple(_ROW_TYPES)}")
     n, H, P, D = k_pages.shape
+    _fit32(pages=n, page_tokens=P, max_pages=page_table.shape[1])
     sn, sh, sp, _ = k_pages.stride()
     return Pages(page_table.shape[0], H, D, _ROW_TYPES[k_pages.dtype], P, n, page_table.shape[1], sn, sh, sp)
 
@@ -767,6 +777,8 @@ def fathom_paged_append(pages: Pages, k_pages, v_pages, page_table, k_new, v_new
     if k_new is None or k_new.dim() != 3:
         raise ValueError("k_new: expected [tokens][kv_heads][D]")
     T = k_new.shape[0]
+    if T >> 31:
+        _fit32(new_tokens=T)
     _check_strided(k_new, "k_new", (dtype,), (T, H, D))
     _check_strided(v_new, "v_new", (dtype,), (T, H, D))
     stride = k_new.stride()
@@ -836,6 +848,7 @@ def fathom_paged_evict(pages: Pages, k_pages, v_pages, page_table, lens, mass, k
     _check(dst_table, "dst_table", (torch.int32,))
     if dst_table.dim() != 2 or dst_table.shape[0] != seqs:
         raise ValueError(f"dst_table: shape {tuple(dst_table.shape)} is not [{seqs}][pages]")
+    _fit32(keep=keep, n_sink=int(n_sink), n_recent=int(n_recent), dst_pages=dst_table.shape[1])
     if mass_out is None:
         mass_out = mass
     _check_mass(mass_out, "mass_out", units, keep)

@@ -287,3 +287,27 @@ def test_rows_as_pages_names_every_row_once():
         B.rows_as_pages(rows, H, 48)
     with pytest.raises(ValueError):
         B.rows_as_pages(rows, 4, P)
+
+
+def test_counts_beyond_32_bits_are_refused(no_library):
+    """The library's counts are 32-bit; a larger one must not wrap around into one that it accepts."""
+    big = (1 << 32) + 5
+    kw = _prefill_args()
+    kw.update(q=z(1, 8, 64, dtype=BF).expand(big, 8, 64), out=z(1, 8, 64, dtype=BF).expand(big, 8, 64), lse=None)
+    with pytest.raises(ValueError, match="32 bits"):
+        B.fathom_prefill_attn(**kw)
+    kw = _prefill_args()
+    kw.update(k=z(1, 2, 64, dtype=BF).expand(big, 2, 64), v=z(1, 2, 64, dtype=BF).expand(big, 2, 64))
+    with pytest.raises(ValueError, match="32 bits"):
+        B.fathom_prefill_attn(**kw)
+    with pytest.raises(ValueError, match="32 bits"):
+        B.make_pages(z(1, 2, 16, 64, dtype=BF).expand(big, 2, 16, 64), z(3, 4, dtype=I32))
+    kw = _append_args()
+    kw.update(k_new=z(1, 2, 64, dtype=BF).expand(big, 2, 64), v_new=z(1, 2, 64, dtype=BF).expand(big, 2, 64))
+    with pytest.raises(ValueError, match="32 bits"):
+        B.fathom_paged_append(**kw)
+    for name in ("keep", "n_sink", "n_recent"):
+        kw = _evict_args()
+        kw.update({name: (1 << 32) + kw.get(name, 4)}, mass_out=z(6, 48), kept_idx=None)
+        with pytest.raises(ValueError, match="32 bits"):
+            B.fathom_paged_evict(**kw)
