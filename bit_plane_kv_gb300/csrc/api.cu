@@ -37,23 +37,25 @@ int launch_status(const char *what) {
 
 static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-bool smem_attr_needed(const void *func, size_t bytes) {
-    struct Entry { const void *f; int dev; size_t bytes; };
+// Set before the lock is given back: another thread's first call of the same kernel must find it set.
+void raise_func_attr(const void *func, cudaFuncAttribute attr, int value) {
+    struct Entry { const void *f; cudaFuncAttribute attr; int dev, value; };
     static std::mutex mu;
     static Entry table[64];
     static int used = 0;
     int dev = 0;
     cudaGetDevice(&dev);
     std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < used; ++i) {
-        if (table[i].f == func && table[i].dev == dev) {
-            if (table[i].bytes >= bytes) return false;
-            table[i].bytes = bytes;
-            return true;
-        }
+    int i = 0;
+    while (i < used && (table[i].f != func || table[i].attr != attr || table[i].dev != dev)) ++i;
+    if (i < used && table[i].value >= value) return;
+    if (cudaFuncSetAttribute(func, attr, value) != cudaSuccess) {
+        cudaGetLastError();   // the launch says what is wrong
+        return;
     }
-    if (used < 64) table[used++] = Entry{func, dev, bytes};
-    return true;
+    if (i == used && used == 64) return;   // set again the next time
+    table[i] = Entry{func, attr, dev, value};
+    if (i == used) ++used;
 }
 
 // Streaming multiprocessors of the current device (0 if no device answers).

@@ -312,8 +312,8 @@ int launch_paged_evict(const fathom_pages &p, void *kp, void *vp, const int32_t 
     attr[1].val.clusterDim.x = (unsigned)team;
     cfg.numAttrs = team > 1 ? 2 : 1;
     // the row loads in flight need the L1, of which the selection's shared memory would leave little
-    if (smem_attr_needed((const void *)evict_move_kernel, 0))
-        cudaFuncSetAttribute(evict_move_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxL1);
+    raise_func_attr((const void *)evict_move_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                    cudaSharedmemCarveoutMaxL1);
     e = cudaLaunchKernelEx(&cfg, evict_move_kernel, p, lg, team, slices, (int4 *)kp, (int4 *)vp, table, lens, keep, dst_table,
                            dst_pages, (const int32_t *)kept, mass, mass_stride, mass_out, mass_out_stride);
     if (e != cudaSuccess) { set_error("evict_move_kernel: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }

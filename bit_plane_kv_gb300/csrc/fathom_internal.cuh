@@ -204,13 +204,12 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     return cudaLaunchKernelEx(&cfg, kernel, (KArgs)args...);
 }
 
-// Raise a kernel's dynamic shared-memory limit once per (kernel, device, size);
-// later launches skip the driver call.
-bool smem_attr_needed(const void *func, size_t bytes);   // thread-safe cache lookup/insert
+// Raise an attribute of a kernel once per (kernel, device, value); later launches skip the
+// driver call.  Any number of threads.
+void raise_func_attr(const void *func, cudaFuncAttribute attr, int value);
 template <typename F>
-inline void ensure_smem(F *func, size_t bytes) {
-    if (smem_attr_needed((const void *)func, bytes))
-        cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+inline void ensure_smem(F *func, size_t bytes) {   // the kernel's dynamic shared-memory limit
+    raise_func_attr((const void *)func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
 // ---------------------------------------------------------------- launchers

@@ -506,6 +506,56 @@ print("same")
     assert r.returncode == 0 and r.stdout.strip() == "same", r.stdout + r.stderr[-2000:]
 
 
+def test_first_calls_of_a_process_by_several_threads_at_once():
+    """Every form of the kernels with large shared memory, called for the first time by eight threads together."""
+    code = """
+import sys, threading
+sys.path.insert(0, %r); sys.path.insert(0, %r)
+import torch
+from bit_plane_kv_gb300 import binding as B
+import paged_cases as P
+N = 8
+jobs = []
+for dt in (torch.bfloat16, torch.float16):
+    for D in (64, 96, 128):
+        x = torch.randn(3000, 3, D, device="cuda").to(dt)
+        for lq, lk in ((16, 3000), (300, 300)):                          # by clusters, and not
+            cq, ck = P.cumulated([lq]), P.cumulated([lk])
+            jobs.append(lambda s, x=x, lq=lq, lk=lk, cq=cq, ck=ck:
+                        B.fathom_prefill_attn(x[:lq, :1], x[:lk, 1:2], x[:lk, 2:], cq, ck, stream=s)[0])
+    for D in (64, 128):
+        for G in (4, 8):
+            kp, vp, table, _ = P.pool(1, 2, D, 16, 40, dt)
+            pages, q = B.make_pages(kp, table), torch.randn(2, G, D, device="cuda")
+            lens = torch.full((1,), 600, dtype=torch.int32, device="cuda")
+            for mass in (False, True):
+                jobs.append(lambda s, a=(pages, q, kp, vp, table, lens), G=G, mass=mass:
+                            B.fathom_paged_attn(*a, B.alloc_paged_workspace(a[0], G=G, mass=mass),
+                                                mass=torch.zeros(2, 640, device="cuda") if mass else None, stream=s))
+torch.cuda.synchronize()
+streams = [torch.cuda.Stream() for _ in range(N)]
+got, wrong, gate = [[None] * len(jobs) for _ in range(N)], [], threading.Barrier(N)
+
+def run(i):
+    for j, job in enumerate(jobs):
+        gate.wait()
+        try:
+            torch.cuda.set_device(0)
+            got[i][j] = job(streams[i])
+        except Exception as e:
+            wrong.append((j, repr(e)))
+
+threads = [threading.Thread(target=run, args=(i,)) for i in range(N)]
+[t.start() for t in threads], [t.join() for t in threads]
+torch.cuda.synchronize()
+assert not wrong, (len(wrong), wrong[:3])
+assert all(torch.equal(got[i][j], got[0][j]) for i in range(N) for j in range(len(jobs)))
+print("same")
+""" % (os.path.dirname(os.path.dirname(os.path.abspath(__file__))), os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stdout + r.stderr[-2000:]
+
+
 # ------------------------------------------------------------------ together
 def test_prompt_append_decode_evict_decode():
     """A serving loop: packed prompts, their rows into the pages, decode steps that gather mass,
