@@ -35,6 +35,12 @@ int launch_status(const char *what) {
     return FATHOM_OK;
 }
 
+int launch_failed(const char *what, cudaError_t e) {
+    cudaGetLastError();   // reported here, and not once more by the caller's next look at the last error
+    set_error("%s: %s", what, cudaGetErrorString(e));
+    return FATHOM_ECUDA;
+}
+
 static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Set before the lock is given back: another thread's first call of the same kernel must find it set.
@@ -390,7 +396,7 @@ int fathom_debug_status(int mode, uint64_t *first_failure) {
         debug_read_attn_plant();
     }
     const cudaError_t e = cudaDeviceSynchronize();
-    if (e != cudaSuccess) { set_error("debug_status: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }
+    if (e != cudaSuccess) return launch_failed("debug_status", e);
     first_failure[0] = debug_read_scan(mode == 1);
     first_failure[1] = debug_read_gather(mode == 1);
     first_failure[2] = debug_read_attn(mode == 1);
@@ -405,7 +411,7 @@ int fathom_debug_status(int mode, uint64_t *first_failure) {
 int fathom_wait_status(void) {
     g_err[0] = 0;
     const cudaError_t e = cudaDeviceSynchronize();
-    if (e != cudaSuccess) { set_error("wait_status: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }
+    if (e != cudaSuccess) return launch_failed("wait_status", e);
     const bool expired = wait_expired_prefill();
     const int rc = launch_status("wait_status");
     if (rc) return rc;

@@ -296,7 +296,7 @@ int launch_paged_evict(const fathom_pages &p, void *kp, void *vp, const int32_t 
     cfg.numAttrs = parts > 1 ? 2 : 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, parts, room, lens, mass, mass_stride, keep, n_sink,
                                        n_recent, kept, lens_out);
-    if (e != cudaSuccess) { set_error("evict_select_kernel: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }
+    if (e != cudaSuccess) return launch_failed("evict_select_kernel", e);
     // In place: CTAs of a team (8 would cost 5 us more at the start), then halves of the channels, until they fill
     // the device.  To other pages: CTAs per unit, until two waves of four per SM have work.
     const int chunk = kMoveThreads / (p.D / 8) * (kMoveUnroll / 2), chunks = (keep + chunk - 1) / chunk;
@@ -316,7 +316,7 @@ int launch_paged_evict(const fathom_pages &p, void *kp, void *vp, const int32_t 
                     cudaSharedmemCarveoutMaxL1);
     e = cudaLaunchKernelEx(&cfg, evict_move_kernel, p, lg, team, slices, (int4 *)kp, (int4 *)vp, table, lens, keep, dst_table,
                            dst_pages, (const int32_t *)kept, mass, mass_stride, mass_out, mass_out_stride);
-    if (e != cudaSuccess) { set_error("evict_move_kernel: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }
+    if (e != cudaSuccess) return launch_failed("evict_move_kernel", e);
     return launch_status("paged_evict");
 }
 

@@ -15,6 +15,7 @@ namespace fathom {
 // ---------------------------------------------------------------- errors
 void set_error(const char *fmt, ...);
 int launch_status(const char *what);   // FATHOM_OK or FATHOM_ECUDA (+ message)
+int launch_failed(const char *what, cudaError_t e);   // FATHOM_ECUDA (+ message), for a launch that returned e
 
 // ---------------------------------------------------------------- debug checks
 // A build with -DFATHOM_DEBUG checks, before each load or store whose index

@@ -801,12 +801,12 @@ int launch_paged_attn(const fathom_pages &p, int G, const float *q, const void *
         e = p.D <= 64 ? launch_dec_form<__nv_bfloat16, 64>(a, w.ctas, st) : launch_dec_form<__nv_bfloat16, 128>(a, w.ctas, st);
     else
         e = p.D <= 64 ? launch_dec_form<__half, 64>(a, w.ctas, st) : launch_dec_form<__half, 128>(a, w.ctas, st);
-    if (e != cudaSuccess) { set_error("paged_attn_kernel: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }
+    if (e != cudaSuccess) return launch_failed("paged_attn_kernel", e);
     if (mass) {
         const int units = p.seqs * p.kv_heads, want = (a.cap + 1023) / 1024, most = (w.ctas * 8 + units - 1) / units;
         e = launch_pdl(paged_mass_kernel, dim3(want < most ? want : most, units), dim3(256), 0, st, p, a.cap, a.logit_stride, G,
                        lens, (const float *)a.logits, (const float *)a.lse, mass, mass_stride);
-        if (e != cudaSuccess) { set_error("paged_mass_kernel: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }
+        if (e != cudaSuccess) return launch_failed("paged_mass_kernel", e);
     }
     return launch_status("paged_attn");
 }

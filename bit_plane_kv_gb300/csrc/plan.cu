@@ -420,7 +420,7 @@ int launch_plan(const fathom_shape &s, const float *q, const float *var, const i
                 cudaStream_t st) {
     const cudaError_t e = launch_pdl(plan_kernel, dim3(s.units), dim3(kPT), 0, st, s.units, s.n,
                                      cap_blocks(s), s.D, s.G, q, var, budget, bracket, depth, theta, runs);
-    if (e != cudaSuccess) { set_error("plan_kernel: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }
+    if (e != cudaSuccess) return launch_failed("plan_kernel", e);
     return launch_status("plan_kernel");
 }
 
@@ -429,7 +429,7 @@ int launch_plan_fixed(const fathom_shape &s, const float *q, const float *var, i
     const int grid = (s.units + kPlanWarps - 1) / kPlanWarps;
     const cudaError_t e = launch_pdl(plan_fixed_kernel, dim3(grid), dim3(32 * kPlanWarps), 0, st, s.units, s.n,
                                      cap_blocks(s), s.D, s.G, q, var, n_sel, t_fixed, depth, runs);
-    if (e != cudaSuccess) { set_error("plan_fixed_kernel: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }
+    if (e != cudaSuccess) return launch_failed("plan_fixed_kernel", e);
     return launch_status("plan_fixed_kernel");
 }
 

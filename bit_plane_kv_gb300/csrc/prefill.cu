@@ -994,7 +994,7 @@ int launch_prefill_attn(const fathom_prompts &p, const void *q, const void *k, c
     else if (p.D <= 96) { if (bf) FATHOM_PREFILL(6, FATHOM_BF16); else FATHOM_PREFILL(6, FATHOM_F16); }
     else { if (bf) FATHOM_PREFILL(8, FATHOM_BF16); else FATHOM_PREFILL(8, FATHOM_F16); }
 #undef FATHOM_PREFILL
-    if (e != cudaSuccess) { set_error("prefill_kernel: %s", cudaGetErrorString(e)); return FATHOM_ECUDA; }
+    if (e != cudaSuccess) return launch_failed("prefill_kernel", e);
     return launch_status("prefill_kernel");
 }
 

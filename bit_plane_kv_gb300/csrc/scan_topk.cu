@@ -1448,7 +1448,7 @@ static int launch_g(const fathom_shape &s, const uint64_t *planes, const uint16_
                 else if (scores_opt) FATHOM_SCAN_LAUNCH(false, true, false);
                 else FATHOM_SCAN_LAUNCH(false, false, false);
             }
-            if (le != cudaSuccess) { set_error("scan_kernel: %s", cudaGetErrorString(le)); return FATHOM_ECUDA; }
+            if (le != cudaSuccess) return launch_failed("scan_kernel", le);
             const int rc0 = launch_status("scan_kernel");
             if (rc0) return rc0;
         }
@@ -1462,7 +1462,7 @@ static int launch_g(const fathom_shape &s, const uint64_t *planes, const uint16_
         if (small_merge) FATHOM_MERGE_LAUNCH(kMThreadsS, kMBufS);
         else FATHOM_MERGE_LAUNCH(kMThreads, kMBuf);
 #undef FATHOM_MERGE_LAUNCH
-        if (le != cudaSuccess) { set_error("merge_kernel: %s", cudaGetErrorString(le)); return FATHOM_ECUDA; }
+        if (le != cudaSuccess) return launch_failed("merge_kernel", le);
         const int rc = launch_status("merge_kernel");
         if (rc) return rc;
         if (k_sel == 0) break;   // nothing selected: no second pass needed

@@ -563,7 +563,7 @@ static int launch_sparse_attn_src(const fathom_shape &s, const KSource &ks, cons
         default: set_error("sparse_attn: unsupported G=%d", s.G); return FATHOM_EINVAL;
     }
 #undef FATHOM_ATTN_LAUNCH
-    if (le != cudaSuccess) { set_error("attn_kernel: %s", cudaGetErrorString(le)); return FATHOM_ECUDA; }
+    if (le != cudaSuccess) return launch_failed("attn_kernel", le);
     return launch_status("attn_kernel");
 }
 
@@ -618,10 +618,7 @@ int launch_sparse_attn_noalloc(const fathom_shape &s, const uint16_t *krows, con
     if (rc) return rc;
     // the tickets must start at zero; the partial states are written before they are read
     cudaError_t e = cudaMemsetAsync(scratch + wl.ticket_off, 0, wl.total - wl.ticket_off, st);
-    if (e != cudaSuccess) {
-        set_error("sparse_attn_noalloc: cudaMemsetAsync: %s", cudaGetErrorString(e));
-        return FATHOM_ECUDA;
-    }
+    if (e != cudaSuccess) return launch_failed("sparse_attn_noalloc: cudaMemsetAsync", e);
     return launch_sparse_attn(s, krows, vrows, q, idx, out, scratch, st);
 }
 

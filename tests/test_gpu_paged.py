@@ -506,6 +506,58 @@ print("same")
     assert r.returncode == 0 and r.stdout.strip() == "same", r.stdout + r.stderr[-2000:]
 
 
+def test_a_launch_that_fails_leaves_no_error_behind():
+    """A launch that the runtime refuses (on the default stream, while a stream that waits for it is being captured):
+    the call reports it, the next call of somebody else's does not."""
+    code = """
+import ctypes, sys
+sys.path.insert(0, %r); sys.path.insert(0, %r)
+import torch
+from bit_plane_kv_gb300 import binding as B
+import paged_cases as P
+kp, vp, table, free = P.pool(2, 2, 128, 16, 8, torch.bfloat16, extra=8)
+pages, L = B.make_pages(kp, table), B.lib()
+ws = B.alloc_paged_workspace(pages, G=4, mass=True)
+q, x = torch.randn(4, 4, 128, device="cuda"), torch.randn(40, 8, 128, device="cuda").bfloat16()
+lens, cu = torch.full((2,), 100, dtype=torch.int32, device="cuda"), P.cumulated([7, 33])
+mass, dst = torch.zeros(4, 128, device="cuda"), free.reshape(2, 4).contiguous()
+out, kept = torch.zeros_like(x), torch.zeros(4, 60, dtype=torch.int32, device="cuda")
+o, lens2, mass2 = torch.zeros_like(q), torch.zeros_like(lens), torch.zeros(4, 64, device="cuda")
+a = [t.data_ptr() for t in (kp, vp, table)]
+pr = B.Prompts(2, 8, 2, 128, B.BF16, 40, 40, 1024, 128, 1024, 128, 1024, 128, 1024, 128)
+calls = {
+    "prefill": lambda: L.fathom_prefill_attn(ctypes.byref(pr), x.data_ptr(), x.data_ptr(), x.data_ptr(), cu.data_ptr(),
+                                             cu.data_ptr(), out.data_ptr(), None, None),
+    "append": lambda: L.fathom_paged_append(ctypes.byref(pages), *a, x.data_ptr(), x.data_ptr(), 2, 1024, 128,
+                                            lens.data_ptr(), None, None),
+    "attn": lambda: L.fathom_paged_attn(ctypes.byref(pages), 4, q.data_ptr(), *a, lens.data_ptr(), o.data_ptr(), None, 0,
+                                        ws.data_ptr(), ws.numel(), None),
+    "mass": lambda: L.fathom_paged_attn(ctypes.byref(pages), 4, q.data_ptr(), *a, lens.data_ptr(), o.data_ptr(),
+                                        mass.data_ptr(), 128, ws.data_ptr(), ws.numel(), None),
+    "evict": lambda: L.fathom_paged_evict(ctypes.byref(pages), *a, lens.data_ptr(), mass.data_ptr(), 128, 60, 4, 32,
+                                          dst.data_ptr(), 4, kept.data_ptr(), lens2.data_ptr(), mass2.data_ptr(), 64, None),
+}
+for call in calls.values():
+    assert call() == 0
+torch.cuda.synchronize()
+rt = ctypes.CDLL("libcudart.so.%%s" %% torch.version.cuda.split(".")[0])
+for name, call in calls.items():
+    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    assert rt.cudaStreamCreate(ctypes.byref(stream)) == 0
+    assert rt.cudaStreamBeginCapture(stream, 0) == 0
+    status, left = call(), rt.cudaGetLastError()
+    rt.cudaStreamEndCapture(stream, ctypes.byref(graph))
+    rt.cudaGetLastError()
+    assert rt.cudaStreamDestroy(stream) == 0
+    assert status == 2 and left == 0, (name, status, left)
+    assert call() == 0
+torch.cuda.synchronize()
+print("clear")
+""" % (os.path.dirname(os.path.dirname(os.path.abspath(__file__))), os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "clear", r.stdout + r.stderr[-2000:]
+
+
 def test_first_calls_of_a_process_by_several_threads_at_once():
     """Every form of the kernels with large shared memory, called for the first time by eight threads together."""
     code = """
