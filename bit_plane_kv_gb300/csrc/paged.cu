@@ -139,7 +139,7 @@ struct DecArgs {
     const void *kp, *vp;
     const int32_t *table, *lens;
     float *out, *part_o, *part_ml, *lse, *logits;   // shares: [CTA][2][G][D] and [CTA][2][G][2] = (m, l)
-    unsigned *ticket, *group_ticket;   // of a unit's shares, and of a group of them; at the first share's place
+    unsigned *ticket, *group_ticket;   // of a unit's shares, by its first CTA; of a group, at its first share's place
 };
 
 // Join of a unit's shares, 32 at a time; in the place of DecSmem::o.
@@ -572,7 +572,7 @@ paged_attn_kernel(const DecArgs a) {
             const int shares = (int)(c_last - c_first) + 1;
             long long x_first = c_first;   // what is joined: shares x_first, x_first + every, ...
             int every = 1, n = shares;
-            unsigned *ticket = a.ticket + slot_of(c_first);
+            unsigned *ticket = a.ticket + c_first;   // of all units that it holds a share of, one goes on behind it
             bool final = shares <= 32;
             if (!final) {
                 x_first += (cta - c_first) / kGroup * kGroup;
@@ -689,7 +689,7 @@ paged_attn_kernel(const DecArgs a) {
                 x_first = c_first;
                 every = kGroup;
                 n = (shares + kGroup - 1) / kGroup;
-                ticket = a.ticket + slot_of(c_first);
+                ticket = a.ticket + c_first;
                 final = true;
             }
         }
@@ -731,10 +731,6 @@ paged_mass_kernel(fathom_pages p, int cap, int stride, int G, const int32_t *__r
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Places of partial results, two per CTA: as many tickets of units, and of groups of shares.  A place names its
-// unit: the unit's first share lies there, and no other unit's does.
-size_t paged_tickets(int sms) { return 2 * (size_t)kMaxDecCtas * sms; }
-
 template <typename T, int kD, int kTwo, bool kMass>
 cudaError_t launch_dec(const DecArgs &a, int ctas, cudaStream_t st) {
     const size_t smem = sizeof(DecSmem<kD>);
@@ -771,7 +767,7 @@ PagedWorkspace paged_workspace_layout(const fathom_pages &p, int G, bool mass) {
     // largest of several calls serves them all.  (A ticket per unit, with the data behind the last one, put a
     // smaller call's partial results into a larger one's tickets.)
     w.ticket_off = 0;
-    w.lse_off = align256(2 * paged_tickets(sms) * sizeof(uint32_t));
+    w.lse_off = align256(3 * (size_t)kMaxDecCtas * sms * sizeof(uint32_t));
     w.part_off = align256(w.lse_off + (mass ? rows * sizeof(float) : 0));
     w.ml_off = align256(w.part_off + (size_t)w.ctas * 2 * G * p.D * sizeof(float));
     w.logit_off = align256(w.ml_off + (size_t)w.ctas * 2 * G * 2 * sizeof(float));
@@ -791,7 +787,7 @@ int launch_paged_attn(const fathom_pages &p, int G, const float *q, const void *
     a.logit_stride = (a.cap + 3) / 4 * 4;
     a.q = q; a.kp = kp; a.vp = vp; a.table = table; a.lens = lens; a.out = out;
     a.ticket = (unsigned *)((char *)ws + w.ticket_off);
-    a.group_ticket = a.ticket + (w.lse_off - w.ticket_off) / sizeof(unsigned) / 2;
+    a.group_ticket = a.ticket + (w.lse_off - w.ticket_off) / sizeof(unsigned) / 3;
     a.part_o = (float *)((char *)ws + w.part_off);
     a.part_ml = (float *)((char *)ws + w.ml_off);
     a.lse = mass ? (float *)((char *)ws + w.lse_off) : nullptr;

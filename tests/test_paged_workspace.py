@@ -51,10 +51,10 @@ def test_no_call_leaves_data_where_another_looks_for_tickets(layout_of):
 
 
 def test_every_cta_has_its_tickets(layout_of):
-    """Two for each of a CTA's two partial units: of the unit, and of the group of shares it begins."""
+    """One of the unit that goes on behind it, two of groups of shares that it begins."""
     for c in _calls():
         w = layout_of(*c)
-        assert w.lse_off - w.ticket_off >= 4 * 2 * 2 * w.ctas
+        assert w.lse_off - w.ticket_off >= 4 * 3 * w.ctas
 
 
 def test_parts_do_not_overlap(layout_of):
