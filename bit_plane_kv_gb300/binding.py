@@ -839,7 +839,8 @@ def fathom_paged_evict(pages: Pages, k_pages, v_pages, page_table, lens, mass, k
     """Cut every unit back to `keep` tokens by attention mass; the kept rows move, in order,
     to the pages of dst_table [seqs][pages] (page_table itself: in place).  -> (kept_idx
     [units][keep] int32, ascending and then -1, lens_out [seqs] int32, mass_out
-    [units][M] fp32; mass_out None: mass itself, in place)."""
+    [units][M] fp32; mass_out None: mass itself, in place).  Mass behind the kept tokens
+    is left as it was: set it to 0 before new tokens take those places."""
     _, seqs, H, _, cap = _check_cache(pages, k_pages, v_pages, page_table)
     keep, units = int(keep), seqs * H
     if not _ok(lens, torch.int32, (seqs,)):

@@ -3,9 +3,9 @@
 // Measured, 128 channels, bf16, both kernels, to other pages and in place: 256 units of
 // 16k tokens cut back to 4096 each 204 and 222 us (1.0 GB moved in rows of 256 bytes, 2 KB
 // apart; about 25 us of it choose the kept sets); 8 units of 8192 tokens cut to 2048 14.5
-// and 21 us; 8 units of 131072 cut to 16384 68 and 126 us.  In place the move has an order
-// to keep.  Tried for that order: bulk copies through shared memory (210 us for the 256
-// units' move alone; 76 us for the 8 units).
+// and 21 us; 8 units of 131072 cut to 16384 68 and 126 us.  In place a chunk of rows is
+// loaded, met for and stored before the next one's loads start.  Tried for that: bulk
+// copies through shared memory (210 us for the 256 units' move alone; 76 us for the 8 units).
 #include "blackwell.cuh"
 
 namespace fathom {

@@ -8,7 +8,9 @@
 // while the tensor cores multiply for one, four warps exponentiate the other's
 // scores (thread = row).  Per tile and 128 keys:
 //   S = Q K^T           both operands in shared memory, S in tensor memory
-//   P = exp2(c S - m)   registers; P back to tensor memory in the rows' type
+//   P = exp2(c S - m)   registers; P back to tensor memory, rounded to the rows' type (both
+//                       operands of an instruction have one type; in pieces that would keep
+//                       fp32, as the decode attention's, P V would take three times as long)
 //   O = O + P V         P from tensor memory, V from shared memory
 // with c = log2(e) / sqrt(D) and the running maximum m, sum l of a softmax in one
 // pass.  The exponentials of a row are taken against a maximum that may be up to
@@ -23,13 +25,14 @@
 // S in tensor memory, which S, P and O of two tiles fill, so the next S waits for it):
 // about 2700 clocks per 128 keys and two tiles where the products alone take 2050.
 // Measured, 32 query heads on 8 KV heads, 128 channels, bf16: one prompt of 16384
-// tokens 1342 us (2.2 TFLOP, 1.64 PFLOP/s; 1.90 measured for library products), 12
-// prompts of up to 2048 tokens 164 us (1.12 PFLOP/s), 16 tokens against 8192 27 us.
+// tokens 1330 us (2.2 TFLOP, 1.65 PFLOP/s; 1.90 measured for library products), 12
+// prompts of up to 2048 tokens 168 us (1.10 PFLOP/s), 16 tokens against 8192 24 us.
 // What the steps gave on the 16k prompt: one thread per row with a full pass for the
 // maximum 2029 us; matrix instructions behind an elected lane instead of lane 0
 // 1883 -> 1445 us (their issue, not their execution, had been the bound); CTAs that
 // take over work 1445 -> 1370 us, and 237 -> 182 us for the packed prompts; whole-line
-// stores 173 -> 165 us there.
+// stores 173 -> 165 us there (the second look at rows that are not finite, below, took 4 of
+// them back).
 #include <cuda.h>
 #include <cuda_bf16.h>
 

@@ -492,7 +492,9 @@ int fathom_sparse_attn_noalloc(const fathom_shape *shape, const uint16_t *k_rows
  *   lse_opt NULL, or [total_q][heads] fp32 (out)
  * Key and value rows that a query does not see (later tokens, other sequences,
  * padding) never reach its outputs, whatever they hold, NaN and infinities
- * included. */
+ * included.  A NaN in a query, or in a key that it sees, makes its o and lse NaN; one
+ * in a value that it sees its channel of o.  An item of 256 rows with a result that is
+ * not finite takes a second pass, about as long as the first. */
 int fathom_prefill_attn(const fathom_prompts *prompts, const void *q, const void *k, const void *v,
                         const int32_t *cu_q, const int32_t *cu_k, void *out, float *lse_opt, void *stream);
 
@@ -505,7 +507,8 @@ int fathom_prefill_attn(const fathom_prompts *prompts, const void *q, const void
  *   k_new, v_new [total_new][kv_heads][D] of the cache's type, element (t, h, c) at
  *   t * new_token + h * new_head + c (positive multiples of 8, pointers 16-byte
  *   aligned), start [seqs] int32, cu_new [seqs + 1] int32 or NULL; device
- * Two new tokens for one place: one of the two rows, unspecified which. */
+ * Two new tokens for one place: each 8 channels of its rows are those of one of the
+ * two, unspecified which. */
 int fathom_paged_append(const fathom_pages *pages, void *k_pages, void *v_pages, const int32_t *page_table,
                         const void *k_new, const void *v_new, int32_t total_new, int64_t new_token,
                         int64_t new_head, const int32_t *start, const int32_t *cu_new, void *stream);
@@ -554,7 +557,8 @@ int fathom_paged_attn(const fathom_pages *pages, int32_t G, const float *q, cons
  *   lens_out [seqs] int32 (out, not lens): min(lens[s], keep)
  *   mass_out [units][mass_out_stride] fp32 (out), mass_out_stride >= keep: may be
  *   mass itself with the same stride
- * Destination rows and mass behind the kept ones are left as they were.
+ * Destination rows and mass behind the kept ones are left as they were: a caller that
+ * goes on to gather mass in place sets it to 0 there first.
  * n_sink, n_recent >= 0, n_sink + n_recent <= keep, keep in 1 .. 2^28.  All device
  * (the pages: device or pinned host). */
 int fathom_paged_evict(const fathom_pages *pages, void *k_pages, void *v_pages, const int32_t *page_table,
