@@ -66,3 +66,33 @@ def test_parts_do_not_overlap(layout_of):
         assert w.logit_off - w.ml_off >= w.ctas * 2 * G * 2 * 4
         assert w.total - w.logit_off >= (4 * rows * 256 if mass else 0)
         assert all(x % 256 == 0 for x in (w.lse_off, w.part_off, w.ml_off, w.logit_off, w.total))
+
+
+def test_a_ticket_belongs_to_one_unit():
+    """The kernel's shares, restated: CTA c of NC takes tiles c W / NC to (c + 1) W / NC of the W tiles of all units.
+    Units that several CTAs share have first CTAs of their own, and the first shares of their groups of 16 lie at
+    places of their own."""
+    rng = random.Random(8)
+    for _ in range(3000):
+        ctas = rng.choice([1, 2, 3, 7, 304, 456])
+        heads, seqs = rng.choice([1, 2, 8]), rng.randint(1, 12)
+        top = rng.choice([2, 5, 30, 300, 3000])
+        tiles = [t for _ in range(seqs) for t in [rng.randint(0, top)] * heads if t]
+        W = sum(tiles)
+        if W == 0:
+            continue
+        per_sm = 3 if ctas % 3 == 0 else 2
+        NC = min(ctas, max(1, max(W // 4, min(W, ctas // per_sm))))
+        firsts, groups, w0 = set(), set(), 0
+        for n in tiles:
+            first, last = ((w0 + 1) * NC - 1) // W, ((w0 + n) * NC - 1) // W
+            assert first * W // NC <= w0 < (first + 1) * W // NC and last * W // NC < w0 + n <= (last + 1) * W // NC
+            if first != last:
+                assert first not in firsts
+                firsts.add(first)
+                before = first * W // NC < w0
+                places = [2 * c + (before if c == first else 0) for c in range(first, last + 1, 16)] if last - first >= 32 else []
+                assert not groups & set(places)
+                groups |= set(places)
+            w0 += n
+        assert all(0 <= c < ctas for c in firsts) and all(0 <= x < 2 * ctas for x in groups)
