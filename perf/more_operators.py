@@ -171,8 +171,8 @@ def prepare(case, seed):
             st["q"] = 2 * torch.randn(S * H, case["G"], D, generator=g, device="cuda")
             if own:   # what a program keeps from call to call
                 from bit_plane_kv_gb300 import binding as B
-                st["pages"] = B.make_pages4(st["kv"], st["table"], D)
-                st["ws"] = B.alloc_paged4_workspace(st["pages"], G=case["G"])
+                st["pages"] = B.make_nibble_pages(st["kv"], st["table"], D)
+                st["ws"] = B.alloc_nibble_workspace(st["pages"], G=case["G"])
         else:
             st.update(first=torch.zeros_like(st["lens"]), cu=_cumulated(lens), total=sum(lens),
                       seq=torch.repeat_interleave(torch.arange(S), torch.tensor(lens)).cuda())
@@ -206,20 +206,21 @@ def _own(st, op):
     from bit_plane_kv_gb300 import binding as B
     c = st["case"]
     if op == "attn4":
-        return {"out": B.fathom_paged4_attn(st["pages"], st["q"], st["kv"], st["table"], st["lens"], st["ws"])}
+        return {"out": B.fathom_nibble_attn(st["pages"], st["q"], st["kv"], st["table"], st["lens"], st["ws"])}
+    cu = None if c.get("new") == 1 else st["cu"]     # a decode step: one token per sequence
     if op == "rope":
         pages = B.make_pages(st["k_pages"], st["table"])
         _, _, q = B.fathom_paged_append_rope(pages, st["k_pages"], st["v_pages"], st["table"], st["k_new"], st["v_new"],
-                                             st["start"], st["rope"], st["cu"], interleaved=c["pairs"], q=st["q"],
+                                             st["start"], st["rope"], cu, interleaved=c["pairs"], q=st["q"],
                                              q_dtype=st["q_type"])
         return {"k": st["k_pages"], "v": st["v_pages"], "q": q}
-    pages = B.make_pages4(st["kv"], st["table"], c["D"])
+    pages = B.make_nibble_pages(st["kv"], st["table"], c["D"])
     q, first = {}, st.get("first")
     if op == "append4":
         first = st["start"]
-        q["q"] = B.fathom_paged4_append(pages, st["kv"], st["table"], st["k_new"], st["v_new"], first, st["cu"],
+        q["q"] = B.fathom_nibble_append(pages, st["kv"], st["table"], st["k_new"], st["v_new"], first, cu,
                                         rope=st["rope"], interleaved=c["pairs"], q=st["q"], q_dtype=st["q_type"])[1]
-    k, v = B.fathom_paged4_read(pages, st["kv"], st["table"], first, st["cu"], st["total"], dtype=DTYPES[c["dtype"]])
+    k, v = B.fathom_nibble_read(pages, st["kv"], st["table"], first, st["cu"], st["total"], dtype=DTYPES[c["dtype"]])
     return {"k": k, "v": v, **q}
 
 
