@@ -56,7 +56,7 @@ class Pages(ctypes.Structure):
                [(f, ctypes.c_int64) for f in ("page_stride", "head_stride", "token_stride")]
 
     def __repr__(self):
-        return "Pages(" + ", ".join(f"{f}={getattr(self, f)}" for f, _ in self._fields_) + ")"
+        return type(self).__name__ + "(" + ", ".join(f"{f}={getattr(self, f)}" for f, _ in self._fields_) + ")"
 
     @property
     def units(self) -> int:
@@ -66,6 +66,21 @@ class Pages(ctypes.Structure):
     def cap(self) -> int:
         """Tokens a row of the page table can name."""
         return self.max_pages * self.page_tokens
+
+
+class NibblePages(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("seqs", "kv_heads", "D", "page_tokens", "num_pages", "max_pages")] + \
+               [(f, ctypes.c_int64) for f in ("page_stride", "head_stride")]
+
+    __repr__ = Pages.__repr__
+    units = Pages.units
+    cap = Pages.cap
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("table", _vp), ("rows", _i32), ("rot", _i32), ("interleaved", _i32), ("positions", _vp), ("q", _vp),
+                ("q_out", _vp), ("q_heads", _i32), ("q_dtype", _i32), ("q_token", _i64), ("q_head", _i64),
+                ("out_token", _i64), ("out_head", _i64)]
 
 
 RUN_FIELDS = ("src_word", "n_words", "dst_word", "src_scale", "n_scales", "dst_scale")
@@ -102,6 +117,14 @@ SIGNATURES = {
     "fathom_paged_evict": (ctypes.c_int, [ctypes.POINTER(Pages), _vp, _vp, _vp, _vp, _vp, _sz, _i32, _i32, _i32, _vp,
                                           _i32, _vp, _vp, _vp, _sz, _vp]),
     "fathom_paged_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(Pages), _i32, ctypes.c_int]),
+    "fathom_paged_append_rope": (ctypes.c_int, [ctypes.POINTER(Pages), _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _vp,
+                                                _vp, ctypes.POINTER(Rope), _vp]),
+    "fathom_nibble_append": (ctypes.c_int, [ctypes.POINTER(NibblePages), _vp, _vp, _i32, _vp, _vp, _i32, _i64, _i64, _vp,
+                                            _vp, ctypes.POINTER(Rope), _vp]),
+    "fathom_nibble_read": (ctypes.c_int, [ctypes.POINTER(NibblePages), _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i64,
+                                          _i64, _vp]),
+    "fathom_nibble_attn": (ctypes.c_int, [ctypes.POINTER(NibblePages), _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "fathom_nibble_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(NibblePages), _i32]),
     "fathom_wait_status": (ctypes.c_int, []),
     "fathom_rel_err": (ctypes.c_int, [_i32, _i32, _vp, _vp, _vp, _vp]),
     "fathom_set_overlap": (ctypes.c_int, [_i32, _i32, _vp, _vp, _vp, _vp]),
@@ -868,6 +891,223 @@ def fathom_paged_evict(pages: Pages, k_pages, v_pages, page_table, lens, mass, k
               dst_table.shape[1], kept_idx.data_ptr(), lens_out.data_ptr(), mass_out.data_ptr(), mass_out.shape[1],
               handle)
     return kept_idx, lens_out, mass_out
+
+
+# ------------------------------------------------------- position rotation and the 4-bit cache
+_OUT_TYPES = {torch.float32: F32, **_ROW_TYPES}
+
+
+def _check_rope(rope, positions, interleaved, q, q_out, q_dtype, dtype, T, D):
+    """-> the rotation's arguments but q_out's pointer and strides, which _rope_args adds."""
+    if rope is None:
+        if positions is not None or q is not None or q_out is not None or q_dtype is not None:
+            raise ValueError("rope is required with positions, q, q_out or q_dtype")
+        return None
+    _check(rope, "rope", (torch.float32,))
+    if rope.dim() != 2 or rope.shape[0] < 1:
+        raise ValueError(f"rope: shape {tuple(rope.shape)} is not [positions][rotated channels]")
+    if not _on_device(rope):
+        raise ValueError("rope must be a CUDA tensor")
+    rows, rot = rope.shape
+    _fit32(positions=rows, rotated_channels=rot)
+    if positions is not None and not _ok(positions, torch.int32, (T,)):
+        _check(positions, "positions", (torch.int32,), (T,))
+    r = Rope(rope.data_ptr(), rows, rot, int(bool(interleaved)), positions.data_ptr() if positions is not None else None)
+    if q is None:
+        if q_out is not None or q_dtype is not None:
+            raise ValueError("q is required with q_out or q_dtype")
+        return r
+    if q.dim() != 3:
+        raise ValueError("q: expected [tokens][heads][D]")
+    heads = q.shape[1]
+    _check_strided(q, "q", (dtype,), (T, heads, D))
+    if q_dtype is None:
+        q_dtype = q_out.dtype if q_out is not None else dtype
+    if q_dtype not in (dtype, torch.float32):
+        raise TypeError(f"q_dtype: {q_dtype} is neither {dtype} nor torch.float32")
+    if q_out is not None:
+        _check_strided(q_out, "q_out", (q_dtype,), (T, heads, D))
+    r.q, r.q_heads, r.q_dtype, r.q_token, r.q_head = q.data_ptr(), heads, _OUT_TYPES[q_dtype], q.stride(0), q.stride(1)
+    return r
+
+
+def _rope_args(r, q, q_out, q_dtype):
+    """Adds the rotated queries' place (allocated here unless given): -> the queries or None."""
+    if r is None or q is None:
+        return None
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q_dtype or q.dtype, device=q.device)
+    r.q_out, r.out_token, r.out_head = q_out.data_ptr(), q_out.stride(0), q_out.stride(1)
+    return q_out
+
+
+def _check_new(k_new, v_new, start, cu_new, dtype, seqs, H, D):
+    """-> (new tokens, their strides)."""
+    if k_new is None or k_new.dim() != 3:
+        raise ValueError("k_new: expected [tokens][kv_heads][D]")
+    T = k_new.shape[0]
+    if T >> 31:
+        _fit32(new_tokens=T)
+    _check_strided(k_new, "k_new", (dtype,), (T, H, D))
+    _check_strided(v_new, "v_new", (dtype,), (T, H, D))
+    stride = k_new.stride()
+    if stride != v_new.stride() and any(a > 1 and x != y for a, x, y in zip((T, H), stride, v_new.stride())):
+        raise ValueError("v_new: strides differ from k_new's")
+    if not _ok(start, torch.int32, (seqs,)):
+        _check(start, "start", (torch.int32,), (seqs,))
+    if cu_new is not None:
+        if not _ok(cu_new, torch.int32, (seqs + 1,)):
+            _check(cu_new, "cu_new", (torch.int32,), (seqs + 1,))
+    elif T != seqs:
+        raise ValueError(f"k_new: {T} tokens for {seqs} sequences without cu_new")
+    return T, stride
+
+
+def fathom_paged_append_rope(pages: Pages, k_pages, v_pages, page_table, k_new, v_new, start, rope, cu_new=None,
+                             positions=None, interleaved=False, q=None, q_out=None, q_dtype=None, stream=None):
+    """fathom_paged_append with the position rotation: rope [positions][rot] fp32 holds cos, then sin, of
+    each position's rot / 2 angles; keys, and queries q [T][heads][D] if given, are rotated on the way.
+    positions [T] int32 (None: a token's place in its sequence).  -> (k_pages, v_pages, rotated queries
+    of q_dtype, the rows' type or torch.float32, or None)."""
+    dtype, seqs, H, D, _ = _check_cache(pages, k_pages, v_pages, page_table)
+    T, stride = _check_new(k_new, v_new, start, cu_new, dtype, seqs, H, D)
+    if rope is None:
+        raise ValueError("rope is required")
+    r = _check_rope(rope, positions, interleaved, q, q_out, q_dtype, dtype, T, D)
+    context, handle = _on(stream, (k_pages, v_pages, page_table, k_new, v_new, start, cu_new, rope, positions, q, q_out))
+    with context:
+        q_out = _rope_args(r, q, q_out, q_dtype)
+        _call("fathom_paged_append_rope", pages, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+              k_new.data_ptr(), v_new.data_ptr(), T, stride[0], stride[1], start.data_ptr(),
+              cu_new.data_ptr() if cu_new is not None else None, r, handle)
+    return k_pages, v_pages, q_out
+
+
+def alloc_nibble_pages(num_pages, kv_heads, page_tokens, D, device="cuda") -> torch.Tensor:
+    """Pages of a 4-bit cache, all zeros (values 0): [num_pages][kv_heads][bytes of a page]."""
+    return torch.zeros(num_pages, kv_heads, page_tokens // 16 * 18 * D, dtype=torch.uint8, device=device)
+
+
+def make_nibble_pages(kv_pages, page_table, D) -> NibblePages:
+    """The layout of a 4-bit cache: kv_pages uint8 [pages][kv_heads][bytes of a page, 18 D per 16
+    tokens] (pages and heads strided as they are), page_table [seqs][max_pages] int32."""
+    if kv_pages.dim() != 3 or page_table.dim() != 2:
+        raise ValueError("kv_pages: expected [pages][kv_heads][bytes], page_table: [seqs][max_pages]")
+    if kv_pages.dtype != torch.uint8:
+        raise TypeError(f"kv_pages: dtype {kv_pages.dtype} is not torch.uint8")
+    n, H, size = kv_pages.shape
+    if D < 1 or size == 0 or size % (18 * D):
+        raise ValueError(f"kv_pages: {size} bytes are no blocks of 18 * {D}")
+    _fit32(pages=n, page_tokens=size // (18 * D) * 16, max_pages=page_table.shape[1])
+    sn, sh, _ = kv_pages.stride()
+    return NibblePages(page_table.shape[0], H, D, size // (18 * D) * 16, n, page_table.shape[1], sn, sh)
+
+
+def _check_nibble(pages, kv_pages, page_table):
+    """-> (sequences, KV heads, D)."""
+    seqs, H, D, P, n, per = pages.seqs, pages.kv_heads, pages.D, pages.page_tokens, pages.num_pages, pages.max_pages
+    shape, stride = (n, H, P // 16 * 18 * D), (pages.page_stride, pages.head_stride, 1)
+    if not (kv_pages is not None and kv_pages.dtype is torch.uint8 and kv_pages.shape == shape
+            and kv_pages.stride() == stride and kv_pages.is_cuda):
+        _check_strided(kv_pages, "kv_pages", (torch.uint8,), shape)
+        if any(a > 1 and x != y for a, x, y in zip(shape, kv_pages.stride(), stride)):
+            raise ValueError(f"kv_pages: strides {kv_pages.stride()[:2]} are not those of pages")
+    if not _ok(page_table, torch.int32, (seqs, per)):
+        _check(page_table, "page_table", (torch.int32,), (seqs, per))
+    return seqs, H, D
+
+
+def fathom_nibble_append(pages: NibblePages, kv_pages, page_table, k_new, v_new, start, cu_new=None, rope=None,
+                         positions=None, interleaved=False, q=None, q_out=None, q_dtype=None, stream=None):
+    """Write new rows k_new, v_new [T][kv_heads][D] (bf16 or fp16) into a 4-bit cache, in place, keys and
+    queries rotated on the way if rope is given; tokens, rotation and queries as in
+    fathom_paged_append_rope.  -> (kv_pages, rotated queries or None)."""
+    seqs, H, D = _check_nibble(pages, kv_pages, page_table)
+    dtype = k_new.dtype if k_new is not None else None
+    if dtype not in _ROW_TYPES:
+        raise TypeError(f"k_new: dtype {dtype} not in {tuple(_ROW_TYPES)}")
+    T, stride = _check_new(k_new, v_new, start, cu_new, dtype, seqs, H, D)
+    r = _check_rope(rope, positions, interleaved, q, q_out, q_dtype, dtype, T, D)
+    context, handle = _on(stream, (kv_pages, page_table, k_new, v_new, start, cu_new, rope, positions, q, q_out))
+    with context:
+        q_out = _rope_args(r, q, q_out, q_dtype)
+        _call("fathom_nibble_append", pages, kv_pages.data_ptr(), page_table.data_ptr(), _ROW_TYPES[dtype],
+              k_new.data_ptr(), v_new.data_ptr(), T, stride[0], stride[1], start.data_ptr(),
+              cu_new.data_ptr() if cu_new is not None else None, r, handle)
+    return kv_pages, q_out
+
+
+def fathom_nibble_read(pages: NibblePages, kv_pages, page_table, start, cu, total, dtype=torch.bfloat16, k_out=None,
+                       v_out=None, stream=None):
+    """Rows of a 4-bit cache: token i of sequence s's part (packed at cu[s] + i, `total` rows in all) is
+    the one at position start[s] + i.  -> (k_out, v_out) [total][kv_heads][D] of dtype (bf16, fp16 or
+    fp32; that of k_out if given); rows without a place in the cache are not written."""
+    seqs, H, D = _check_nibble(pages, kv_pages, page_table)
+    total = int(total)
+    _fit32(total=total)
+    if not _ok(start, torch.int32, (seqs,)):
+        _check(start, "start", (torch.int32,), (seqs,))
+    if not _ok(cu, torch.int32, (seqs + 1,)):
+        _check(cu, "cu", (torch.int32,), (seqs + 1,))
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out: both or neither")
+    if k_out is not None:
+        dtype = k_out.dtype
+        _check_strided(k_out, "k_out", tuple(_OUT_TYPES), (total, H, D))
+        _check_strided(v_out, "v_out", (dtype,), (total, H, D))
+        if any(a > 1 and x != y for a, x, y in zip((total, H), k_out.stride(), v_out.stride())):
+            raise ValueError("v_out: strides differ from k_out's")
+    elif dtype not in _OUT_TYPES:
+        raise TypeError(f"dtype: {dtype} not in {tuple(_OUT_TYPES)}")
+    elif total < 0:
+        raise ValueError(f"total: {total} is negative")
+    context, handle = _on(stream, (kv_pages, page_table, start, cu, k_out, v_out))
+    with context:
+        if k_out is None:
+            k_out = torch.empty((total, H, D), dtype=dtype, device=kv_pages.device)
+            v_out = torch.empty((total, H, D), dtype=dtype, device=kv_pages.device)
+        _call("fathom_nibble_read", pages, kv_pages.data_ptr(), page_table.data_ptr(), start.data_ptr(), cu.data_ptr(),
+              total, k_out.data_ptr(), v_out.data_ptr(), _OUT_TYPES[dtype], k_out.stride(0), k_out.stride(1), handle)
+    return k_out, v_out
+
+
+def nibble_workspace_size(pages: NibblePages, G: int) -> int:
+    return int(lib().fathom_nibble_workspace_size(ctypes.byref(pages), int(G)))
+
+
+def alloc_nibble_workspace(pages: NibblePages, G=4, device="cuda") -> torch.Tensor:
+    """Workspace of fathom_nibble_attn.  One that is large enough for several calls of different sizes serves them in
+    any order."""
+    nbytes = nibble_workspace_size(pages, G)
+    if nbytes == 0:
+        raise FathomError("fathom_nibble_workspace_size", 1, lib().fathom_last_error().decode())
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def fathom_nibble_attn(pages: NibblePages, q, kv_pages, page_table, lens, workspace, out=None, lse=None, want_lse=False,
+                       stream=None):
+    """Decode attention over a 4-bit cache: q [units][G][D] fp32, lens [seqs] int32 -> out [units][G][D]
+    fp32, or (out, lse [units][G] fp32) where lse is given or wanted."""
+    seqs, H, D = _check_nibble(pages, kv_pages, page_table)
+    if q is None or q.dim() != 3:
+        raise ValueError("q: expected [units][G][D]")
+    G = q.shape[1]
+    shape = (seqs * H, G, D)
+    for t, name, s in ((q, "q", shape), (out, "out", shape), (lse, "lse", shape[:2])):
+        if (t is not None or name == "q") and not _ok(t, torch.float32, s):
+            _check(t, name, (torch.float32,), s)
+    if not _ok(lens, torch.int32, (seqs,)):
+        _check(lens, "lens", (torch.int32,), (seqs,))
+    _check(workspace, "workspace", (torch.uint8,))
+    context, handle = _on(stream, (q, kv_pages, page_table, lens, workspace, out, lse))
+    with context:
+        if out is None:
+            out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        if lse is None and want_lse:
+            lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+        _call("fathom_nibble_attn", pages, G, q.data_ptr(), kv_pages.data_ptr(), page_table.data_ptr(), lens.data_ptr(),
+              out.data_ptr(), lse.data_ptr() if lse is not None else None, workspace.data_ptr(), workspace.numel(), handle)
+    return out if lse is None else (out, lse)
 
 
 def fathom_wait_status():

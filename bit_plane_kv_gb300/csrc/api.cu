@@ -383,7 +383,7 @@ extern "C" {
 
 const char *fathom_last_error(void) { return g_err; }
 
-const char *fathom_version(void) { return "fathom-gb300 0.3 (sm_103a)"; }
+const char *fathom_version(void) { return "fathom-gb300 0.4 (sm_103a)"; }
 
 int fathom_debug_status(int mode, uint64_t *first_failure) {
     g_err[0] = 0;
@@ -1005,6 +1005,192 @@ int fathom_paged_evict(const fathom_pages *pages, void *k_pages, void *v_pages, 
     return launch_paged_evict(*pages, k_pages, v_pages, page_table, lens, mass, mass_stride, keep, n_sink, n_recent,
                               dst_table, dst_pages, kept_idx, lens_out, mass_out, mass_out_stride,
                               (cudaStream_t)stream);
+}
+
+// ---------------------------------------------------------------- rotation and the 4-bit cache
+static int check_new_rows(const char *what, int32_t seqs, int32_t kv_heads, int32_t total_new, int64_t new_token,
+                          int64_t new_head, const int32_t *cu_new) {
+    if (total_new < 0 || total_new > (1 << 28) || (!cu_new && total_new > seqs)) {
+        set_error("%s: total_new must be in [0, 2^28], at most seqs without cu_new (got %d)", what, total_new);
+        return FATHOM_EINVAL;
+    }
+    if (!stride_ok(new_token, total_new) || !stride_ok(new_head, kv_heads)) {
+        set_error("%s: strides must be positive multiples of 8 elements", what); return FATHOM_EINVAL;
+    }
+    return FATHOM_OK;
+}
+
+static int check_rope(const fathom_rope &r, int D, int row_dtype, int32_t total_new) {
+    NONNULL(r.table);
+    if (!aligned16(r.table)) { set_error("rope: table must be 16-byte aligned"); return FATHOM_EINVAL; }
+    if (r.rows < 1) { set_error("rope: rows must be at least 1 (got %d)", r.rows); return FATHOM_EINVAL; }
+    if (r.rot < 2 || r.rot > D || r.rot % 2) { set_error("rope: rot must be even, in [2, %d] (got %d)", D, r.rot); return FATHOM_EINVAL; }
+    if (r.interleaved != 0 && r.interleaved != 1) {
+        set_error("rope: interleaved must be 0 or 1 (got %d)", r.interleaved); return FATHOM_EINVAL;
+    }
+    if (!r.q) return FATHOM_OK;
+    if (!r.q_out) { set_error("rope: q_out is NULL"); return FATHOM_EINVAL; }
+    if (r.q_out == r.q) { set_error("rope: q_out may not be q"); return FATHOM_EINVAL; }
+    if (r.q_heads < 1 || r.q_heads > 65535) { set_error("rope: q_heads must be in [1, 65535] (got %d)", r.q_heads); return FATHOM_EINVAL; }
+    if (r.q_dtype != row_dtype && r.q_dtype != FATHOM_F32) {
+        set_error("rope: q_dtype must be the rows' type or FATHOM_F32 (got %d)", r.q_dtype); return FATHOM_EINVAL;
+    }
+    if (!stride_ok(r.q_token, total_new) || !stride_ok(r.q_head, r.q_heads) || !stride_ok(r.out_token, total_new) ||
+        !stride_ok(r.out_head, r.q_heads)) {
+        set_error("rope: strides must be positive multiples of 8 elements"); return FATHOM_EINVAL;
+    }
+    if (!aligned16(r.q) || !aligned16(r.q_out)) { set_error("rope: q and q_out must be 16-byte aligned"); return FATHOM_EINVAL; }
+    return FATHOM_OK;
+}
+
+int fathom_paged_append_rope(const fathom_pages *pages, void *k_pages, void *v_pages, const int32_t *page_table,
+                             const void *k_new, const void *v_new, int32_t total_new, int64_t new_token,
+                             int64_t new_head, const int32_t *start, const int32_t *cu_new, const fathom_rope *rope,
+                             void *stream) {
+    g_err[0] = 0;
+    int rc = check_pages(pages);
+    if (rc) return rc;
+    rc = check_new_rows("paged_append_rope", pages->seqs, pages->kv_heads, total_new, new_token, new_head, cu_new);
+    if (rc) return rc;
+    NONNULL(rope);
+    rc = check_rope(*rope, pages->D, pages->dtype, total_new);
+    if (rc) return rc;
+    if (total_new == 0) return FATHOM_OK;
+    rc = check_page_pointers(k_pages, v_pages, page_table);
+    if (rc) return rc;
+    NONNULL(k_new);
+    NONNULL(v_new);
+    NONNULL(start);
+    if (!aligned16(k_new) || !aligned16(v_new)) {
+        set_error("paged_append_rope: k_new and v_new must be 16-byte aligned"); return FATHOM_EINVAL;
+    }
+    FAULT_POINT("fathom_paged_append_rope");
+    return launch_paged_append_rope(*pages, k_pages, v_pages, page_table, k_new, v_new, total_new, new_token, new_head,
+                                    start, cu_new, *rope, (cudaStream_t)stream);
+}
+
+static bool byte_stride_ok(int64_t stride, int64_t count) {
+    return count <= 1 || (stride >= 16 && stride % 16 == 0 && stride < ((int64_t)1 << 39));
+}
+
+static int check_nibble_pages(const fathom_nibble_pages *pages) {
+    NONNULL(pages);
+    const fathom_nibble_pages &p = *pages;
+    if (p.seqs < 1 || p.kv_heads < 1 || (long long)p.seqs * p.kv_heads > 65535) {
+        set_error("nibble_pages: need seqs, kv_heads >= 1 and seqs * kv_heads <= 65535 (got %d, %d)", p.seqs, p.kv_heads);
+        return FATHOM_EINVAL;
+    }
+    if (p.D < 32 || p.D > FATHOM_MAX_D || p.D % 32) {
+        set_error("nibble_pages: D must be 32, 64, 96 or 128 (got %d)", p.D); return FATHOM_EINVAL;
+    }
+    if (p.page_tokens < 16 || (p.page_tokens & (p.page_tokens - 1))) {
+        set_error("nibble_pages: page_tokens must be a power of two, at least 16 (got %d)", p.page_tokens); return FATHOM_EINVAL;
+    }
+    if (p.num_pages < 1 || p.max_pages < 1 || (long long)p.max_pages * p.page_tokens > (1 << 28)) {
+        set_error("nibble_pages: need num_pages, max_pages >= 1 and max_pages * page_tokens <= 2^28 (got %d, %d, %d)",
+                  p.num_pages, p.max_pages, p.page_tokens);
+        return FATHOM_EINVAL;
+    }
+    if (!byte_stride_ok(p.page_stride, p.num_pages) || !byte_stride_ok(p.head_stride, p.kv_heads)) {
+        set_error("nibble_pages: strides must be positive multiples of 16 bytes"); return FATHOM_EINVAL;
+    }
+    return FATHOM_OK;
+}
+
+static int check_nibble_pointers(const void *kv_pages, const int32_t *page_table) {
+    NONNULL(kv_pages);
+    NONNULL(page_table);
+    if (!aligned16(kv_pages)) { set_error("kv_pages must be 16-byte aligned"); return FATHOM_EINVAL; }
+    return FATHOM_OK;
+}
+
+int fathom_nibble_append(const fathom_nibble_pages *pages, void *kv_pages, const int32_t *page_table, int32_t row_dtype,
+                         const void *k_new, const void *v_new, int32_t total_new, int64_t new_token, int64_t new_head,
+                         const int32_t *start, const int32_t *cu_new, const fathom_rope *rope, void *stream) {
+    g_err[0] = 0;
+    int rc = check_nibble_pages(pages);
+    if (rc) return rc;
+    rc = check_row_type("nibble_append", pages->D, row_dtype);
+    if (rc) return rc;
+    rc = check_new_rows("nibble_append", pages->seqs, pages->kv_heads, total_new, new_token, new_head, cu_new);
+    if (rc) return rc;
+    if (rope && (rc = check_rope(*rope, pages->D, row_dtype, total_new))) return rc;
+    if (total_new == 0) return FATHOM_OK;
+    rc = check_nibble_pointers(kv_pages, page_table);
+    if (rc) return rc;
+    NONNULL(k_new);
+    NONNULL(v_new);
+    NONNULL(start);
+    if (!aligned16(k_new) || !aligned16(v_new)) {
+        set_error("nibble_append: k_new and v_new must be 16-byte aligned"); return FATHOM_EINVAL;
+    }
+    FAULT_POINT("fathom_nibble_append");
+    return launch_nibble_append(*pages, kv_pages, page_table, row_dtype, k_new, v_new, total_new, new_token, new_head, start,
+                                cu_new, rope, (cudaStream_t)stream);
+}
+
+int fathom_nibble_read(const fathom_nibble_pages *pages, const void *kv_pages, const int32_t *page_table,
+                       const int32_t *start, const int32_t *cu, int32_t total, void *k_out, void *v_out,
+                       int32_t out_dtype, int64_t out_token, int64_t out_head, void *stream) {
+    g_err[0] = 0;
+    int rc = check_nibble_pages(pages);
+    if (rc) return rc;
+    if (total < 0 || total > (1 << 28)) { set_error("nibble_read: total must be in [0, 2^28] (got %d)", total); return FATHOM_EINVAL; }
+    if (out_dtype != FATHOM_F32 && out_dtype != FATHOM_BF16 && out_dtype != FATHOM_F16) {
+        set_error("nibble_read: out_dtype must be FATHOM_F32, FATHOM_BF16 or FATHOM_F16 (got %d)", out_dtype); return FATHOM_EINVAL;
+    }
+    if (!stride_ok(out_token, total) || !stride_ok(out_head, pages->kv_heads)) {
+        set_error("nibble_read: strides must be positive multiples of 8 elements"); return FATHOM_EINVAL;
+    }
+    if (total == 0) return FATHOM_OK;
+    rc = check_nibble_pointers(kv_pages, page_table);
+    if (rc) return rc;
+    NONNULL(start);
+    NONNULL(cu);
+    NONNULL(k_out);
+    NONNULL(v_out);
+    if (!aligned16(k_out) || !aligned16(v_out)) {
+        set_error("nibble_read: k_out and v_out must be 16-byte aligned"); return FATHOM_EINVAL;
+    }
+    FAULT_POINT("fathom_nibble_read");
+    return launch_nibble_read(*pages, kv_pages, page_table, start, cu, total, k_out, v_out, out_dtype, out_token, out_head,
+                              (cudaStream_t)stream);
+}
+
+static int check_nibble_heads(const fathom_nibble_pages *pages, int32_t G) {
+    const int rc = check_nibble_pages(pages);
+    if (rc) return rc;
+    if (G < 1 || G > FATHOM_MAX_G) { set_error("nibble_attn: G must be in [1, %d] (got %d)", FATHOM_MAX_G, G); return FATHOM_EINVAL; }
+    return FATHOM_OK;
+}
+
+size_t fathom_nibble_workspace_size(const fathom_nibble_pages *pages, int32_t G) {
+    g_err[0] = 0;
+    if (check_nibble_heads(pages, G)) return 0;
+    return nibble_workspace_layout(*pages, G).total;
+}
+
+int fathom_nibble_attn(const fathom_nibble_pages *pages, int32_t G, const float *q, const void *kv_pages,
+                       const int32_t *page_table, const int32_t *lens, float *out, float *lse_opt, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+    g_err[0] = 0;
+    int rc = check_nibble_heads(pages, G);
+    if (rc) return rc;
+    NONNULL(q);
+    rc = check_nibble_pointers(kv_pages, page_table);
+    if (rc) return rc;
+    NONNULL(lens);
+    NONNULL(out);
+    NONNULL(workspace);
+    if (!aligned16(q) || !aligned16(out)) { set_error("nibble_attn: q and out must be 16-byte aligned"); return FATHOM_EINVAL; }
+    const size_t need = nibble_workspace_layout(*pages, G).total;
+    if (workspace_bytes < need) {
+        set_error("nibble_attn workspace too small: %zu < %zu bytes", workspace_bytes, need);
+        return FATHOM_ENOMEM;
+    }
+    if (((uintptr_t)workspace & 255) != 0) { set_error("workspace must be 256-byte aligned"); return FATHOM_EINVAL; }
+    FAULT_POINT("fathom_nibble_attn");
+    return launch_nibble_attn(*pages, G, q, kv_pages, page_table, lens, out, lse_opt, workspace, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -282,6 +282,23 @@ int launch_paged_evict(const fathom_pages &p, void *kp, void *vp, const int32_t 
                        const int32_t *dst_table, int dst_pages, int32_t *kept, int32_t *lens_out, float *mass_out,
                        size_t mass_out_stride, cudaStream_t st);
 
+int launch_paged_append_rope(const fathom_pages &p, void *kp, void *vp, const int32_t *table, const void *kn, const void *vn,
+                             int total, int64_t new_token, int64_t new_head, const int32_t *start, const int32_t *cu,
+                             const fathom_rope &rope, cudaStream_t st);
+int launch_nibble_append(const fathom_nibble_pages &p, void *kv, const int32_t *table, int dtype, const void *kn, const void *vn,
+                         int total, int64_t new_token, int64_t new_head, const int32_t *start, const int32_t *cu,
+                         const fathom_rope *rope, cudaStream_t st);
+int launch_nibble_read(const fathom_nibble_pages &p, const void *kv, const int32_t *table, const int32_t *start,
+                       const int32_t *cu, int total, void *k_out, void *v_out, int dtype, int64_t out_token,
+                       int64_t out_head, cudaStream_t st);
+struct NibbleWorkspace {   // tickets at 0, partial softmax states, two per CTA
+    int sms;
+    size_t part_off, ml_off, total;
+};
+NibbleWorkspace nibble_workspace_layout(const fathom_nibble_pages &p, int G);
+int launch_nibble_attn(const fathom_nibble_pages &p, int G, const float *q, const void *kv, const int32_t *table,
+                       const int32_t *lens, float *out, float *lse, void *ws, cudaStream_t st);
+
 bool wait_expired_prefill();   // whether a bounded wait of its kernel ran out; clears the note
 
 int launch_rel_err(int rows, int D, const float *a, const float *ref, double *err, cudaStream_t st);

@@ -1,0 +1,586 @@
+// nibble.cu -- decode attention of one new token per sequence over a paged cache held in
+// 4 bits: o_h = sum_i softmax_i(q_h . k_i / sqrt(D)) v_i with k, v = (c - 7.5) a / 8.
+#include "nibble.cuh"
+#include "shares.cuh"
+
+namespace fathom {
+
+namespace {
+
+// Bound by the cache's bytes, 9 D / 8 per token and KV head, as long as a block of 16 tokens
+// costs fewer instructions than the SM issues while its 18 D bytes arrive (392 for D = 128).
+//
+// Equal shares of 64-token tiles per CTA (shares.cuh); in a tile each warp takes its own
+// block of 16 tokens, in 16-byte asynchronous copies to a ring of its own, so that warps wait
+// for their own copies only.
+//
+// Products run on the tensor cores, the fp32 operands in two pieces, hi + lo: a 16 x 8
+// operand holds a head's values in two columns, so four heads fill one instruction.
+// A query's pieces are whole numbers of 12 bits (to 2^-25 of its largest channel), so that
+// the sums over a group of channels are exact whatever the tensor cores cut off; a weight's
+// are fp16 (22 bits, and down to 2^-38 of the largest).
+//
+// Codes become fp16 in one logical operation: four bits left in the low bits of a 16-bit
+// half are the subnormal c 2^-24, four bits above them 16 c 2^-24.  For K that is the
+// operand itself: the factor of 16 goes into q, and - 7.5 sum(q) into the sum's start value.
+// Sums over V run over all tokens, where an offset would cancel away what is left of the
+// sum, so V is centred, (c - 7.5) 2^-9, one multiply-add per two values, exactly; and they
+// move to shared memory every kFlush blocks, because the tensor cores cut a sum off at its
+// last bit each time, always towards zero.
+//
+// K's scales multiply a group's partial sums (32 channels), V's the softmax weights:
+// (hi + lo) a in three fp16 operations for two tokens, the rounding error of hi a going to
+// the second piece; the weights are kept 2^13, the scales 2^k larger (k by the largest scale
+// so far), so that these errors stay clear of the subnormals.  The scores' layout (tokens by
+// heads) becomes the weights' operand (heads by tokens) by one 8 x 8 transposition in
+// registers per 8 tokens and group.
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kTile = kNibTokens * kWarps;
+// CTAs resident per SM, and stages of a warp's ring, by the number of heads
+__host__ __device__ constexpr int nib_ctas(int nb) { return nb == 1 ? 4 : 3; }
+__host__ __device__ constexpr int nib_stages(int nb) { return nb == 1 ? 5 : 6; }
+constexpr int kMaxCtas = 4;   // the larger
+
+struct NibArgs {
+    fathom_nibble_pages p;
+    int lg, G, cap;
+    const float *q;
+    const unsigned char *kv;
+    const int32_t *table, *lens;
+    float *out, *lse;
+    Parts parts;
+};
+
+struct Todo {   // a unit to be joined: its CTAs, and whether the first has a share of an earlier one
+    int unit, first, last;
+    bool before;
+};
+template <int kD, int kNB>
+struct NibSmem {
+    alignas(128) unsigned char ring[kWarps][nib_stages(kNB)][nib_block_bytes(kD)];
+    float o[kWarps][4 * kNB][kD + 8];   // rows 8 words apart: four heads' stores meet in no bank
+    float m[kWarps][FATHOM_MAX_G], l[kWarps][FATHOM_MAX_G];
+    Share z;
+    Todo todo[2];
+    int next_seq[kWarps], next_head[kWarps];   // where a warp's copies have got to
+    ShareSmem<kWarps> share;
+    JoinSmem join;
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1, const float (&c)[4]) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+// One or two groups' codes of 16 tokens: registers 2 g, 2 g + 1 hold tokens 0-7 and 8-15.
+template <bool kTrans, bool kPair>
+__device__ __forceinline__ void load_codes(uint32_t (&r)[4], uint32_t addr) {
+    if (kPair) {
+        if (kTrans)
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+        else
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+    } else {
+        if (kTrans)
+            asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+        else
+            asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+    }
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 halves(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+__device__ __forceinline__ uint32_t fma_h2(uint32_t x, uint32_t y, uint32_t z) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_h2(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_h2(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+__device__ __forceinline__ uint32_t half_pair(float x) { return pack_half2(x, x); }
+
+constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+constexpr float kQueryPiece = 1.0f / 4096;   // what the second piece counts
+constexpr float kUp = 13.0f;                 // weights are 2^13 larger
+constexpr int kFlush = 16;
+// (c - 7.5) 2^-9 of a code in low or high position: times 2^15 or 2^11, minus 7.5 2^-9
+__device__ __forceinline__ uint32_t centred_low(uint32_t x) { return fma_h2(x & kLow, 0x78007800u, 0xa380a380u); }
+__device__ __forceinline__ uint32_t centred_high(uint32_t x) { return fma_h2(x & kHigh, 0x68006800u, 0xa380a380u); }
+
+// Scales of tokens r and r + 8, group by group.
+template <int kGroups>
+__device__ __forceinline__ void load_scales(uint32_t (&s)[kGroups], const unsigned char *at, int r) {
+    if constexpr (kGroups == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(at + 16 * r);
+        s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
+    } else if constexpr (kGroups == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(at + 8 * r);
+        s[0] = v.x; s[1] = v.y;
+    } else {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) s[g] = *reinterpret_cast<const uint32_t *>(at + 4 * (kGroups * r + g));
+    }
+}
+
+// Elements e .. e + 3 of a unit's result from its joined sums: 2^9 of the codes, a / 8.
+template <int kD>
+struct Finish {
+    float *out, *lse;   // of the unit
+    __device__ __forceinline__ void operator()(int e, float4 o, float m, float l) const {
+        const float inv = l > 0.0f ? 64.0f / l : 0.0f;
+        *reinterpret_cast<float4 *>(out + e) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (lse && e % kD == 0) lse[e / kD] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+    }
+};
+
+template <int kD, int kNB>   // kNB: four heads each
+__global__ void __launch_bounds__(kThreads, nib_ctas(kNB))
+nibble_attn_kernel(const NibArgs a) {
+    pdl_enter();
+    using Smem = NibSmem<kD, kNB>;
+    constexpr int kStages = nib_stages(kNB), kGroups = kD / 32, kBlock = nib_block_bytes(kD);
+    extern __shared__ __align__(128) unsigned char nib_smem[];
+    Smem &sm = *reinterpret_cast<Smem *>(nib_smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
+    const int H = a.p.kv_heads, G = a.G;
+    auto length = [&](int s) { return min(max(a.lens[s], 0), a.cap); };
+    auto tiles_of = [&](int n) { return (n + kTile - 1) / kTile; };
+
+    int seq, head, tok, n;   // of the block being computed: its unit, its first token, the sequence's tokens
+    int count;
+    {
+        const Share z = find_share<kWarps>(a.p.seqs, H, 4, gridDim.x / nib_ctas(kNB), [&](int s) { return tiles_of(length(s)); }, sm.share);
+        for (int u = blockIdx.x; u < a.p.seqs * H; u += gridDim.x)   // units of empty sequences
+            if (length(u / H) == 0) {
+                for (int e = tid; e < G * kD; e += kThreads) a.out[(size_t)u * G * kD + e] = 0.0f;
+                if (a.lse && tid < G) a.lse[(size_t)u * G + tid] = -CUDART_INF_F;
+            }
+        if (z.w0 >= z.w1) return;
+        count = (int)(z.w1 - z.w0);
+        seq = z.seq;
+        n = length(seq);
+        const int tiles = tiles_of(n);
+        head = (int)div_small(z.w0 - z.first, tiles);
+        tok = (int)(z.w0 - z.first - (long long)head * tiles) * kTile + warp * kNibTokens;
+        if (tid == 0) sm.z = z;   // read again at the units' ends
+    }
+    // the next unit with tokens (none: seq = seqs)
+    auto next_unit = [&](int &s, int &h, int &len) {
+        if (++h < H) return;
+        h = 0;
+        do len = ++s < a.p.seqs ? length(s) : 1; while (len == 0);
+    };
+
+    // ---- copies: the page of a warp's block is looked up one block ahead (-1: none)
+    int ld_tok = tok, ld_n = n, page;
+    const int32_t *ld_row;          // the sequence's row of the page table
+    const unsigned char *ld_kv;     // the head's part of page 0
+    {
+        ld_row = a.table + (size_t)seq * a.p.max_pages;
+        ld_kv = a.kv + head * a.p.head_stride;
+        if (lane == 0) { sm.next_seq[warp] = seq; sm.next_head[warp] = head; }
+        __syncwarp();
+    }
+    auto lookup = [&]() {
+        if (ld_tok >= ld_n) return -1;
+        const int x = __ldg(ld_row + (ld_tok >> a.lg));
+        return x >= a.p.num_pages ? -1 : x;
+    };
+    auto ld_advance = [&]() {
+        ld_tok += kTile;
+        if (ld_tok - warp * kNibTokens < ld_n) return;
+        int s = sm.next_seq[warp], h = sm.next_head[warp];
+        next_unit(s, h, ld_n);
+        __syncwarp();
+        if (lane == 0) { sm.next_seq[warp] = s; sm.next_head[warp] = h; }
+        __syncwarp();
+        ld_tok = warp * kNibTokens;
+        if (s >= a.p.seqs) { ld_n = 0; return; }   // no page from here on
+        ld_row = a.table + (size_t)s * a.p.max_pages;
+        ld_kv = a.kv + h * a.p.head_stride;
+    };
+    const uint32_t ring = smem_addr(sm.ring[warp]) + 16 * lane;
+    unsigned filled = 0;   // stages with a block
+    auto issue = [&](int st, int pg) {
+        if (pg < 0) return;
+        filled |= 1u << st;
+        const unsigned char *src = ld_kv + pg * a.p.page_stride + (ld_tok & (a.p.page_tokens - 1)) / kNibTokens * kBlock + 16 * lane;
+        const uint32_t dst = ring + st * kBlock;
+#pragma unroll
+        for (int k = 0; k < (kBlock + 511) / 512; ++k)
+            if (512 * (k + 1) <= kBlock || 16 * lane < kBlock - 512 * k)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512 * k), "l"(src + 512 * k) : "memory");
+    };
+    page = lookup();
+#pragma unroll 1
+    for (int st = 0; st < kStages - 1; ++st) {
+        if (st < count) {
+            issue(st, page);
+            ld_advance();
+            page = lookup();
+        }
+        cp_async_commit();
+    }
+
+    const float to_log2 = 1.4426950408889634f / sqrtf((float)kD);
+    uint32_t qb[kNB][kGroups][2][2];   // q's pieces: columns 2 h + piece, see the products below
+    float bias[kNB][kGroups][2], unscale[kNB];
+    // of head c + 4 nb: the largest score (before unscale), 13 - it, the weights' sum of this lane's tokens, and
+    // what the sums in shared memory refer to
+    float m[kNB], shift[kNB], l[kNB], kept[kNB], o[kNB][2 * kGroups][4];
+    uint32_t grow = 0, bound = 0;      // 2^k, and the scale above which k changes, as pairs
+    bool in_smem = false;
+    int blocks = 0;                    // since the sums moved
+    auto flush = [&]() {               // sums in shared memory: relative to 2^(max - 13), without 2^k
+        const float down = 1.0f / halves(grow).x;
+#pragma unroll
+        for (int nb = 0; nb < kNB; ++nb) {
+            const float f = kept[nb] == shift[nb] ? 1.0f : exp2_approx(shift[nb] - kept[nb]);
+            kept[nb] = shift[nb];
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                float(&u)[4] = o[nb][2 * g], (&v)[4] = o[nb][2 * g + 1];
+                float4 *to = reinterpret_cast<float4 *>(&sm.o[warp][4 * nb + c][32 * g + 4 * r]);
+                float4 x = make_float4((u[0] + u[1]) * down, (u[2] + u[3]) * down, (v[0] + v[1]) * down, (v[2] + v[3]) * down);
+                if (in_smem) {
+                    const float4 y = *to;
+                    x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
+                }
+                *to = x;
+                u[0] = u[1] = u[2] = u[3] = v[0] = v[1] = v[2] = v[3] = 0.0f;
+            }
+        }
+        in_smem = true;
+        blocks = 0;
+    };
+    int st = 0, joins = 0;
+
+#pragma unroll 1
+    for (int i = 0; i < count;) {
+        {   // a new unit: its queries in pieces, empty sums
+#pragma unroll
+            for (int nb = 0; nb < kNB; ++nb) {
+                const int mine = 4 * nb + (r >> 1);
+                const float *qr = a.q + ((size_t)(seq * H + head) * G + mine) * kD + 8 * c;
+                float x[kGroups][8], big = 0.0f;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float4 v = mine < G ? __ldg(reinterpret_cast<const float4 *>(qr + 32 * g) + e)
+                                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        x[g][4 * e] = v.x; x[g][4 * e + 1] = v.y; x[g][4 * e + 2] = v.z; x[g][4 * e + 3] = v.w;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[g][e]));
+                }
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                // a power of two that brings the largest to 2^10 .. 2^11; a code in high position counts 16 times
+                const int up = big > 0.0f && big < CUDART_INF_F ? min(max(10 - ilogbf(big), -126), 126) : 0;
+                const float scale = ldexpf(1.0f, up);
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    float piece[8], sum = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float y = x[g][e] * scale, hi = rintf(y);
+                        piece[e] = r & 1 ? rintf((y - hi) * 4096.0f) : hi;
+                        sum += piece[e];
+                    }
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    sum *= -7.5f / 16777216.0f;
+                    bias[nb][g][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
+                    bias[nb][g][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {   // channels 8 c + 2 k and 4 on (low position), and their neighbours (high)
+                        qb[nb][g][k][0] = pack_half2(piece[2 * k], piece[2 * k + 4]);
+                        qb[nb][g][k][1] = pack_half2(piece[2 * k + 1] * 0.0625f, piece[2 * k + 5] * 0.0625f);
+                    }
+                }
+                // a / 8 of the scales, 2^-24 of the codes
+                unscale[nb] = __shfl_sync(0xffffffffu, ldexpf(to_log2, 21 - up), 8 * c);
+                m[nb] = -CUDART_INF_F;
+                shift[nb] = kUp;
+                kept[nb] = kUp;
+                l[nb] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 2 * kGroups; ++j) o[nb][j][0] = o[nb][j][1] = o[nb][j][2] = o[nb][j][3] = 0.0f;
+            }
+            grow = 0x74007400u;    // 2^14
+            bound = 0x0c000c00u;   // 2^-12
+            in_smem = false;
+            blocks = 0;
+        }
+        const int first_tile = tok / kTile, last = min(count, i + tiles_of(n) - first_tile);
+#pragma unroll 1
+        for (; i < last; ++i, tok += kTile) {
+            // the copy kStages - 1 blocks ahead, into the stage that was read last
+            if (i + kStages - 1 < count) {
+                issue(st == 0 ? kStages - 1 : st - 1, page);
+                ld_advance();
+                page = lookup();
+            }
+            cp_async_commit();
+            cp_async_wait<kStages - 1>();
+            __syncwarp();
+            if (filled >> st & 1u) {
+                filled ^= 1u << st;
+                const unsigned char *blk = sm.ring[warp][st];
+                const uint32_t codes = ring + st * kBlock;
+                // ---- scores of tokens r and r + 8: columns 2 c, 2 c + 1 are the two pieces of head c
+                float s[kNB][2];
+                {
+                    uint32_t sc[kGroups];
+                    load_scales<kGroups>(sc, blk + nib_scales(kD), r);
+#pragma unroll
+                    for (int g0 = 0; g0 < kGroups; g0 += 2) {
+                        uint32_t x[4];
+                        if (g0 + 1 < kGroups) load_codes<false, true>(x, codes + g0 * 256);
+                        else load_codes<false, false>(x, codes + g0 * 256);
+#pragma unroll
+                        for (int g = g0; g < g0 + 2 && g < kGroups; ++g) {
+                            const uint32_t x0 = x[2 * (g - g0)], x1 = x[2 * (g - g0) + 1], y0 = x0 >> 8, y1 = x1 >> 8;
+                            const float2 f = halves(sc[g]);
+#pragma unroll
+                            for (int nb = 0; nb < kNB; ++nb) {
+                                const float b[4] = {bias[nb][g][0], bias[nb][g][1], bias[nb][g][0], bias[nb][g][1]};
+                                float t[4];
+                                mma_f16(t, x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh, qb[nb][g][0][0], qb[nb][g][0][1], b);
+                                mma_f16(t, y0 & kLow, y1 & kLow, y0 & kHigh, y1 & kHigh, qb[nb][g][1][0], qb[nb][g][1][1], t);
+                                t[0] = fmaf(t[1], kQueryPiece, t[0]);
+                                t[2] = fmaf(t[3], kQueryPiece, t[2]);
+                                s[nb][0] = g ? fmaf(f.x, t[0], s[nb][0]) : f.x * t[0];
+                                s[nb][1] = g ? fmaf(f.y, t[2], s[nb][1]) : f.y * t[2];
+                            }
+                        }
+                    }
+                }
+                uint32_t vs[kGroups];
+                load_scales<kGroups>(vs, blk + nib_half(kD) + nib_scales(kD), r);
+                if (tok + kNibTokens > n) {   // tokens behind the last: no weight, whatever their places hold
+                    const int left = n - tok;
+#pragma unroll
+                    for (int nb = 0; nb < kNB; ++nb) {
+                        if (r >= left) s[nb][0] = -CUDART_INF_F;
+                        if (r + 8 >= left) s[nb][1] = -CUDART_INF_F;
+                    }
+                    const uint32_t keep = (r < left ? 0xffffu : 0u) | (r + 8 < left ? 0xffff0000u : 0u);
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) vs[g] &= keep;
+                }
+                uint32_t most = vs[0];
+#pragma unroll
+                for (int g = 1; g < kGroups; ++g) most = max_h2(most, vs[g]);
+                bool raise = __hbgt2(*reinterpret_cast<const __half2 *>(&bound), *reinterpret_cast<const __half2 *>(&most)) ? false : true;
+#pragma unroll
+                for (int nb = 0; nb < kNB; ++nb) raise |= fmaxf(s[nb][0], s[nb][1]) > m[nb];
+                if (__any_sync(0xffffffffu, raise)) {
+                    float2 mh = halves(most);
+                    float top_scale = fmaxf(mh.x, mh.y), ratio = 1.0f;
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) top_scale = fmaxf(top_scale, __shfl_xor_sync(0xffffffffu, top_scale, d));
+                    if (top_scale >= halves(bound).x) {   // k brings the largest scale to 1 .. 2, and holds until 4
+                        const int k = top_scale < CUDART_INF_F ? min(max(-ilogbf(top_scale), -14), 14) : -14;
+                        const float now = ldexpf(1.0f, k);
+                        ratio = now / halves(grow).x;
+                        grow = half_pair(now);
+                        bound = half_pair(fminf(4.0f / now, 65504.0f * 2));
+                    }
+#pragma unroll
+                    for (int nb = 0; nb < kNB; ++nb) {
+                        float top = fmaxf(s[nb][0], s[nb][1]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        top = fmaxf(top, m[nb]);
+                        float f = 1.0f;
+                        if (top > m[nb]) {
+                            const float to = fmaf(-top, unscale[nb], kUp);
+                            if (m[nb] != -CUDART_INF_F) f = exp2_approx(to - shift[nb]);   // empty sums: 0, or NaN
+                            else kept[nb] = to;                                            // nor is anything else in shared memory
+                            m[nb] = top;
+                            shift[nb] = to;
+                        }
+                        l[nb] *= f;
+                        f *= ratio;
+#pragma unroll
+                        for (int j = 0; j < 2 * kGroups; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[nb][j][e] *= f;
+                    }
+                }
+                uint32_t hi[kNB], lo[kNB];   // weights of tokens r (low half) and r + 8
+#pragma unroll
+                for (int nb = 0; nb < kNB; ++nb) {
+                    const float w0 = exp2_approx(fmaf(s[nb][0], unscale[nb], shift[nb]));
+                    const float w1 = exp2_approx(fmaf(s[nb][1], unscale[nb], shift[nb]));
+                    l[nb] += w0 + w1;
+                    hi[nb] = pack_half2(w0, w1);
+                    const float2 h = halves(hi[nb]);
+                    lo[nb] = pack_half2(w0 - h.x, w1 - h.y);
+                }
+                // ---- weights times V: channels 4 r + (0, 1) and 4 r + (2, 3) of a group are two products' rows
+#pragma unroll
+                for (int g0 = 0; g0 < kGroups; g0 += 2) {
+                    uint32_t x[4];
+                    if (g0 + 1 < kGroups) load_codes<true, true>(x, codes + nib_half(kD) + g0 * 256);
+                    else load_codes<true, false>(x, codes + nib_half(kD) + g0 * 256);
+#pragma unroll
+                    for (int g = g0; g < g0 + 2 && g < kGroups; ++g) {
+                        const uint32_t x0 = x[2 * (g - g0)], x1 = x[2 * (g - g0) + 1], y0 = x0 >> 8, y1 = x1 >> 8;
+                        const uint32_t f = mul_h2(vs[g], grow);
+                        uint32_t b[kNB][2];
+#pragma unroll
+                        for (int nb = 0; nb < kNB; ++nb) {
+                            const uint32_t h = mul_h2(hi[nb], f);
+                            const uint32_t e = fma_h2(lo[nb], f, fma_h2(hi[nb], f, h ^ 0x80008000u));
+                            b[nb][0] = transpose8(__byte_perm(h, e, 0x5410));
+                            b[nb][1] = transpose8(__byte_perm(h, e, 0x7632));
+                        }
+                        const uint32_t a0 = centred_low(x0), a1 = centred_high(x0), a2 = centred_low(x1), a3 = centred_high(x1);
+                        const uint32_t c0 = centred_low(y0), c1 = centred_high(y0), c2 = centred_low(y1), c3 = centred_high(y1);
+#pragma unroll
+                        for (int nb = 0; nb < kNB; ++nb) {
+                            mma_f16(o[nb][2 * g], a0, a1, a2, a3, b[nb][0], b[nb][1], o[nb][2 * g]);
+                            mma_f16(o[nb][2 * g + 1], c0, c1, c2, c3, b[nb][0], b[nb][1], o[nb][2 * g + 1]);
+                        }
+                    }
+                }
+                if (++blocks == kFlush) flush();
+                __syncwarp();   // the stage is read before its next copy starts
+            }
+            st = st + 1 == kStages ? 0 : st + 1;
+        }
+
+        // ---- end of the unit, or of this CTA's share of it
+        const int unit = seq * H + head, tiles = tiles_of(n);
+#pragma unroll
+        for (int nb = 0; nb < kNB; ++nb) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], d);
+            if (r == 0) {
+                sm.m[warp][4 * nb + c] = m[nb] == -CUDART_INF_F ? -CUDART_INF_F : -shift[nb];
+                sm.l[warp][4 * nb + c] = l[nb];
+            }
+        }
+        flush();
+        __syncthreads();
+        // the CTA's state of each head: (m, l, o), to `out` when the unit is all here
+        const long long W = sm.z.W, NC = sm.z.NC, unit_w0 = sm.z.w0 + i - tok / kTile;   // index of the unit's first tile
+        const long long c_first = div_small((unit_w0 + 1) * NC - 1, W), c_last = div_small((unit_w0 + tiles) * NC - 1, W);
+        const bool whole = c_first == c_last;
+        const Finish<kD> finish{a.out + (size_t)unit * G * kD, a.lse ? a.lse + (size_t)unit * G : nullptr};
+        const size_t slot = 2 * (size_t)blockIdx.x + (sm.z.w0 < unit_w0 ? 1 : 0);
+        for (int e = 4 * tid; e < G * kD; e += 4 * kThreads) {
+            const int h = e / kD, d = e % kD;
+            float M = -CUDART_INF_F, L = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kWarps; ++v) M = fmaxf(M, sm.m[v][h]);
+            float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int v = 0; v < kWarps; ++v) {
+                // a warp without a maximum has nothing, or NaN that stays
+                const float f = sm.m[v][h] == -CUDART_INF_F ? 1.0f : exp2_approx(sm.m[v][h] - M);
+                const float4 x = *reinterpret_cast<const float4 *>(&sm.o[v][h][d]);
+                O.x = fmaf(x.x, f, O.x); O.y = fmaf(x.y, f, O.y); O.z = fmaf(x.z, f, O.z); O.w = fmaf(x.w, f, O.w);
+                L = fmaf(sm.l[v][h], f, L);
+            }
+            if (whole) {
+                finish(e, O, M, L);
+            } else {
+                *reinterpret_cast<float4 *>(a.parts.o + slot * G * kD + e) = O;
+                if (d == 0) *reinterpret_cast<float2 *>(a.parts.ml + (slot * G + h) * 2) = make_float2(M, L);
+            }
+        }
+        if (!whole) {
+            if (tid == 0) sm.todo[joins] = Todo{unit, (int)c_first, (int)c_last, share_start(c_first, W, NC) < unit_w0};
+            ++joins;
+        }
+        next_unit(seq, head, n);
+        tok = warp * kNibTokens;
+        __syncthreads();   // the merge buffers are free again
+    }
+    cp_async_wait<0>();
+    // the first unit and the last one may have other CTAs' shares; joined here, where the loop's registers are free
+#pragma unroll 1
+    for (int k = 0; k < joins; ++k) {
+        const Todo t = sm.todo[k];
+        const Finish<kD> finish{a.out + (size_t)t.unit * G * kD, a.lse ? a.lse + (size_t)t.unit * G : nullptr};
+        join_parts<kWarps, kD, 4 * kNB>(a.parts, G, t.first, t.last, t.before, sm.join, finish);
+        __syncthreads();
+    }
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+template <int kD, int kNB>
+cudaError_t launch(const NibArgs &a, int sms, cudaStream_t st) {
+    using Smem = NibSmem<kD, kNB>;
+    static_assert(nib_ctas(kNB) * (sizeof(Smem) + 1024) <= 228 * 1024, "resident CTAs");
+    ensure_smem(nibble_attn_kernel<kD, kNB>, sizeof(Smem));
+    return launch_pdl(nibble_attn_kernel<kD, kNB>, dim3(nib_ctas(kNB) * sms), dim3(kThreads), sizeof(Smem), st, a);
+}
+template <int kD>
+cudaError_t launch_heads(const NibArgs &a, int sms, cudaStream_t st) {
+    return a.G > 4 ? launch<kD, 2>(a, sms, st) : launch<kD, 1>(a, sms, st);
+}
+
+}  // namespace
+
+NibbleWorkspace nibble_workspace_layout(const fathom_nibble_pages &p, int G) {
+    NibbleWorkspace w;
+    w.sms = device_sm_count();
+    if (w.sms <= 0) w.sms = 152;
+    const size_t ctas = (size_t)kMaxCtas * w.sms;
+    // Tickets first, as many whatever the call, so that one buffer serves calls of different sizes:
+    // one for each CTA's unit that goes on behind it, two for groups of shares that begin at it.
+    w.part_off = align256(3 * ctas * sizeof(uint32_t));
+    w.ml_off = align256(w.part_off + ctas * 2 * G * p.D * sizeof(float));
+    w.total = align256(w.ml_off + ctas * 2 * G * 2 * sizeof(float));
+    return w;
+}
+
+int launch_nibble_attn(const fathom_nibble_pages &p, int G, const float *q, const void *kv, const int32_t *table,
+                       const int32_t *lens, float *out, float *lse, void *ws, cudaStream_t st) {
+    const NibbleWorkspace w = nibble_workspace_layout(p, G);
+    NibArgs a;
+    a.p = p;
+    a.lg = 0;
+    while ((1 << a.lg) < p.page_tokens) ++a.lg;
+    a.G = G;
+    a.cap = p.max_pages * p.page_tokens;
+    a.q = q; a.kv = (const unsigned char *)kv; a.table = table; a.lens = lens; a.out = out; a.lse = lse;
+    a.parts.ticket = (unsigned *)ws;
+    a.parts.group_ticket = a.parts.ticket + kMaxCtas * w.sms;
+    a.parts.o = (float *)((char *)ws + w.part_off);
+    a.parts.ml = (float *)((char *)ws + w.ml_off);
+    cudaError_t e;
+    if (p.D == 128) e = launch_heads<128>(a, w.sms, st);
+    else if (p.D == 96) e = launch_heads<96>(a, w.sms, st);
+    else if (p.D == 64) e = launch_heads<64>(a, w.sms, st);
+    else e = launch_heads<32>(a, w.sms, st);
+    if (e != cudaSuccess) return launch_failed("nibble_attn_kernel", e);
+    return launch_status("nibble_attn");
+}
+
+}  // namespace fathom

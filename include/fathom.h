@@ -24,8 +24,8 @@
  *   synchronisation, no host read of device results.  Results are valid once
  *   the stream reaches them.  The kernels of fathom_plan, fathom_plan_fixed,
  *   fathom_scan_topk, fathom_scan, fathom_select, fathom_exact_topk, fathom_sparse_attn,
- *   fathom_sparse_attn_planes, fathom_sparse_attn_noalloc, fathom_paged_attn and
- *   fathom_paged_evict are launched with programmatic stream serialisation: each may
+ *   fathom_sparse_attn_planes, fathom_sparse_attn_noalloc, fathom_paged_attn,
+ *   fathom_paged_evict, fathom_paged_append_rope and the fathom_nibble calls are launched with programmatic stream serialisation: each may
  *   be scheduled while the work before it on the stream is finishing, but it waits for
  *   that work to complete before it reads or writes memory, so the stream order is
  *   unchanged.
@@ -165,6 +165,50 @@ typedef struct {
     int32_t max_pages;    /* entries of a page table row; max_pages * page_tokens <= 2^28 */
     int64_t page_stride, head_stride, token_stride;   /* elements, positive multiples of 8 */
 } fathom_pages;
+
+/* A paged KV cache of one layer held in 4 bits: 32 channels of a token share a
+ * scale a (fp16), and a code c in 0 .. 15 stands for (c - 7.5) a / 8.  A page of
+ * one KV head is page_tokens / 16 blocks of 16 tokens, one after the other, of
+ * 18 D bytes each:
+ *   codes of K [D / 32][16 tokens][16 bytes], channel 2 b of a group of 32 in the
+ *   low and 2 b + 1 in the high four bits of byte b; scales of K, fp16,
+ *   [8][D / 32][2] (tokens r and r + 8 of the block side by side); codes and
+ *   scales of V, the same
+ * and block j of (page, head) lies at byte
+ *   page * page_stride + head * head_stride + 18 D j
+ * of kv_pages.  Any 18 D bytes are a block (zeros: scale 0, values 0).  The page
+ * table is that of fathom_pages. */
+typedef struct {
+    int32_t seqs;         /* sequences, 1 .. 65535 */
+    int32_t kv_heads;     /* KV heads per sequence; seqs * kv_heads <= 65535 */
+    int32_t D;            /* channels: 32, 64, 96 or 128 */
+    int32_t page_tokens;  /* a power of two, at least 16 */
+    int32_t num_pages;    /* >= 1 */
+    int32_t max_pages;    /* entries of a page table row; max_pages * page_tokens <= 2^28 */
+    int64_t page_stride, head_stride;   /* bytes, positive multiples of 16 */
+} fathom_nibble_pages;
+
+/* Position rotation of new rows on their way into a cache, and of the step's
+ * queries: the first rot channels of a row are pairs (x, y), channels i and
+ * i + rot / 2 or, interleaved, 2 i and 2 i + 1, and pair i of a token at position
+ * p becomes (x cos - y sin, y cos + x sin), cos = table[p][i], sin =
+ * table[p][rot / 2 + i].  Channels from rot on stay as they are.  The angles are
+ * the caller's (any base, any scaling of long contexts), worked out in 64 bits
+ * where positions are far.  A token whose position lies outside the table is
+ * skipped: neither its rows nor its queries are written. */
+typedef struct {
+    const float *table;          /* [rows][rot] fp32, 16-byte aligned */
+    int32_t rows;                /* positions 0 .. rows - 1 */
+    int32_t rot;                 /* even, 2 .. D */
+    int32_t interleaved;         /* 0 or 1 */
+    const int32_t *positions;    /* [total_new], or NULL: a token's place in its sequence (after an
+                                    eviction the two differ) */
+    const void *q;               /* NULL, or queries [total_new][q_heads][D] of the new rows' type */
+    void *q_out;                 /* [total_new][q_heads][D], not q */
+    int32_t q_heads;             /* 1 .. 65535 */
+    int32_t q_dtype;             /* of q_out: the new rows' type, or FATHOM_F32 (what the decode calls take) */
+    int64_t q_token, q_head, out_token, out_head;   /* elements, positive multiples of 8 */
+} fathom_rope;
 
 /* ---------------------------------------------------------------------- */
 
@@ -566,6 +610,65 @@ int fathom_paged_evict(const fathom_pages *pages, void *k_pages, void *v_pages, 
                        int32_t n_sink, int32_t n_recent, const int32_t *dst_table, int32_t dst_pages,
                        int32_t *kept_idx, int32_t *lens_out, float *mass_out, size_t mass_out_stride,
                        void *stream);
+
+/* fathom_paged_append with the position rotation: new keys, and the queries that rope
+ * names, are rotated in fp32 (with the products' rounding errors) and rounded once to
+ * where they go; values are copied.  A token without a place in the cache is not
+ * written there, but its queries are.
+ *   rope: not NULL; other arguments as fathom_paged_append. */
+int fathom_paged_append_rope(const fathom_pages *pages, void *k_pages, void *v_pages, const int32_t *page_table,
+                             const void *k_new, const void *v_new, int32_t total_new, int64_t new_token,
+                             int64_t new_head, const int32_t *start, const int32_t *cu_new, const fathom_rope *rope,
+                             void *stream);
+
+/* New rows into a 4-bit cache, rotated on the way or not (rope NULL).  Per token, head and
+ * group of 32 channels, of the exact (rotated, not rounded) values x: a = max |x| rounded
+ * to fp16 (65504 at most), c = clip(floor(x / (a / 8)), -8, 7) + 8 as in
+ * fathom_quantize_pack (a = 0: c = 8); codes are those of the real-number arithmetic,
+ * however near a value lies to a border between two.  A NaN makes its group's scale, so its
+ * 32 values, NaN; an infinity counts as a value larger than all fp16 numbers.
+ *   kv_pages (device, in and out), 16-byte aligned; k_new, v_new of row_dtype (FATHOM_BF16
+ *   or FATHOM_F16); other arguments and the tokens that are skipped as in
+ *   fathom_paged_append and fathom_rope
+ * Two new tokens for one place leave unspecified values there. */
+int fathom_nibble_append(const fathom_nibble_pages *pages, void *kv_pages, const int32_t *page_table, int32_t row_dtype,
+                         const void *k_new, const void *v_new, int32_t total_new, int64_t new_token, int64_t new_head,
+                         const int32_t *start, const int32_t *cu_new, const fathom_rope *rope, void *stream);
+
+/* Rows of a 4-bit cache as they are used, (c - 7.5) a / 8 rounded once to out_dtype (exact
+ * in fp32): token i of sequence s's part, packed at cu[s] + i, is the one at position
+ * start[s] + i.  With k_out and v_out the prompt attention of a later chunk reads what
+ * earlier ones left in the cache.
+ *   start [seqs] int32, cu [seqs + 1] int32, total rows in all
+ *   k_out, v_out [total][kv_heads][D] of out_dtype (FATHOM_F32, FATHOM_BF16 or FATHOM_F16) at
+ *   t * out_token + h * out_head + c, strides positive multiples of 8; device
+ * Rows of tokens outside the page table's row, in no page, or behind cu[seqs] are left as
+ * they were. */
+int fathom_nibble_read(const fathom_nibble_pages *pages, const void *kv_pages, const int32_t *page_table,
+                       const int32_t *start, const int32_t *cu, int32_t total, void *k_out, void *v_out,
+                       int32_t out_dtype, int64_t out_token, int64_t out_head, void *stream);
+
+/* Decode attention of one new token per sequence over a 4-bit cache: fathom_paged_attn's
+ * sum over the values that the codes stand for, nothing rounded to fewer than 22 bits on
+ * the way.  lse_opt: log sum_i exp(q_h . k_i / sqrt(D)) (-inf when there is no token), with
+ * which a caller joins the result with attention over other rows (say, recent tokens kept
+ * in 16 bits).  No atomics on values: the same inputs give the same bits.
+ *   G query heads per KV head, 1 .. 8
+ *   q [units][G][D] fp32, kv_pages, page_table, lens [seqs] int32 (clamped to
+ *   [0, max_pages * page_tokens]), out [units][G][D] fp32 (out), lse_opt NULL or [units][G]
+ *   fp32 (out); all device memory; q, kv_pages and out 16-byte aligned
+ *   workspace: at least fathom_nibble_workspace_size(pages, G) bytes, rules as
+ *   fathom_paged_attn's: one that is large enough serves calls of different sizes
+ * Queries and scales are meant to be finite: a NaN in a unit's query or in a scale of K that
+ * it attends to makes its head's (all its heads') outputs NaN, one in a scale of V the
+ * group's channels; an infinity may do the same.  Other units never depend on them, nor does
+ * anything on tokens behind lens[s]. */
+int fathom_nibble_attn(const fathom_nibble_pages *pages, int32_t G, const float *q, const void *kv_pages,
+                       const int32_t *page_table, const int32_t *lens, float *out, float *lse_opt, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of fathom_nibble_attn (0 if an argument is invalid). */
+size_t fathom_nibble_workspace_size(const fathom_nibble_pages *pages, int32_t G);
 
 /* Workspace bytes of fathom_paged_attn, with (mass != 0) or without its mass
  * argument (0 if an argument is invalid). */
