@@ -15,18 +15,22 @@ namespace {
 // K, of the queries, of V), so that the rotation's cos and sin, the page and the place are
 // found once.  Bound by the bytes: each row read and written once.
 //
-// A pair (x, y) turns by (x cos - y sin, y cos + x sin).  The products and their sum are
-// taken with the rounding errors that two fused multiply-adds give exactly, so a result is
-// off by 2^-23 of itself, also where the two products nearly cancel.
+// A pair (x, y) turns by (x cos - y sin, y cos + x sin), a product and a fused multiply-add
+// in fp32, off by 2^-24 of |x cos| + |y sin| and of the result.
 //
 // In 4 bits, 32 channels of a token share a = fp16(max |x|) and are coded as
-// clip(floor(x / (a / 8)), -8, 7) + 8.  Borders between codes are numbers of 14 bits and
-// the roundings to fp16 look at 12, so a rotated key is first rounded to odd in fp32 (cut
-// off, the last bit set where something was cut): every comparison and rounding after that
-// is that of the unrounded key, and codes do not depend on how the rotation was computed.
+// clip(floor(x / (a / 8)), -8, 7) + 8 of the exact x.  Values are exact: a quotient that is
+// never too large gives the code or the one below it, and one fused multiply-add tells
+// which.  Rotated keys are coded from fp32 like the queries, with a bound on what that is
+// off by; where a border between two codes, or between two scales, is nearer than the
+// bound (one group of 2000), the group is worked out again exactly: the products' errors
+// and the sum's are exact, and the result is rounded to odd (cut off to 24 bits, the last
+// bit set where something was cut), after which comparisons with the borders, numbers of
+// 14 bits, and the rounding to fp16 are those of the unrounded key.
 
 constexpr int kThreads = 128;
-constexpr int kBatch = 4;   // rows loaded together
+constexpr int kBatch = 2;       // rows loaded together
+constexpr int kReadBatch = 4;   // when read back
 
 struct AppendArgs {
     fathom_pages p;              // one of the two caches
@@ -76,11 +80,12 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     return make_uint4(to_pair(x[0], x[1], T()), to_pair(x[2], x[3], T()), to_pair(x[4], x[5], T()), to_pair(x[6], x[7], T()));
 }
 
-// x c + y s, off by 2^-23 of the result: both products' errors and the sum's are exact.
-__device__ __forceinline__ float turn(float x, float y, float c, float s) {
-    const float p = __fmul_rn(x, c), r = fmaf(y, s, p);
-    return fabsf(r) < CUDART_INF_F ? r + fmaf(x, c, -p) : r;   // the error of an infinity is NaN
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
+
 // x c + y s rounded to odd: cut off to 24 bits, the last bit set where something was cut.
 __device__ __forceinline__ float turn_odd(float x, float y, float c, float s) {
     const float p = __fmul_rn(x, c), q = __fmul_rn(y, s);
@@ -120,15 +125,24 @@ __device__ __forceinline__ Turn load_turn(const float *row, int c0, int rot, boo
     const int half = rot / 2;
     t.live = c0 + 8 <= rot ? 0xffu : c0 < rot ? (1u << (rot - c0)) - 1u : 0u;
     t.from = pairs ? -1 : vec ? partner_of(c0, half) : -2;
-    if (!t.live) return t;
-    if (vec && !pairs) {
-        const int i = c0 < half ? c0 : c0 - half;
-        const float sign = c0 < half ? -1.0f : 1.0f;
+    if (vec && t.live) {
+        const float4 *c = reinterpret_cast<const float4 *>(row + (pairs ? c0 / 2 : c0 < half ? c0 : c0 - half));
+        const float4 *s = c + half / 4;
+        const float4 a = __ldg(c), b = __ldg(s);
+        if (pairs) {
+            const float ca[4] = {a.x, a.y, a.z, a.w}, sa[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(row + i) + e), b = __ldg(reinterpret_cast<const float4 *>(row + half + i) + e);
-            t.cs[4 * e] = a.x; t.cs[4 * e + 1] = a.y; t.cs[4 * e + 2] = a.z; t.cs[4 * e + 3] = a.w;
-            t.sn[4 * e] = sign * b.x; t.sn[4 * e + 1] = sign * b.y; t.sn[4 * e + 2] = sign * b.z; t.sn[4 * e + 3] = sign * b.w;
+            for (int e = 0; e < 8; ++e) {
+                t.cs[e] = ca[e / 2];
+                t.sn[e] = e & 1 ? sa[e / 2] : -sa[e / 2];
+            }
+        } else {
+            const float4 a2 = __ldg(c + 1), b2 = __ldg(s + 1);
+            const float g = c0 < half ? -1.0f : 1.0f;
+            t.cs[0] = a.x; t.cs[1] = a.y; t.cs[2] = a.z; t.cs[3] = a.w;
+            t.cs[4] = a2.x; t.cs[5] = a2.y; t.cs[6] = a2.z; t.cs[7] = a2.w;
+            t.sn[0] = g * b.x; t.sn[1] = g * b.y; t.sn[2] = g * b.z; t.sn[3] = g * b.w;
+            t.sn[4] = g * b2.x; t.sn[5] = g * b2.y; t.sn[6] = g * b2.z; t.sn[7] = g * b2.w;
         }
         return t;
     }
@@ -144,6 +158,207 @@ __device__ __forceinline__ Turn load_turn(const float *row, int c0, int rot, boo
         t.sn[e] = first ? -__ldg(row + half + i) : __ldg(row + half + i);
     }
     return t;
+}
+
+// The partners of a row's 8 channels, 0 for those that do not turn.
+template <typename T>
+__device__ __forceinline__ uint4 load_partners(const T *row, const uint4 &own, int c0, int rot, const Turn &z) {
+    if (z.from >= 0) return __ldg(reinterpret_cast<const uint4 *>(row + z.from));
+    uint32_t w[4];
+    if (z.from == -1) {
+        const uint32_t o[4] = {own.x, own.y, own.z, own.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = z.live >> (2 * i) & 1u ? __byte_perm(o[i], 0, 0x1032) : 0u;
+    } else {
+        const uint16_t *p = reinterpret_cast<const uint16_t *>(row);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = z.live >> (2 * i) & 1u ? __ldg(p + partner_of(c0 + 2 * i, rot / 2)) : 0u;
+            const uint32_t hi = z.live >> (2 * i + 1) & 1u ? __ldg(p + partner_of(c0 + 2 * i + 1, rot / 2)) : 0u;
+            w[i] = lo | hi << 16;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A group's scale and the codes of a thread's 8 channels, the lanes of `quad` together.
+struct Coded {
+    uint32_t word;
+    __half a;
+};
+constexpr float kMagic = 8388624.0f;   // 2^23 + 16: a sum with it, rounded down, ends in 16 + floor
+// Eight such sums are the digits of a word; what they share is taken off at the end.
+__device__ __forceinline__ uint32_t add_digit(uint32_t word, float sum, int e) { return word + (__float_as_uint(sum) << (4 * e)); }
+__device__ __forceinline__ uint32_t digits_done(uint32_t word) {
+    constexpr uint32_t kBits = 0x4b000008u;   // the bits of 2^23 + 8
+    constexpr uint32_t kAll = kBits + (kBits << 4) + (kBits << 8) + (kBits << 12) + (kBits << 16) + (kBits << 20) + (kBits << 24) + (kBits << 28);
+    return word - kAll;
+}
+__device__ __forceinline__ float over_quad(float x, unsigned quad) {
+    x = max_nan(x, __shfl_xor_sync(quad, x, 1));
+    return max_nan(x, __shfl_xor_sync(quad, x, 2));
+}
+
+// Any values: NaN makes the scale NaN, what is larger than fp16 holds counts as its largest.
+__device__ __noinline__ Coded code_any(const float (&y)[8], unsigned quad) {
+    float big = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) big = max_nan(big, fabsf(y[e]));
+    big = over_quad(big, quad);
+    Coded r;
+    r.a = big == big ? __float2half_rn(fminf(big, 65504.0f)) : __ushort_as_half((unsigned short)0x7fff);
+    r.word = 0x88888888u;
+    const float a = __half2float(r.a);
+    if (a > 0.0f) {
+        const float step = a * 0.125f, inv = 1.0f / step;
+        r.word = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float f = floorf(fminf(fmaxf(y[e] * inv, -9.0f), 8.0f));
+            if (f * step > y[e]) f -= 1.0f;                     // (f + 1) step has 14 bits
+            else if ((f + 1.0f) * step <= y[e]) f += 1.0f;
+            r.word |= (uint32_t)((int)fminf(fmaxf(f, -8.0f), 7.0f) + 8) << (4 * e);
+        }
+    }
+    return r;
+}
+// Larger or smaller ones than these take the general way.
+__device__ __forceinline__ bool ordinary(float big) { return big > 1.0f / 4096 && big < 32768.0f; }
+
+__device__ __forceinline__ Coded code_exact(const float (&y)[8], unsigned quad) {
+    float big = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) big = max_nan(big, fabsf(y[e]));
+    big = over_quad(big, quad);
+    if (!ordinary(big)) return code_any(y, quad);
+    Coded r;
+    r.a = __float2half_rn(big);
+    // two reciprocals around the true one: the lesser product is at most the quotient, and above it less 2^-19
+    const float step = __half2float(r.a) * 0.125f, inv = 1.0f / step, under = inv * (1.0f - 0x1p-22f), over = inv * (1.0f + 0x1p-22f);
+    const float lowest = -8.0f * step, highest = 7.5f * step;
+    uint32_t word = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float x = fminf(fmaxf(y[e], lowest), highest);
+        float t = __fadd_rd(fminf(x * under, x * over), kMagic);
+        const float next = t - (kMagic - 1.0f);              // the code above
+        if (fmaf(-next, step, x) >= 0.0f) t += 1.0f;
+        word = add_digit(word, t, e);
+    }
+    r.word = digits_done(word);
+    return r;
+}
+
+// Rotated keys: x, their partners and what turns them.
+__device__ __forceinline__ Coded code_turned(const float (&x)[8], const float (&p)[8], const Turn &z, unsigned quad) {
+    float y[8], big = 0.0f, part = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float q = __fmul_rn(p[e], z.sn[e]);
+        y[e] = fmaf(x[e], z.cs[e], q);
+        big = max_nan(big, fabsf(y[e]));
+        part = max_nan(part, fabsf(q));
+    }
+    const float off = 0x1.02p-24f * (part + big);            // of any y here
+    big = over_quad(big, quad);
+    const float all = over_quad(off, quad);
+    if (ordinary(big) && all < big) {
+        Coded r;
+        r.a = __float2half_rn(big);
+        bool near = __half_as_ushort(__float2half_rn(big - 2.0f * all)) != __half_as_ushort(__float2half_rn(big + 2.0f * all));
+        const float inv = 8.0f / __half2float(r.a);
+        uint32_t word = 0;
+        float far = 0.0f;                                    // the largest distance from the middle between two borders
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float v = fminf(fmaxf(y[e] * inv, -7.5f), 7.5f);
+            const float t = __fadd_rd(v, kMagic);
+            far = fmaxf(far, fabsf(v - (t - kMagic) - 0.5f));
+            word = add_digit(word, t, e);
+        }
+        near |= far > 0.5f - (off * inv + 0x1p-19f);
+        if (!(__ballot_sync(quad, near) & quad)) {
+            r.word = digits_done(word);
+            return r;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = z.live >> e & 1u ? turn_odd(x[e], p[e], z.cs[e], z.sn[e]) : x[e];
+    return code_any(y, quad);
+}
+
+enum Rows { kKeys, kQueries, kValues };
+
+// A thread's part of rows lo .. hi - 1 of one kind, `src` the token's first one, head_stride apart.
+template <typename T, bool kNibble, Rows kKind>
+__device__ __forceinline__ void move_rows(const AppendArgs &a, const T *src, int64_t stride, int lo, int hi, int t, int c0, int page,
+                                          int slot, const Turn &z, unsigned quad) {
+    const bool turns = kKind != kValues && z.live, rotated = a.rope != nullptr;
+#pragma unroll 1
+    for (int r0 = lo; r0 < hi; r0 += kBatch) {
+        uint4 own[kBatch], other[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (r0 + b < hi) {
+                const T *row = src + (r0 + b) * stride;
+                own[b] = __ldg(reinterpret_cast<const uint4 *>(row + c0));
+                other[b] = make_uint4(0, 0, 0, 0);
+                if (turns) other[b] = load_partners<T>(row, own[b], c0, a.rot, z);
+            }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int head = r0 + b;
+            if (head >= hi) break;
+            float x[8], p[8];
+            if constexpr (kNibble && kKind != kQueries) {
+                unsigned char *blk = (unsigned char *)a.kp + nib_block(a.n, page, head, slot) + (kKind == kValues ? nib_half(a.n.D) : 0);
+                const int g = c0 / 32, sub = c0 / 8 & 3, in = slot & (kNibTokens - 1);
+                unpack8<T>(own[b], x);
+                Coded c;
+                if (kKind == kKeys && rotated) {   // also the channels of a group that stay: its four lanes go together
+                    unpack8<T>(other[b], p);
+                    c = code_turned(x, p, z, quad);
+                } else {
+                    c = code_exact(x, quad);
+                }
+                *reinterpret_cast<uint32_t *>(blk + nib_code(g, in) + 4 * sub) = c.word;
+                if (sub == 0) *reinterpret_cast<__half *>(blk + nib_scales(a.n.D) + nib_scale(a.n.D, g, in)) = c.a;
+                continue;
+            }
+            uint4 out = own[b];
+            float y[8];
+            if (turns || (kKind == kQueries && a.q_f32)) {
+                unpack8<T>(own[b], x);
+                if (turns) {
+                    unpack8<T>(other[b], p);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = fmaf(x[e], z.cs[e], __fmul_rn(p[e], z.sn[e]));
+                    if (z.live != 0xffu) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (!(z.live >> e & 1u)) y[e] = x[e];
+                    }
+                    out = pack8<T>(y);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = x[e];
+                }
+            }
+            if (kKind == kQueries) {
+                const int64_t to = t * a.out_token + head * a.out_head + c0;
+                if (a.q_f32) {
+                    float4 *q = reinterpret_cast<float4 *>((float *)a.q_out + to);
+                    q[0] = make_float4(y[0], y[1], y[2], y[3]);
+                    q[1] = make_float4(y[4], y[5], y[6], y[7]);
+                } else {
+                    *reinterpret_cast<uint4 *>((T *)a.q_out + to) = out;
+                }
+            } else {
+                T *rows = (T *)(kKind == kValues ? a.vp : a.kp);
+                *reinterpret_cast<uint4 *>(rows + page * a.p.page_stride + head * a.p.head_stride + slot * a.p.token_stride + c0) = out;
+            }
+        }
+    }
 }
 
 // kNibble: threads in the order (group, token, 8 channels), so that a group's codes of
@@ -176,9 +391,7 @@ append_kernel(const AppendArgs a) {
     if (!find_token(a.cu, kNibble ? a.n.seqs : a.p.seqs, t, s, i)) return;
     const long long pos = (long long)a.start[s] + i;
     const int max_pages = kNibble ? a.n.max_pages : a.p.max_pages, num_pages = kNibble ? a.n.num_pages : a.p.num_pages;
-    Turn z;
-    z.live = 0;
-    z.from = -1;
+    Turn z = {};
     if (a.rope) {
         const long long at = a.positions ? (long long)a.positions[t] : pos;
         if (at < 0 || at >= a.rope_rows) return;
@@ -188,100 +401,12 @@ append_kernel(const AppendArgs a) {
     if (pos >= 0 && pos < (long long)max_pages << a.lg) page = a.table[(size_t)s * max_pages + (pos >> a.lg)];
     if (page >= num_pages) page = -1;
     const int slot = (int)(pos & ((1 << a.lg) - 1));
-    const int r1 = min(a.rows, ((int)blockIdx.y + 1) * a.per_slice);
-    for (int r0 = blockIdx.y * a.per_slice; r0 < r1; r0 += kBatch) {
-        uint4 own[kBatch], other[kBatch];
-        const T *src[kBatch];
-        // rows: 0 .. H - 1 keys, then the queries, then the values
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int row = r0 + b;
-            if (row >= r1) continue;
-            const bool q = row >= H && row < H + a.q_heads;
-            if (!q && page < 0) continue;
-            if (q) src[b] = (const T *)a.q + t * a.q_token + (row - H) * a.q_head;
-            else if (row < H) src[b] = (const T *)a.kn + t * a.new_token + row * a.new_head;
-            else src[b] = (const T *)a.vn + t * a.new_token + (row - H - a.q_heads) * a.new_head;
-            own[b] = __ldg(reinterpret_cast<const uint4 *>(src[b] + c0));
-            if (z.live && z.from >= 0 && row < H + a.q_heads) other[b] = __ldg(reinterpret_cast<const uint4 *>(src[b] + z.from));
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int row = r0 + b;
-            if (row >= r1) continue;
-            const bool q = row >= H && row < H + a.q_heads, v = row >= H + a.q_heads;
-            if (!q && page < 0) continue;
-            float x[8], y[8];
-            unpack8<T>(own[b], x);
-            if (!v && z.live) {
-                if (z.from >= 0) {
-                    unpack8<T>(other[b], y);
-                } else if (z.from == -1) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        y[e] = z.live >> e & 1u ? (float)src[b][partner_of(c0 + e, a.rot / 2)] : 0.0f;
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (!(z.live >> e & 1u)) y[e] = x[e];
-                    else y[e] = kNibble && !q ? turn_odd(x[e], y[e], z.cs[e], z.sn[e]) : turn(x[e], y[e], z.cs[e], z.sn[e]);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = x[e];
-            }
-            if (q) {
-                const int64_t to = t * a.out_token + (row - H) * a.out_head + c0;
-                if (a.q_f32) {
-                    float4 *out = reinterpret_cast<float4 *>((float *)a.q_out + to);
-                    out[0] = make_float4(y[0], y[1], y[2], y[3]);
-                    out[1] = make_float4(y[4], y[5], y[6], y[7]);
-                } else {
-                    *reinterpret_cast<uint4 *>((T *)a.q_out + to) = z.live ? pack8<T>(y) : own[b];
-                }
-                continue;
-            }
-            const int head = v ? row - H - a.q_heads : row;
-            if constexpr (!kNibble) {
-                const int64_t to = page * a.p.page_stride + head * a.p.head_stride + slot * a.p.token_stride + c0;
-                *reinterpret_cast<uint4 *>((T *)(v ? a.vp : a.kp) + to) = v || !z.live ? own[b] : pack8<T>(y);
-            } else {
-                // NaN anywhere in the group makes its scale NaN; larger values than fp16 holds count as its largest
-                float big = 0.0f;
-                bool nan = false;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    big = fmaxf(big, fabsf(y[e]));
-                    nan |= y[e] != y[e];
-                }
-#pragma unroll
-                for (int d = 1; d < 4; d <<= 1) {
-                    big = fmaxf(big, __shfl_xor_sync(quad, big, d));
-                    nan |= __shfl_xor_sync(quad, (int)nan, d) != 0;
-                }
-                const __half ah = nan ? __ushort_as_half((unsigned short)0x7fff) : __float2half_rn(fminf(big, 65504.0f));
-                const float a16 = __half2float(ah), step = a16 * 0.125f, inv = a16 > 0.0f ? 1.0f / step : 0.0f;
-                uint32_t word = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    // floor of the exact quotient, clipped: the product by 1 / step is within one of it, and
-                    // (f + 1) step has 14 bits
-                    float f = floorf(fminf(fmaxf(y[e] * inv, -9.0f), 8.0f));
-                    if (f * step > y[e]) f -= 1.0f;
-                    else if ((f + 1.0f) * step <= y[e]) f += 1.0f;
-                    f = fminf(fmaxf(f, -8.0f), 7.0f);
-                    word |= (uint32_t)(a16 > 0.0f ? (int)f + 8 : 8) << (4 * e);
-                }
-                unsigned char *blk = (unsigned char *)a.kp + nib_block(a.n, page, head, slot) + (v ? nib_half(D) : 0);
-                const int g = piece >> 2, in = slot & (kNibTokens - 1);
-                *reinterpret_cast<uint32_t *>(blk + nib_code(g, in) + 4 * (piece & 3)) = word;
-                if ((piece & 3) == 0) *reinterpret_cast<__half *>(blk + nib_scales(D) + nib_scale(D, g, in)) = ah;
-            }
-        }
-    }
+    // rows: 0 .. H - 1 keys, then the queries, then the values
+    const int Q = a.q_heads, r0 = blockIdx.y * a.per_slice, r1 = min(a.rows, r0 + a.per_slice);
+    if (page >= 0) move_rows<T, kNibble, kKeys>(a, (const T *)a.kn + t * a.new_token, a.new_head, r0, min(r1, H), t, c0, page, slot, z, quad);
+    move_rows<T, kNibble, kQueries>(a, (const T *)a.q + t * a.q_token, a.q_head, max(r0 - H, 0), min(r1 - H, Q), t, c0, page, slot, z, quad);
+    if (page >= 0)
+        move_rows<T, kNibble, kValues>(a, (const T *)a.vn + t * a.new_token, a.new_head, max(r0 - H - Q, 0), min(r1 - H - Q, H), t, c0, page, slot, z, quad);
 }
 
 // ---------------------------------------------------------------- read back
@@ -313,11 +438,11 @@ nibble_read_kernel(const ReadArgs a) {
     const int slot = (int)(pos & (a.n.page_tokens - 1)), in = slot & (kNibTokens - 1);
     const unsigned char *blk = a.kv + nib_block(a.n, page, 0, slot);
     const int r1 = min(2 * H, ((int)blockIdx.y + 1) * a.per_slice);
-    for (int r0 = blockIdx.y * a.per_slice; r0 < r1; r0 += kBatch) {
-        uint32_t word[kBatch];
-        __half scale[kBatch];
+    for (int r0 = blockIdx.y * a.per_slice; r0 < r1; r0 += kReadBatch) {
+        uint32_t word[kReadBatch];
+        __half scale[kReadBatch];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {   // rows: the heads of K, then of V
+        for (int b = 0; b < kReadBatch; ++b) {   // rows: the heads of K, then of V
             const int row = r0 + b;
             if (row >= r1) continue;
             const unsigned char *part = blk + (row < H ? row : row - H) * a.n.head_stride + (row < H ? 0 : nib_half(D));
@@ -325,7 +450,7 @@ nibble_read_kernel(const ReadArgs a) {
             scale[b] = *reinterpret_cast<const __half *>(part + nib_scales(D) + nib_scale(D, g, in));
         }
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
+        for (int b = 0; b < kReadBatch; ++b) {
             const int row = r0 + b;
             if (row >= r1) continue;
             const float step = __half2float(scale[b]) * 0.125f;
@@ -390,7 +515,7 @@ AppendArgs append_args(const int32_t *table, const void *kn, const void *vn, int
         a.rope_rows = rope->rows;
         a.rot = rope->rot;
         a.pairs = rope->interleaved != 0;
-        a.vec = !a.pairs && rope->rot % 16 == 0;   // 8 channels have 8 partners side by side
+        a.vec = rope->rot % (a.pairs ? 8 : 16) == 0;   // 8 channels' numbers, and halves' partners, side by side
         a.positions = rope->positions;
         if (rope->q) {
             a.q = rope->q; a.q_out = rope->q_out;

@@ -612,7 +612,7 @@ int fathom_paged_evict(const fathom_pages *pages, void *k_pages, void *v_pages, 
                        void *stream);
 
 /* fathom_paged_append with the position rotation: new keys, and the queries that rope
- * names, are rotated in fp32 (with the products' rounding errors) and rounded once to
+ * names, are rotated in fp32 (a product and a fused multiply-add) and rounded once to
  * where they go; values are copied.  A token without a place in the cache is not
  * written there, but its queries are.
  *   rope: not NULL; other arguments as fathom_paged_append. */

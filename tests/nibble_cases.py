@@ -1,10 +1,9 @@
 """Plain 64-bit forms of the rotated append and of the 4-bit cache, and how far a kernel
 may be from them.
 
-Rotation into 16-bit rows: both products, their sum and the rounding errors of each are
-fp32, which leaves at most 2^-23 of the result; then one rounding to the rows' type:
-u |y| (1 + 2^-10), u = eps / 2 of the type, and half a subnormal step.  Queries in fp32:
-2^-22 |y|.
+Rotation, y = x c + p s: the product p s is rounded to fp32 and the fused sum once more, so a
+result in fp32 is within 2^-24 (|p s| + |y|) <= 2^-23 Y, Y = |x c| + |p s|; in 16 bits one more
+rounding, u (|y| + 2^-23 Y), u = eps / 2 of the type, or half a subnormal step.
 
 Codes, scales and what is read back in fp32 are exact: the same numbers.  Read back in 16
 bits: the exact value's rounding, the same bits.
@@ -44,6 +43,28 @@ def rotated(x, table, pos, pairs):
     xa, xb = x[..., a].double(), x[..., b].double()
     y[..., a], y[..., b] = xa * c - xb * s, xb * c + xa * s
     return y
+
+
+def turn_size(x, table, pos, pairs):
+    """Y of each channel (0 where nothing turns)."""
+    R = table.shape[1]
+    y = torch.zeros(x.shape, dtype=torch.float64, device=x.device)
+    c, s = table[pos].double().abs()[:, None].chunk(2, -1)
+    i = torch.arange(R // 2, device=x.device)
+    a, b = (2 * i, 2 * i + 1) if pairs else (i, i + R // 2)
+    xa, xb = x[..., a].double().abs(), x[..., b].double().abs()
+    y[..., a], y[..., b] = xa * c + xb * s, xb * c + xa * s
+    return y
+
+
+def near_rotated(got, x, table, pos, pairs):
+    """Whether `got` is x rotated, within the bound above."""
+    want, size = rotated(x, table, pos, pairs), turn_size(x, table, pos, pairs)
+    tol = 2.0 ** -23 * size
+    if got.dtype != torch.float32:
+        u = torch.finfo(got.dtype).eps / 2
+        tol = tol + u * (want.abs() + tol) + (2.0 ** -25 if got.dtype == torch.float16 else 2.0 ** -134)
+    return bool(((got.double() - want).abs() <= tol).all())
 
 
 def to_half(x):

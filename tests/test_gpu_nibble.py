@@ -287,12 +287,6 @@ def new_rows(name, seed=0):
     return qkv[:, :Hq], qkv[:, Hq:Hq + H], qkv[:, Hq + H:], pos, seq, table
 
 
-def near_16(got, want, dt):
-    u = torch.finfo(dt).eps / 2
-    tol = want.abs() * u * (1 + 2.0 ** -10) + (2.0 ** -25 if dt == FP else 1e-40)
-    assert bool(((got.double() - want).abs() <= tol).all())
-
-
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("name", list(APPEND))
 def test_rotated_append_matches_the_plain_form(name, f32):
@@ -304,18 +298,14 @@ def test_rotated_append_matches_the_plain_form(name, f32):
     _, _, qr = B.fathom_paged_append_rope(B.make_pages(kp, table), kp, vp, table, k, v, i32(old), rope, P.cumulated(new),
                                           interleaved=pairs, q=q, q_dtype=torch.float32 if f32 else None)
     at, slot = table[seq, pos // page].long(), pos % page
-    y = N.rotated(k, rope, pos, pairs)
-    near_16(kp[at, :, slot], y, dt)
+    assert N.near_rotated(kp[at, :, slot], k, rope, pos, pairs)
     assert torch.equal(kp[at, :, slot][..., R:], k[..., R:])
     v0[at, :, slot] = v
     assert torch.equal(vp, v0)
     k0[at, :, slot] = kp[at, :, slot]
     assert torch.equal(kp, k0)                                   # nothing else was written
-    y = N.rotated(q, rope, pos, pairs)
-    if f32:
-        assert qr.dtype == torch.float32 and bool(((qr.double() - y).abs() <= 2.0 ** -22 * y.abs() + 1e-40).all())
-    else:
-        near_16(qr, y, dt)
+    assert qr.dtype == (torch.float32 if f32 else dt) and N.near_rotated(qr, q, rope, pos, pairs)
+    assert f32 or torch.equal(qr[..., R:], q[..., R:])
 
 
 @pytest.mark.parametrize("rotate", [True, False])
@@ -335,8 +325,7 @@ def test_4_bit_append_holds_the_exact_codes(name, rotate):
     got = N.unpack(kv, D)
     assert torch.equal(got[0], want_k) and torch.equal(got[1], want_v)
     if rotate:
-        y = N.rotated(q, rope, pos, pairs)
-        assert bool(((qr.double() - y).abs() <= 2.0 ** -22 * y.abs() + 1e-40).all())
+        assert N.near_rotated(qr, q, rope, pos, pairs)
     else:
         assert qr is None
     for t in (torch.float32, BF, FP):                            # and read back
@@ -344,16 +333,24 @@ def test_4_bit_append_holds_the_exact_codes(name, rotate):
         assert torch.equal(a, want_k[at, :, slot].float().to(t)) and torch.equal(b, want_v[at, :, slot].float().to(t))
 
 
-def test_codes_of_many_rotated_keys_are_exact():
-    """A million and a half of them: a code taken from a key rounded to fp32 would differ here and there."""
-    T, H, D = 3000, 4, 128
-    k, v = rnd(T, H, D).to(BF), rnd(T, H, D, seed=1).to(BF)
+@pytest.mark.parametrize("dt,table", [(BF, "angles"), (FP, "angles"), (BF, "quarters"), (FP, "any")])
+def test_codes_of_many_rotated_keys_are_exact(dt, table):
+    """Millions of them: a code taken from a key rounded to fp32 would differ here and there.  Quarter turns put
+    keys on borders; a table may also hold numbers that are no cos and sin."""
+    T, H, D = 6000, 4, 128
+    k, v = rnd(T, H, D).to(dt), rnd(T, H, D, seed=1).to(dt)
     rope = N.rope_table(T, D)
+    if table == "quarters":
+        turns = torch.arange(T * 64, device="cuda").reshape(T, 64) % 4
+        rope = torch.cat([torch.tensor([1.0, 0.0, -1.0, 0.0], device="cuda")[turns],
+                          torch.tensor([0.0, 1.0, 0.0, -1.0], device="cuda")[turns]], 1)
+    elif table == "any":
+        rope = 3 * rnd(T, D, seed=2)
     kv, table = B.alloc_nibble_pages(-(-T // 64), H, 64, D), torch.arange(-(-T // 64), dtype=torch.int32, device="cuda")[None].contiguous()
     B.fathom_nibble_append(B.make_nibble_pages(kv, table, D), kv, table, k, v, i32([0]), i32([0, T]), rope=rope)
     K, V = N.unpack(kv, D)
     pos = torch.arange(T, device="cuda")
-    want = N.held(N.rotated(k, rope, pos, False))[0]
+    want = N.held(N.rotated(k, rope, pos, False))[0]   # the products are exact in fp64, their sum to 2^-53
     assert torch.equal(K.transpose(1, 2).reshape(-1, H, D)[:T], want)
     assert torch.equal(V.transpose(1, 2).reshape(-1, H, D)[:T], N.held(v.double())[0])
 
@@ -416,7 +413,7 @@ def test_decode_steps_take_one_token_per_sequence_and_other_positions():
     K[at, :, slot], V[at, :, slot] = N.held(y)[0], N.held(v.double())[0]
     got = N.unpack(kv, D)
     assert torch.equal(got[0], K) and torch.equal(got[1], V)
-    near_16(kp[t16[s, start.long() // page].long(), :, slot], y, BF)
+    assert N.near_rotated(kp[t16[s, start.long() // page].long(), :, slot], k, rope, positions.long(), False)
 
 
 def test_tokens_without_a_place_are_skipped():
@@ -459,7 +456,7 @@ def test_tokens_without_a_place_are_skipped():
     B.fathom_paged_append_rope(B.make_pages(kp, t16), kp, vp, t16, k, v, start, rope, cu)
     p16 = t16[seq, (pos // page).clamp(0, 1)].long()
     ok = turned & (p16 >= 0) & (p16 < kp.shape[0])
-    near_16(kp[p16[ok], :, pos[ok] % page], y[ok], BF)
+    assert N.near_rotated(kp[p16[ok], :, pos[ok] % page], k[:55][ok], rope, pos[ok], False)
     k0[p16[ok], :, pos[ok] % page] = kp[p16[ok], :, pos[ok] % page]
     assert torch.equal(kp, k0)
 
