@@ -897,48 +897,59 @@ def fathom_paged_evict(pages: Pages, k_pages, v_pages, page_table, lens, mass, k
 _OUT_TYPES = {torch.float32: F32, **_ROW_TYPES}
 
 
-def _check_rope(rope, positions, interleaved, q, q_out, q_dtype, dtype, T, D):
-    """-> the rotation's arguments but q_out's pointer and strides, which _rope_args adds."""
+def _rows_ok(t, dtype, shape):
+    """Rows of this type and these sizes with a contiguous last axis on a GPU (the common case)."""
+    return t is not None and t.dtype is dtype and t.shape == shape and t.stride(2) == 1 and t.is_cuda
+
+
+def _check_rope(rope, positions, q, q_out, q_dtype, dtype, T, D):
+    """-> the type of the rotated queries (None: there are none)."""
     if rope is None:
         if positions is not None or q is not None or q_out is not None or q_dtype is not None:
             raise ValueError("rope is required with positions, q, q_out or q_dtype")
         return None
-    _check(rope, "rope", (torch.float32,))
-    if rope.dim() != 2 or rope.shape[0] < 1:
-        raise ValueError(f"rope: shape {tuple(rope.shape)} is not [positions][rotated channels]")
-    if not _on_device(rope):
-        raise ValueError("rope must be a CUDA tensor")
+    if not (rope.dtype is torch.float32 and rope.dim() == 2 and rope.is_cuda and rope.is_contiguous()):
+        _check(rope, "rope", (torch.float32,))
+        if rope.dim() != 2:
+            raise ValueError(f"rope: shape {tuple(rope.shape)} is not [positions][rotated channels]")
+        if not _on_device(rope):
+            raise ValueError("rope must be a CUDA tensor")
     rows, rot = rope.shape
-    _fit32(positions=rows, rotated_channels=rot)
+    if not 0 < rows < 1 << 31 or rot >> 31:
+        raise ValueError(f"rope: {rows} positions of {rot} channels")
     if positions is not None and not _ok(positions, torch.int32, (T,)):
         _check(positions, "positions", (torch.int32,), (T,))
-    r = Rope(rope.data_ptr(), rows, rot, int(bool(interleaved)), positions.data_ptr() if positions is not None else None)
     if q is None:
         if q_out is not None or q_dtype is not None:
             raise ValueError("q is required with q_out or q_dtype")
-        return r
+        return None
     if q.dim() != 3:
         raise ValueError("q: expected [tokens][heads][D]")
-    heads = q.shape[1]
-    _check_strided(q, "q", (dtype,), (T, heads, D))
+    shape = (T, q.shape[1], D)
+    if not _rows_ok(q, dtype, shape):
+        _check_strided(q, "q", (dtype,), shape)
     if q_dtype is None:
         q_dtype = q_out.dtype if q_out is not None else dtype
-    if q_dtype not in (dtype, torch.float32):
+    if q_dtype is not dtype and q_dtype is not torch.float32:
         raise TypeError(f"q_dtype: {q_dtype} is neither {dtype} nor torch.float32")
-    if q_out is not None:
-        _check_strided(q_out, "q_out", (q_dtype,), (T, heads, D))
-    r.q, r.q_heads, r.q_dtype, r.q_token, r.q_head = q.data_ptr(), heads, _OUT_TYPES[q_dtype], q.stride(0), q.stride(1)
-    return r
+    if q_out is not None and not _rows_ok(q_out, q_dtype, shape):
+        _check_strided(q_out, "q_out", (q_dtype,), shape)
+    return q_dtype
 
 
-def _rope_args(r, q, q_out, q_dtype):
-    """Adds the rotated queries' place (allocated here unless given): -> the queries or None."""
-    if r is None or q is None:
-        return None
+def _make_rope(rope, positions, interleaved, q, q_out, q_dtype):
+    """-> (the call's rotation or None, the rotated queries' place, allocated here unless given, or None)."""
+    if rope is None:
+        return None, None
+    rows, rot = rope.shape
+    at = positions.data_ptr() if positions is not None else None
+    if q is None:
+        return Rope(rope.data_ptr(), rows, rot, 1 if interleaved else 0, at), None
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q_dtype or q.dtype, device=q.device)
-    r.q_out, r.out_token, r.out_head = q_out.data_ptr(), q_out.stride(0), q_out.stride(1)
-    return q_out
+        q_out = torch.empty(q.shape, dtype=q_dtype, device=q.device)
+    (qt, qh, _), (ot, oh, _) = q.stride(), q_out.stride()
+    return Rope(rope.data_ptr(), rows, rot, 1 if interleaved else 0, at, q.data_ptr(), q_out.data_ptr(), q.shape[1],
+                _OUT_TYPES[q_dtype], qt, qh, ot, oh), q_out
 
 
 def _check_new(k_new, v_new, start, cu_new, dtype, seqs, H, D):
@@ -948,9 +959,11 @@ def _check_new(k_new, v_new, start, cu_new, dtype, seqs, H, D):
     T = k_new.shape[0]
     if T >> 31:
         _fit32(new_tokens=T)
-    _check_strided(k_new, "k_new", (dtype,), (T, H, D))
-    _check_strided(v_new, "v_new", (dtype,), (T, H, D))
-    stride = k_new.stride()
+    shape, stride = (T, H, D), k_new.stride()
+    if not _rows_ok(k_new, dtype, shape):
+        _check_strided(k_new, "k_new", (dtype,), shape)
+    if not _rows_ok(v_new, dtype, shape):
+        _check_strided(v_new, "v_new", (dtype,), shape)
     if stride != v_new.stride() and any(a > 1 and x != y for a, x, y in zip((T, H), stride, v_new.stride())):
         raise ValueError("v_new: strides differ from k_new's")
     if not _ok(start, torch.int32, (seqs,)):
@@ -973,10 +986,10 @@ def fathom_paged_append_rope(pages: Pages, k_pages, v_pages, page_table, k_new, 
     T, stride = _check_new(k_new, v_new, start, cu_new, dtype, seqs, H, D)
     if rope is None:
         raise ValueError("rope is required")
-    r = _check_rope(rope, positions, interleaved, q, q_out, q_dtype, dtype, T, D)
+    q_dtype = _check_rope(rope, positions, q, q_out, q_dtype, dtype, T, D)
     context, handle = _on(stream, (k_pages, v_pages, page_table, k_new, v_new, start, cu_new, rope, positions, q, q_out))
     with context:
-        q_out = _rope_args(r, q, q_out, q_dtype)
+        r, q_out = _make_rope(rope, positions, interleaved, q, q_out, q_dtype)
         _call("fathom_paged_append_rope", pages, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
               k_new.data_ptr(), v_new.data_ptr(), T, stride[0], stride[1], start.data_ptr(),
               cu_new.data_ptr() if cu_new is not None else None, r, handle)
@@ -1027,10 +1040,10 @@ def fathom_nibble_append(pages: NibblePages, kv_pages, page_table, k_new, v_new,
     if dtype not in _ROW_TYPES:
         raise TypeError(f"k_new: dtype {dtype} not in {tuple(_ROW_TYPES)}")
     T, stride = _check_new(k_new, v_new, start, cu_new, dtype, seqs, H, D)
-    r = _check_rope(rope, positions, interleaved, q, q_out, q_dtype, dtype, T, D)
+    q_dtype = _check_rope(rope, positions, q, q_out, q_dtype, dtype, T, D)
     context, handle = _on(stream, (kv_pages, page_table, k_new, v_new, start, cu_new, rope, positions, q, q_out))
     with context:
-        q_out = _rope_args(r, q, q_out, q_dtype)
+        r, q_out = _make_rope(rope, positions, interleaved, q, q_out, q_dtype)
         _call("fathom_nibble_append", pages, kv_pages.data_ptr(), page_table.data_ptr(), _ROW_TYPES[dtype],
               k_new.data_ptr(), v_new.data_ptr(), T, stride[0], stride[1], start.data_ptr(),
               cu_new.data_ptr() if cu_new is not None else None, r, handle)

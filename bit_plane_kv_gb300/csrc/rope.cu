@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kBatch = 2;       // rows loaded together
+constexpr int kCtas = 6;        // per SM: registers for 24 warps and their loads
 constexpr int kReadBatch = 4;   // when read back
 
 struct AppendArgs {
@@ -98,19 +99,34 @@ __device__ __forceinline__ float turn_odd(float x, float y, float c, float s) {
     return __uint_as_float(u);
 }
 
-// The sequence of packed token t and its place in it (false: behind the last one).
-__device__ __forceinline__ bool find_token(const int32_t *cu, int seqs, int t, int &s, int &i) {
+// The sequence of packed token t and its place in it (false: behind the last one).  Whole
+// warps: `first` is the least t of the warp.
+__device__ __forceinline__ bool find_token(const int32_t *cu, int seqs, int first, int t, int &s, int &i) {
     s = t;
     i = 0;
     if (!cu) return true;
-    int lo = 0, hi = seqs;   // the last sequence that starts at or before t
+    int lo = 0, hi = seqs;   // the last sequence that starts at or before `first`: 32 borders at a time
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= t) lo = mid; else hi = mid;
+        const int step = (hi - lo + 31) / 32, at = lo + (threadIdx.x & 31) * step;
+        const unsigned below = __ballot_sync(0xffffffffu, at < hi && __ldg(cu + at) <= first);
+        if (below) lo += (31 - __clz(below)) * step;
+        hi = min(lo + step, hi);
     }
     s = lo;
-    i = t - cu[s];
-    return i >= 0 && t < cu[s + 1];
+    int next = __ldg(cu + s + 1);
+    if (t >= next) {         // later tokens of the warp: most often the next sequences
+        for (int k = 0; k < 4 && t >= next && s + 1 < seqs; ++k) next = __ldg(cu + ++s + 1);
+        if (t >= next) {
+            for (lo = s, hi = seqs; hi - lo > 1;) {
+                const int mid = (lo + hi) >> 1;
+                if (__ldg(cu + mid) <= t) lo = mid; else hi = mid;
+            }
+            s = lo;
+            next = __ldg(cu + s + 1);
+        }
+    }
+    i = t - __ldg(cu + s);
+    return i >= 0 && t < next;
 }
 
 // What a thread's 8 channels, from c0 on, need of the table's row at a position.
@@ -249,7 +265,29 @@ __device__ __forceinline__ Coded code_exact(const float (&y)[8], unsigned quad) 
     return r;
 }
 
-// Rotated keys: x, their partners and what turns them.
+// Rotated keys in fp32, off by at most `off`: codes as long as no border is that near, else near is set.
+__device__ __forceinline__ Coded code_fast(const float (&y)[8], float big, float off, unsigned quad, bool &near) {
+    big = over_quad(big, quad);
+    const float all = over_quad(off, quad);
+    Coded r;
+    r.a = __float2half_rn(big);
+    near |= !(ordinary(big) && all < big) ||
+            __half_as_ushort(__float2half_rn(big - 2.0f * all)) != __half_as_ushort(__float2half_rn(big + 2.0f * all));
+    const float inv = 8.0f / __half2float(r.a);
+    uint32_t word = 0;
+    float far = 0.0f;                                    // the largest distance from the middle between two borders
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float v = fminf(fmaxf(y[e] * inv, -7.5f), 7.5f);
+        const float t = __fadd_rd(v, kMagic);
+        far = fmaxf(far, fabsf(v - (t - kMagic) - 0.5f));
+        word = add_digit(word, t, e);
+    }
+    near |= far > 0.5f - (off * inv + 0x1p-19f);
+    r.word = digits_done(word);
+    return r;
+}
+// x, their partners and what turns them, for a chunk of 8 channels.
 __device__ __forceinline__ Coded code_turned(const float (&x)[8], const float (&p)[8], const Turn &z, unsigned quad) {
     float y[8], big = 0.0f, part = 0.0f;
 #pragma unroll
@@ -259,29 +297,9 @@ __device__ __forceinline__ Coded code_turned(const float (&x)[8], const float (&
         big = max_nan(big, fabsf(y[e]));
         part = max_nan(part, fabsf(q));
     }
-    const float off = 0x1.02p-24f * (part + big);            // of any y here
-    big = over_quad(big, quad);
-    const float all = over_quad(off, quad);
-    if (ordinary(big) && all < big) {
-        Coded r;
-        r.a = __float2half_rn(big);
-        bool near = __half_as_ushort(__float2half_rn(big - 2.0f * all)) != __half_as_ushort(__float2half_rn(big + 2.0f * all));
-        const float inv = 8.0f / __half2float(r.a);
-        uint32_t word = 0;
-        float far = 0.0f;                                    // the largest distance from the middle between two borders
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float v = fminf(fmaxf(y[e] * inv, -7.5f), 7.5f);
-            const float t = __fadd_rd(v, kMagic);
-            far = fmaxf(far, fabsf(v - (t - kMagic) - 0.5f));
-            word = add_digit(word, t, e);
-        }
-        near |= far > 0.5f - (off * inv + 0x1p-19f);
-        if (!(__ballot_sync(quad, near) & quad)) {
-            r.word = digits_done(word);
-            return r;
-        }
-    }
+    bool near = false;
+    const Coded r = code_fast(y, big, 0x1.02p-24f * (part + big), quad, near);
+    if (!(__ballot_sync(quad, near) & quad)) return r;
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = z.live >> e & 1u ? turn_odd(x[e], p[e], z.cs[e], z.sn[e]) : x[e];
     return code_any(y, quad);
@@ -361,34 +379,101 @@ __device__ __forceinline__ void move_rows(const AppendArgs &a, const T *src, int
     }
 }
 
-// kNibble: threads in the order (group, token, 8 channels), so that a group's codes of
-// consecutive tokens are written side by side; else (token, 8 channels).
-template <typename T, bool kNibble>
-__global__ void __launch_bounds__(kThreads)
+// The same where all channels turn in halves: a thread has 8 channels of the first half and their partners.
+template <typename T, bool kNibble, Rows kKind>
+__device__ __forceinline__ void move_halves(const AppendArgs &a, const T *src, int64_t stride, int lo, int hi, int t, int c0, int page,
+                                            int slot, const float (&cs)[8], const float (&sn)[8], unsigned quad) {
+    const int D = kNibble ? a.n.D : a.p.D, c1 = c0 + D / 2;
+#pragma unroll 1
+    for (int r0 = lo; r0 < hi; r0 += kBatch) {
+        uint4 first[kBatch], second[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (r0 + b < hi) {
+                const T *row = src + (r0 + b) * stride;
+                first[b] = __ldg(reinterpret_cast<const uint4 *>(row + c0));
+                second[b] = __ldg(reinterpret_cast<const uint4 *>(row + c1));
+            }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int head = r0 + b;
+            if (head >= hi) break;
+            float x0[8], x1[8], y0[8], y1[8], big0 = 0.0f, big1 = 0.0f, part0 = 0.0f, part1 = 0.0f;
+            if (kNibble || kKind != kValues) {
+                unpack8<T>(first[b], x0);
+                unpack8<T>(second[b], x1);
+            }
+            if (kKind != kValues) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float p0 = __fmul_rn(x1[e], -sn[e]), p1 = __fmul_rn(x0[e], sn[e]);
+                    y0[e] = fmaf(x0[e], cs[e], p0);
+                    y1[e] = fmaf(x1[e], cs[e], p1);
+                    if (kNibble && kKind == kKeys) {
+                        big0 = max_nan(big0, fabsf(y0[e]));
+                        big1 = max_nan(big1, fabsf(y1[e]));
+                        part0 = max_nan(part0, fabsf(p0));
+                        part1 = max_nan(part1, fabsf(p1));
+                    }
+                }
+            }
+            if constexpr (kNibble && kKind != kQueries) {
+                Coded a0, a1;
+                if (kKind == kKeys) {
+                    bool near = false;
+                    a0 = code_fast(y0, big0, 0x1.02p-24f * (part0 + big0), quad, near);
+                    a1 = code_fast(y1, big1, 0x1.02p-24f * (part1 + big1), quad, near);
+                    if (__ballot_sync(quad, near) & quad) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            y0[e] = turn_odd(x0[e], x1[e], cs[e], -sn[e]);
+                            y1[e] = turn_odd(x1[e], x0[e], cs[e], sn[e]);
+                        }
+                        a0 = code_any(y0, quad);
+                        a1 = code_any(y1, quad);
+                    }
+                } else {
+                    a0 = code_exact(x0, quad);
+                    a1 = code_exact(x1, quad);
+                }
+                unsigned char *blk = (unsigned char *)a.kp + nib_block(a.n, page, head, slot) + (kKind == kValues ? nib_half(D) : 0);
+                const int g0 = c0 / 32, g1 = c1 / 32, sub = c0 / 8 & 3, in = slot & (kNibTokens - 1);
+                *reinterpret_cast<uint32_t *>(blk + nib_code(g0, in) + 4 * sub) = a0.word;
+                *reinterpret_cast<uint32_t *>(blk + nib_code(g1, in) + 4 * sub) = a1.word;
+                if (sub < 2)
+                    *reinterpret_cast<__half *>(blk + nib_scales(D) + nib_scale(D, sub ? g1 : g0, in)) = sub ? a1.a : a0.a;
+                continue;
+            }
+            if (kKind == kQueries && a.q_f32) {
+                float *q = (float *)a.q_out + t * a.out_token + head * a.out_head;
+                *reinterpret_cast<float4 *>(q + c0) = make_float4(y0[0], y0[1], y0[2], y0[3]);
+                *reinterpret_cast<float4 *>(q + c0 + 4) = make_float4(y0[4], y0[5], y0[6], y0[7]);
+                *reinterpret_cast<float4 *>(q + c1) = make_float4(y1[0], y1[1], y1[2], y1[3]);
+                *reinterpret_cast<float4 *>(q + c1 + 4) = make_float4(y1[4], y1[5], y1[6], y1[7]);
+                continue;
+            }
+            T *to = kKind == kQueries ? (T *)a.q_out + t * a.out_token + head * a.out_head
+                                      : (T *)(kKind == kValues ? a.vp : a.kp) + page * a.p.page_stride + head * a.p.head_stride + slot * a.p.token_stride;
+            *reinterpret_cast<uint4 *>(to + c0) = kKind == kValues ? first[b] : pack8<T>(y0);
+            *reinterpret_cast<uint4 *>(to + c1) = kKind == kValues ? second[b] : pack8<T>(y1);
+        }
+    }
+}
+
+// kHalves: two chunks of 8 channels per thread, as above, else one.  The four lanes of a
+// group of 32 channels are neighbours.
+template <typename T, bool kNibble, bool kHalves>
+__global__ void __launch_bounds__(kThreads, kCtas)
 append_kernel(const AppendArgs a) {
     pdl_enter();
-    const int D = kNibble ? a.n.D : a.p.D, H = a.heads, pieces = D / 8;
-    const int lane = threadIdx.x & 31;
-    int piece, tl, per;
-    if (kNibble) {
-        const int groups = D / 32;
-        per = kThreads / 4 / groups & ~7;   // tokens of a CTA: 8, 8, 16 or 32
-        const int g = threadIdx.x / (4 * per);
-        tl = threadIdx.x / 4 % per;
-        piece = 4 * g + (threadIdx.x & 3);
-        if (g >= groups) return;
-    } else {
-        per = kThreads / pieces;
-        tl = threadIdx.x / pieces;
-        piece = threadIdx.x - tl * pieces;
-        if (tl >= per) return;
-    }
+    const int D = kNibble ? a.n.D : a.p.D, H = a.heads, pieces = kHalves ? D / 16 : D / 8;
+    const int per = kThreads / pieces, tl = threadIdx.x / pieces, piece = threadIdx.x - tl * pieces;
     const long long tt = (long long)blockIdx.x * per + tl;
-    if (tt >= a.total) return;
-    const int t = (int)tt, c0 = 8 * piece;
-    const unsigned quad = 0xfu << (lane & ~3);   // the lanes of a group of channels (4 bits)
+    const int t = (int)min(tt, (long long)a.total), c0 = 8 * piece;
+    const unsigned quad = 0xfu << (threadIdx.x & 28);
     int s, i;
-    if (!find_token(a.cu, kNibble ? a.n.seqs : a.p.seqs, t, s, i)) return;
+    const bool in = find_token(a.cu, kNibble ? a.n.seqs : a.p.seqs, __shfl_sync(0xffffffffu, t, 0), t, s, i);
+    if (tl >= per || tt >= a.total || !in) return;
     const long long pos = (long long)a.start[s] + i;
     const int max_pages = kNibble ? a.n.max_pages : a.p.max_pages, num_pages = kNibble ? a.n.num_pages : a.p.num_pages;
     Turn z = {};
@@ -396,6 +481,10 @@ append_kernel(const AppendArgs a) {
         const long long at = a.positions ? (long long)a.positions[t] : pos;
         if (at < 0 || at >= a.rope_rows) return;
         z = load_turn(a.rope + at * a.rot, c0, a.rot, a.pairs, a.vec);
+        if (kHalves) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z.sn[e] = -z.sn[e];   // of the second half
+        }
     }
     int page = -1;
     if (pos >= 0 && pos < (long long)max_pages << a.lg) page = a.table[(size_t)s * max_pages + (pos >> a.lg)];
@@ -403,10 +492,17 @@ append_kernel(const AppendArgs a) {
     const int slot = (int)(pos & ((1 << a.lg) - 1));
     // rows: 0 .. H - 1 keys, then the queries, then the values
     const int Q = a.q_heads, r0 = blockIdx.y * a.per_slice, r1 = min(a.rows, r0 + a.per_slice);
-    if (page >= 0) move_rows<T, kNibble, kKeys>(a, (const T *)a.kn + t * a.new_token, a.new_head, r0, min(r1, H), t, c0, page, slot, z, quad);
-    move_rows<T, kNibble, kQueries>(a, (const T *)a.q + t * a.q_token, a.q_head, max(r0 - H, 0), min(r1 - H, Q), t, c0, page, slot, z, quad);
-    if (page >= 0)
-        move_rows<T, kNibble, kValues>(a, (const T *)a.vn + t * a.new_token, a.new_head, max(r0 - H - Q, 0), min(r1 - H - Q, H), t, c0, page, slot, z, quad);
+    const T *k = (const T *)a.kn + t * a.new_token, *q = (const T *)a.q + t * a.q_token, *v = (const T *)a.vn + t * a.new_token;
+    const int q0 = max(r0 - H, 0), q1 = min(r1 - H, Q), v0 = max(r0 - H - Q, 0), v1 = min(r1 - H - Q, H);
+    if constexpr (kHalves) {
+        if (page >= 0) move_halves<T, kNibble, kKeys>(a, k, a.new_head, r0, min(r1, H), t, c0, page, slot, z.cs, z.sn, quad);
+        move_halves<T, kNibble, kQueries>(a, q, a.q_head, q0, q1, t, c0, page, slot, z.cs, z.sn, quad);
+        if (page >= 0) move_halves<T, kNibble, kValues>(a, v, a.new_head, v0, v1, t, c0, page, slot, z.cs, z.sn, quad);
+    } else {
+        if (page >= 0) move_rows<T, kNibble, kKeys>(a, k, a.new_head, r0, min(r1, H), t, c0, page, slot, z, quad);
+        move_rows<T, kNibble, kQueries>(a, q, a.q_head, q0, q1, t, c0, page, slot, z, quad);
+        if (page >= 0) move_rows<T, kNibble, kValues>(a, v, a.new_head, v0, v1, t, c0, page, slot, z, quad);
+    }
 }
 
 // ---------------------------------------------------------------- read back
@@ -419,51 +515,77 @@ struct ReadArgs {
     int64_t out_token, out_head;
 };
 
-// The threads of append_kernel, the other way round: 4 bytes of codes, 8 channels.
+// 8 channels' codes as they are used.  The codes become (c - 7.5) / 8 in fp16 (in the low
+// bits of a half c is the subnormal c 2^-24, four bits up 16 c 2^-24), times a exactly in fp32.
 template <typename T>
+__device__ __forceinline__ void store_values(T *out, uint32_t word, __half a) {
+    uint32_t v[4];   // channels (0, 4), (1, 5), (2, 6), (3, 7)
+    const uint32_t up = word >> 8;
+    const uint32_t low[4] = {word & 0x000f000fu, word & 0x00f000f0u, up & 0x000f000fu, up & 0x00f000f0u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)   // times 2^15 or 2^11, minus 7.5 2^-9
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(v[i]) : "r"(low[i]), "r"(i & 1 ? 0x68006800u : 0x78007800u), "r"(0xa380a380u));
+    const float scale = __half2float(a) * 64.0f;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v[i]));
+        x[i] = f.x * scale;
+        x[i + 4] = f.y * scale;
+    }
+    if constexpr (std::is_same<T, float>::value) {
+        reinterpret_cast<float4 *>(out)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4 *>(out)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        *reinterpret_cast<uint4 *>(out) = pack8<T>(x);
+    }
+}
+
+// A thread has 8 channels of a token, or (kTwo: whole groups in each half of a row) those and
+// the 8 that lie half a row on, and goes over some of its rows.
+template <typename T, bool kTwo>
 __global__ void __launch_bounds__(kThreads)
 nibble_read_kernel(const ReadArgs a) {
     pdl_enter();
-    const int D = a.n.D, H = a.n.kv_heads, groups = D / 32;
-    const int per = kThreads / 4 / groups & ~7, g = threadIdx.x / (4 * per), tl = threadIdx.x / 4 % per, sub = threadIdx.x & 3;
+    const int D = a.n.D, H = a.n.kv_heads, pieces = kTwo ? D / 16 : D / 8;
+    const int per = kThreads / pieces, tl = threadIdx.x / pieces, piece = threadIdx.x - tl * pieces;
     const long long tt = (long long)blockIdx.x * per + tl;
-    if (g >= groups || tt >= a.total) return;
-    const int t = (int)tt;
+    const int t = (int)min(tt, (long long)a.total);
     int s, i;
-    if (!find_token(a.cu, a.n.seqs, t, s, i)) return;
+    const bool inside = find_token(a.cu, a.n.seqs, __shfl_sync(0xffffffffu, t, 0), t, s, i);
+    if (tl >= per || tt >= a.total || !inside) return;
     const long long pos = (long long)a.start[s] + i;
     if (pos < 0 || pos >= (long long)a.n.max_pages << a.lg) return;
     const int page = a.table[(size_t)s * a.n.max_pages + (pos >> a.lg)];
     if (page < 0 || page >= a.n.num_pages) return;
     const int slot = (int)(pos & (a.n.page_tokens - 1)), in = slot & (kNibTokens - 1);
-    const unsigned char *blk = a.kv + nib_block(a.n, page, 0, slot);
+    const int g = piece >> 2, more = D / 64;   // its group, and the other one's distance
+    const unsigned char *blk = a.kv + nib_block(a.n, page, 0, slot) + nib_code(g, in) + 4 * (piece & 3);
+    const int scale_at = nib_scales(D) + nib_scale(D, g, in) - nib_code(g, in) - 4 * (piece & 3);   // from there
+    const int64_t to = t * a.out_token + 8 * piece;
     const int r1 = min(2 * H, ((int)blockIdx.y + 1) * a.per_slice);
+#pragma unroll 1
     for (int r0 = blockIdx.y * a.per_slice; r0 < r1; r0 += kReadBatch) {
-        uint32_t word[kReadBatch];
-        __half scale[kReadBatch];
+        uint32_t word[kReadBatch][2];
+        __half scale[kReadBatch][2];
 #pragma unroll
         for (int b = 0; b < kReadBatch; ++b) {   // rows: the heads of K, then of V
             const int row = r0 + b;
-            if (row >= r1) continue;
-            const unsigned char *part = blk + (row < H ? row : row - H) * a.n.head_stride + (row < H ? 0 : nib_half(D));
-            word[b] = *reinterpret_cast<const uint32_t *>(part + nib_code(g, in) + 4 * sub);
-            scale[b] = *reinterpret_cast<const __half *>(part + nib_scales(D) + nib_scale(D, g, in));
+            if (row >= r1) break;
+            const unsigned char *part = blk + (row < H ? row * a.n.head_stride : (row - H) * a.n.head_stride + nib_half(D));
+#pragma unroll
+            for (int k = 0; k < (kTwo ? 2 : 1); ++k) {
+                word[b][k] = __ldg(reinterpret_cast<const uint32_t *>(part + k * nib_code(more, 0)));
+                scale[b][k] = __ldg(reinterpret_cast<const __half *>(part + scale_at + 4 * k * more));
+            }
         }
 #pragma unroll
         for (int b = 0; b < kReadBatch; ++b) {
             const int row = r0 + b;
-            if (row >= r1) continue;
-            const float step = __half2float(scale[b]) * 0.125f;
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = ((float)(word[b] >> (4 * e) & 15u) - 7.5f) * step;   // exact
-            T *out = (T *)(row < H ? a.k_out : a.v_out) + t * a.out_token + (row < H ? row : row - H) * a.out_head + 32 * g + 8 * sub;
-            if constexpr (std::is_same<T, float>::value) {
-                reinterpret_cast<float4 *>(out)[0] = make_float4(x[0], x[1], x[2], x[3]);
-                reinterpret_cast<float4 *>(out)[1] = make_float4(x[4], x[5], x[6], x[7]);
-            } else {
-                *reinterpret_cast<uint4 *>(out) = pack8<T>(x);
-            }
+            if (row >= r1) break;
+            T *out = row < H ? (T *)a.k_out + to + row * a.out_head : (T *)a.v_out + to + (row - H) * a.out_head;
+            store_values<T>(out, word[b][0], scale[b][0]);
+            if (kTwo) store_values<T>(out + D / 2, word[b][1], scale[b][1]);
         }
     }
 }
@@ -483,23 +605,32 @@ int rows_per_slice(long long ctas, int rows) {
     return (int)(n < 1 ? 1 : n > 16 ? 16 : n);
 }
 
+template <typename T, bool kNibble>
+cudaError_t launch_form(const AppendArgs &a, bool halves, dim3 grid, cudaStream_t st) {
+    return halves ? launch_pdl(append_kernel<T, kNibble, true>, grid, dim3(kThreads), 0, st, a)
+                  : launch_pdl(append_kernel<T, kNibble, false>, grid, dim3(kThreads), 0, st, a);
+}
+
 int launch_append(AppendArgs &a, bool nibble, int dtype, const char *what, cudaStream_t st) {
     const int D = nibble ? a.n.D : a.p.D;
-    const int per = nibble ? kThreads / 4 / (D / 32) & ~7 : kThreads / (D / 8);
+    // whole rows that turn in halves: both partners in one thread; in 4 bits each half has whole groups
+    const bool halves = a.rope && !a.pairs && a.rot == D && D % (nibble ? 64 : 16) == 0;
+    const int per = kThreads / (halves ? D / 16 : D / 8);
     const long long ctas = ((long long)a.total + per - 1) / per;
     a.per_slice = rows_per_slice(ctas, a.rows);
     const int slices = (a.rows + a.per_slice - 1) / a.per_slice;
     if (ctas > 0x7fffffffLL || slices > 65535) { set_error("%s: too many rows for one launch", what); return FATHOM_EINVAL; }
-    const dim3 grid((unsigned)ctas, slices), block(kThreads);
-    cudaError_t e;
-    if (nibble)
-        e = dtype == FATHOM_BF16 ? launch_pdl(append_kernel<__nv_bfloat16, true>, grid, block, 0, st, a)
-                                 : launch_pdl(append_kernel<__half, true>, grid, block, 0, st, a);
-    else
-        e = dtype == FATHOM_BF16 ? launch_pdl(append_kernel<__nv_bfloat16, false>, grid, block, 0, st, a)
-                                 : launch_pdl(append_kernel<__half, false>, grid, block, 0, st, a);
+    const dim3 grid((unsigned)ctas, slices);
+    const cudaError_t e = nibble ? (dtype == FATHOM_BF16 ? launch_form<__nv_bfloat16, true>(a, halves, grid, st) : launch_form<__half, true>(a, halves, grid, st))
+                                 : (dtype == FATHOM_BF16 ? launch_form<__nv_bfloat16, false>(a, halves, grid, st) : launch_form<__half, false>(a, halves, grid, st));
     if (e != cudaSuccess) return launch_failed(what, e);
     return launch_status(what);
+}
+
+template <typename T>
+cudaError_t launch_read(const ReadArgs &a, bool two, dim3 grid, cudaStream_t st) {
+    return two ? launch_pdl(nibble_read_kernel<T, true>, grid, dim3(kThreads), 0, st, a)
+               : launch_pdl(nibble_read_kernel<T, false>, grid, dim3(kThreads), 0, st, a);
 }
 
 AppendArgs append_args(const int32_t *table, const void *kn, const void *vn, int total, int64_t new_token, int64_t new_head,
@@ -565,15 +696,16 @@ int launch_nibble_read(const fathom_nibble_pages &p, const void *kv, const int32
     a.lg = log2_of(p.page_tokens);
     a.k_out = k_out; a.v_out = v_out;
     a.out_token = out_token; a.out_head = out_head;
-    const int per = kThreads / 4 / (p.D / 32) & ~7;
+    const bool two = p.D % 64 == 0;
+    const int per = kThreads / (two ? p.D / 16 : p.D / 8);
     const long long ctas = ((long long)total + per - 1) / per;
     a.per_slice = rows_per_slice(ctas, 2 * p.kv_heads);
     const int slices = (2 * p.kv_heads + a.per_slice - 1) / a.per_slice;
     if (ctas > 0x7fffffffLL || slices > 65535) { set_error("nibble_read: too many rows for one launch"); return FATHOM_EINVAL; }
-    const dim3 grid((unsigned)ctas, slices), block(kThreads);
-    const cudaError_t e = dtype == FATHOM_F32    ? launch_pdl(nibble_read_kernel<float>, grid, block, 0, st, a)
-                          : dtype == FATHOM_BF16 ? launch_pdl(nibble_read_kernel<__nv_bfloat16>, grid, block, 0, st, a)
-                                                 : launch_pdl(nibble_read_kernel<__half>, grid, block, 0, st, a);
+    const dim3 grid((unsigned)ctas, slices);
+    const cudaError_t e = dtype == FATHOM_F32    ? launch_read<float>(a, two, grid, st)
+                          : dtype == FATHOM_BF16 ? launch_read<__nv_bfloat16>(a, two, grid, st)
+                                                 : launch_read<__half>(a, two, grid, st);
     if (e != cudaSuccess) return launch_failed("nibble_read", e);
     return launch_status("nibble_read");
 }
