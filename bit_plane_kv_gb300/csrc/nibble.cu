@@ -10,23 +10,26 @@ namespace {
 // Bound by the cache's bytes, 9 D / 8 per token and KV head, as long as a block of 16 tokens
 // costs fewer instructions than the SM issues while its 18 D bytes arrive (392 for D = 128).
 //
-// Equal shares of 64-token tiles per CTA (shares.cuh); in a tile each warp takes its own
-// block of 16 tokens, in 16-byte asynchronous copies to a ring of its own, so that warps wait
-// for their own copies only.
+// Equal shares of 128-token tiles per CTA (shares.cuh); in a tile each warp takes two blocks
+// of 16 tokens, in 16-byte asynchronous copies to a ring of its own, so that warps wait for
+// their own copies only.
 //
 // Products run on the tensor cores, the fp32 operands in two pieces, hi + lo: a 16 x 8
 // operand holds a head's values in two columns, so four heads fill one instruction.
-// A query's pieces are whole numbers of 12 bits (to 2^-25 of its largest channel), so that
+// A query's pieces are whole numbers of 12 bits (to 2^-24 of its largest channel), so that
 // the sums over a group of channels are exact whatever the tensor cores cut off; a weight's
 // are fp16 (22 bits, and down to 2^-38 of the largest).
 //
-// Codes become fp16 in one logical operation: four bits left in the low bits of a 16-bit
-// half are the subnormal c 2^-24, four bits above them 16 c 2^-24.  For K that is the
-// operand itself: the factor of 16 goes into q, and - 7.5 sum(q) into the sum's start value.
-// Sums over V run over all tokens, where an offset would cancel away what is left of the
-// sum, so V is centred, (c - 7.5) 2^-9, one multiply-add per two values, exactly; and they
-// move to shared memory every kFlush blocks, because the tensor cores cut a sum off at its
-// last bit each time, always towards zero.
+// Codes become fp16 in one operation: four bits left in the low bits of a 16-bit half are
+// the subnormal c 2^-24, and a whole byte is (c + 16 c') 2^-24 with its neighbour c'.  Bytes
+// take one operation less to lay out than single codes, so the operands hold c and c + 16 c',
+// and what that adds is taken out at the other end: for K from the query, q c + q' c' =
+// (q - q' / 16) c + (q' / 16) (c + 16 c'), for V from the result.  For K that is the operand
+// itself, with - 7.5 sum(q) added to a group's sum.  Sums over V run over all tokens, where
+// an offset would cancel away what is left of the sum, so V is centred, (c - 7.5) 2^-9 and
+// (c' + c / 16 - 7.5 17 / 16) 2^-9, one multiply-add per two values, exactly; and they move
+// to shared memory every kFlush steps, because the tensor cores cut a sum off at its last
+// bit each time, always towards zero.
 //
 // K's scales multiply a group's partial sums (32 channels), V's the softmax weights:
 // (hi + lo) a in three fp16 operations for two tokens, the rounding error of hi a going to
@@ -35,10 +38,13 @@ namespace {
 // heads) becomes the weights' operand (heads by tokens) by one 8 x 8 transposition in
 // registers per 8 tokens and group.
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kTile = kNibTokens * kWarps;
-// CTAs resident per SM, and stages of a warp's ring, by the number of heads
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kStep = 2 * kNibTokens, kTile = kStep * kWarps;
+// CTAs resident per SM (their registers), and the stages of a warp's ring that then fit beside the sums.
 __host__ __device__ constexpr int nib_ctas(int nb) { return nb == 1 ? 4 : 3; }
-__host__ __device__ constexpr int nib_stages(int nb) { return nb == 1 ? 5 : 6; }
+__host__ __device__ constexpr int nib_stages(int d, int nb) {
+    const int left = 228 * 1024 / nib_ctas(nb) - 4608 - kWarps * 4 * nb * (d + 8) * 4, n = left / (kWarps * 2 * nib_block_bytes(d));
+    return n > 6 ? 6 : n;
+}
 constexpr int kMaxCtas = 4;   // the larger
 
 struct NibArgs {
@@ -57,7 +63,7 @@ struct Todo {   // a unit to be joined: its CTAs, and whether the first has a sh
 };
 template <int kD, int kNB>
 struct NibSmem {
-    alignas(128) unsigned char ring[kWarps][nib_stages(kNB)][nib_block_bytes(kD)];
+    alignas(128) unsigned char ring[kWarps][nib_stages(kD, kNB)][2][nib_block_bytes(kD)];
     float o[kWarps][4 * kNB][kD + 8];   // rows 8 words apart: four heads' stores meet in no bank
     float m[kWarps][FATHOM_MAX_G], l[kWarps][FATHOM_MAX_G];
     Share z;
@@ -69,7 +75,7 @@ struct NibSmem {
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1, const float (&c)[4]) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
@@ -106,6 +112,11 @@ __device__ __forceinline__ uint32_t fma_h2(uint32_t x, uint32_t y, uint32_t z) {
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
     return r;
 }
+__device__ __forceinline__ uint32_t fms_h2(uint32_t x, uint32_t y, uint32_t z) {   // x y - z
+    uint32_t r;
+    asm("{\n.reg .b32 n;\nneg.f16x2 n, %3;\nfma.rn.f16x2 %0, %1, %2, n;\n}\n" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+    return r;
+}
 __device__ __forceinline__ uint32_t mul_h2(uint32_t x, uint32_t y) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
@@ -118,13 +129,30 @@ __device__ __forceinline__ uint32_t max_h2(uint32_t x, uint32_t y) {
 }
 __device__ __forceinline__ uint32_t half_pair(float x) { return pack_half2(x, x); }
 
-constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 constexpr float kQueryPiece = 1.0f / 4096;   // what the second piece counts
 constexpr float kUp = 13.0f;                 // weights are 2^13 larger
-constexpr int kFlush = 16;
-// (c - 7.5) 2^-9 of a code in low or high position: times 2^15 or 2^11, minus 7.5 2^-9
-__device__ __forceinline__ uint32_t centred_low(uint32_t x) { return fma_h2(x & kLow, 0x78007800u, 0xa380a380u); }
-__device__ __forceinline__ uint32_t centred_high(uint32_t x) { return fma_h2(x & kHigh, 0x68006800u, 0xa380a380u); }
+constexpr int kFlush = 8;   // steps
+// Four codes of each half of x: the first and third, and both bytes.
+struct Codes {
+    uint32_t c0, b0, c1, b1;
+};
+__device__ __forceinline__ Codes split_codes(uint32_t x) {
+    Codes r;
+    r.c0 = x & 0x000f000fu;
+    r.b0 = x & 0x00ff00ffu;
+    r.b1 = __byte_perm(x, 0, 0x4341);
+    r.c1 = r.b1 & 0x000f000fu;
+    return r;
+}
+// c: (c - 7.5) 2^-9, times 2^15 minus 7.5 2^-9; c + 16 c': (c' + c / 16 - 7.5 17 / 16) 2^-9, times 2^11
+__device__ __forceinline__ Codes centred(const Codes &x) {
+    return Codes{fma_h2(x.c0, 0x78007800u, 0xa380a380u), fma_h2(x.b0, 0x68006800u, 0xa3f8a3f8u),
+                 fma_h2(x.c1, 0x78007800u, 0xa380a380u), fma_h2(x.b1, 0x68006800u, 0xa3f8a3f8u)};
+}
+
+// floor(log2(x)) of a normal x > 0 (-127 of a smaller one), and 2^e for -126 <= e <= 127.
+__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
+__device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // Scales of tokens r and r + 8, group by group.
 template <int kGroups>
@@ -157,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, nib_ctas(kNB))
 nibble_attn_kernel(const NibArgs a) {
     pdl_enter();
     using Smem = NibSmem<kD, kNB>;
-    constexpr int kStages = nib_stages(kNB), kGroups = kD / 32, kBlock = nib_block_bytes(kD);
+    constexpr int kStages = nib_stages(kD, kNB), kGroups = kD / 32, kBlock = nib_block_bytes(kD);
     extern __shared__ __align__(128) unsigned char nib_smem[];
     Smem &sm = *reinterpret_cast<Smem *>(nib_smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
@@ -165,10 +193,10 @@ nibble_attn_kernel(const NibArgs a) {
     auto length = [&](int s) { return min(max(a.lens[s], 0), a.cap); };
     auto tiles_of = [&](int n) { return (n + kTile - 1) / kTile; };
 
-    int seq, head, tok, n;   // of the block being computed: its unit, its first token, the sequence's tokens
+    int seq, head, tok, n;   // of the step being computed: its unit, its first token, the sequence's tokens
     int count;
     {
-        const Share z = find_share<kWarps>(a.p.seqs, H, 4, gridDim.x / nib_ctas(kNB), [&](int s) { return tiles_of(length(s)); }, sm.share);
+        const Share z = find_share<kWarps>(a.p.seqs, H, [&](int s) { return tiles_of(length(s)); }, sm.share);
         for (int u = blockIdx.x; u < a.p.seqs * H; u += gridDim.x)   // units of empty sequences
             if (length(u / H) == 0) {
                 for (int e = tid; e < G * kD; e += kThreads) a.out[(size_t)u * G * kD + e] = 0.0f;
@@ -180,9 +208,14 @@ nibble_attn_kernel(const NibArgs a) {
         n = length(seq);
         const int tiles = tiles_of(n);
         head = (int)div_small(z.w0 - z.first, tiles);
-        tok = (int)(z.w0 - z.first - (long long)head * tiles) * kTile + warp * kNibTokens;
+        tok = (int)(z.w0 - z.first - (long long)head * tiles) * kTile + warp * kStep;
         if (tid == 0) sm.z = z;   // read again at the units' ends
     }
+    // a unit's queries on their way to this SM
+    auto fetch_queries = [&](int unit) {
+        if (warp == 0 && 32 * lane < G * kD) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q + (size_t)unit * G * kD + 32 * lane));
+    };
+    fetch_queries(seq * H + head);
     // the next unit with tokens (none: seq = seqs)
     auto next_unit = [&](int &s, int &h, int &len) {
         if (++h < H) return;
@@ -190,8 +223,8 @@ nibble_attn_kernel(const NibArgs a) {
         do len = ++s < a.p.seqs ? length(s) : 1; while (len == 0);
     };
 
-    // ---- copies: the page of a warp's block is looked up one block ahead (-1: none)
-    int ld_tok = tok, ld_n = n, page;
+    // ---- copies: the pages of a warp's two blocks are looked up one step ahead (-1: none)
+    int ld_tok = tok, ld_n = n, page[2];
     const int32_t *ld_row;          // the sequence's row of the page table
     const unsigned char *ld_kv;     // the head's part of page 0
     {
@@ -200,56 +233,65 @@ nibble_attn_kernel(const NibArgs a) {
         if (lane == 0) { sm.next_seq[warp] = seq; sm.next_head[warp] = head; }
         __syncwarp();
     }
-    auto lookup = [&]() {
-        if (ld_tok >= ld_n) return -1;
-        const int x = __ldg(ld_row + (ld_tok >> a.lg));
+    auto lookup = [&](int t) {
+        if (t >= ld_n) return -1;
+        const int x = __ldg(ld_row + (t >> a.lg));
         return x >= a.p.num_pages ? -1 : x;
+    };
+    auto look_ahead = [&]() {   // both blocks lie in one page where pages hold two
+        page[0] = lookup(ld_tok);
+        page[1] = a.lg > 4 ? (ld_tok + kNibTokens < ld_n ? page[0] : -1) : lookup(ld_tok + kNibTokens);
     };
     auto ld_advance = [&]() {
         ld_tok += kTile;
-        if (ld_tok - warp * kNibTokens < ld_n) return;
+        if (ld_tok - warp * kStep < ld_n) return;
         int s = sm.next_seq[warp], h = sm.next_head[warp];
         next_unit(s, h, ld_n);
         __syncwarp();
         if (lane == 0) { sm.next_seq[warp] = s; sm.next_head[warp] = h; }
         __syncwarp();
-        ld_tok = warp * kNibTokens;
+        ld_tok = warp * kStep;
         if (s >= a.p.seqs) { ld_n = 0; return; }   // no page from here on
         ld_row = a.table + (size_t)s * a.p.max_pages;
         ld_kv = a.kv + h * a.p.head_stride;
+        fetch_queries(s * H + h);
     };
     const uint32_t ring = smem_addr(sm.ring[warp]) + 16 * lane;
-    unsigned filled = 0;   // stages with a block
-    auto issue = [&](int st, int pg) {
-        if (pg < 0) return;
-        filled |= 1u << st;
-        const unsigned char *src = ld_kv + pg * a.p.page_stride + (ld_tok & (a.p.page_tokens - 1)) / kNibTokens * kBlock + 16 * lane;
-        const uint32_t dst = ring + st * kBlock;
+    unsigned filled = 0;   // which blocks of the stages are there, a bit each
+    auto issue = [&](int st) {
 #pragma unroll
-        for (int k = 0; k < (kBlock + 511) / 512; ++k)
-            if (512 * (k + 1) <= kBlock || 16 * lane < kBlock - 512 * k)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512 * k), "l"(src + 512 * k) : "memory");
+        for (int b = 0; b < 2; ++b) {
+            if (page[b] < 0) continue;
+            filled |= 1u << (2 * st + b);
+            const int slot = (ld_tok + b * kNibTokens) & (a.p.page_tokens - 1);
+            const unsigned char *src = ld_kv + page[b] * a.p.page_stride + slot / kNibTokens * kBlock + 16 * lane;
+            const uint32_t dst = ring + (2 * st + b) * kBlock;
+#pragma unroll
+            for (int k = 0; k < (kBlock + 511) / 512; ++k)
+                if (512 * (k + 1) <= kBlock || 16 * lane < kBlock - 512 * k)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512 * k), "l"(src + 512 * k) : "memory");
+        }
     };
-    page = lookup();
+    look_ahead();
 #pragma unroll 1
     for (int st = 0; st < kStages - 1; ++st) {
         if (st < count) {
-            issue(st, page);
+            issue(st);
             ld_advance();
-            page = lookup();
+            look_ahead();
         }
         cp_async_commit();
     }
 
     const float to_log2 = 1.4426950408889634f / sqrtf((float)kD);
     uint32_t qb[kNB][kGroups][2][2];   // q's pieces: columns 2 h + piece, see the products below
-    float bias[kNB][kGroups][2], unscale[kNB];
+    float bias[kNB][kGroups], unscale[kNB];   // - 7.5 sum(q) of a group
     // of head c + 4 nb: the largest score (before unscale), 13 - it, the weights' sum of this lane's tokens, and
     // what the sums in shared memory refer to
     float m[kNB], shift[kNB], l[kNB], kept[kNB], o[kNB][2 * kGroups][4];
     uint32_t grow = 0, bound = 0;      // 2^k, and the scale above which k changes, as pairs
     bool in_smem = false;
-    int blocks = 0;                    // since the sums moved
+    int steps = 0;                     // since the sums moved
     auto flush = [&]() {               // sums in shared memory: relative to 2^(max - 13), without 2^k
         const float down = 1.0f / halves(grow).x;
 #pragma unroll
@@ -260,7 +302,8 @@ nibble_attn_kernel(const NibArgs a) {
             for (int g = 0; g < kGroups; ++g) {
                 float(&u)[4] = o[nb][2 * g], (&v)[4] = o[nb][2 * g + 1];
                 float4 *to = reinterpret_cast<float4 *>(&sm.o[warp][4 * nb + c][32 * g + 4 * r]);
-                float4 x = make_float4((u[0] + u[1]) * down, (u[2] + u[3]) * down, (v[0] + v[1]) * down, (v[2] + v[3]) * down);
+                float4 x = make_float4(u[0] + u[1], u[2] + u[3], v[0] + v[1], v[2] + v[3]);
+                x = make_float4(x.x * down, fmaf(x.x, -0.0625f, x.y) * down, x.z * down, fmaf(x.z, -0.0625f, x.w) * down);
                 if (in_smem) {
                     const float4 y = *to;
                     x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
@@ -270,7 +313,7 @@ nibble_attn_kernel(const NibArgs a) {
             }
         }
         in_smem = true;
-        blocks = 0;
+        steps = 0;
     };
     int st = 0, joins = 0;
 
@@ -295,31 +338,31 @@ nibble_attn_kernel(const NibArgs a) {
                 }
                 big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
                 big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                // a power of two that brings the largest to 2^10 .. 2^11; a code in high position counts 16 times
-                const int up = big > 0.0f && big < CUDART_INF_F ? min(max(10 - ilogbf(big), -126), 126) : 0;
-                const float scale = ldexpf(1.0f, up);
+                // a power of two that brings the largest to 2^10 .. 2^11, with room for a 16th of its neighbour
+                big *= 1.0625f;
+                const int up = big > 0.0f && big < CUDART_INF_F ? min(max(10 - exponent(big), -100), 126) : 0;
+                const float scale = power(up);
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     float piece[8], sum = 0.0f;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float y = x[g][e] * scale, hi = rintf(y);
+                        const float y = e & 1 ? x[g][e] * scale : fmaf(x[g][e + 1] * scale, -0.0625f, x[g][e] * scale), hi = rintf(y);
                         piece[e] = r & 1 ? rintf((y - hi) * 4096.0f) : hi;
-                        sum += piece[e];
+                        sum = fmaf(piece[e], e & 1 ? 1.0625f : 1.0f, sum);   // q' counts in c + 16 c' too
                     }
                     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    sum *= -7.5f / 16777216.0f;
-                    bias[nb][g][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
-                    bias[nb][g][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+                    const float lo_sum = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+                    bias[nb][g] = fmaf(lo_sum, kQueryPiece, __shfl_sync(0xffffffffu, sum, 8 * c)) * (-7.5f / 16777216.0f);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {   // channels 8 c + 2 k and 4 on (low position), and their neighbours (high)
+                    for (int k = 0; k < 2; ++k) {   // channels 8 c + 2 k and 4 on, and their neighbours
                         qb[nb][g][k][0] = pack_half2(piece[2 * k], piece[2 * k + 4]);
                         qb[nb][g][k][1] = pack_half2(piece[2 * k + 1] * 0.0625f, piece[2 * k + 5] * 0.0625f);
                     }
                 }
                 // a / 8 of the scales, 2^-24 of the codes
-                unscale[nb] = __shfl_sync(0xffffffffu, ldexpf(to_log2, 21 - up), 8 * c);
+                unscale[nb] = __shfl_sync(0xffffffffu, to_log2 * power(21 - up), 8 * c);
                 m[nb] = -CUDART_INF_F;
                 shift[nb] = kUp;
                 kept[nb] = kUp;
@@ -330,86 +373,92 @@ nibble_attn_kernel(const NibArgs a) {
             grow = 0x74007400u;    // 2^14
             bound = 0x0c000c00u;   // 2^-12
             in_smem = false;
-            blocks = 0;
+            steps = 0;
         }
         const int first_tile = tok / kTile, last = min(count, i + tiles_of(n) - first_tile);
 #pragma unroll 1
         for (; i < last; ++i, tok += kTile) {
-            // the copy kStages - 1 blocks ahead, into the stage that was read last
+            // the copies kStages - 1 steps ahead, into the stage that was read last
             if (i + kStages - 1 < count) {
-                issue(st == 0 ? kStages - 1 : st - 1, page);
+                issue(st == 0 ? kStages - 1 : st - 1);
                 ld_advance();
-                page = lookup();
+                look_ahead();
             }
             cp_async_commit();
             cp_async_wait<kStages - 1>();
             __syncwarp();
-            if (filled >> st & 1u) {
-                filled ^= 1u << st;
-                const unsigned char *blk = sm.ring[warp][st];
-                const uint32_t codes = ring + st * kBlock;
-                // ---- scores of tokens r and r + 8: columns 2 c, 2 c + 1 are the two pieces of head c
-                float s[kNB][2];
-                {
+            const unsigned there = filled >> (2 * st) & 3u;
+            if (there) {
+                filled ^= there << (2 * st);
+                const unsigned char *blk = sm.ring[warp][st][0];
+                const uint32_t codes = ring + 2 * st * kBlock;
+                // ---- scores of tokens r and r + 8 of each block: columns 2 c, 2 c + 1 are the two pieces of head c
+                float s[2][kNB][2];
+                uint32_t vs[2][kGroups];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
                     uint32_t sc[kGroups];
-                    load_scales<kGroups>(sc, blk + nib_scales(kD), r);
+                    load_scales<kGroups>(sc, blk + b * kBlock + nib_scales(kD), r);
+                    load_scales<kGroups>(vs[b], blk + b * kBlock + nib_half(kD) + nib_scales(kD), r);
 #pragma unroll
                     for (int g0 = 0; g0 < kGroups; g0 += 2) {
                         uint32_t x[4];
-                        if (g0 + 1 < kGroups) load_codes<false, true>(x, codes + g0 * 256);
-                        else load_codes<false, false>(x, codes + g0 * 256);
+                        if (g0 + 1 < kGroups) load_codes<false, true>(x, codes + b * kBlock + g0 * 256);
+                        else load_codes<false, false>(x, codes + b * kBlock + g0 * 256);
 #pragma unroll
                         for (int g = g0; g < g0 + 2 && g < kGroups; ++g) {
-                            const uint32_t x0 = x[2 * (g - g0)], x1 = x[2 * (g - g0) + 1], y0 = x0 >> 8, y1 = x1 >> 8;
+                            const Codes u = split_codes(x[2 * (g - g0)]), v = split_codes(x[2 * (g - g0) + 1]);
                             const float2 f = halves(sc[g]);
 #pragma unroll
                             for (int nb = 0; nb < kNB; ++nb) {
-                                const float b[4] = {bias[nb][g][0], bias[nb][g][1], bias[nb][g][0], bias[nb][g][1]};
+                                const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                                 float t[4];
-                                mma_f16(t, x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh, qb[nb][g][0][0], qb[nb][g][0][1], b);
-                                mma_f16(t, y0 & kLow, y1 & kLow, y0 & kHigh, y1 & kHigh, qb[nb][g][1][0], qb[nb][g][1][1], t);
-                                t[0] = fmaf(t[1], kQueryPiece, t[0]);
-                                t[2] = fmaf(t[3], kQueryPiece, t[2]);
-                                s[nb][0] = g ? fmaf(f.x, t[0], s[nb][0]) : f.x * t[0];
-                                s[nb][1] = g ? fmaf(f.y, t[2], s[nb][1]) : f.y * t[2];
+                                mma_f16(t, u.c0, v.c0, u.b0, v.b0, qb[nb][g][0][0], qb[nb][g][0][1], none);
+                                mma_f16(t, u.c1, v.c1, u.b1, v.b1, qb[nb][g][1][0], qb[nb][g][1][1], t);
+                                t[0] = fmaf(t[1], kQueryPiece, t[0] + bias[nb][g]);
+                                t[2] = fmaf(t[3], kQueryPiece, t[2] + bias[nb][g]);
+                                s[b][nb][0] = g ? fmaf(f.x, t[0], s[b][nb][0]) : f.x * t[0];
+                                s[b][nb][1] = g ? fmaf(f.y, t[2], s[b][nb][1]) : f.y * t[2];
                             }
                         }
                     }
                 }
-                uint32_t vs[kGroups];
-                load_scales<kGroups>(vs, blk + nib_half(kD) + nib_scales(kD), r);
-                if (tok + kNibTokens > n) {   // tokens behind the last: no weight, whatever their places hold
-                    const int left = n - tok;
+                if (there != 3u || tok + kStep > n) {   // tokens that are not there: no weight, whatever their places hold
 #pragma unroll
-                    for (int nb = 0; nb < kNB; ++nb) {
-                        if (r >= left) s[nb][0] = -CUDART_INF_F;
-                        if (r + 8 >= left) s[nb][1] = -CUDART_INF_F;
+                    for (int b = 0; b < 2; ++b) {
+                        const int left = there >> b & 1u ? n - tok - b * kNibTokens : 0;
+#pragma unroll
+                        for (int nb = 0; nb < kNB; ++nb) {
+                            if (r >= left) s[b][nb][0] = -CUDART_INF_F;
+                            if (r + 8 >= left) s[b][nb][1] = -CUDART_INF_F;
+                        }
+                        const uint32_t keep = (r < left ? 0xffffu : 0u) | (r + 8 < left ? 0xffff0000u : 0u);
+#pragma unroll
+                        for (int g = 0; g < kGroups; ++g) vs[b][g] &= keep;
                     }
-                    const uint32_t keep = (r < left ? 0xffffu : 0u) | (r + 8 < left ? 0xffff0000u : 0u);
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g) vs[g] &= keep;
                 }
-                uint32_t most = vs[0];
+                uint32_t most = max_h2(vs[0][0], vs[1][0]);
 #pragma unroll
-                for (int g = 1; g < kGroups; ++g) most = max_h2(most, vs[g]);
-                bool raise = __hbgt2(*reinterpret_cast<const __half2 *>(&bound), *reinterpret_cast<const __half2 *>(&most)) ? false : true;
+                for (int g = 1; g < kGroups; ++g) most = max_h2(most, max_h2(vs[0][g], vs[1][g]));
+                bool raise = !__hbgt2(*reinterpret_cast<const __half2 *>(&bound), *reinterpret_cast<const __half2 *>(&most));
 #pragma unroll
-                for (int nb = 0; nb < kNB; ++nb) raise |= fmaxf(s[nb][0], s[nb][1]) > m[nb];
+                for (int nb = 0; nb < kNB; ++nb)
+                    raise |= fmaxf(fmaxf(s[0][nb][0], s[0][nb][1]), fmaxf(s[1][nb][0], s[1][nb][1])) > m[nb];
                 if (__any_sync(0xffffffffu, raise)) {
-                    float2 mh = halves(most);
+                    const float2 mh = halves(most);
                     float top_scale = fmaxf(mh.x, mh.y), ratio = 1.0f;
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) top_scale = fmaxf(top_scale, __shfl_xor_sync(0xffffffffu, top_scale, d));
                     if (top_scale >= halves(bound).x) {   // k brings the largest scale to 1 .. 2, and holds until 4
-                        const int k = top_scale < CUDART_INF_F ? min(max(-ilogbf(top_scale), -14), 14) : -14;
-                        const float now = ldexpf(1.0f, k);
+                        const int k = top_scale < CUDART_INF_F ? min(max(-exponent(top_scale), -14), 14) : -14;
+                        const float now = power(k);
                         ratio = now / halves(grow).x;
                         grow = half_pair(now);
                         bound = half_pair(fminf(4.0f / now, 65504.0f * 2));
                     }
 #pragma unroll
                     for (int nb = 0; nb < kNB; ++nb) {
-                        float top = fmaxf(s[nb][0], s[nb][1]);
+                        float top = fmaxf(fmaxf(s[0][nb][0], s[0][nb][1]), fmaxf(s[1][nb][0], s[1][nb][1]));
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                         top = fmaxf(top, m[nb]);
@@ -429,44 +478,45 @@ nibble_attn_kernel(const NibArgs a) {
                             for (int e = 0; e < 4; ++e) o[nb][j][e] *= f;
                     }
                 }
-                uint32_t hi[kNB], lo[kNB];   // weights of tokens r (low half) and r + 8
-#pragma unroll
-                for (int nb = 0; nb < kNB; ++nb) {
-                    const float w0 = exp2_approx(fmaf(s[nb][0], unscale[nb], shift[nb]));
-                    const float w1 = exp2_approx(fmaf(s[nb][1], unscale[nb], shift[nb]));
-                    l[nb] += w0 + w1;
-                    hi[nb] = pack_half2(w0, w1);
-                    const float2 h = halves(hi[nb]);
-                    lo[nb] = pack_half2(w0 - h.x, w1 - h.y);
-                }
                 // ---- weights times V: channels 4 r + (0, 1) and 4 r + (2, 3) of a group are two products' rows
 #pragma unroll
-                for (int g0 = 0; g0 < kGroups; g0 += 2) {
-                    uint32_t x[4];
-                    if (g0 + 1 < kGroups) load_codes<true, true>(x, codes + nib_half(kD) + g0 * 256);
-                    else load_codes<true, false>(x, codes + nib_half(kD) + g0 * 256);
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t hi[kNB], lo[kNB];   // weights of tokens r (low half) and r + 8
 #pragma unroll
-                    for (int g = g0; g < g0 + 2 && g < kGroups; ++g) {
-                        const uint32_t x0 = x[2 * (g - g0)], x1 = x[2 * (g - g0) + 1], y0 = x0 >> 8, y1 = x1 >> 8;
-                        const uint32_t f = mul_h2(vs[g], grow);
-                        uint32_t b[kNB][2];
+                    for (int nb = 0; nb < kNB; ++nb) {
+                        const float w0 = exp2_approx(fmaf(s[b][nb][0], unscale[nb], shift[nb]));
+                        const float w1 = exp2_approx(fmaf(s[b][nb][1], unscale[nb], shift[nb]));
+                        l[nb] += w0 + w1;
+                        hi[nb] = pack_half2(w0, w1);
+                        const float2 h = halves(hi[nb]);
+                        lo[nb] = pack_half2(w0 - h.x, w1 - h.y);
+                    }
 #pragma unroll
-                        for (int nb = 0; nb < kNB; ++nb) {
-                            const uint32_t h = mul_h2(hi[nb], f);
-                            const uint32_t e = fma_h2(lo[nb], f, fma_h2(hi[nb], f, h ^ 0x80008000u));
-                            b[nb][0] = transpose8(__byte_perm(h, e, 0x5410));
-                            b[nb][1] = transpose8(__byte_perm(h, e, 0x7632));
-                        }
-                        const uint32_t a0 = centred_low(x0), a1 = centred_high(x0), a2 = centred_low(x1), a3 = centred_high(x1);
-                        const uint32_t c0 = centred_low(y0), c1 = centred_high(y0), c2 = centred_low(y1), c3 = centred_high(y1);
+                    for (int g0 = 0; g0 < kGroups; g0 += 2) {
+                        uint32_t x[4];
+                        if (g0 + 1 < kGroups) load_codes<true, true>(x, codes + b * kBlock + nib_half(kD) + g0 * 256);
+                        else load_codes<true, false>(x, codes + b * kBlock + nib_half(kD) + g0 * 256);
 #pragma unroll
-                        for (int nb = 0; nb < kNB; ++nb) {
-                            mma_f16(o[nb][2 * g], a0, a1, a2, a3, b[nb][0], b[nb][1], o[nb][2 * g]);
-                            mma_f16(o[nb][2 * g + 1], c0, c1, c2, c3, b[nb][0], b[nb][1], o[nb][2 * g + 1]);
+                        for (int g = g0; g < g0 + 2 && g < kGroups; ++g) {
+                            const uint32_t f = mul_h2(vs[b][g], grow);
+                            uint32_t p[kNB][2];
+#pragma unroll
+                            for (int nb = 0; nb < kNB; ++nb) {
+                                const uint32_t h = mul_h2(hi[nb], f);
+                                const uint32_t e = fma_h2(lo[nb], f, fms_h2(hi[nb], f, h));
+                                p[nb][0] = transpose8(__byte_perm(h, e, 0x5410));
+                                p[nb][1] = transpose8(__byte_perm(h, e, 0x7632));
+                            }
+                            const Codes u = centred(split_codes(x[2 * (g - g0)])), v = centred(split_codes(x[2 * (g - g0) + 1]));
+#pragma unroll
+                            for (int nb = 0; nb < kNB; ++nb) {
+                                mma_f16(o[nb][2 * g], u.c0, u.b0, v.c0, v.b0, p[nb][0], p[nb][1], o[nb][2 * g]);
+                                mma_f16(o[nb][2 * g + 1], u.c1, u.b1, v.c1, v.b1, p[nb][0], p[nb][1], o[nb][2 * g + 1]);
+                            }
                         }
                     }
                 }
-                if (++blocks == kFlush) flush();
+                if (++steps == kFlush) flush();
                 __syncwarp();   // the stage is read before its next copy starts
             }
             st = st + 1 == kStages ? 0 : st + 1;
@@ -517,7 +567,7 @@ nibble_attn_kernel(const NibArgs a) {
             ++joins;
         }
         next_unit(seq, head, n);
-        tok = warp * kNibTokens;
+        tok = warp * kStep;
         __syncthreads();   // the merge buffers are free again
     }
     cp_async_wait<0>();

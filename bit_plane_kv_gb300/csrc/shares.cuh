@@ -27,17 +27,16 @@ struct ShareSmem {
     int part;
 };
 
-// This CTA's share.  tiles_of(s): tiles of one head of sequence s.  Every CTA has one when
-// each then gets `least` tiles, else fewer CTAs have longer ones, down to `few` CTAs.
+// This CTA's share.  tiles_of(s): tiles of one head of sequence s.
 template <int kWarps, typename Tiles>
-__device__ __forceinline__ Share find_share(int seqs, int heads, int least, int few, Tiles tiles_of, ShareSmem<kWarps> &sm) {
+__device__ __forceinline__ Share find_share(int seqs, int heads, Tiles tiles_of, ShareSmem<kWarps> &sm) {
     constexpr int kThreads = 32 * kWarps;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long cta = blockIdx.x;
     Share z{0, 1, 0, 0, 0, 0};
     auto split = [&](long long sum) {
         z.W = sum * heads;
-        z.NC = min((long long)gridDim.x, max(1LL, max(z.W / least, min(z.W, (long long)few))));
+        z.NC = min((long long)gridDim.x, max(1LL, z.W));
         if (cta < z.NC) { z.w0 = share_start(cta, z.W, z.NC); z.w1 = share_start(cta + 1, z.W, z.NC); }
     };
     auto scan = [&](long long x) {   // inclusive sums over the lanes
@@ -137,10 +136,10 @@ __device__ __forceinline__ void join_parts(const Parts &parts, int G, int c_firs
     }
     for (;;) {
         __syncthreads();
-        if (tid == 0) {
-            __threadfence();   // the CTA's state before its ticket
-            jn.last = atomicAdd(ticket, 1u) == (unsigned)(n - 1) ? 1 : 0;
-            __threadfence();
+        if (tid == 0) {   // the CTA's state before its ticket, the others' after it
+            unsigned before_it;
+            asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before_it) : "l"(ticket) : "memory");
+            jn.last = before_it == (unsigned)(n - 1) ? 1 : 0;
         }
         __syncthreads();
         if (!jn.last) return;
