@@ -10,13 +10,13 @@ namespace {
 // Bound by the cache's bytes, 9 D / 8 per token and KV head, as long as a block of 16 tokens
 // costs fewer instructions than the SM issues while its 18 D bytes arrive (392 for D = 128).
 //
-// Equal shares of 128-token tiles per CTA (shares.cuh); in a tile each warp takes two blocks
-// of 16 tokens, in 16-byte asynchronous copies to a ring of its own, so that warps wait for
-// their own copies only.
+// Equal shares of tiles of 128 or 256 tokens per CTA (shares.cuh); in a tile each warp takes
+// two or four blocks of 16 tokens, in 16-byte asynchronous copies to a ring of its own, so
+// that warps wait for their own copies only.
 //
 // Products run on the tensor cores, the fp32 operands in two pieces, hi + lo: a 16 x 8
 // operand holds a head's values in two columns, so four heads fill one instruction.
-// A query's pieces are whole numbers of 12 bits (to 2^-24 of its largest channel), so that
+// A query's pieces are whole numbers of 12 bits (to 2^-22 of its largest channel), so that
 // the sums over a group of channels are exact whatever the tensor cores cut off; a weight's
 // are fp16 (22 bits, and down to 2^-38 of the largest).
 //
@@ -28,7 +28,7 @@ namespace {
 // itself, with - 7.5 sum(q) added to a group's sum.  Sums over V run over all tokens, where
 // an offset would cancel away what is left of the sum, so V is centred, (c - 7.5) 2^-9 and
 // (c' + c / 16 - 7.5 17 / 16) 2^-9, one multiply-add per two values, exactly; and they move
-// to shared memory every kFlush steps, because the tensor cores cut a sum off at its last
+// to shared memory every kFlush blocks, because the tensor cores cut a sum off at its last
 // bit each time, always towards zero.
 //
 // K's scales multiply a group's partial sums (32 channels), V's the softmax weights:
@@ -38,11 +38,14 @@ namespace {
 // heads) becomes the weights' operand (heads by tokens) by one 8 x 8 transposition in
 // registers per 8 tokens and group.
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kStep = 2 * kNibTokens, kTile = kStep * kWarps;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+// Blocks of a step, the more the less a step's bookkeeping costs (32 sequences of up to 32k tokens, 64 channels: two
+// 82 us, four 75; sequences of 100 tokens 53 and 57, their few blocks being fewer warps' work).
+__host__ __device__ constexpr int nib_blocks(int d) { return d <= 64 ? 4 : 2; }
 // CTAs resident per SM (their registers), and the stages of a warp's ring that then fit beside the sums.
 __host__ __device__ constexpr int nib_ctas(int nb) { return nb == 1 ? 4 : 3; }
 __host__ __device__ constexpr int nib_stages(int d, int nb) {
-    const int left = 228 * 1024 / nib_ctas(nb) - 4608 - kWarps * 4 * nb * (d + 8) * 4, n = left / (kWarps * 2 * nib_block_bytes(d));
+    const int left = 228 * 1024 / nib_ctas(nb) - 4608 - kWarps * 4 * nb * (d + 8) * 4, n = left / (kWarps * nib_blocks(d) * nib_block_bytes(d));
     return n > 6 ? 6 : n;
 }
 constexpr int kMaxCtas = 4;   // the larger
@@ -63,7 +66,7 @@ struct Todo {   // a unit to be joined: its CTAs, and whether the first has a sh
 };
 template <int kD, int kNB>
 struct NibSmem {
-    alignas(128) unsigned char ring[kWarps][nib_stages(kD, kNB)][2][nib_block_bytes(kD)];
+    alignas(128) unsigned char ring[kWarps][nib_stages(kD, kNB)][nib_blocks(kD)][nib_block_bytes(kD)];
     float o[kWarps][4 * kNB][kD + 8];   // rows 8 words apart: four heads' stores meet in no bank
     float m[kWarps][FATHOM_MAX_G], l[kWarps][FATHOM_MAX_G];
     Share z;
@@ -131,7 +134,7 @@ __device__ __forceinline__ uint32_t half_pair(float x) { return pack_half2(x, x)
 
 constexpr float kQueryPiece = 1.0f / 4096;   // what the second piece counts
 constexpr float kUp = 13.0f;                 // weights are 2^13 larger
-constexpr int kFlush = 8;   // steps
+constexpr int kFlush = 16;   // blocks
 // Four codes of each half of x: the first and third, and both bytes.
 struct Codes {
     uint32_t c0, b0, c1, b1;
@@ -185,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, nib_ctas(kNB))
 nibble_attn_kernel(const NibArgs a) {
     pdl_enter();
     using Smem = NibSmem<kD, kNB>;
+    constexpr int kBlocks = nib_blocks(kD), kStep = kBlocks * kNibTokens, kTile = kStep * kWarps;
     constexpr int kStages = nib_stages(kD, kNB), kGroups = kD / 32, kBlock = nib_block_bytes(kD);
     extern __shared__ __align__(128) unsigned char nib_smem[];
     Smem &sm = *reinterpret_cast<Smem *>(nib_smem);
@@ -223,8 +227,8 @@ nibble_attn_kernel(const NibArgs a) {
         do len = ++s < a.p.seqs ? length(s) : 1; while (len == 0);
     };
 
-    // ---- copies: the pages of a warp's two blocks are looked up one step ahead (-1: none)
-    int ld_tok = tok, ld_n = n, page[2];
+    // ---- copies: the pages of a warp's blocks are looked up one step ahead (-1: none)
+    int ld_tok = tok, ld_n = n, page[kBlocks];
     const int32_t *ld_row;          // the sequence's row of the page table
     const unsigned char *ld_kv;     // the head's part of page 0
     {
@@ -238,9 +242,12 @@ nibble_attn_kernel(const NibArgs a) {
         const int x = __ldg(ld_row + (t >> a.lg));
         return x >= a.p.num_pages ? -1 : x;
     };
-    auto look_ahead = [&]() {   // both blocks lie in one page where pages hold two
-        page[0] = lookup(ld_tok);
-        page[1] = a.lg > 4 ? (ld_tok + kNibTokens < ld_n ? page[0] : -1) : lookup(ld_tok + kNibTokens);
+    auto look_ahead = [&]() {
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            const int t = ld_tok + b * kNibTokens;
+            page[b] = b && (t & (a.p.page_tokens - 1)) ? (t < ld_n ? page[b - 1] : -1) : lookup(t);   // often one page
+        }
     };
     auto ld_advance = [&]() {
         ld_tok += kTile;
@@ -257,15 +264,16 @@ nibble_attn_kernel(const NibArgs a) {
         fetch_queries(s * H + h);
     };
     const uint32_t ring = smem_addr(sm.ring[warp]) + 16 * lane;
+    constexpr unsigned kAll = (1u << kBlocks) - 1;
     unsigned filled = 0;   // which blocks of the stages are there, a bit each
     auto issue = [&](int st) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kBlocks; ++b) {
             if (page[b] < 0) continue;
-            filled |= 1u << (2 * st + b);
+            filled |= 1u << (kBlocks * st + b);
             const int slot = (ld_tok + b * kNibTokens) & (a.p.page_tokens - 1);
             const unsigned char *src = ld_kv + page[b] * a.p.page_stride + slot / kNibTokens * kBlock + 16 * lane;
-            const uint32_t dst = ring + (2 * st + b) * kBlock;
+            const uint32_t dst = ring + (kBlocks * st + b) * kBlock;
 #pragma unroll
             for (int k = 0; k < (kBlock + 511) / 512; ++k)
                 if (512 * (k + 1) <= kBlock || 16 * lane < kBlock - 512 * k)
@@ -387,16 +395,16 @@ nibble_attn_kernel(const NibArgs a) {
             cp_async_commit();
             cp_async_wait<kStages - 1>();
             __syncwarp();
-            const unsigned there = filled >> (2 * st) & 3u;
+            const unsigned there = filled >> (kBlocks * st) & kAll;
             if (there) {
-                filled ^= there << (2 * st);
+                filled ^= there << (kBlocks * st);
                 const unsigned char *blk = sm.ring[warp][st][0];
-                const uint32_t codes = ring + 2 * st * kBlock;
+                const uint32_t codes = ring + kBlocks * st * kBlock;
                 // ---- scores of tokens r and r + 8 of each block: columns 2 c, 2 c + 1 are the two pieces of head c
-                float s[2][kNB][2];
-                uint32_t vs[2][kGroups];
+                float s[kBlocks][kNB][2];
+                uint32_t vs[kBlocks][kGroups];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
+                for (int b = 0; b < kBlocks; ++b) {
                     uint32_t sc[kGroups];
                     load_scales<kGroups>(sc, blk + b * kBlock + nib_scales(kD), r);
                     load_scales<kGroups>(vs[b], blk + b * kBlock + nib_half(kD) + nib_scales(kD), r);
@@ -423,9 +431,9 @@ nibble_attn_kernel(const NibArgs a) {
                         }
                     }
                 }
-                if (there != 3u || tok + kStep > n) {   // tokens that are not there: no weight, whatever their places hold
+                if (there != kAll || tok + kStep > n) {   // tokens that are not there: no weight, whatever their places hold
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
+                    for (int b = 0; b < kBlocks; ++b) {
                         const int left = there >> b & 1u ? n - tok - b * kNibTokens : 0;
 #pragma unroll
                         for (int nb = 0; nb < kNB; ++nb) {
@@ -437,13 +445,21 @@ nibble_attn_kernel(const NibArgs a) {
                         for (int g = 0; g < kGroups; ++g) vs[b][g] &= keep;
                     }
                 }
-                uint32_t most = max_h2(vs[0][0], vs[1][0]);
+                uint32_t most = 0u;
 #pragma unroll
-                for (int g = 1; g < kGroups; ++g) most = max_h2(most, max_h2(vs[0][g], vs[1][g]));
+                for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) most = max_h2(most, vs[b][g]);
+                float tops[kNB];
+#pragma unroll
+                for (int nb = 0; nb < kNB; ++nb) {
+                    tops[nb] = fmaxf(s[0][nb][0], s[0][nb][1]);
+#pragma unroll
+                    for (int b = 1; b < kBlocks; ++b) tops[nb] = fmaxf(tops[nb], fmaxf(s[b][nb][0], s[b][nb][1]));
+                }
                 bool raise = !__hbgt2(*reinterpret_cast<const __half2 *>(&bound), *reinterpret_cast<const __half2 *>(&most));
 #pragma unroll
-                for (int nb = 0; nb < kNB; ++nb)
-                    raise |= fmaxf(fmaxf(s[0][nb][0], s[0][nb][1]), fmaxf(s[1][nb][0], s[1][nb][1])) > m[nb];
+                for (int nb = 0; nb < kNB; ++nb) raise |= tops[nb] > m[nb];
                 if (__any_sync(0xffffffffu, raise)) {
                     const float2 mh = halves(most);
                     float top_scale = fmaxf(mh.x, mh.y), ratio = 1.0f;
@@ -458,7 +474,7 @@ nibble_attn_kernel(const NibArgs a) {
                     }
 #pragma unroll
                     for (int nb = 0; nb < kNB; ++nb) {
-                        float top = fmaxf(fmaxf(s[0][nb][0], s[0][nb][1]), fmaxf(s[1][nb][0], s[1][nb][1]));
+                        float top = tops[nb];
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                         top = fmaxf(top, m[nb]);
@@ -480,7 +496,7 @@ nibble_attn_kernel(const NibArgs a) {
                 }
                 // ---- weights times V: channels 4 r + (0, 1) and 4 r + (2, 3) of a group are two products' rows
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
+                for (int b = 0; b < kBlocks; ++b) {
                     uint32_t hi[kNB], lo[kNB];   // weights of tokens r (low half) and r + 8
 #pragma unroll
                     for (int nb = 0; nb < kNB; ++nb) {
@@ -516,7 +532,7 @@ nibble_attn_kernel(const NibArgs a) {
                         }
                     }
                 }
-                if (++steps == kFlush) flush();
+                if (++steps == kFlush / kBlocks) flush();
                 __syncwarp();   // the stage is read before its next copy starts
             }
             st = st + 1 == kStages ? 0 : st + 1;

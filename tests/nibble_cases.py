@@ -11,9 +11,13 @@ bits: the exact value's rounding, the same bits.
 Decode attention.  S = max_j sum_c |q_c k_jc| / sqrt(D), Q = max_c |q_c| max_j sum_c |k_jc|
 / sqrt(D), A = sum_j w_j |v_j| per channel with the exact weights w_j, a the largest scale
 of V.
-* q is whole numbers of 24 bits, off by 2^-25 of its largest channel: 2^-25 Q in a score.
-  A group's sum is exact; joining its pieces, four scales, their sums and the factor in
-  front are at most 12 fp32 roundings: ds = 12 * 2^-24 S + 2^-25 Q.
+* q is whole numbers of units of 2^-10 / 1.0625 of its largest channel or less, in two
+  pieces, the second off by 2^-13 of a unit, and a neighbour's by a 16th of that: 2^-22 Q.
+  A group's sum is exact up to 2^24 units / 16, beyond which nothing typical gets, and else off
+  by 2^-24 S; joining its pieces, four scales, their sums and the factor in front are at most
+  12 fp32 roundings.  - 7.5 sum(q) of a group is rounded once, 2^-24 7.5 32 max|q| a / 8, and
+  the group's |k| are a / 16 at least and once 15 a / 16, 2.8 a together: 2^-21.5 Q.  So
+  ds = 16 * 2^-24 S + 2^-20 Q.
 * The exponential's argument is one more fp32 fused operation on numbers of up to 1.45 * 2 S
   + 14, and so is the maximum that it is relative to: 2^-23 (3 S + 14) / 1.4.  The
   exponential itself and two rescalings: 3 * 2^-22.  So a weight's relative error is at most
@@ -142,7 +146,7 @@ def decode(q, K, V, table, lens):
         Q = qq.abs().amax(1) * kk.abs().sum(1).amax() / math.sqrt(D)
         z = torch.logsumexp(x, 1)
         w = torch.exp(x - z[:, None])
-        ds = 12 * 2.0 ** -24 * S + 2.0 ** -25 * Q
+        ds = 16 * 2.0 ** -24 * S + 2.0 ** -20 * Q
         r = 2 * (ds + 2.0 ** -23 * (2.2 * S + 10)) + 3 * 2.0 ** -22
         k = (n / 64 + 128) * 2.0 ** -23
         A = w @ vv.abs()
