@@ -739,10 +739,11 @@ def make_pages(k_pages, page_table) -> Pages:
         raise ValueError("k_pages: expected [pages][kv_heads][page_tokens][D], page_table: [seqs][max_pages]")
     if k_pages.dtype not in _ROW_TYPES:
         raise TypeError(f"k_pages: dtype {k_pages.dtype} not in {tuple(_ROW_TYPES)}")
-    n, H, P, D = k_pages.shape
-    _fit32(pages=n, page_tokens=P, max_pages=page_table.shape[1])
+    (n, H, P, D), (seqs, per) = k_pages.shape, page_table.shape
+    if (n | P | per) >> 31:
+        _fit32(pages=n, page_tokens=P, max_pages=per)
     sn, sh, sp, _ = k_pages.stride()
-    return Pages(page_table.shape[0], H, D, _ROW_TYPES[k_pages.dtype], P, n, page_table.shape[1], sn, sh, sp)
+    return Pages(seqs, H, D, _ROW_TYPES[k_pages.dtype], P, n, per, sn, sh, sp)
 
 
 def rows_as_pages(rows, kv_heads, page_tokens=64, device=None):
@@ -1008,12 +1009,14 @@ def make_nibble_pages(kv_pages, page_table, D) -> NibblePages:
         raise ValueError("kv_pages: expected [pages][kv_heads][bytes], page_table: [seqs][max_pages]")
     if kv_pages.dtype != torch.uint8:
         raise TypeError(f"kv_pages: dtype {kv_pages.dtype} is not torch.uint8")
-    n, H, size = kv_pages.shape
+    (n, H, size), (seqs, per) = kv_pages.shape, page_table.shape
     if D < 1 or size == 0 or size % (18 * D):
         raise ValueError(f"kv_pages: {size} bytes are no blocks of 18 * {D}")
-    _fit32(pages=n, page_tokens=size // (18 * D) * 16, max_pages=page_table.shape[1])
+    tokens = size // (18 * D) * 16
+    if (n | tokens | per) >> 31:
+        _fit32(pages=n, page_tokens=tokens, max_pages=per)
     sn, sh, _ = kv_pages.stride()
-    return NibblePages(page_table.shape[0], H, D, size // (18 * D) * 16, n, page_table.shape[1], sn, sh)
+    return NibblePages(seqs, H, D, tokens, n, per, sn, sh)
 
 
 def _check_nibble(pages, kv_pages, page_table):

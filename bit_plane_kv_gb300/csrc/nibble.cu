@@ -272,7 +272,7 @@ nibble_attn_kernel(const NibArgs a) {
             if (page[b] < 0) continue;
             filled |= 1u << (kBlocks * st + b);
             const int slot = (ld_tok + b * kNibTokens) & (a.p.page_tokens - 1);
-            const unsigned char *src = ld_kv + page[b] * a.p.page_stride + slot / kNibTokens * kBlock + 16 * lane;
+            const unsigned char *src = ld_kv + page[b] * a.p.page_stride + (int64_t)(slot / kNibTokens) * kBlock + 16 * lane;
             const uint32_t dst = ring + (kBlocks * st + b) * kBlock;
 #pragma unroll
             for (int k = 0; k < (kBlock + 511) / 512; ++k)

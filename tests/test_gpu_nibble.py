@@ -225,6 +225,28 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(big.contiguous(), kv)
 
 
+def test_a_page_of_sixteen_million_tokens():
+    """Places more than 2^31 bytes into a page: all tokens zero but the last 50."""
+    D, page, last = 128, 1 << 24, 50
+    kv, table = B.alloc_nibble_pages(1, 1, page, D), i32([[0]])
+    pages = B.make_nibble_pages(kv, table, D)
+    k, v = 3 * rnd(last, 1, D).to(BF), rnd(last, 1, D, seed=1).to(BF)
+    start, cu = i32([page - last]), i32([0, last])
+    B.fathom_nibble_append(pages, kv, table, k, v, start, cu)
+    K, V = B.fathom_nibble_read(pages, kv, table, start, cu, last, dtype=torch.float32)
+    assert torch.equal(K.double(), N.held(k.double())[0]) and torch.equal(V.double(), N.held(v.double())[0])
+    q = 4 * rnd(1, 2, D, seed=5)
+    out, lse = attend(q, kv, table, [page], want_lse=True)
+    x = q[0].double() @ K[:, 0].double().T / math.sqrt(D)
+    z = torch.logaddexp(torch.logsumexp(x, 1), torch.full((2,), math.log(page - last), device="cuda").double())
+    w = torch.exp(x - z[:, None])
+    # the scores of the zeros are exact; their sum of 2^24 / 608 / 64 additions per lane loses 432 * 2^-24 at most
+    S = (q[0].double().abs() @ K[:, 0].double().abs().T / math.sqrt(D)).amax(1)
+    tol = 2.0 ** -14 + 16 * 2.0 ** -24 * S + 2.0 ** -20 * S
+    assert bool(((lse[0].double() - z).abs() <= tol).all())
+    assert bool(((out[0].double() - w @ V[:, 0].double()).abs() <= 3 * tol[:, None] * (w @ V[:, 0].double().abs())).all())
+
+
 def test_one_workspace_serves_calls_of_different_sizes():
     calls = []
     for lens, H, G, D in (([9000, 5], 2, 8, 128), ([40] * 300, 4, 1, 32), ([30000], 1, 4, 64), ([70, 0], 1, 5, 96)):
