@@ -45,7 +45,7 @@ __host__ __device__ constexpr int nib_blocks(int d) { return d <= 64 ? 4 : 2; }
 // CTAs resident per SM (their registers), and the stages of a warp's ring that then fit beside the sums.
 __host__ __device__ constexpr int nib_ctas(int nb) { return nb == 1 ? 4 : 3; }
 __host__ __device__ constexpr int nib_stages(int d, int nb) {
-    const int left = 228 * 1024 / nib_ctas(nb) - 4608 - kWarps * 4 * nb * (d + 8) * 4, n = left / (kWarps * nib_blocks(d) * nib_block_bytes(d));
+    const int left = 228 * 1024 / nib_ctas(nb) - 4608 - kWarps * 4 * nb * (d + 8) * 4 - nb * d / 32 * 544, n = left / (kWarps * nib_blocks(d) * nib_block_bytes(d));
     return n > 6 ? 6 : n;
 }
 constexpr int kMaxCtas = 4;   // the larger
@@ -72,6 +72,8 @@ struct NibSmem {
     Share z;
     Todo todo[2];
     int next_seq[kWarps], next_head[kWarps];   // where a warp's copies have got to
+    uint4 pieces[kNB][kD / 32][32];   // a unit's queries as the products take them
+    float sums[kNB][kD / 32][8];
     ShareSmem<kWarps> share;
     JoinSmem join;
 };
@@ -206,13 +208,12 @@ nibble_attn_kernel(const NibArgs a) {
                 for (int e = tid; e < G * kD; e += kThreads) a.out[(size_t)u * G * kD + e] = 0.0f;
                 if (a.lse && tid < G) a.lse[(size_t)u * G + tid] = -CUDART_INF_F;
             }
-        if (z.w0 >= z.w1) return;
-        count = (int)(z.w1 - z.w0);
+        if (!z.count) return;
+        count = z.count;
         seq = z.seq;
+        head = z.head;
         n = length(seq);
-        const int tiles = tiles_of(n);
-        head = (int)div_small(z.w0 - z.first, tiles);
-        tok = (int)(z.w0 - z.first - (long long)head * tiles) * kTile + warp * kStep;
+        tok = z.tile * kTile + warp * kStep;
         if (tid == 0) sm.z = z;   // read again at the units' ends
     }
     // a unit's queries on their way to this SM
@@ -352,6 +353,7 @@ nibble_attn_kernel(const NibArgs a) {
                 const float scale = power(up);
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
+                    if ((nb * kGroups + g) % kWarps != warp) continue;   // the warps share the work
                     float piece[8], sum = 0.0f;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -361,13 +363,10 @@ nibble_attn_kernel(const NibArgs a) {
                     }
                     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    const float lo_sum = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
-                    bias[nb][g] = fmaf(lo_sum, kQueryPiece, __shfl_sync(0xffffffffu, sum, 8 * c)) * (-7.5f / 16777216.0f);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {   // channels 8 c + 2 k and 4 on, and their neighbours
-                        qb[nb][g][k][0] = pack_half2(piece[2 * k], piece[2 * k + 4]);
-                        qb[nb][g][k][1] = pack_half2(piece[2 * k + 1] * 0.0625f, piece[2 * k + 5] * 0.0625f);
-                    }
+                    if (c == 0) sm.sums[nb][g][r] = sum;
+                    // channels 8 c + 2 k and 4 on, and their neighbours, k = 0, 1
+                    sm.pieces[nb][g][lane] = make_uint4(pack_half2(piece[0], piece[4]), pack_half2(piece[1] * 0.0625f, piece[5] * 0.0625f),
+                                                        pack_half2(piece[2], piece[6]), pack_half2(piece[3] * 0.0625f, piece[7] * 0.0625f));
                 }
                 // a / 8 of the scales, 2^-24 of the codes
                 unscale[nb] = __shfl_sync(0xffffffffu, to_log2 * power(21 - up), 8 * c);
@@ -378,6 +377,15 @@ nibble_attn_kernel(const NibArgs a) {
 #pragma unroll
                 for (int j = 0; j < 2 * kGroups; ++j) o[nb][j][0] = o[nb][j][1] = o[nb][j][2] = o[nb][j][3] = 0.0f;
             }
+            __syncthreads();
+#pragma unroll
+            for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    const uint4 v = sm.pieces[nb][g][lane];
+                    qb[nb][g][0][0] = v.x; qb[nb][g][0][1] = v.y; qb[nb][g][1][0] = v.z; qb[nb][g][1][1] = v.w;
+                    bias[nb][g] = fmaf(sm.sums[nb][g][2 * c + 1], kQueryPiece, sm.sums[nb][g][2 * c]) * (-7.5f / 16777216.0f);
+                }
             grow = 0x74007400u;    // 2^14
             bound = 0x0c000c00u;   // 2^-12
             in_smem = false;
@@ -552,11 +560,18 @@ nibble_attn_kernel(const NibArgs a) {
         flush();
         __syncthreads();
         // the CTA's state of each head: (m, l, o), to `out` when the unit is all here
-        const long long W = sm.z.W, NC = sm.z.NC, unit_w0 = sm.z.w0 + i - tok / kTile;   // index of the unit's first tile
-        const long long c_first = div_small((unit_w0 + 1) * NC - 1, W), c_last = div_small((unit_w0 + tiles) * NC - 1, W);
+        int c_first = sm.z.own_first, c_last = sm.z.own_last;
+        bool second = false, before = false;   // this CTA's share, and the first CTA's, is its second
+        if (c_first < 0) {
+            const long long W = sm.z.W, NC = sm.z.NC, unit_w0 = sm.z.w0 + i - tok / kTile;   // index of the unit's first tile
+            c_first = (int)div_small((unit_w0 + 1) * NC - 1, W);
+            c_last = (int)div_small((unit_w0 + tiles) * NC - 1, W);
+            second = sm.z.w0 < unit_w0;
+            before = share_start(c_first, W, NC) < unit_w0;
+        }
         const bool whole = c_first == c_last;
         const Finish<kD> finish{a.out + (size_t)unit * G * kD, a.lse ? a.lse + (size_t)unit * G : nullptr};
-        const size_t slot = 2 * (size_t)blockIdx.x + (sm.z.w0 < unit_w0 ? 1 : 0);
+        const size_t slot = 2 * (size_t)blockIdx.x + (second ? 1 : 0);
         for (int e = 4 * tid; e < G * kD; e += 4 * kThreads) {
             const int h = e / kD, d = e % kD;
             float M = -CUDART_INF_F, L = 0.0f;
@@ -579,7 +594,7 @@ nibble_attn_kernel(const NibArgs a) {
             }
         }
         if (!whole) {
-            if (tid == 0) sm.todo[joins] = Todo{unit, (int)c_first, (int)c_last, share_start(c_first, W, NC) < unit_w0};
+            if (tid == 0) sm.todo[joins] = Todo{unit, c_first, c_last, before};
             ++joins;
         }
         next_unit(seq, head, n);

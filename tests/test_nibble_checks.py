@@ -3,9 +3,11 @@ checks (nothing is enqueued), the binding's checks before the library call, the 
 launch fault; and the workspace's layout."""
 import ctypes
 import os
+import random
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
 
@@ -298,3 +300,31 @@ def test_no_call_leaves_data_where_another_looks_for_tickets(lib):
                 assert all(x % 256 == 0 for x in (w.part_off, w.ml_off, w.total))
                 starts.add(w.part_off)
     assert len(starts) == 1
+
+
+def test_shares_of_few_units_cover_every_tile_once():
+    """The kernel's own CTAs of a unit, restated: of `grid` CTAs each unit of t > 0 tiles gets
+    min(t, max(1, t * part)), part = (grid - units) / all tiles in fp32; CTA j of its c takes tiles
+    j t / c to (j + 1) t / c.  No more CTAs than there are, and the longest share is an eighth and a tile more than
+    the mean at most."""
+    f = np.float32
+    rng = random.Random(3)
+    for _ in range(4000):
+        grid = 152 * rng.choice([3, 4])
+        heads = rng.choice([1, 2, 3, 8])
+        seqs = rng.randint(1, grid // 8 // heads)
+        top = rng.choice([1, 2, 9, 100, 5000, 1 << 21])
+        tiles = [rng.randint(0, top) for _ in range(seqs)]
+        total = sum(tiles)
+        if not total:
+            continue
+        part = f(grid - seqs * heads) / (f(total) * f(heads))
+        count = [min(t, max(1, int(f(t) * part))) if t else 0 for t in tiles]
+        assert sum(count) * heads <= grid
+        mean = total * heads / (grid - seqs * heads)
+        for t, c in zip(tiles, count):
+            ends = [j * t // c for j in range(c + 1)] if c else [0]
+            assert ends[-1] == t and all(a < b for a, b in zip(ends, ends[1:]))
+            assert all((j + 1) * t < 1 << 32 for j in range(c))
+            longest = max((b - a for a, b in zip(ends, ends[1:])), default=0)
+            assert longest <= 1 + mean * (2 if c < 8 else 1.125)
