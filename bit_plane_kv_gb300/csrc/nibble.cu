@@ -65,15 +65,16 @@ struct NibArgs {
     Parts parts;
 };
 
-struct Todo {   // a unit to be joined: its CTAs, and whether the first has a share of an earlier one
+struct Todo {   // a unit to be joined: its CTAs, whether the first has a share of an earlier one, its scores' factors
     int unit, first, last;
     bool before;
+    float unscale[FATHOM_MAX_G];
 };
 template <int kD, int kNB>
 struct NibSmem {
     alignas(128) unsigned char ring[kWarps][nib_stages(kD, kNB)][nib_blocks(kD)][nib_block_bytes(kD)];
     float o[kWarps][4 * kNB][kD + 8];   // rows 8 words apart: four heads' stores meet in no bank
-    float m[kWarps][FATHOM_MAX_G], l[kWarps][FATHOM_MAX_G];
+    float m[kWarps][FATHOM_MAX_G], l[kWarps][FATHOM_MAX_G], unscale[FATHOM_MAX_G];
     Share z;
     Todo todo[2];
     int next_seq[kWarps], next_head[kWarps];   // where a warp's copies have got to
@@ -183,10 +184,10 @@ __device__ __forceinline__ void load_scales(uint32_t (&s)[kGroups], const unsign
 template <int kD>
 struct Finish {
     float *out, *lse;   // of the unit
-    __device__ __forceinline__ void operator()(int e, float4 o, float m, float l) const {
+    __device__ __forceinline__ void operator()(int e, float4 o, float m, float l, float unscale) const {
         const float inv = l > 0.0f ? 64.0f / l : 0.0f;
         *reinterpret_cast<float4 *>(out + e) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        if (lse && e % kD == 0) lse[e / kD] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+        if (lse && e % kD == 0) lse[e / kD] = l == 0.0f ? -CUDART_INF_F : (fmaf(m, unscale, log2f(l)) - kUp) * 0.6931471805599453f;
     }
 };
 
@@ -201,13 +202,14 @@ nibble_attn_kernel(const NibArgs a) {
     Smem &sm = *reinterpret_cast<Smem *>(nib_smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
     const int H = a.p.kv_heads, G = a.G;
-    auto length = [&](int s) { return min(max(a.lens[s], 0), a.cap); };
+    auto length = [&](int s) { return min(max(__ldg(a.lens + s), 0), a.cap); };
     auto tiles_of = [&](int n) { return (n + kTile - 1) / kTile; };
 
     int seq, head, tok, n;   // of the step being computed: its unit, its first token, the sequence's tokens
     int count;
     {
         const Share z = find_share<kWarps>(a.p.seqs, H, [&](int s) { return tiles_of(length(s)); }, sm.share);
+#pragma unroll 4
         for (int u = blockIdx.x; u < a.p.seqs * H; u += gridDim.x)   // units of empty sequences
             if (length(u / H) == 0) {
                 for (int e = tid; e < G * kD; e += kThreads) a.out[(size_t)u * G * kD + e] = 0.0f;
@@ -300,18 +302,19 @@ nibble_attn_kernel(const NibArgs a) {
     const float to_log2 = 1.4426950408889634f / sqrtf((float)kD);
     uint32_t qb[kNB][kGroups][2][2];   // q's pieces: columns 2 h + piece, see the products below
     float bias[kNB][kGroups], unscale[kNB];   // - 7.5 sum(q) of a group
-    // of head c + 4 nb: the largest score (before unscale), 13 - it, the weights' sum of this lane's tokens, and
-    // what the sums in shared memory refer to
-    float m[kNB], shift[kNB], l[kNB], kept[kNB], o[kNB][2 * kGroups][4];
+    // of head c + 4 nb, before unscale: the largest score, the one that sums in shared memory refer to; and the
+    // weights' sum of this lane's tokens.  Differences of scores are taken before they are scaled: large ones keep
+    // their last bits
+    float m[kNB], kept[kNB], l[kNB], o[kNB][2 * kGroups][4];
     uint32_t grow = 0, bound = 0;      // 2^k, and the scale above which k changes, as pairs
     bool in_smem = false;
     int steps = 0;                     // since the sums moved
-    auto flush = [&]() {               // sums in shared memory: relative to 2^(max - 13), without 2^k
+    auto flush = [&]() {               // sums in shared memory: without 2^k
         const float down = 1.0f / halves(grow).x;
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb) {
-            const float f = kept[nb] == shift[nb] ? 1.0f : exp2_approx(shift[nb] - kept[nb]);
-            kept[nb] = shift[nb];
+            const float f = exp2_approx((kept[nb] - m[nb]) * unscale[nb]);
+            kept[nb] = m[nb];
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
                 float(&u)[4] = o[nb][2 * g], (&v)[4] = o[nb][2 * g + 1];
@@ -354,7 +357,7 @@ nibble_attn_kernel(const NibArgs a) {
                 big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
                 // a power of two that brings the largest to 2^10 .. 2^11, with room for a 16th of its neighbour
                 big *= 1.0625f;
-                const int up = big > 0.0f && big < CUDART_INF_F ? min(max(10 - exponent(big), -100), 126) : 0;
+                const int up = big > 0.0f && big < CUDART_INF_F ? min(max(10 - exponent(big), -117), 126) : 0;
                 const float scale = power(up);
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
@@ -373,11 +376,9 @@ nibble_attn_kernel(const NibArgs a) {
                     sm.pieces[nb][g][lane] = make_uint4(pack_half2(piece[0], piece[4]), pack_half2(piece[1] * 0.0625f, piece[5] * 0.0625f),
                                                         pack_half2(piece[2], piece[6]), pack_half2(piece[3] * 0.0625f, piece[7] * 0.0625f));
                 }
-                // a / 8 of the scales, 2^-24 of the codes
-                unscale[nb] = __shfl_sync(0xffffffffu, to_log2 * power(21 - up), 8 * c);
-                m[nb] = -CUDART_INF_F;
-                shift[nb] = kUp;
-                kept[nb] = kUp;
+                // a / 8 of the scales, 2^-24 of the codes; scores that need more than fp32's range are far apart anyway
+                unscale[nb] = __shfl_sync(0xffffffffu, up < -105 ? 3.0e38f : to_log2 * power(21 - up), 8 * c);
+                m[nb] = kept[nb] = kNoScore;
                 l[nb] = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 2 * kGroups; ++j) o[nb][j][0] = o[nb][j][1] = o[nb][j][2] = o[nb][j][3] = 0.0f;
@@ -491,14 +492,8 @@ nibble_attn_kernel(const NibArgs a) {
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                         top = fmaxf(top, m[nb]);
-                        float f = 1.0f;
-                        if (top > m[nb]) {
-                            const float to = fmaf(-top, unscale[nb], kUp);
-                            if (m[nb] != -CUDART_INF_F) f = exp2_approx(to - shift[nb]);   // empty sums: 0, or NaN
-                            else kept[nb] = to;                                            // nor is anything else in shared memory
-                            m[nb] = top;
-                            shift[nb] = to;
-                        }
+                        float f = exp2_approx((m[nb] - top) * unscale[nb]);   // of no score yet: 0, and its sums 0 or NaN
+                        m[nb] = top;
                         l[nb] *= f;
                         f *= ratio;
 #pragma unroll
@@ -513,8 +508,8 @@ nibble_attn_kernel(const NibArgs a) {
                     uint32_t hi[kNB], lo[kNB];   // weights of tokens r (low half) and r + 8
 #pragma unroll
                     for (int nb = 0; nb < kNB; ++nb) {
-                        const float w0 = exp2_approx(fmaf(s[b][nb][0], unscale[nb], shift[nb]));
-                        const float w1 = exp2_approx(fmaf(s[b][nb][1], unscale[nb], shift[nb]));
+                        const float w0 = exp2_approx(fmaf(s[b][nb][0] - m[nb], unscale[nb], kUp));
+                        const float w1 = exp2_approx(fmaf(s[b][nb][1] - m[nb], unscale[nb], kUp));
                         l[nb] += w0 + w1;
                         hi[nb] = pack_half2(w0, w1);
                         const float2 h = halves(hi[nb]);
@@ -558,8 +553,9 @@ nibble_attn_kernel(const NibArgs a) {
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], d);
             if (r == 0) {
-                sm.m[warp][4 * nb + c] = m[nb] == -CUDART_INF_F ? -CUDART_INF_F : -shift[nb];
+                sm.m[warp][4 * nb + c] = m[nb];
                 sm.l[warp][4 * nb + c] = l[nb];
+                if (warp == 0) sm.unscale[4 * nb + c] = unscale[nb];
             }
         }
         flush();
@@ -579,27 +575,32 @@ nibble_attn_kernel(const NibArgs a) {
         const size_t slot = 2 * (size_t)blockIdx.x + (second ? 1 : 0);
         for (int e = 4 * tid; e < G * kD; e += 4 * kThreads) {
             const int h = e / kD, d = e % kD;
-            float M = -CUDART_INF_F, L = 0.0f;
+            float M = kNoScore, L = 0.0f;
 #pragma unroll
             for (int v = 0; v < kWarps; ++v) M = fmaxf(M, sm.m[v][h]);
             float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int v = 0; v < kWarps; ++v) {
-                // a warp without a maximum has nothing, or NaN that stays
-                const float f = sm.m[v][h] == -CUDART_INF_F ? 1.0f : exp2_approx(sm.m[v][h] - M);
+                const float f = exp2_approx((sm.m[v][h] - M) * sm.unscale[h]);
                 const float4 x = *reinterpret_cast<const float4 *>(&sm.o[v][h][d]);
                 O.x = fmaf(x.x, f, O.x); O.y = fmaf(x.y, f, O.y); O.z = fmaf(x.z, f, O.z); O.w = fmaf(x.w, f, O.w);
                 L = fmaf(sm.l[v][h], f, L);
             }
             if (whole) {
-                finish(e, O, M, L);
+                finish(e, O, M, L, sm.unscale[h]);
             } else {
                 *reinterpret_cast<float4 *>(a.parts.o + slot * G * kD + e) = O;
                 if (d == 0) *reinterpret_cast<float2 *>(a.parts.ml + (slot * G + h) * 2) = make_float2(M, L);
             }
         }
         if (!whole) {
-            if (tid == 0) sm.todo[joins] = Todo{unit, c_first, c_last, before};
+            if (tid == 0) {
+                sm.todo[joins].unit = unit;
+                sm.todo[joins].first = c_first;
+                sm.todo[joins].last = c_last;
+                sm.todo[joins].before = before;
+            }
+            if (tid < G) sm.todo[joins].unscale[tid] = sm.unscale[tid];
             ++joins;
         }
         next_unit(seq, head, n);
@@ -610,9 +611,9 @@ nibble_attn_kernel(const NibArgs a) {
     // the first unit and the last one may have other CTAs' shares; joined here, where the loop's registers are free
 #pragma unroll 1
     for (int k = 0; k < joins; ++k) {
-        const Todo t = sm.todo[k];
+        const Todo &t = sm.todo[k];
         const Finish<kD> finish{a.out + (size_t)t.unit * G * kD, a.lse ? a.lse + (size_t)t.unit * G : nullptr};
-        join_parts<kWarps, kD, 4 * kNB>(a.parts, G, t.first, t.last, t.before, sm.join, finish);
+        join_parts<kWarps, kD, 4 * kNB>(a.parts, G, t.first, t.last, t.before, t.unscale, sm.join, finish);
         __syncthreads();
     }
 }

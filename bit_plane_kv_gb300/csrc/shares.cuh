@@ -145,10 +145,12 @@ __device__ __forceinline__ Share find_share(int seqs, int heads, Tiles tiles_of,
 }
 
 // ---------------------------------------------------------------- partial states
-// A unit that several CTAs hold a share of: each leaves (m, l, o[D]) per head, o and l
-// relative to 2^m, and takes a ticket; the last to arrive joins them, in their order, so
+// A unit that several CTAs hold a share of: each leaves (m, l, o[D]) per head, m its largest
+// score before a factor that turns scores into powers of two, o and l relative to it, and
+// takes a ticket; the last to arrive joins them, in their order, so
 // that the result does not depend on the order of arrival.  Of more than 32 shares,
 // groups of 16 are joined first, each by its last share and into its first one's place.
+constexpr float kNoScore = -3.402823466e38f;   // where there is none yet: finite, so that a difference is a number
 struct Parts {
     float *o, *ml;   // [CTA][2][G][D] and [CTA][2][G][2] = (m, l): a CTA has at most two shares to be joined
     unsigned *ticket, *group_ticket;   // zero between calls: a unit's, by its first CTA; a group's, at its first share's place
@@ -160,10 +162,11 @@ struct JoinSmem {
 
 // Called by every thread of the CTA after the CTA's state of the unit lies in its place.
 // c_first, c_last: the unit's CTAs; before: whether the first of them holds tiles of an
-// earlier unit too (its share of this one is then its second).  done(e, o, m, l) gets the
-// joined sums of elements e .. e + 3 of the unit's [G][D].
+// earlier unit too (its share of this one is then its second); scale [G]: the scores'
+// factors, in shared memory.  done(e, o, m, l, scale) gets the joined sums of elements e ..
+// e + 3 of the unit's [G][D].
 template <int kWarps, int kD, int kHeads, typename Done>
-__device__ __forceinline__ void join_parts(const Parts &parts, int G, int c_first, int c_last, bool before,
+__device__ __forceinline__ void join_parts(const Parts &parts, int G, int c_first, int c_last, bool before, const float *scale,
                                            JoinSmem &jn, Done done) {
     constexpr int kThreads = 32 * kWarps, kGroup = 16;
     constexpr int kVecs = (kHeads * kD / 4 + kThreads - 1) / kThreads;
@@ -190,7 +193,7 @@ __device__ __forceinline__ void join_parts(const Parts &parts, int G, int c_firs
         __syncthreads();
         if (!jn.last) return;
         if (tid == 0) *ticket = 0u;
-        if (tid < G) { jn.m[tid] = -CUDART_INF_F; jn.l[tid] = 0.0f; }
+        if (tid < G) { jn.m[tid] = kNoScore; jn.l[tid] = 0.0f; }
         float4 acc[kVecs];
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -212,7 +215,7 @@ __device__ __forceinline__ void join_parts(const Parts &parts, int G, int c_firs
 #pragma unroll
             for (int i = 0; i < (kHeads + kWarps - 1) / kWarps; ++i) {
                 const int h = warp + i * kWarps;
-                mls[i] = make_float2(-CUDART_INF_F, 0.0f);
+                mls[i] = make_float2(kNoScore, 0.0f);
                 if (lane < nx && h < G)
                     mls[i] = __ldcg(reinterpret_cast<const float2 *>(
                         parts.ml + ((size_t)slot_of(x_first + (x0 + lane) * every) * G + h) * 2));
@@ -228,16 +231,16 @@ __device__ __forceinline__ void join_parts(const Parts &parts, int G, int c_firs
 #pragma unroll
                 for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                 const float old = jn.m[h], mn = fmaxf(old, mx);
-                const float wt = ml.x == -CUDART_INF_F ? 0.0f : exp2_approx(ml.x - mn);
-                float ls = ml.x == -CUDART_INF_F ? ml.y : ml.y * wt;   // a NaN of a share without a maximum stays
+                const float wt = exp2_approx((ml.x - mn) * scale[h]);
+                float ls = ml.y * wt;   // a NaN stays
 #pragma unroll
                 for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
                 jn.weight[h][lane] = wt;
                 __syncwarp();
                 if (lane == 0) {
-                    const float fo = old == -CUDART_INF_F ? 0.0f : exp2_approx(old - mn);
+                    const float fo = exp2_approx((old - mn) * scale[h]);
                     jn.f[h] = fo;
-                    jn.l[h] = old == -CUDART_INF_F ? jn.l[h] + ls : jn.l[h] * fo + ls;
+                    jn.l[h] = jn.l[h] * fo + ls;
                     jn.m[h] = mn;
                 }
             }
@@ -273,7 +276,7 @@ __device__ __forceinline__ void join_parts(const Parts &parts, int G, int c_firs
             if (e >= G * kD) continue;
             const int h = e / kD;
             if (final) {
-                done(e, acc[k], jn.m[h], jn.l[h]);
+                done(e, acc[k], jn.m[h], jn.l[h], scale[h]);
             } else {
                 const size_t to = (size_t)slot_of(x_first);
                 *reinterpret_cast<float4 *>(parts.o + to * G * kD + e) = acc[k];

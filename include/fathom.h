@@ -167,7 +167,7 @@ typedef struct {
 } fathom_pages;
 
 /* A paged KV cache of one layer held in 4 bits: 32 channels of a token share a
- * scale a (fp16), and a code c in 0 .. 15 stands for (c - 7.5) a / 8.  A page of
+ * scale a >= 0 (fp16), and a code c in 0 .. 15 stands for (c - 7.5) a / 8.  A page of
  * one KV head is page_tokens / 16 blocks of 16 tokens, one after the other, of
  * 18 D bytes each:
  *   codes of K [D / 32][16 tokens][16 bytes], channel 2 b of a group of 32 in the
@@ -176,8 +176,8 @@ typedef struct {
  *   scales of V, the same
  * and block j of (page, head) lies at byte
  *   page * page_stride + head * head_stride + 18 D j
- * of kv_pages.  Any 18 D bytes are a block (zeros: scale 0, values 0).  The page
- * table is that of fathom_pages. */
+ * of kv_pages; zeros are scales 0 and values 0.  The page table is that of
+ * fathom_pages. */
 typedef struct {
     int32_t seqs;         /* sequences, 1 .. 65535 */
     int32_t kv_heads;     /* KV heads per sequence; seqs * kv_heads <= 65535 */

@@ -18,9 +18,9 @@ of V.
   12 fp32 roundings.  - 7.5 sum(q) of a group is rounded once, 2^-24 7.5 32 max|q| a / 8, and
   the group's |k| are a / 16 at least and once 15 a / 16, 2.8 a together: 2^-21.5 Q.  So
   ds = 16 * 2^-24 S + 2^-20 Q.
-* The exponential's argument is one more fp32 fused operation on numbers of up to 1.45 * 2 S
-  + 14, and so is the maximum that it is relative to: 2^-23 (3 S + 14) / 1.4.  The
-  exponential itself and two rescalings: 3 * 2^-22.  So a weight's relative error is at most
+* The exponential's argument is an fp32 difference of scores, of up to 1.45 * 2 S in its
+  units, and a fused operation that adds 13: 2^-23 (3 S + 14) / 1.4.  The exponential itself
+  and two rescalings: 3 * 2^-22.  So a weight's relative error is at most
   r = 2 (ds + 2^-23 (2.2 S + 10)) + 3 * 2^-22 (the first factor for e^x - 1).
 * A weight times a scale in two fp16 pieces: 2^-21 of it, and 2^-24 where pieces are
   subnormal, the largest product being at least 2^13 a / 4 there: 2^-35 a per token in units

@@ -111,6 +111,25 @@ def test_large_queries_meet_small_keys():
     check_attend(out, lse, q, kv, table, [513, 70])
 
 
+@pytest.mark.parametrize("power", [100, 115, 118, 123])
+def test_huge_queries_choose_the_best_key(power):
+    """Scores of 2^100 and more: one token has all the weight.  Channels of q are +-2^power, so scores are 2^power
+    times sums of keys, whose differences are far above 2^-100."""
+    kv, table = cache(1, 2, 64, 16, 40, scale_k=2.0 ** -3)
+    q = rnd(2, 4, 64, seed=5).sign() * 2.0 ** power
+    K, V = N.unpack(kv, 64)
+    out, lse = attend(q, kv, table, [600], want_lse=True)
+    for u in range(2):
+        kk, vv = (x[table[0].long(), u].reshape(-1, 64)[:600] for x in (K, V))
+        x = q[u].double() @ kk.T
+        top = x.topk(2, 1)
+        assert bool((top.values[:, 0] - top.values[:, 1] > 2.0 ** (power - 20)).all())
+        # one weight of 1: its two pieces and the value, 2^-21
+        assert bool(((out[u].double() - vv[top.indices[:, 0]]).abs() <= 2.0 ** -20 * vv[top.indices[:, 0]].abs()).all())
+        if power < 115:
+            assert bool(((lse[u].double() - top.values[:, 0] / 8).abs() <= 2.0 ** -20 * x.abs().amax(1) / 8).all())
+
+
 def test_channels_of_very_different_sizes():
     q = 2 * rnd(4, 4, 128, seed=5)
     q[..., ::3] *= 2.0 ** -14
