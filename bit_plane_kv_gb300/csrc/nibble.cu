@@ -39,8 +39,8 @@ namespace {
 // registers per 8 tokens and group.
 //
 // Measured, 128 channels, 4 heads per unit: 32 sequences of up to 32k tokens, 8 KV heads,
-// 649 MB, 124 us, 5.2 TB/s (8 heads per unit 188 us; 64 channels 76); one of 131072 tokens
-// 39 us, one of 4096 10.3.  290 instructions per block: 62 % of the issue slots, 47 % of the
+// 649 MB, 124 us, 5.2 TB/s (8 heads per unit 183 us; 64 channels 76); one of 131072 tokens
+// 39 us, one of 4096 10.2.  290 instructions per block: 62 % of the issue slots, 47 % of the
 // logic pipe, and in the rest dependent instructions of 16 warps.
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
