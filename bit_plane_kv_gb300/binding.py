@@ -626,6 +626,8 @@ _ROW_TYPES = {torch.bfloat16: BF16, torch.float16: F16}
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_NO_CONTEXT = contextlib.nullcontext()
 
 
 def _on(stream, tensors):
@@ -634,16 +636,17 @@ def _on(stream, tensors):
     that stream, so that outputs allocated inside belong to the stream that writes them."""
     device = -1
     for t in tensors:
-        d = t.get_device() if t is not None else -1
-        if d != device and d >= 0:
-            if device >= 0:
-                raise ValueError(f"tensors on several devices: cuda:{device} and cuda:{d}")
-            device = d
+        if t is not None:
+            d = t.get_device()
+            if d != device and d >= 0:
+                if device >= 0:
+                    raise ValueError(f"tensors on several devices: cuda:{device} and cuda:{d}")
+                device = d
     if stream is None:
         if device < 0:
-            return contextlib.nullcontext(), _stream(None)
-        if device == torch.cuda.current_device():
-            return contextlib.nullcontext(), _raw_stream(device) if _raw_stream else _stream(None)
+            return _NO_CONTEXT, _stream(None)
+        if device == _current_device():
+            return _NO_CONTEXT, _raw_stream(device) if _raw_stream else _stream(None)
         with torch.cuda.device(device):
             return torch.cuda.device(device), _stream(None)
     if device >= 0 and stream.device_index != device:
@@ -961,9 +964,9 @@ def _check_new(k_new, v_new, start, cu_new, dtype, seqs, H, D):
     if T >> 31:
         _fit32(new_tokens=T)
     shape, stride = (T, H, D), k_new.stride()
-    if not _rows_ok(k_new, dtype, shape):
+    if not (k_new.dtype is dtype and k_new.shape == shape and stride[2] == 1 and k_new.is_cuda):
         _check_strided(k_new, "k_new", (dtype,), shape)
-    if not _rows_ok(v_new, dtype, shape):
+    if v_new is None or not (v_new.dtype is dtype and v_new.shape == shape and v_new.stride() == stride and v_new.is_cuda):
         _check_strided(v_new, "v_new", (dtype,), shape)
     if stride != v_new.stride() and any(a > 1 and x != y for a, x, y in zip((T, H), stride, v_new.stride())):
         raise ValueError("v_new: strides differ from k_new's")
@@ -1109,12 +1112,16 @@ def fathom_nibble_attn(pages: NibblePages, q, kv_pages, page_table, lens, worksp
         raise ValueError("q: expected [units][G][D]")
     G = q.shape[1]
     shape = (seqs * H, G, D)
-    for t, name, s in ((q, "q", shape), (out, "out", shape), (lse, "lse", shape[:2])):
-        if (t is not None or name == "q") and not _ok(t, torch.float32, s):
-            _check(t, name, (torch.float32,), s)
+    if not _ok(q, torch.float32, shape):
+        _check(q, "q", (torch.float32,), shape)
     if not _ok(lens, torch.int32, (seqs,)):
         _check(lens, "lens", (torch.int32,), (seqs,))
-    _check(workspace, "workspace", (torch.uint8,))
+    if workspace is None or not (workspace.dtype is torch.uint8 and workspace.is_cuda and workspace.is_contiguous()):
+        _check(workspace, "workspace", (torch.uint8,))
+    if out is not None and not _ok(out, torch.float32, shape):
+        _check(out, "out", (torch.float32,), shape)
+    if lse is not None and not _ok(lse, torch.float32, shape[:2]):
+        _check(lse, "lse", (torch.float32,), shape[:2])
     context, handle = _on(stream, (q, kv_pages, page_table, lens, workspace, out, lse))
     with context:
         if out is None:
