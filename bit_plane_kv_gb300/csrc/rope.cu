@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kBatch = 2;       // rows loaded together
-constexpr int kCtas = 6;        // per SM: 24 warps' loads in flight (4: 97 us, 8, with spilled registers: 129)
+constexpr int kCtas = 6;        // per SM: 24 warps' loads in flight (the prompts above: 5 CTAs 77 us, in 4 bits and back 108 instead of 103)
 constexpr int kReadBatch = 4;   // when read back
 
 struct AppendArgs {
