@@ -396,6 +396,23 @@ def test_codes_of_many_rotated_keys_are_exact(dt, table):
     assert torch.equal(V.transpose(1, 2).reshape(-1, H, D)[:T], N.held(v.double())[0])
 
 
+@pytest.mark.parametrize("D", [32, 96, 128])
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_codes_of_small_and_large_rows_are_exact(dt, D):
+    """Rows from far below fp16's smallest number to beyond its largest, where the ways of coding change."""
+    sizes = [2.0 ** e for e in (-27, -25, -24, -20, -15, -14, -13, -12, -11, 0, 13, 14, 15)] + ([2.0 ** 16, 2.0 ** 60] if dt == BF else [])
+    T, H = 40 * len(sizes), 2
+    size = torch.tensor(sizes, device="cuda").repeat_interleave(40)[:, None, None]
+    k, v = ((rnd(T, H, D, seed=i) * size).clamp(-6e4, 6e4).to(dt) if dt == FP else (rnd(T, H, D, seed=i) * size).to(dt) for i in (0, 1))
+    pages = -(-T // 16)
+    kv, table = B.alloc_nibble_pages(pages, H, 16, D), torch.arange(pages, dtype=torch.int32, device="cuda")[None].contiguous()
+    rope, pos = N.rope_table(T, D), torch.arange(T, device="cuda")
+    B.fathom_nibble_append(B.make_nibble_pages(kv, table, D), kv, table, k, v, i32([0]), i32([0, T]), rope=rope)
+    K, V = N.unpack(kv, D)
+    assert torch.equal(K.transpose(1, 2).reshape(-1, H, D)[:T], N.held(N.rotated(k, rope, pos, False))[0])
+    assert torch.equal(V.transpose(1, 2).reshape(-1, H, D)[:T], N.held(v.double())[0])
+
+
 @pytest.mark.parametrize("dt", [BF, FP])
 def test_values_on_borders_zeros_infinities_and_nan(dt):
     D = 64
