@@ -34,12 +34,17 @@ namespace {
 // K's scales multiply a group's partial sums (32 channels), V's the softmax weights:
 // (hi + lo) a in three fp16 operations for two tokens, the rounding error of hi a going to
 // the second piece; the weights are kept 2^13, the scales 2^k larger (k by the largest scale
-// so far), so that these errors stay clear of the subnormals.  The scores' layout (tokens by
-// heads) becomes the weights' operand (heads by tokens) by one 8 x 8 transposition in
-// registers per 8 tokens and group.
+// so far), so that these errors stay clear of the subnormals: off by 2^-22, or by 2^-35 of
+// the largest weight and scale.  That is little beside the sum as long as all scales of the unit
+// that the warp has seen lie within 2^9 of each other (2^-24.5 of it per token at most).  From where they do
+// not on, a small group or a light token of large values would cost the others their bits: products
+// are then taken in fp32, each block's brought to 2^13 .. 2^14 by their largest of a head and
+// group, and added to the sums in shared memory (32 x 32k tokens 128 -> 207 us, 8 heads per unit 197 -> 383).
+// The scores' layout (tokens by heads) becomes the weights' operand (heads by tokens) by one
+// 8 x 8 transposition in registers per 8 tokens and group.
 //
 // Measured, 128 channels, 4 heads per unit: 32 sequences of up to 32k tokens, 8 KV heads,
-// 649 MB, 124 us, 5.2 TB/s (8 heads per unit 183 us; 64 channels 76); one of 131072 tokens
+// 649 MB, 128 us, 5.1 TB/s (8 heads per unit 197 us; 64 channels 77); one of 131072 tokens
 // 39 us, one of 4096 10.2.  290 instructions per block: 62 % of the issue slots, 47 % of the
 // logic pipe, and in the rest dependent instructions of 16 warps.
 
@@ -140,6 +145,12 @@ __device__ __forceinline__ uint32_t max_h2(uint32_t x, uint32_t y) {
 }
 __device__ __forceinline__ uint32_t half_pair(float x) { return pack_half2(x, x); }
 
+// Both halves x < y.
+__device__ __forceinline__ bool h2_less(uint32_t x, uint32_t y) {
+    return __hblt2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y));
+}
+constexpr uint32_t kTop = 0x44004400u, kLow = 0x1fff1fffu;   // 4, and what is next below 2^-7, as pairs
+
 constexpr float kQueryPiece = 1.0f / 4096;   // what the second piece counts
 constexpr float kUp = 13.0f;                 // weights are 2^13 larger
 constexpr int kFlush = 16;   // blocks
@@ -159,6 +170,18 @@ __device__ __forceinline__ Codes split_codes(uint32_t x) {
 __device__ __forceinline__ Codes centred(const Codes &x) {
     return Codes{fma_h2(x.c0, 0x78007800u, 0xa380a380u), fma_h2(x.b0, 0x68006800u, 0xa3f8a3f8u),
                  fma_h2(x.c1, 0x78007800u, 0xa380a380u), fma_h2(x.b1, 0x68006800u, 0xa3f8a3f8u)};
+}
+
+// Two products' sums u and v times down, added to four channels of a head that count f times (add false: set).
+__device__ __forceinline__ void add_sums(float *at, const float (&u)[4], const float (&v)[4], float down, float f, bool add) {
+    float4 *to = reinterpret_cast<float4 *>(at);
+    float4 x = make_float4(u[0] + u[1], u[2] + u[3], v[0] + v[1], v[2] + v[3]);
+    x = make_float4(x.x * down, fmaf(x.x, -0.0625f, x.y) * down, x.z * down, fmaf(x.z, -0.0625f, x.w) * down);
+    if (add) {
+        const float4 y = *to;
+        x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
+    }
+    *to = x;
 }
 
 // floor(log2(x)) of a normal x > 0 (-127 of a smaller one), and 2^e for -126 <= e <= 127.
@@ -306,7 +329,8 @@ nibble_attn_kernel(const NibArgs a) {
     // weights' sum of this lane's tokens.  Differences of scores are taken before they are scaled: large ones keep
     // their last bits
     float m[kNB], kept[kNB], l[kNB], o[kNB][2 * kGroups][4];
-    uint32_t grow = 0, bound = 0;      // 2^k, and the scale above which k changes, as pairs
+    uint32_t grow = 0, least = 0;      // 2^k, and V's smallest scale so far, as pairs
+    bool wide = false;                 // scales too far apart for one 2^k
     bool in_smem = false;
     int steps = 0;                     // since the sums moved
     auto flush = [&]() {               // sums in shared memory: without 2^k
@@ -318,14 +342,7 @@ nibble_attn_kernel(const NibArgs a) {
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
                 float(&u)[4] = o[nb][2 * g], (&v)[4] = o[nb][2 * g + 1];
-                float4 *to = reinterpret_cast<float4 *>(&sm.o[warp][4 * nb + c][32 * g + 4 * r]);
-                float4 x = make_float4(u[0] + u[1], u[2] + u[3], v[0] + v[1], v[2] + v[3]);
-                x = make_float4(x.x * down, fmaf(x.x, -0.0625f, x.y) * down, x.z * down, fmaf(x.z, -0.0625f, x.w) * down);
-                if (in_smem) {
-                    const float4 y = *to;
-                    x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
-                }
-                *to = x;
+                add_sums(&sm.o[warp][4 * nb + c][32 * g + 4 * r], u, v, down, f, in_smem);
                 u[0] = u[1] = u[2] = u[3] = v[0] = v[1] = v[2] = v[3] = 0.0f;
             }
         }
@@ -393,7 +410,8 @@ nibble_attn_kernel(const NibArgs a) {
                     bias[nb][g] = fmaf(sm.sums[nb][g][2 * c + 1], kQueryPiece, sm.sums[nb][g][2 * c]) * (-7.5f / 16777216.0f);
                 }
             grow = 0x74007400u;    // 2^14
-            bound = 0x0c000c00u;   // 2^-12
+            least = 0x7bff7bffu;   // fp16's largest
+            wide = false;
             in_smem = false;
             steps = 0;
         }
@@ -445,7 +463,8 @@ nibble_attn_kernel(const NibArgs a) {
                         }
                     }
                 }
-                if (there != kAll || tok + kStep > n) {   // tokens that are not there: no weight, whatever their places hold
+                const bool tail = there != kAll || tok + kStep > n;
+                if (tail) {   // tokens that are not there: no weight, whatever their places hold
 #pragma unroll
                     for (int b = 0; b < kBlocks; ++b) {
                         const int left = there >> b & 1u ? n - tok - b * kNibTokens : 0;
@@ -456,14 +475,21 @@ nibble_attn_kernel(const NibArgs a) {
                         }
                         const uint32_t keep = (r < left ? 0xffffu : 0u) | (r + 8 < left ? 0xffff0000u : 0u);
 #pragma unroll
-                        for (int g = 0; g < kGroups; ++g) vs[b][g] &= keep;
+                        for (int g = 0; g < kGroups; ++g) {
+                            vs[b][g] &= keep;
+                            least = __vminu2(vs[b][g] | ~keep, least);
+                        }
                     }
                 }
                 uint32_t most = 0u;
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g) most = max_h2(most, vs[b][g]);
+                    for (int g = 0; g < kGroups; ++g) {
+                        most = max_h2(most, vs[b][g]);
+                        if (!tail && (g & 1)) least = __vimin3_u16x2(vs[b][g], vs[b][g - 1], least);
+                        if (!tail && g + 1 == kGroups && !(g & 1)) least = __vminu2(vs[b][g], least);
+                    }
                 float tops[kNB];
 #pragma unroll
                 for (int nb = 0; nb < kNB; ++nb) {
@@ -471,7 +497,7 @@ nibble_attn_kernel(const NibArgs a) {
 #pragma unroll
                     for (int b = 1; b < kBlocks; ++b) tops[nb] = fmaxf(tops[nb], fmaxf(s[b][nb][0], s[b][nb][1]));
                 }
-                bool raise = !__hbgt2(*reinterpret_cast<const __half2 *>(&bound), *reinterpret_cast<const __half2 *>(&most));
+                bool raise = !wide && !(h2_less(mul_h2(most, grow), kTop) && h2_less(kLow, mul_h2(least, grow)));
 #pragma unroll
                 for (int nb = 0; nb < kNB; ++nb) raise |= tops[nb] > m[nb];
                 if (__any_sync(0xffffffffu, raise)) {
@@ -479,12 +505,17 @@ nibble_attn_kernel(const NibArgs a) {
                     float top_scale = fmaxf(mh.x, mh.y), ratio = 1.0f;
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) top_scale = fmaxf(top_scale, __shfl_xor_sync(0xffffffffu, top_scale, d));
-                    if (top_scale >= halves(bound).x) {   // k brings the largest scale to 1 .. 2, and holds until 4
-                        const int k = top_scale < CUDART_INF_F ? min(max(-exponent(top_scale), -14), 14) : -14;
-                        const float now = power(k);
-                        ratio = now / halves(grow).x;
-                        grow = half_pair(now);
-                        bound = half_pair(fminf(4.0f / now, 65504.0f * 2));
+                    if (!wide) {
+                        const float2 lh = halves(__vminu2(least, __byte_perm(least, 0, 0x1032)));
+                        const float low = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(lh.x)));
+                        float now = halves(grow).x;
+                        if (top_scale * now >= 4.0f) {   // k brings the largest scale to 1 .. 2, and holds until 4
+                            const float old = now;
+                            now = power(top_scale < CUDART_INF_F ? min(max(-exponent(top_scale), -14), 14) : -14);
+                            ratio = now / old;
+                            grow = half_pair(now);
+                        }
+                        wide = !(low * now >= 1.0f / 128);   // k stays from here on
                     }
 #pragma unroll
                     for (int nb = 0; nb < kNB; ++nb) {
@@ -503,44 +534,86 @@ nibble_attn_kernel(const NibArgs a) {
                     }
                 }
                 // ---- weights times V: channels 4 r + (0, 1) and 4 r + (2, 3) of a group are two products' rows
+                if (!wide) {
 #pragma unroll
-                for (int b = 0; b < kBlocks; ++b) {
-                    uint32_t hi[kNB], lo[kNB];   // weights of tokens r (low half) and r + 8
+                    for (int b = 0; b < kBlocks; ++b) {
+                        uint32_t hi[kNB], lo[kNB];   // weights of tokens r (low half) and r + 8
 #pragma unroll
-                    for (int nb = 0; nb < kNB; ++nb) {
-                        const float w0 = exp2_approx(fmaf(s[b][nb][0] - m[nb], unscale[nb], kUp));
-                        const float w1 = exp2_approx(fmaf(s[b][nb][1] - m[nb], unscale[nb], kUp));
-                        l[nb] += w0 + w1;
-                        hi[nb] = pack_half2(w0, w1);
-                        const float2 h = halves(hi[nb]);
-                        lo[nb] = pack_half2(w0 - h.x, w1 - h.y);
-                    }
+                        for (int nb = 0; nb < kNB; ++nb) {
+                            const float w0 = exp2_approx(fmaf(s[b][nb][0] - m[nb], unscale[nb], kUp));
+                            const float w1 = exp2_approx(fmaf(s[b][nb][1] - m[nb], unscale[nb], kUp));
+                            l[nb] += w0 + w1;
+                            hi[nb] = pack_half2(w0, w1);
+                            const float2 h = halves(hi[nb]);
+                            lo[nb] = pack_half2(w0 - h.x, w1 - h.y);
+                        }
 #pragma unroll
-                    for (int g0 = 0; g0 < kGroups; g0 += 2) {
-                        uint32_t x[4];
-                        if (g0 + 1 < kGroups) load_codes<true, true>(x, codes + b * kBlock + nib_half(kD) + g0 * 256);
-                        else load_codes<true, false>(x, codes + b * kBlock + nib_half(kD) + g0 * 256);
+                        for (int g0 = 0; g0 < kGroups; g0 += 2) {
+                            uint32_t x[4];
+                            if (g0 + 1 < kGroups) load_codes<true, true>(x, codes + b * kBlock + nib_half(kD) + g0 * 256);
+                            else load_codes<true, false>(x, codes + b * kBlock + nib_half(kD) + g0 * 256);
 #pragma unroll
-                        for (int g = g0; g < g0 + 2 && g < kGroups; ++g) {
-                            const uint32_t f = mul_h2(vs[b][g], grow);
-                            uint32_t p[kNB][2];
+                            for (int g = g0; g < g0 + 2 && g < kGroups; ++g) {
+                                const uint32_t f = mul_h2(vs[b][g], grow);
+                                uint32_t p[kNB][2];
 #pragma unroll
-                            for (int nb = 0; nb < kNB; ++nb) {
-                                const uint32_t h = mul_h2(hi[nb], f);
-                                const uint32_t e = fma_h2(lo[nb], f, fms_h2(hi[nb], f, h));
-                                p[nb][0] = transpose8(__byte_perm(h, e, 0x5410));
-                                p[nb][1] = transpose8(__byte_perm(h, e, 0x7632));
-                            }
-                            const Codes u = centred(split_codes(x[2 * (g - g0)])), v = centred(split_codes(x[2 * (g - g0) + 1]));
+                                for (int nb = 0; nb < kNB; ++nb) {
+                                    const uint32_t h = mul_h2(hi[nb], f);
+                                    const uint32_t e = fma_h2(lo[nb], f, fms_h2(hi[nb], f, h));
+                                    p[nb][0] = transpose8(__byte_perm(h, e, 0x5410));
+                                    p[nb][1] = transpose8(__byte_perm(h, e, 0x7632));
+                                }
+                                const Codes u = centred(split_codes(x[2 * (g - g0)])), v = centred(split_codes(x[2 * (g - g0) + 1]));
 #pragma unroll
-                            for (int nb = 0; nb < kNB; ++nb) {
-                                mma_f16(o[nb][2 * g], u.c0, u.b0, v.c0, v.b0, p[nb][0], p[nb][1], o[nb][2 * g]);
-                                mma_f16(o[nb][2 * g + 1], u.c1, u.b1, v.c1, v.b1, p[nb][0], p[nb][1], o[nb][2 * g + 1]);
+                                for (int nb = 0; nb < kNB; ++nb) {
+                                    mma_f16(o[nb][2 * g], u.c0, u.b0, v.c0, v.b0, p[nb][0], p[nb][1], o[nb][2 * g]);
+                                    mma_f16(o[nb][2 * g + 1], u.c1, u.b1, v.c1, v.b1, p[nb][0], p[nb][1], o[nb][2 * g + 1]);
+                                }
                             }
                         }
                     }
                 }
-                if (++steps == kFlush / kBlocks) flush();
+                if (wide || ++steps == kFlush / kBlocks) flush();
+                if (wide) {   // block by block to the sums in shared memory
+#pragma unroll
+                    for (int b = 0; b < kBlocks; ++b) {
+                        const unsigned char *half = blk + b * kBlock + nib_half(kD);
+                        float w[kNB][2];
+#pragma unroll
+                        for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                w[nb][i] = exp2_approx(fmaf(s[b][nb][i] - m[nb], unscale[nb], kUp));
+                                l[nb] += w[nb][i];
+                            }
+#pragma unroll 1
+                        for (int g = 0; g < kGroups; ++g) {
+                            uint32_t x[4];
+                            load_codes<true, false>(x, codes + b * kBlock + nib_half(kD) + g * 256);
+                            const Codes u = centred(split_codes(x[0])), v = centred(split_codes(x[1]));
+                            const float2 f = halves(*reinterpret_cast<const uint32_t *>(half + nib_scales(kD) + 4 * (kGroups * r + g)));
+#pragma unroll
+                            for (int nb = 0; nb < kNB; ++nb) {
+                                const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                float p0 = s[b][nb][0] == -CUDART_INF_F ? 0.0f : w[nb][0] * f.x;   // not there: any scale
+                                float p1 = s[b][nb][1] == -CUDART_INF_F ? 0.0f : w[nb][1] * f.y, top = fmaxf(p0, p1);
+#pragma unroll
+                                for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                                const int up = min(13 - exponent(top), 110);
+                                p0 *= power(up);
+                                p1 *= power(up);
+                                const uint32_t h = pack_half2(p0, p1);
+                                const float2 back = halves(h);
+                                const uint32_t e = pack_half2(p0 - back.x, p1 - back.y);
+                                const uint32_t q0 = transpose8(__byte_perm(h, e, 0x5410)), q1 = transpose8(__byte_perm(h, e, 0x7632));
+                                float t[4], z[4];
+                                mma_f16(t, u.c0, u.b0, v.c0, v.b0, q0, q1, none);
+                                mma_f16(z, u.c1, u.b1, v.c1, v.b1, q0, q1, none);
+                                add_sums(&sm.o[warp][4 * nb + c][32 * g + 4 * r], t, z, power(-up), 1.0f, true);
+                            }
+                        }
+                    }
+                }
                 __syncwarp();   // the stage is read before its next copy starts
             }
             st = st + 1 == kStages ? 0 : st + 1;

@@ -1,0 +1,121 @@
+"""Decode attention over the 4-bit cache where channel groups, tokens and queries differ in size by
+many powers of two, on the GPU against 64 bits.
+
+Bounds as derived in nibble_cases, with two terms of their own:
+* Rows of V.  A weight times a scale is held in two fp16 pieces.  Where all scales that a warp has seen in the
+  unit lie within a factor of 2^9 of each other, they are scaled to 2^-7 .. 4: the second piece of a weight is off by
+  2^-25 times the scale, the product's pieces by 2^-24 together, so 2^-22.5 per token at most, beside the
+  largest weight's 2^13 times a scale of 2^-7 and more times a value of a 16th of it and more, 2^2: 2^-24.5 of the
+  sum A of w |v| in the same channel per token of the warp, of which there are n / 4 + 32 at most.
+  Elsewhere products are scaled block by block by their largest, 2^-38 of it per token, 2^-30 A in all.
+  So (n / 4 + 32) 2^-24 A, and nothing that depends on the largest scale.
+* Queries.  A channel is held to 2^-22 of its group's largest, and of the row's largest to 2^-45:
+  Q = sum over groups of max |q| sum |k|, and 2^-44 of max |q| sum |k| over the row."""
+import math
+
+import pytest
+import torch
+
+from bit_plane_kv_gb300 import binding as B
+
+import nibble_cases as N
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def gen(seed=0):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def rnd(*shape, seed=0):
+    return torch.randn(*shape, generator=gen(seed), device="cuda").double()
+
+
+def attend(q, k, v, lens):
+    """(out, lse, what the cache holds of K, of V) with pages of 16 tokens; k, v [sequences][heads][tokens][D]."""
+    S, H, n, D = k.shape
+    per = n // 16
+    rows = [x.reshape(S, H, per, 16, D).transpose(1, 2).reshape(S * per, H, 16, D) for x in (k, v)]
+    kv, table = N.pack(*rows), torch.arange(S * per, dtype=torch.int32, device="cuda").reshape(S, per)
+    pages = B.make_nibble_pages(kv, table, D)
+    out, lse = B.fathom_nibble_attn(pages, q, kv, table, i32(lens), B.alloc_nibble_workspace(pages, G=q.shape[1]), want_lse=True)
+    held = [x.reshape(S, per, H, 16, D).transpose(1, 2).reshape(S, H, n, D) for x in N.unpack(kv, D)]
+    return out, lse, *held
+
+
+def check(out, lse, q, K, V, lens):
+    U, G, D = q.shape
+    H = K.shape[1]
+    for u in range(U):
+        s, h = divmod(u, H)
+        n = lens[s]
+        kk, vv, qq = K[s, h, :n], V[s, h, :n], q[u].double()
+        x = qq @ kk.T / math.sqrt(D)
+        S = (qq.abs() @ kk.abs().T / math.sqrt(D)).amax(1)
+        most, size = qq.abs().reshape(G, -1, 32).amax(2), kk.abs().reshape(n, -1, 32).sum(2)
+        Q = (most @ size.T).amax(1) / math.sqrt(D) + 2.0 ** -24 * most.amax(1) * size.sum(1).amax() / math.sqrt(D)
+        z = torch.logsumexp(x, 1)
+        A = torch.exp(x - z[:, None]) @ vv.abs()
+        ds = 16 * 2.0 ** -24 * S + 2.0 ** -20 * Q
+        r = 2 * (ds + 2.0 ** -23 * (2.2 * S + 10)) + 3 * 2.0 ** -22
+        k = (n / 64 + 128) * 2.0 ** -23
+        far = (out[u].double() - torch.exp(x - z[:, None]) @ vv).abs()
+        tol = (2 * r + 2.0 ** -21 + 2 * k + (n / 4 + 32) * 2.0 ** -24)[:, None] * A
+        assert bool((r < 0.1).all())                              # the first order is enough
+        assert torch.isfinite(out[u]).all()
+        assert bool((far <= tol).all()), f"unit {u}: worst {(far / tol.clamp(min=1e-300)).max().item():.3g} of the tolerance"
+        assert bool(((lse[u].double() - z).abs() <= r + k + ds + 2.0 ** -22 * z.abs()).all())
+
+
+# ------------------------------------------------------------------ values
+@pytest.mark.parametrize("D,G", [(128, 4), (128, 8), (64, 3), (64, 7), (96, 5), (96, 1), (32, 4), (32, 8)])
+@pytest.mark.parametrize("kind", ["groups", "groups, the other way", "first tokens", "last tokens", "tokens and groups"])
+def test_values_of_very_different_sizes(kind, D, G):
+    """A group or a token of large values takes nothing from the others."""
+    S, H, n = 2, 2, 1504
+    k, v = 0.3 * rnd(S, H, n, D), rnd(S, H, n, D, seed=1)
+    g = torch.arange(D, device="cuda") // 32
+    if kind.startswith("groups"):
+        v *= 2.0 ** (8 - 7 * (g if kind == "groups" else D // 32 - 1 - g))
+    elif kind == "tokens and groups":
+        v *= 2.0 ** torch.randint(-13, 14, (S, H, n, D // 32, 1), generator=gen(3), device="cuda").double().expand(-1, -1, -1, -1, 32).reshape(S, H, n, D)
+    else:
+        v[:, :, :70 if kind == "first tokens" else None] *= 2.0 ** 12
+        if kind == "last tokens":
+            v[:, :, :-70] *= 2.0 ** -25
+        else:
+            v[:, :, 70:] *= 2.0 ** -10
+    q = rnd(S * H, G, D, seed=5).float()
+    lens = [n - 5, 333]
+    out, lse, K, V = attend(q, k, v, lens)
+    check(out, lse, q, K, V, lens)
+
+
+@pytest.mark.parametrize("D,G", [(128, 4), (128, 8), (64, 4), (96, 6), (32, 2)])
+@pytest.mark.parametrize("where", ["first", "middle", "last", "every fifth"])
+def test_large_values_of_negligible_weight(where, D, G):
+    """Tokens of values 2^22 times the others' whose softmax weights are below 2^-50."""
+    S, H, n = 2, 1, 1104
+    sign = rnd(S, H, 1, D, seed=2).sign()
+    k, v = sign + 0.2 * rnd(S, H, n, D), 2.0 ** -11 * rnd(S, H, n, D, seed=1)
+    big = {"first": slice(0, 40), "middle": slice(500, 520), "last": slice(1060, 1104), "every fifth": slice(2, None, 5)}[where]
+    k[:, :, big] *= -1
+    v[:, :, big] *= 2.0 ** 22
+    q = (sign.reshape(S, 1, D) * (25 / math.sqrt(D)) + 0.1 * rnd(S, G, D, seed=5)).float()
+    lens = [n, 1090]
+    out, lse, K, V = attend(q, k, v, lens)
+    check(out, lse, q, K, V, lens)
+
+
+def test_large_and_small_values_over_many_shares():
+    """The same where CTAs share a unit."""
+    D, n = 128, 24000
+    size = 2.0 ** torch.randint(-12, 12, (1, 1, n // 16, 1), generator=gen(3), device="cuda").double().repeat_interleave(16, 2)
+    k, v = rnd(1, 1, n, D), rnd(1, 1, n, D, seed=1) * size * 2.0 ** (3 * (torch.arange(D, device="cuda") // 32) - 6)
+    q = rnd(1, 4, D, seed=5).float()
+    out, lse, K, V = attend(q, k, v, [n])
+    check(out, lse, q, K, V, [n])
