@@ -638,8 +638,8 @@ nibble_attn_kernel(const NibArgs a) {
         bool second = false, before = false;   // this CTA's share, and the first CTA's, is its second
         if (c_first < 0) {
             const long long W = sm.z.W, NC = sm.z.NC, unit_w0 = sm.z.w0 + i - tok / kTile;   // index of the unit's first tile
-            c_first = (int)div_small((unit_w0 + 1) * NC - 1, W);
-            c_last = (int)div_small((unit_w0 + tiles) * NC - 1, W);
+            c_first = share_owner(unit_w0, W, NC);
+            c_last = share_owner(unit_w0 + tiles - 1, W, NC);
             second = sm.z.w0 < unit_w0;
             before = share_start(c_first, W, NC) < unit_w0;
         }

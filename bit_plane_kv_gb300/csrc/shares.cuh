@@ -1,23 +1,11 @@
 // shares.cuh -- equal shares of work over sequences of unequal lengths, and the join of
 // softmax states that several CTAs hold of one unit.
-//
-// The tiles of all units, in the order (sequence, head, tile), are dealt out to the CTAs
-// in contiguous shares that differ by one tile at most: CTA c of NC takes tiles c W / NC
-// to (c + 1) W / NC of W.  Where units are few (eight CTAs each or more), every unit gets
-// CTAs of its own instead, by its tiles: no CTA then ends one unit and begins another, or
-// joins two (seven sequences of up to 9001 tokens, 21 units: 21 -> 14 us), and the longest
-// share grows by an eighth at most and by a tile.
 #pragma once
 
 #include "blackwell.cuh"
+#include "share_rule.cuh"
 
 namespace fathom {
-
-// Division of numbers that mostly fit 32 bits.
-__device__ __forceinline__ long long div_small(long long x, long long y) {
-    return (unsigned long long)(x | y) >> 32 ? x / y : (long long)((unsigned)x / (unsigned)y);
-}
-__device__ __forceinline__ long long share_start(long long c, long long W, long long NC) { return div_small(c * W, NC); }
 
 struct Share {
     long long W, NC, w0;      // all tiles, CTAs that have some, this CTA's first tile
@@ -66,16 +54,16 @@ __device__ __forceinline__ Share find_share(int seqs, int heads, Tiles tiles_of,
         }
         int upto = scan(sum);
         const int all = __shfl_sync(0xffffffffu, upto, 31);
-        const bool own = seqs * heads * 8 <= grid;
+        const bool own = share_own(seqs * heads, grid);
         int c[4];   // what is searched: tiles, or CTAs
 #pragma unroll
         for (int e = 0; e < 4; ++e) c[e] = t[e];
-        if (own) {   // its part of all CTAs but one per unit, which pays for the least of one and for roundings
-            const float part = (float)(grid - seqs * heads) / ((float)all * (float)heads);
+        if (own) {
+            const int limit = share_limit(all, heads, seqs * heads, grid);
             sum = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                c[e] = t[e] ? min(t[e], max(1, (int)((float)t[e] * part))) : 0;
+                c[e] = share_parts(t[e], limit);
                 sum += c[e];
             }
             upto = scan(sum);
@@ -102,11 +90,11 @@ __device__ __forceinline__ Share find_share(int seqs, int heads, Tiles tiles_of,
         if (own) {
             z.count = 0;
             if (!hit) return z;
-            const unsigned i = (unsigned)(at - before), j = i % mine, first = j * (unsigned)tiles / mine;   // below 2^32: 608 2^21
-            z.head = i / mine;
-            z.tile = first;
-            z.count = (j + 1) * (unsigned)tiles / mine - first;
-            z.own_first = cta - j;
+            const OwnShare o = share_of((unsigned)(at - before), mine, tiles);
+            z.head = o.head;
+            z.tile = o.first;
+            z.count = o.count;
+            z.own_first = cta - o.j;
             z.own_last = z.own_first + mine - 1;
         } else if (z.count) {
             begin(before, tiles);
