@@ -73,13 +73,13 @@ struct NibArgs {
 struct Todo {   // a unit to be joined: its CTAs, whether the first has a share of an earlier one, its scores' factors
     int unit, first, last;
     bool before;
-    float unscale[FATHOM_MAX_G];
+    float unscale[FATHOM_MAX_G], beyond[FATHOM_MAX_G];
 };
 template <int kD, int kNB>
 struct NibSmem {
     alignas(128) unsigned char ring[kWarps][nib_stages(kD, kNB)][nib_blocks(kD)][nib_block_bytes(kD)];
     float o[kWarps][4 * kNB][kD + 8];   // rows 8 words apart: four heads' stores meet in no bank
-    float m[kWarps][FATHOM_MAX_G], l[kWarps][FATHOM_MAX_G], unscale[FATHOM_MAX_G];
+    float m[kWarps][FATHOM_MAX_G], l[kWarps][FATHOM_MAX_G], unscale[FATHOM_MAX_G], beyond[FATHOM_MAX_G];
     Share z;
     Todo todo[2];
     int next_seq[kWarps], next_head[kWarps];   // where a warp's copies have got to
@@ -206,11 +206,13 @@ __device__ __forceinline__ void load_scales(uint32_t (&s)[kGroups], const unsign
 // Elements e .. e + 3 of a unit's result from its joined sums: 2^9 of the codes, a / 8.
 template <int kD>
 struct Finish {
-    float *out, *lse;   // of the unit
+    float *out, *lse;      // of the unit
+    const float *beyond;   // what its heads' scores count beyond unscale
     __device__ __forceinline__ void operator()(int e, float4 o, float m, float l, float unscale) const {
-        const float inv = l > 0.0f ? 64.0f / l : 0.0f;
+        const float inv = l > 0.0f ? 64.0f / l : 0.0f, ln2 = 0.6931471805599453f;
         *reinterpret_cast<float4 *>(out + e) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        if (lse && e % kD == 0) lse[e / kD] = l == 0.0f ? -CUDART_INF_F : (fmaf(m, unscale, log2f(l)) - kUp) * 0.6931471805599453f;
+        if (lse && e % kD == 0)   // in natural units from the start: scores up to fp32's largest
+            lse[e / kD] = l == 0.0f ? -CUDART_INF_F : fmaf(m * (unscale * ln2), beyond[e / kD], (log2f(l) - kUp) * ln2);
     }
 };
 
@@ -373,8 +375,7 @@ nibble_attn_kernel(const NibArgs a) {
                 big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
                 big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
                 // a power of two that brings the largest to 2^10 .. 2^11, with room for a 16th of its neighbour
-                big *= 1.0625f;
-                const int up = big > 0.0f && big < CUDART_INF_F ? min(max(10 - exponent(big), -117), 126) : 0;
+                const int up = big > 0.0f && big < CUDART_INF_F ? min(9 - exponent(0.53125f * big), 126) : 0;
                 const float scale = power(up);
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
@@ -393,8 +394,10 @@ nibble_attn_kernel(const NibArgs a) {
                     sm.pieces[nb][g][lane] = make_uint4(pack_half2(piece[0], piece[4]), pack_half2(piece[1] * 0.0625f, piece[5] * 0.0625f),
                                                         pack_half2(piece[2], piece[6]), pack_half2(piece[3] * 0.0625f, piece[7] * 0.0625f));
                 }
-                // a / 8 of the scales, 2^-24 of the codes; scores that need more than fp32's range are far apart anyway
-                unscale[nb] = __shfl_sync(0xffffffffu, up < -105 ? 3.0e38f : to_log2 * power(21 - up), 8 * c);
+                // a / 8 of the scales, 2^-24 of the codes.  Up to 2^126, the rest in the log-sum-exp alone: scores that
+                // differ at all are further apart than any weight shows
+                unscale[nb] = __shfl_sync(0xffffffffu, to_log2 * power(min(21 - up, 126)), 8 * c);
+                if (warp == 0 && !(lane & 7)) sm.beyond[4 * nb + (lane >> 3)] = power(max(21 - up, 126) - 126);
                 m[nb] = kept[nb] = kNoScore;
                 l[nb] = 0.0f;
 #pragma unroll
@@ -644,7 +647,7 @@ nibble_attn_kernel(const NibArgs a) {
             before = share_start(c_first, W, NC) < unit_w0;
         }
         const bool whole = c_first == c_last;
-        const Finish<kD> finish{a.out + (size_t)unit * G * kD, a.lse ? a.lse + (size_t)unit * G : nullptr};
+        const Finish<kD> finish{a.out + (size_t)unit * G * kD, a.lse ? a.lse + (size_t)unit * G : nullptr, sm.beyond};
         const size_t slot = 2 * (size_t)blockIdx.x + (second ? 1 : 0);
         for (int e = 4 * tid; e < G * kD; e += 4 * kThreads) {
             const int h = e / kD, d = e % kD;
@@ -673,7 +676,10 @@ nibble_attn_kernel(const NibArgs a) {
                 sm.todo[joins].last = c_last;
                 sm.todo[joins].before = before;
             }
-            if (tid < G) sm.todo[joins].unscale[tid] = sm.unscale[tid];
+            if (tid < G) {
+                sm.todo[joins].unscale[tid] = sm.unscale[tid];
+                sm.todo[joins].beyond[tid] = sm.beyond[tid];
+            }
             ++joins;
         }
         next_unit(seq, head, n);
@@ -685,7 +691,7 @@ nibble_attn_kernel(const NibArgs a) {
 #pragma unroll 1
     for (int k = 0; k < joins; ++k) {
         const Todo &t = sm.todo[k];
-        const Finish<kD> finish{a.out + (size_t)t.unit * G * kD, a.lse ? a.lse + (size_t)t.unit * G : nullptr};
+        const Finish<kD> finish{a.out + (size_t)t.unit * G * kD, a.lse ? a.lse + (size_t)t.unit * G : nullptr, t.beyond};
         join_parts<kWarps, kD, 4 * kNB>(a.parts, G, t.first, t.last, t.before, t.unscale, sm.join, finish);
         __syncthreads();
     }

@@ -119,3 +119,56 @@ def test_large_and_small_values_over_many_shares():
     q = rnd(1, 4, D, seed=5).float()
     out, lse, K, V = attend(q, k, v, [n])
     check(out, lse, q, K, V, [n])
+
+
+# ------------------------------------------------------------------ queries
+LARGEST = torch.finfo(torch.float32).max
+
+
+@pytest.mark.parametrize("D,G,n", [(64, 4, 608), (128, 8, 608), (32, 1, 20000)])
+@pytest.mark.parametrize("size", [2.0 ** p for p in (100, 105, 112, 114, 115, 116, 117, 118, 122, 126, 127)] + [LARGEST])
+def test_scores_up_to_the_largest_numbers(size, D, G, n):
+    """Queries of up to fp32's largest number: one token has all the weight, and the log-sum-exp is its score.
+    Channels of q are +-size, so the scores, size times sums of keys, are far apart."""
+    k, v = 2.0 ** -13 * rnd(1, 2, n, D), rnd(1, 2, n, D, seed=1)
+    q = (rnd(2, G, D, seed=5).sign() * size).float()
+    out, lse, K, V = attend(q, k, v, [n])
+    for u in range(2):
+        kk, vv = K[0, u], V[0, u]
+        x = q[u].double() @ kk.T
+        top = x.topk(2, 1)
+        assert bool((top.values[:, 0] - top.values[:, 1] > size * 2.0 ** -24).all())
+        # one weight of 1: its two pieces and the value, 2^-21
+        assert bool(((out[u].double() - vv[top.indices[:, 0]]).abs() <= 2.0 ** -20 * vv[top.indices[:, 0]].abs()).all())
+        # the score's roundings, ds above with Q <= S, and fewer than 16 of the factor's
+        want, S = top.values[:, 0] / math.sqrt(D), (q[u].double().abs() @ kk.abs().T).amax(1) / math.sqrt(D)
+        assert bool((want < LARGEST).all())
+        assert bool(((lse[u].double() - want).abs() <= 2.0 ** -18 * S).all()), f"{lse[u]} for {want}"
+
+
+@pytest.mark.parametrize("n", [16, 30000])
+@pytest.mark.parametrize("score", [1e37, 1e38, 2.3e38, 2.5e38, 3.3e38])
+def test_a_log_sum_exp_next_to_the_largest_number(score, n):
+    """In powers of two the last two lie beyond it."""
+    D, G = 64, 4
+    sign = rnd(1, 1, 1, D, seed=2).sign()
+    k, v = torch.zeros(1, 1, n, D, device="cuda").double(), rnd(1, 1, n, D, seed=1)
+    k[:, :, n // 3] = sign
+    q = (sign.reshape(1, 1, D) * (score / math.sqrt(D) / (15 / 16))).float().repeat(1, G, 1)
+    q[:, 1] *= -1                                               # the others' score, 0, is the largest
+    out, lse, K, V = attend(q, k, v, [n])
+    x = q[0].double() @ K[0, 0].T / math.sqrt(D)
+    want = torch.logsumexp(x, 1)
+    assert bool((want < LARGEST).all()) and torch.isfinite(lse).all()
+    assert bool(((lse[0].double() - want).abs() <= 2.0 ** -18 * x.abs().amax(1)).all())
+    assert bool(((out[0, 0].double() - V[0, 0, n // 3]).abs() <= 2.0 ** -20 * V[0, 0, n // 3].abs()).all())
+    assert bool(((lse[0, 1] - math.log(n - 1)).abs() <= 2.0 ** -12)) and torch.isfinite(out).all()
+
+
+def test_a_log_sum_exp_beyond_the_largest_number_is_infinite():
+    D = 64
+    k, v = torch.ones(1, 1, 32, D, device="cuda").double(), rnd(1, 1, 32, D, seed=1)
+    q = torch.full((1, 2, D), LARGEST, device="cuda")
+    q[0, 1] = -q[0, 1]
+    out, lse, K, V = attend(q, k, v, [32])
+    assert lse[0, 0] == math.inf and lse[0, 1] == -math.inf and torch.isfinite(out).all()
