@@ -16,8 +16,9 @@ namespace {
 //
 // Products run on the tensor cores, the fp32 operands in two pieces, hi + lo: a 16 x 8
 // operand holds a head's values in two columns, so four heads fill one instruction.
-// A query's pieces are whole numbers of 12 bits (to 2^-22 of its largest channel), so that
-// the sums over a group of channels are exact whatever the tensor cores cut off; a weight's
+// A query's pieces are whole numbers of 12 bits (to 2^-22 of its group's largest channel, as
+// long as that is not below 2^-23 of the row's), so that the sums over a group of 32 channels
+// are exact whatever the tensor cores cut off; a weight's
 // are fp16 (22 bits, and down to 2^-38 of the largest).
 //
 // Codes become fp16 in one operation: four bits left in the low bits of a 16-bit half are
@@ -376,11 +377,17 @@ nibble_attn_kernel(const NibArgs a) {
                 big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
                 // a power of two that brings the largest to 2^10 .. 2^11, with room for a 16th of its neighbour
                 const int up = big > 0.0f && big < CUDART_INF_F ? min(9 - exponent(0.53125f * big), 126) : 0;
-                const float scale = power(up);
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     if ((nb * kGroups + g) % kWarps != warp) continue;   // the warps share the work
-                    float piece[8], sum = 0.0f;
+                    float piece[8], sum = 0.0f, part = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) part = fmaxf(part, fabsf(x[g][e]));
+                    part = fmaxf(part, __shfl_xor_sync(0xffffffffu, part, 1));
+                    part = fmaxf(part, __shfl_xor_sync(0xffffffffu, part, 2));
+                    // a group of smaller channels counts 2^-more, from 2^4 down to where fp16 still holds its 16ths
+                    const int more = part > 0.0f && part < CUDART_INF_F ? min(max(9 - exponent(0.53125f * part) - up, 0), min(24, 127 - up)) : 0;
+                    const float scale = power(up + more), count = power(4 - more);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float y = e & 1 ? x[g][e] * scale : fmaf(x[g][e + 1] * scale, -0.0625f, x[g][e] * scale), hi = rintf(y);
@@ -389,15 +396,17 @@ nibble_attn_kernel(const NibArgs a) {
                     }
                     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    if (c == 0) sm.sums[nb][g][r] = sum;
+                    if (c == 0) sm.sums[nb][g][r] = sum * count;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) piece[e] *= e & 1 ? 0.0625f * count : count;
                     // channels 8 c + 2 k and 4 on, and their neighbours, k = 0, 1
-                    sm.pieces[nb][g][lane] = make_uint4(pack_half2(piece[0], piece[4]), pack_half2(piece[1] * 0.0625f, piece[5] * 0.0625f),
-                                                        pack_half2(piece[2], piece[6]), pack_half2(piece[3] * 0.0625f, piece[7] * 0.0625f));
+                    sm.pieces[nb][g][lane] = make_uint4(pack_half2(piece[0], piece[4]), pack_half2(piece[1], piece[5]),
+                                                        pack_half2(piece[2], piece[6]), pack_half2(piece[3], piece[7]));
                 }
-                // a / 8 of the scales, 2^-24 of the codes.  Up to 2^126, the rest in the log-sum-exp alone: scores that
+                // a / 8 of the scales, 2^-24 of the codes, 2^4 of the pieces.  Up to 2^126, the rest in the log-sum-exp alone: scores that
                 // differ at all are further apart than any weight shows
-                unscale[nb] = __shfl_sync(0xffffffffu, to_log2 * power(min(21 - up, 126)), 8 * c);
-                if (warp == 0 && !(lane & 7)) sm.beyond[4 * nb + (lane >> 3)] = power(max(21 - up, 126) - 126);
+                unscale[nb] = __shfl_sync(0xffffffffu, to_log2 * power(min(17 - up, 126)), 8 * c);
+                if (warp == 0 && !(lane & 7)) sm.beyond[4 * nb + (lane >> 3)] = power(max(17 - up, 126) - 126);
                 m[nb] = kept[nb] = kNoScore;
                 l[nb] = 0.0f;
 #pragma unroll

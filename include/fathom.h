@@ -649,8 +649,10 @@ int fathom_nibble_read(const fathom_nibble_pages *pages, const void *kv_pages, c
                        int32_t out_dtype, int64_t out_token, int64_t out_head, void *stream);
 
 /* Decode attention of one new token per sequence over a 4-bit cache: fathom_paged_attn's
- * sum over the values that the codes stand for, nothing rounded to fewer than 22 bits on
- * the way.  lse_opt: log sum_i exp(q_h . k_i / sqrt(D)) (-inf when there is no token), with
+ * sum over the values that the codes stand for.  A query's channel is held to 2^-22 of the
+ * largest one in its group of 32, or to 2^-45 of the row's largest where that is more; a softmax
+ * weight times a value to 2^-21 of it, or to 2^-24 of the channel's sum of |weight value|
+ * where that is more; sums are fp32.  lse_opt: log sum_i exp(q_h . k_i / sqrt(D)) (-inf when there is no token), with
  * which a caller joins the result with attention over other rows (say, recent tokens kept
  * in 16 bits).  No atomics on values: the same inputs give the same bits.
  *   G query heads per KV head, 1 .. 8

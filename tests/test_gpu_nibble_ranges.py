@@ -122,6 +122,31 @@ def test_large_and_small_values_over_many_shares():
 
 
 # ------------------------------------------------------------------ queries
+@pytest.mark.parametrize("D,G", [(128, 4), (128, 7), (64, 8), (64, 1), (96, 3)])
+@pytest.mark.parametrize("bits", [-27, -24, -20, -12, -5, 5, 12, 20, 24, 27])
+def test_large_channels_of_a_query_over_small_ones_of_the_keys(bits, D, G):
+    """Groups whose queries differ by up to 2^27 and whose keys by the inverse of it, so that all count alike."""
+    S, H, n = 2, 2, 1104
+    g = torch.arange(D, device="cuda").double().div(32, rounding_mode="floor") / (D // 32 - 1)
+    k, v = rnd(S, H, n, D) * 2.0 ** (bits * (g - 0.5)), rnd(S, H, n, D, seed=1)
+    q = (rnd(S * H, G, D, seed=5) * 2.0 ** (-bits * (g - 0.5))).float()
+    lens = [n, 75]
+    out, lse, K, V = attend(q, k, v, lens)
+    check(out, lse, q, K, V, lens)
+
+
+@pytest.mark.parametrize("factor", [64.0, 1000.0, 1e6])
+def test_one_large_channel_of_a_query(factor):
+    S, H, n, D = 1, 2, 1104, 128
+    k, v = rnd(S, H, n, D), rnd(S, H, n, D, seed=1)
+    k[..., :32] /= factor
+    q = rnd(S * H, 4, D, seed=5)
+    q[..., 5] *= factor
+    q = q.float()
+    out, lse, K, V = attend(q, k, v, [n])
+    check(out, lse, q, K, V, [n])
+
+
 LARGEST = torch.finfo(torch.float32).max
 
 
