@@ -14,6 +14,7 @@
 #include <cmath>
 
 #include "fathom_internal.cuh"
+#include "row_ranges.cuh"
 
 namespace fathom {
 
@@ -1043,6 +1044,24 @@ static int check_rope(const fathom_rope &r, int D, int row_dtype, int32_t total_
     return FATHOM_OK;
 }
 
+// The rotated queries' place may share no byte with what is read: rows are read more than once, by
+// several threads.  Checked last, of arguments that are in order.
+static int check_rope_place(const fathom_rope *r, int D, const void *k_new, const void *v_new, int32_t kv_heads,
+                            int32_t total_new, int64_t new_token, int64_t new_head) {
+    if (!r || !r->q) return FATHOM_OK;
+    auto rows = [&](const void *p, int64_t heads, int64_t token, int64_t head, int64_t size) {
+        return RowSet{(uint64_t)(uintptr_t)p, {total_new, heads}, {token * size, head * size}, D * size};
+    };
+    const RowSet out = rows(r->q_out, r->q_heads, r->out_token, r->out_head, r->q_dtype == FATHOM_F32 ? 4 : 2);
+    const char *what = rows_meet(out, rows(r->q, r->q_heads, r->q_token, r->q_head, 2))       ? "q"
+                       : rows_meet(out, rows(k_new, kv_heads, new_token, new_head, 2)) ? "k_new"
+                       : rows_meet(out, rows(v_new, kv_heads, new_token, new_head, 2)) ? "v_new"
+                                                                                       : nullptr;
+    if (!what) return FATHOM_OK;
+    set_error("rope: q_out overlaps %s", what);
+    return FATHOM_EINVAL;
+}
+
 int fathom_paged_append_rope(const fathom_pages *pages, void *k_pages, void *v_pages, const int32_t *page_table,
                              const void *k_new, const void *v_new, int32_t total_new, int64_t new_token,
                              int64_t new_head, const int32_t *start, const int32_t *cu_new, const fathom_rope *rope,
@@ -1065,6 +1084,8 @@ int fathom_paged_append_rope(const fathom_pages *pages, void *k_pages, void *v_p
         set_error("paged_append_rope: k_new and v_new must be 16-byte aligned"); return FATHOM_EINVAL;
     }
     FAULT_POINT("fathom_paged_append_rope");
+    rc = check_rope_place(rope, pages->D, k_new, v_new, pages->kv_heads, total_new, new_token, new_head);
+    if (rc) return rc;
     return launch_paged_append_rope(*pages, k_pages, v_pages, page_table, k_new, v_new, total_new, new_token, new_head,
                                     start, cu_new, *rope, (cudaStream_t)stream);
 }
@@ -1125,6 +1146,8 @@ int fathom_nibble_append(const fathom_nibble_pages *pages, void *kv_pages, const
         set_error("nibble_append: k_new and v_new must be 16-byte aligned"); return FATHOM_EINVAL;
     }
     FAULT_POINT("fathom_nibble_append");
+    rc = check_rope_place(rope, pages->D, k_new, v_new, pages->kv_heads, total_new, new_token, new_head);
+    if (rc) return rc;
     return launch_nibble_append(*pages, kv_pages, page_table, row_dtype, k_new, v_new, total_new, new_token, new_head, start,
                                 cu_new, rope, (cudaStream_t)stream);
 }

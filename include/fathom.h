@@ -204,7 +204,9 @@ typedef struct {
     const int32_t *positions;    /* [total_new], or NULL: a token's place in its sequence (after an
                                     eviction the two differ) */
     const void *q;               /* NULL, or queries [total_new][q_heads][D] of the new rows' type */
-    void *q_out;                 /* [total_new][q_heads][D], not q */
+    void *q_out;                 /* [total_new][q_heads][D]; shares no byte with q, k_new or v_new (rows of
+                                    one buffer may lie between each other's where their strides in bytes
+                                    are equal) */
     int32_t q_heads;             /* 1 .. 65535 */
     int32_t q_dtype;             /* of q_out: the new rows' type, or FATHOM_F32 (what the decode calls take) */
     int64_t q_token, q_head, out_token, out_head;   /* elements, positive multiples of 8 */
