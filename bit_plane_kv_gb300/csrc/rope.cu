@@ -89,16 +89,37 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either 
     return r;
 }
 
-// x c + y s rounded to odd: cut off to 24 bits, the last bit set where something was cut.
+// x c + y s rounded to odd: cut off to 24 bits, the last bit set where something was cut.  r is
+// the sum rounded in some way, and what that leaves out makes its size more or less.
+__device__ __forceinline__ float to_odd(float r, bool more, bool less) {
+    uint32_t u = __float_as_uint(r);
+    if ((more || less) && !(u & 1u)) u += more ? 1u : 0xffffffffu;
+    return __uint_as_float(u);
+}
+// Any numbers.  In 64 bits the products are exact (35 bits, none too small or too large), and so is
+// the sum with what it leaves out.
+__device__ __noinline__ float turn_far(float x, float y, float c, float s) {
+    const double p = (double)x * c, q = (double)y * s, h = p + q, b = h - p, e = (p - (h - b)) + (q - b);
+    const float r = __double2float_rz(h);
+    if (!(fabs(h) < CUDART_INF)) return r;                     // infinities and NaN
+    const double d = h - r, rest = d != 0.0 ? d : e;           // |e| is less than h's last bit, d a multiple of it
+    return to_odd(r, rest != 0.0 && (rest > 0.0) == (h > 0.0), rest != 0.0 && (rest > 0.0) != (h > 0.0));
+}
+__device__ __forceinline__ float add_exact(float a, float b, float &left) {
+    const float h = a + b, z = h - a;
+    left = (a - (h - z)) + (b - z);
+    return h;
+}
+// In 32 bits where the products' errors are numbers too and what their sums leave out cannot change
+// the sign of the rest (64 bits for all: one decode step of 61 sessions with its read-back 7.5 -> 16.8 us).
 __device__ __forceinline__ float turn_odd(float x, float y, float c, float s) {
     const float p = __fmul_rn(x, c), q = __fmul_rn(y, s);
-    const float h = p + q, b = h - p;
-    const float e = (p - (h - b)) + (q - b) + (fmaf(x, c, -p) + fmaf(y, s, -q));   // what h leaves out
-    const float r = h + e, d = e - (r - h);                                        // |e| < |h|
-    if (!(fabsf(r) < CUDART_INF_F)) return fabsf(h) < CUDART_INF_F ? r : h;        // the errors of an infinity are NaN
-    uint32_t u = __float_as_uint(r);
-    if (d != 0.0f && !(u & 1u)) u += (d > 0.0f) == (r > 0.0f) ? 1u : 0xffffffffu;
-    return __uint_as_float(u);
+    float t, w2, e2, d;
+    const float h = add_exact(p, q, t), w = add_exact(fmaf(x, c, -p), fmaf(y, s, -q), w2);
+    const float e = add_exact(t, w, e2), r = add_exact(h, e, d), tail = fabsf(w2) + fabsf(e2);
+    auto whole = [](float x, float c, float p) { return (fabsf(p) >= 0x1p-100f && fabsf(p) < 0x1p126f) || x == 0.0f || c == 0.0f; };
+    if (!(whole(x, c, p) && whole(y, s, q) && (tail == 0.0f || fabsf(d) > 2.0f * tail))) return turn_far(x, y, c, s);
+    return to_odd(r, d != 0.0f && (d > 0.0f) == (r > 0.0f), d != 0.0f && (d > 0.0f) != (r > 0.0f));
 }
 
 // The sequence of packed token t and its place in it (false: behind the last one).  Whole
