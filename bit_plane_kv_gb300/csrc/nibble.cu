@@ -18,8 +18,8 @@ namespace {
 // operand holds a head's values in two columns, so four heads fill one instruction.
 // A query's pieces are whole numbers of 12 bits (to 2^-22 of its group's largest channel, as
 // long as that is not below 2^-23 of the row's), so that the sums over a group of 32 channels
-// are exact whatever the tensor cores cut off; a weight's
-// are fp16 (22 bits, and down to 2^-38 of the largest).
+// are exact whatever the tensor cores cut off; a weight's are fp16 (22 bits, and down to
+// 2^-38 of the largest).
 //
 // Codes become fp16 in one operation: four bits left in the low bits of a 16-bit half are
 // the subnormal c 2^-24, and a whole byte is (c + 16 c') 2^-24 with its neighbour c'.  Bytes
@@ -36,17 +36,18 @@ namespace {
 // (hi + lo) a in three fp16 operations for two tokens, the rounding error of hi a going to
 // the second piece; the weights are kept 2^13, the scales 2^k larger (k by the largest scale
 // so far), so that these errors stay clear of the subnormals: off by 2^-22, or by 2^-35 of
-// the largest weight and scale.  That is little beside the sum as long as all scales of the unit
-// that the warp has seen lie within 2^9 of each other (2^-24.5 of it per token at most).  From where they do
-// not on, a small group or a light token of large values would cost the others their bits: products
-// are then taken in fp32, each block's brought to 2^13 .. 2^14 by their largest of a head and
-// group, and added to the sums in shared memory (32 x 32k tokens 128 -> 207 us, 8 heads per unit 197 -> 383).
-// The scores' layout (tokens by heads) becomes the weights' operand (heads by tokens) by one
-// 8 x 8 transposition in registers per 8 tokens and group.
+// the largest weight and scale.  That is little beside the sum as long as all scales of the
+// unit that the warp has seen lie within 2^9 of each other (2^-24.5 of it per token at most).
+// Once they do not, a small group or a light token of large values would cost the others
+// their bits: from there on products are taken in fp32, each block's brought to 2^13 .. 2^14
+// by their largest of a head and group, and added to the sums in shared memory (32 x 32k
+// tokens 128 -> 207 us, 8 heads per unit 196 -> 384).  The scores' layout (tokens by
+// heads) becomes the weights' operand (heads by tokens) by one 8 x 8 transposition in
+// registers per 8 tokens and group.
 //
 // Measured, 128 channels, 4 heads per unit: 32 sequences of up to 32k tokens, 8 KV heads,
-// 649 MB, 128 us, 5.1 TB/s (8 heads per unit 197 us; 64 channels 77); one of 131072 tokens
-// 39 us, one of 4096 10.2.  290 instructions per block: 62 % of the issue slots, 47 % of the
+// 649 MB, 128 us, 5.1 TB/s (8 heads per unit 196 us; 64 channels 77); one of 131072 tokens
+// 40 us, one of 4096 10.4.  300 instructions per block: 63 % of the issue slots, 47 % of the
 // logic pipe, and in the rest dependent instructions of 16 warps.
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;

@@ -15,7 +15,7 @@ namespace {
 // K, of the queries, of V), so that the rotation's cos and sin, the page and the place are
 // found once.  Bound by the bytes, each row read and written once: prompts of 19k tokens, 8
 // KV heads and 32 query heads of 128 channels, 473 MB, 75 us, 6.3 TB/s.  In 4 bits the
-// coding's instructions and the bytes take about as long: the same rows 86 us.
+// coding's instructions and the bytes take about as long: the same rows 85 us.
 //
 // A pair (x, y) turns by (x cos - y sin, y cos + x sin), a product and a fused multiply-add
 // in fp32, off by 2^-24 of |x cos| + |y sin| and of the result.
@@ -25,10 +25,15 @@ namespace {
 // never too large gives the code or the one below it, and one fused multiply-add tells
 // which.  Rotated keys are coded from fp32 like the queries, with a bound on what that is
 // off by; where a border between two codes, or between two scales, is nearer than the
-// bound (one group of 2000), the group is worked out again exactly: the products' errors
-// and the sum's are exact, and the result is rounded to odd (cut off to 24 bits, the last
-// bit set where something was cut), after which comparisons with the borders, numbers of
-// 14 bits, and the rounding to fp16 are those of the unrounded key.
+// bound (one group of 2000), the group is worked out again exactly, and the result is
+// rounded to odd (cut off to 24 bits, the last bit set where something was cut), after
+// which comparisons with the borders, numbers of 14 bits, and the rounding to fp16 are
+// those of the unrounded key.
+//
+// Rows that turn whole, in halves, have both partners in one thread.  Other rotations take a
+// chunk of 8 channels per thread, partners in the other half loaded again: the prompts above
+// with 64 of 128 channels rotated 98 us into 16 bits and 150 into 4, in neighbouring pairs
+// 118 and 138.
 
 constexpr int kThreads = 128;
 constexpr int kBatch = 2;       // rows loaded together

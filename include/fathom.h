@@ -25,10 +25,10 @@
  *   the stream reaches them.  The kernels of fathom_plan, fathom_plan_fixed,
  *   fathom_scan_topk, fathom_scan, fathom_select, fathom_exact_topk, fathom_sparse_attn,
  *   fathom_sparse_attn_planes, fathom_sparse_attn_noalloc, fathom_paged_attn,
- *   fathom_paged_evict, fathom_paged_append_rope and the fathom_nibble calls are launched with programmatic stream serialisation: each may
- *   be scheduled while the work before it on the stream is finishing, but it waits for
- *   that work to complete before it reads or writes memory, so the stream order is
- *   unchanged.
+ *   fathom_paged_evict, fathom_paged_append_rope and the fathom_nibble calls are
+ *   launched with programmatic stream serialisation: each may be scheduled while the
+ *   work before it on the stream is finishing, but it waits for that work to complete
+ *   before it reads or writes memory, so the stream order is unchanged.
  * - Every call returns a fathom_status.  Argument errors return FATHOM_EINVAL
  *   before anything is enqueued; CUDA launch errors return FATHOM_ECUDA.
  *   fathom_last_error() returns the calling thread's last message.  Nothing
