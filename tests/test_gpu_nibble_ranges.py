@@ -197,3 +197,65 @@ def test_a_log_sum_exp_beyond_the_largest_number_is_infinite():
     q[0, 1] = -q[0, 1]
     out, lse, K, V = attend(q, k, v, [32])
     assert lse[0, 0] == math.inf and lse[0, 1] == -math.inf and torch.isfinite(out).all()
+
+
+# ------------------------------------------------------------------ what may lie beside values of different sizes
+def wide_cache(S, H, n, D):
+    """Pages whose V scales are 2^-21 to 2^15."""
+    k, v = rnd(S * n // 16, H, 16, D), rnd(S * n // 16, H, 16, D, seed=1)
+    v *= 2.0 ** torch.randint(-11, 12, (S * n // 16, H, 16, 1), generator=gen(3), device="cuda").double()
+    v *= 2.0 ** (2 - 3 * (torch.arange(D, device="cuda") // 32))
+    return N.pack(k, v), torch.arange(S * n // 16, dtype=torch.int32, device="cuda").reshape(S, n // 16)
+
+
+@pytest.mark.parametrize("D,G", [(128, 4), (64, 8), (96, 3)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_places_behind_the_length_and_missing_pages_beside_values_of_different_sizes(bad, D, G):
+    S, H, n = 3, 2, 1024
+    kv, table = wide_cache(S, H, n, D)
+    lens, q = [1003, 70, 1], rnd(S * H, G, D, seed=5).float()
+    table[0, 5], table[0, 33], table[1, 0] = -1, 1 << 30, kv.shape[0]
+    pages = B.make_nibble_pages(kv, table, D)
+    ws = B.alloc_nibble_workspace(pages, G=G)
+    want, z = B.fathom_nibble_attn(pages, q, kv, table, i32(lens), ws, want_lse=True)
+    K, V = N.unpack(kv, D)
+    keep = torch.ones(S, n, dtype=torch.bool, device="cuda")
+    for s, p in ((0, 5), (0, 33), (1, 0)):
+        keep[s, 16 * p:16 * p + 16] = False
+    for s in range(S):
+        for h in range(H):
+            rows = [x[s * n // 16:(s + 1) * n // 16, h].reshape(n, D)[:lens[s]][keep[s, :lens[s]]] for x in (K, V)]
+            u = s * H + h
+            check(want[u:u + 1], z[u:u + 1], q[u:u + 1], rows[0][None, None], rows[1][None, None], [rows[0].shape[0]])
+    x = kv.view(S, n // 16, H, 18 * D)                                      # a page is a block
+    bits = torch.tensor([bad], dtype=torch.float16, device="cuda").view(torch.uint8)
+    for s in range(S):
+        for p in range(n // 16):
+            for t in range(16):
+                if 16 * p + t >= lens[s] or not keep[s, 16 * p]:
+                    for base in (8 * D, 17 * D):
+                        for g in range(D // 32):
+                            at = base + 4 * ((t & 7) * (D // 32) + g) + 2 * (t >> 3)
+                            x[s, p, :, at:at + 2] = bits
+    n_of = i32(lens)
+    graph, out, lse = torch.cuda.CUDAGraph(), torch.empty_like(want), torch.empty_like(z)
+    with torch.cuda.graph(graph):
+        B.fathom_nibble_attn(pages, q, kv, table, n_of, ws, out=out, lse=lse)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, z)
+
+
+def test_a_nan_beside_values_of_different_sizes_stays_in_its_group():
+    D, n = 128, 1024
+    kv, table = wide_cache(2, 2, n, D)
+    pages, q = B.make_nibble_pages(kv, table, D), rnd(4, 4, D, seed=5).float()
+    ws = B.alloc_nibble_workspace(pages)
+    want = B.fathom_nibble_attn(pages, q, kv, table, i32([n, n]), ws)
+    at = 17 * D + 4 * ((600 % 8) * 4 + 2) + 2 * (600 % 16 // 8)             # token 600 of unit 1, group 2 of V
+    kv[600 // 16, 1, at:at + 2] = torch.tensor([float("nan")], dtype=torch.float16, device="cuda").view(torch.uint8)
+    got = B.fathom_nibble_attn(pages, q, kv, table, i32([n, n]), ws)
+    assert torch.isnan(got[1, :, 64:96]).all()
+    got[1, :, 64:96] = want[1, :, 64:96]
+    assert torch.equal(got, want)
